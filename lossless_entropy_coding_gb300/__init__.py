@@ -1,8 +1,10 @@
 """Python binding of libecc_gb300: lossless fixed-codebook coding of e4m3
-byte tensors on GB300 (Quad Length Codes and single-stage canonical Huffman).
+byte tensors on GB300 (Quad Length Codes and single-stage canonical Huffman),
+and the language-model operators next to the coders (layer norm, the matrix
+product with a fused epilogue, token log probabilities, and their gradients).
 
 Argument marshalling only.  Every entry point has the name of the C function
-it calls (see include/ecc.h for the contract); PyTorch supplies device memory
+it calls (see include/ecc.h and include/ecc_lm.h for the contract); PyTorch supplies device memory
 and the current CUDA stream.  All coding work runs in the library's CUDA
 kernels or its host codebook builders -- there is no other code path: if the
 shared library has not been built, importing the binding still works but
@@ -11,7 +13,9 @@ every call raises.
 from __future__ import annotations
 
 import ctypes as ct
+import functools
 import os
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -65,6 +69,7 @@ def _load():
                                "`python -m lossless_entropy_coding_gb300.build`")
         lib = ct.CDLL(LIB_PATH)
         P, Z, U32, U64, I32, D = ct.c_void_p, ct.c_size_t, ct.c_uint32, ct.c_uint64, ct.c_int32, ct.c_double
+        F = ct.c_float
         sig = {
             "ecc_codebook_bytes": (Z, []),
             "qlc_build_tables": (I32, [P, P, P]),
@@ -97,6 +102,15 @@ def _load():
             "bf16_escape_max_encoded_bytes": (Z, [Z, U32]),
             "bf16_escape_encode": (I32, [P, Z, P, U32, U32, P, Z, P, P, P, P, Z, P, P]),
             "bf16_escape_decode": (I32, [P, Z, P, P, Z, U32, U32, P, P, P, P]),
+            "ecc_layer_norm": (I32, [P, U64, U32, P, P, U32, U64, U64, F, P, U64, U32, F, P, P, P]),
+            "ecc_layer_norm_grad_workspace_bytes": (Z, [U64, U64]),
+            "ecc_layer_norm_grad": (I32, [P, U64, P, U64, U32, P, U32, P, P, U64, U64, P, U64, P, P, P, Z, P]),
+            "ecc_linear_workspace_bytes": (Z, [P]),
+            "ecc_linear": (I32, [P, P, Z, P, P]),
+            "ecc_linear_grad_workspace_bytes": (Z, [P]),
+            "ecc_linear_grad": (I32, [P, P, Z, P, P]),
+            "ecc_token_logprob": (I32, [P, U64, U32, P, U64, U64, F, U32, P, P, P, P, P, P]),
+            "ecc_token_logprob_grad": (I32, [P, U64, U32, P, U64, U64, F, P, P, P, P, P, U64, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -525,3 +539,300 @@ def bf16_escape_decode(enc: Encoded, top7, out=None, status=None, stream=None):
                                       _dptr(enc.sub_bits), enc.n, enc.C, enc.S, _np_ptr(top7), _dptr(out),
                                       _dptr(status), _stream_ptr(stream)), "bf16_escape_decode")
     return out, status
+
+
+# ---------------------------------------------------------------- language-model operators
+# Matrices are torch tensors [..., columns] whose last dimension is contiguous
+# and whose leading dimensions collapse to rows of one stride.  e4m3 tensors
+# are uint8 (the coders' bytes) or torch.float8_e4m3fn.  A call on another
+# stream than the current one allocates its outputs and scratch for that
+# stream; the caller orders the streams, as for the coding calls.
+
+F32, BF16, F16, E4M3 = range(4)
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+MAX_TOP = 32
+
+_types = {}
+
+
+def _type(t, what: str) -> int:
+    if not _types:
+        torch = _torch()
+        _types.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3,
+                       torch.uint8: E4M3})
+    code = _types.get(t)
+    if code is None:
+        raise EccError(ERR_ARG, f"{what}: element type {t}")
+    return code
+
+
+def _refuse(ok: bool, what: str):
+    if not ok:
+        raise EccError(ERR_ARG, what)
+
+
+def _matrix(t, what: str):
+    """(rows, columns, leading dimension) of a tensor of rows."""
+    shape, stride = t.shape, t.stride()
+    n = len(shape)
+    _refuse(n >= 1 and (shape[-1] <= 1 or stride[-1] == 1), f"{what}: rows are not contiguous")
+    cols = shape[-1]
+    if n == 2:
+        rows = shape[0]
+        return rows, cols, stride[0] if rows > 1 else cols
+    rows, ld = 1, cols
+    for i in range(n - 2, -1, -1):
+        if shape[i] == 1:
+            continue
+        if rows == 1:
+            ld = stride[i]
+        else:
+            _refuse(shape[i] == 0 or stride[i] == rows * ld, f"{what}: leading dimensions do not collapse")
+        rows *= shape[i]
+    return rows, cols, ld
+
+
+def _vector(t, n: int, dev: int, what: str, dtype=None):
+    """Pointer of a contiguous tensor of n elements (0 for None)."""
+    if t is None:
+        return 0
+    _refuse(t.numel() == n and t.is_contiguous() and t.get_device() == dev and (dtype is None or t.dtype == dtype), what)
+    return t.data_ptr()
+
+
+def _on_stream(f):
+    """Run f with the device of its first tensor current and, where a stream is
+    given, with that stream current (so that what f allocates belongs to it);
+    f gets the stream's handle."""
+    @functools.wraps(f)
+    def call(x, *args, stream=None, **kw):
+        torch = _torch()
+        _refuse(isinstance(x, torch.Tensor) and x.is_cuda, f"{f.__name__}: needs CUDA tensors")
+        dev = x.get_device()
+        if stream is None and dev == torch.cuda.current_device():
+            return f(x, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+        with torch.cuda.device(dev):
+            s = torch.cuda.current_stream() if stream is None else stream
+            with torch.cuda.stream(s):
+                return f(x, *args, stream=s.cuda_stream, **kw)
+    return call
+
+
+@_on_stream
+def ecc_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, out_dtype=None, out_scale: float = 1.0,
+                   mean=None, rstd=None, stream=None):
+    """Layer norm over the last dimension of device tensor x; returns (out,
+    mean, rstd).  out_dtype: x's type (default), or uint8 / float8_e4m3fn for
+    e4m3 values of out * out_scale.  weight, bias: of x's type or float32."""
+    torch = _torch()
+    dev = x.get_device()
+    rows, cols, ldx = _matrix(x, "ecc_layer_norm: x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    _refuse(out.shape == x.shape and out.get_device() == dev, "ecc_layer_norm: out")
+    _, _, ldy = _matrix(out, "ecc_layer_norm: out")
+    if mean is None:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    p_dtype = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
+    _check(_load().ecc_layer_norm(
+        x.data_ptr(), ldx, _type(x.dtype, "ecc_layer_norm"),
+        _vector(weight, cols, dev, "ecc_layer_norm: weight"), _vector(bias, cols, dev, "ecc_layer_norm: bias", p_dtype),
+        _type(p_dtype, "ecc_layer_norm"), rows, cols, eps, out.data_ptr(), ldy, _type(out.dtype, "ecc_layer_norm"),
+        out_scale, _vector(mean, rows, dev, "ecc_layer_norm: mean", torch.float32),
+        _vector(rstd, rows, dev, "ecc_layer_norm: rstd", torch.float32), stream), "ecc_layer_norm")
+    return out, mean, rstd
+
+
+def layer_norm_grad_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_load().ecc_layer_norm_grad_workspace_bytes(rows, cols))
+
+
+@_on_stream
+def ecc_layer_norm_grad(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, ws=None, stream=None):
+    """Backward pass of ecc_layer_norm; returns (dx, dweight, dbias), the last
+    two float32.  weight None: ones (dweight and dbias are still summed)."""
+    torch = _torch()
+    dev = dy.get_device()
+    rows, cols, ldx = _matrix(x, "ecc_layer_norm_grad: x")
+    _refuse(x.shape == dy.shape and x.dtype == dy.dtype and x.get_device() == dev, "ecc_layer_norm_grad: x")
+    _, _, lddy = _matrix(dy, "ecc_layer_norm_grad: dy")
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _refuse(dx.shape == x.shape and dx.dtype == x.dtype and dx.get_device() == dev, "ecc_layer_norm_grad: dx")
+    _, _, lddx = _matrix(dx, "ecc_layer_norm_grad: dx")
+    if dweight is None:
+        dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
+    if dbias is None:
+        dbias = torch.empty(cols, dtype=torch.float32, device=x.device)
+    lib = _load()
+    if ws is None:
+        ws = torch.empty(lib.ecc_layer_norm_grad_workspace_bytes(rows, cols), dtype=torch.uint8, device=x.device)
+    _refuse(mean is not None and rstd is not None, "ecc_layer_norm_grad: mean and rstd")
+    _check(lib.ecc_layer_norm_grad(
+        dy.data_ptr(), lddy, x.data_ptr(), ldx, _type(x.dtype, "ecc_layer_norm_grad"),
+        _vector(weight, cols, dev, "ecc_layer_norm_grad: weight"),
+        _type(x.dtype if weight is None else weight.dtype, "ecc_layer_norm_grad"),
+        _vector(mean, rows, dev, "ecc_layer_norm_grad: mean", torch.float32),
+        _vector(rstd, rows, dev, "ecc_layer_norm_grad: rstd", torch.float32), rows, cols, dx.data_ptr(), lddx,
+        _vector(dweight, cols, dev, "ecc_layer_norm_grad: dweight", torch.float32),
+        _vector(dbias, cols, dev, "ecc_layer_norm_grad: dbias", torch.float32), ws.data_ptr(), ws.numel(), stream),
+        "ecc_layer_norm_grad")
+    return dx, dweight, dbias
+
+
+_LINEAR_JOB = struct.Struct("@6P8Q2f6I")        # ecc_linear_job
+_LINEAR_GRAD_JOB = struct.Struct("@7P9Qf5I")    # ecc_linear_grad_job
+
+
+def _activation(act: str, what: str) -> int:
+    _refuse(act in ACTIVATIONS, f"{what}: activation {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _operand(t, rows: int, cols: int, dev: int, what: str):
+    """(pointer, leading dimension, type) of a [rows, cols] tensor (zeros for None)."""
+    if t is None:
+        return 0, 0, 0
+    r, c, ld = _matrix(t, what)
+    _refuse(r == rows and c == cols and t.get_device() == dev, f"{what}: shape or device")
+    return t.data_ptr(), ld, _type(t.dtype, what)
+
+
+@_on_stream
+def ecc_linear(x, w, bias=None, residual=None, act: str = "none", scale: float = 1.0, out=None, out_dtype=None,
+               out_scale: float = 1.0, pre=None, ws=None, status=None, stream=None):
+    """act(scale * x w^T + bias) + residual of device tensors x [..., K] and
+    w [N, K] (bfloat16, float16 or e4m3); returns (out [..., N], status).
+    out_dtype: x's type by default, bfloat16 for e4m3 operands; uint8 or
+    float8_e4m3fn: e4m3 values of out * out_scale.  pre: a tensor [..., N]
+    that receives the activation's argument, for ecc_linear_grad."""
+    torch = _torch()
+    dev = x.get_device()
+    M, K, ldx = _matrix(x, "ecc_linear: x")
+    in_type = _type(x.dtype, "ecc_linear: x")
+    _refuse(w.dim() == 2, "ecc_linear: w")
+    N = w.shape[0]
+    pw, ldw, w_type = _operand(w, N, K, dev, "ecc_linear: w")
+    _refuse(w_type == in_type, "ecc_linear: x and w of different types")
+    if out is None:
+        out = torch.empty((*x.shape[:-1], N), device=x.device,
+                          dtype=out_dtype or (torch.bfloat16 if in_type == E4M3 else x.dtype))
+    if status is None:
+        status = torch.empty(1, dtype=torch.int32, device=x.device)
+    pout, ldout, out_type = _operand(out, M, N, dev, "ecc_linear: out")
+    pres, ldres, res_type = _operand(residual, M, N, dev, "ecc_linear: residual")
+    ppre, ldpre, pre_type = _operand(pre, M, N, dev, "ecc_linear: pre")
+    job = _LINEAR_JOB.pack(x.data_ptr(), pw, _vector(bias, N, dev, "ecc_linear: bias"), pres, pout, ppre, M, N, K, ldx,
+                           ldw, ldres, ldout, ldpre, scale, out_scale, in_type,
+                           0 if bias is None else _type(bias.dtype, "ecc_linear: bias"), res_type, out_type, pre_type,
+                           _activation(act, "ecc_linear"))
+    lib = _load()
+    if ws is None:
+        need = lib.ecc_linear_workspace_bytes(job)
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _check(lib.ecc_linear(job, 0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                          _vector(status, 1, dev, "ecc_linear: status", torch.int32), stream), "ecc_linear")
+    return out, status
+
+
+@_on_stream
+def ecc_linear_grad(dy, x, w, pre=None, act: str = "none", scale: float = 1.0, dx=None, dw=None, dbias=None,
+                    dw_dtype=None, want=("dx", "dw", "dbias"), ws=None, status=None, stream=None):
+    """Backward pass of ecc_linear's product; returns (dx, dw, dbias, status),
+    None for what `want` leaves out.  pre: the activation's argument (needed
+    unless act is "none").  dw_dtype: x's type (default) or float32; dbias is
+    float32."""
+    torch = _torch()
+    dev = dy.get_device()
+    M, N, lddy = _matrix(dy, "ecc_linear_grad: dy")
+    in_type = _type(dy.dtype, "ecc_linear_grad: dy")
+    K = x.shape[-1]
+    px, ldx, x_type = _operand(x, M, K, dev, "ecc_linear_grad: x")
+    pw, ldw, w_type = _operand(w, N, K, dev, "ecc_linear_grad: w")
+    _refuse(x_type == in_type and w_type == in_type, "ecc_linear_grad: dy, x and w of different types")
+    ppre, ldpre, pre_type = _operand(pre, M, N, dev, "ecc_linear_grad: pre")
+    if dx is None and "dx" in want:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dw is None and "dw" in want:
+        dw = torch.empty((N, K), dtype=dw_dtype or x.dtype, device=x.device)
+    if dbias is None and "dbias" in want:
+        dbias = torch.empty(N, dtype=torch.float32, device=x.device)
+    if status is None:
+        status = torch.empty(1, dtype=torch.int32, device=x.device)
+    pdx, lddx, dx_type = _operand(dx, M, K, dev, "ecc_linear_grad: dx")
+    _refuse(dx is None or dx_type == in_type, "ecc_linear_grad: dx")
+    pdw, lddw, dw_type = _operand(dw, N, K, dev, "ecc_linear_grad: dw")
+    job = _LINEAR_GRAD_JOB.pack(dy.data_ptr(), px, pw, ppre, pdx, pdw,
+                                _vector(dbias, N, dev, "ecc_linear_grad: dbias", torch.float32), M, N, K, lddy, ldx,
+                                ldw, ldpre, lddx, lddw, scale, in_type, pre_type, dw_type,
+                                _activation(act, "ecc_linear_grad"), 0)
+    lib = _load()
+    if ws is None:
+        need = lib.ecc_linear_grad_workspace_bytes(job)
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _check(lib.ecc_linear_grad(job, 0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                               _vector(status, 1, dev, "ecc_linear_grad: status", torch.int32), stream),
+           "ecc_linear_grad")
+    return dx, dw, dbias, status
+
+
+@dataclass
+class TokenLogprob:
+    """Device tensors of ecc_token_logprob (None where not asked for), in nats."""
+    logprob: object
+    entropy: object
+    lse: object
+    top_logprob: object
+    top_index: object
+
+
+@_on_stream
+def ecc_token_logprob(logits, tokens=None, top: int = 0, scale: float = 1.0, stream=None) -> TokenLogprob:
+    """Log probabilities of tokens (int64 [...], negative: none) under softmax
+    of scale * logits [..., vocab], with each row's entropy, log partition and
+    `top` most probable tokens (at most 32)."""
+    torch = _torch()
+    dev = logits.get_device()
+    rows, vocab, ld = _matrix(logits, "ecc_token_logprob: logits")
+    lead = logits.shape[:-1]
+    _refuse(0 <= top <= MAX_TOP, "ecc_token_logprob: top")
+    ptok = _vector(tokens, rows, dev, "ecc_token_logprob: tokens", torch.int64)
+    stat = torch.empty((3, *lead), dtype=torch.float32, device=logits.device)
+    logprob, entropy, lse = stat.unbind(0)
+    top_logprob = top_index = None
+    if top:
+        top_logprob = torch.empty((*lead, top), dtype=torch.float32, device=logits.device)
+        top_index = torch.empty((*lead, top), dtype=torch.int32, device=logits.device)
+    _check(_load().ecc_token_logprob(
+        logits.data_ptr(), ld, _type(logits.dtype, "ecc_token_logprob"), ptok, rows, vocab, scale, top,
+        logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logprob.data_ptr() if top else 0,
+        top_index.data_ptr() if top else 0, stream), "ecc_token_logprob")
+    return TokenLogprob(logprob if tokens is not None else None, entropy, lse, top_logprob, top_index)
+
+
+@_on_stream
+def ecc_token_logprob_grad(logits, tokens, lse, entropy=None, dlogprob=None, dentropy=None, scale: float = 1.0,
+                           dlogits=None, stream=None):
+    """Gradient with respect to the logits of sum(dlogprob * logprob +
+    dentropy * entropy); returns dlogits (which may be given as logits
+    itself)."""
+    torch = _torch()
+    dev = logits.get_device()
+    rows, vocab, ld = _matrix(logits, "ecc_token_logprob_grad: logits")
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    _refuse(dlogits.shape == logits.shape and dlogits.dtype == logits.dtype and dlogits.get_device() == dev,
+            "ecc_token_logprob_grad: dlogits")
+    _, _, ldd = _matrix(dlogits, "ecc_token_logprob_grad: dlogits")
+    f = torch.float32
+    _check(_load().ecc_token_logprob_grad(
+        logits.data_ptr(), ld, _type(logits.dtype, "ecc_token_logprob_grad"),
+        _vector(tokens, rows, dev, "ecc_token_logprob_grad: tokens", torch.int64), rows, vocab, scale,
+        _vector(lse, rows, dev, "ecc_token_logprob_grad: lse", f),
+        _vector(entropy, rows, dev, "ecc_token_logprob_grad: entropy", f),
+        _vector(dlogprob, rows, dev, "ecc_token_logprob_grad: dlogprob", f),
+        _vector(dentropy, rows, dev, "ecc_token_logprob_grad: dentropy", f), dlogits.data_ptr(), ldd, stream),
+        "ecc_token_logprob_grad")
+    return dlogits

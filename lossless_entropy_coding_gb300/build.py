@@ -37,7 +37,7 @@ def sources():
 
 def _deps():
     files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    files.append(os.path.join(INCLUDE, "ecc.h"))
+    files += [os.path.join(INCLUDE, f) for f in ("ecc.h", "ecc_lm.h")]
     return files
 
 

@@ -1,0 +1,77 @@
+// ecc_lm.cuh -- element types, conversions and block reductions shared by the
+// language-model operators (layer norm, matrix product, token log
+// probabilities).
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "../../include/ecc_lm.h"
+#include "ecc_launch.h"
+
+namespace ecc {
+
+using bf16 = __nv_bfloat16;
+struct e4m3 {
+    uint8_t b;
+};
+
+template <typename T> struct TypeCode;
+template <> struct TypeCode<float> { static constexpr uint32_t value = ECC_F32; };
+template <> struct TypeCode<bf16> { static constexpr uint32_t value = ECC_BF16; };
+template <> struct TypeCode<__half> { static constexpr uint32_t value = ECC_F16; };
+template <> struct TypeCode<e4m3> { static constexpr uint32_t value = ECC_E4M3; };
+
+inline uint32_t type_bytes(uint32_t t) { return t == ECC_F32 ? 4u : t == ECC_E4M3 ? 1u : 2u; }
+inline bool wide_type(uint32_t t) { return t == ECC_F32 || t == ECC_BF16 || t == ECC_F16; }
+inline bool aligned_to(const void *p, uint32_t t) { return ((uintptr_t)p & (type_bytes(t) - 1)) == 0; }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(e4m3 v)
+{
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(v.b, __NV_E4M3)));
+}
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ bf16 from_f32<bf16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ e4m3 from_f32<e4m3>(float v)
+{
+    return e4m3{(uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3)};
+}
+
+// element i of an array whose type is known at run time
+__device__ __forceinline__ float load_any(const void *p, uint64_t i, uint32_t type)
+{
+    if (type == ECC_F32)
+        return static_cast<const float *>(p)[i];
+    if (type == ECC_BF16)
+        return to_f32(static_cast<const bf16 *>(p)[i]);
+    return to_f32(static_cast<const __half *>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void *p, uint64_t i, uint32_t type, float v)
+{
+    if (type == ECC_F32)
+        static_cast<float *>(p)[i] = v;
+    else if (type == ECC_BF16)
+        static_cast<bf16 *>(p)[i] = from_f32<bf16>(v);
+    else if (type == ECC_F16)
+        static_cast<__half *>(p)[i] = from_f32<__half>(v);
+    else
+        static_cast<e4m3 *>(p)[i] = from_f32<e4m3>(v);
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+} // namespace ecc
