@@ -1,0 +1,612 @@
+// ecc_gemm.cu -- matrix products on the tensor cores (tcgen05, operands by
+// tiled TMA, accumulators in tensor memory) with the linear operators'
+// epilogue.
+//
+// out[r, c] = act(scale * sum_k Q[r, k] P[c, k] + bias[c]) + residual[r, c].
+// P, whose rows are the output's columns, is the product's 128-row side, so
+// that a lane of tensor memory is a column of the output: a warp stores 32
+// neighbouring values of a row at once, whatever the rows' alignment, and a
+// thread needs one bias value a tile.  The other side, Q, gives the tile's
+// width: 16 for a few tokens up to 256 for a training batch.
+//
+// gemm_pair_kernel: for many tiles.  Persistent pairs of CTAs (tcgen05
+// cta_group::2, 256 x `bn` a pair); per CTA a TMA warp, a product warp (of
+// the pair's first CTA) and four epilogue warps, which work on one
+// accumulator while the products fill the other.
+// gemm_split_kernel: for few tiles.  One 128 x `bn` tile a cluster of up to 8
+// CTAs that share its reduction; the parts are joined through distributed
+// shared memory in the order of the CTAs' ranks.  Two CTAs an SM.
+
+#include <algorithm>
+
+#include "ecc_gemm.h"
+#include "ecc_tensor.cuh"
+
+namespace ecc {
+
+constexpr int kGemmThreads = 192; // TMA warp, product warp, 4 epilogue warps
+constexpr uint32_t kPTile = 128;  // P rows of a CTA
+constexpr uint32_t kMaxStages = 12;
+constexpr uint32_t kPBytes = kPTile * kTileBytes;
+constexpr uint32_t kPairSmem = 226 * 1024, kSplitSmem = 112 * 1024;
+constexpr uint32_t kSmemHead = 1024; // room to align the stages to 1024 bytes
+
+struct GemmArgs {
+    Epilogue e;
+    uint64_t rows, cols;
+    uint32_t kblocks; // reduction blocks of 128 bytes (64 reduction indices for MN-major operands)
+    uint32_t ptiles, qtiles, bn, stages, idesc, split;
+    uint32_t *status;
+    bool clear_status;
+    uint64_t limit_ns;
+};
+
+struct GemmBars {
+    uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+    uint32_t tmem;
+};
+
+// ---------------------------------------------------------------- epilogue
+__device__ __forceinline__ float act_of(uint32_t act, float a)
+{
+    switch (act) {
+    case ECC_ACT_RELU:
+        return a < 0.f ? 0.f : a; // NaN stays
+    case ECC_ACT_GELU:
+        return 0.5f * a * (1.f + erff(a * 0.70710678f));
+    case ECC_ACT_GELU_TANH: // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+        return __fdividef(a, 1.f + __expf(-1.59576912f * (a + 0.044715f * a * a * a)));
+    case ECC_ACT_SILU:
+        return __fdividef(a, 1.f + __expf(-a));
+    default:
+        return a;
+    }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store_rows(void *base, uint64_t ld, uint64_t at, uint32_t n, const float (&a)[W], float s)
+{
+    T *p = static_cast<T *>(base) + at;
+#pragma unroll
+    for (int j = 0; j < W; ++j, p += ld)
+        if (j < n)
+            *p = from_f32<T>(a[j] * s);
+}
+template <typename T, int W>
+__device__ __forceinline__ void add_rows(const void *base, uint64_t ld, uint64_t at, uint32_t n, float (&a)[W])
+{
+    const T *p = static_cast<const T *>(base) + at;
+    T v[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j, p += ld)
+        if (j < n)
+            v[j] = *p;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        if (j < n)
+            a[j] += to_f32(v[j]);
+}
+
+// W rows from row `r0` (the first n of them in range) of this thread's column c
+template <int W>
+__device__ __forceinline__ void finish(const Epilogue &e, float (&a)[W], uint64_t r0, uint32_t n, uint64_t c, float bias)
+{
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        a[j] = a[j] * e.scale + bias;
+    if (e.pre) {
+        const uint64_t at = r0 * e.ldpre + c;
+        if (e.pre_type == ECC_F32)
+            store_rows<float>(e.pre, e.ldpre, at, n, a, 1.f);
+        else if (e.pre_type == ECC_BF16)
+            store_rows<bf16>(e.pre, e.ldpre, at, n, a, 1.f);
+        else
+            store_rows<__half>(e.pre, e.ldpre, at, n, a, 1.f);
+    }
+    if (e.act == ECC_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            a[j] = act_of(ECC_ACT_RELU, a[j]);
+    } else if (e.act == ECC_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            a[j] = act_of(ECC_ACT_GELU, a[j]);
+    } else if (e.act == ECC_ACT_GELU_TANH) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            a[j] = act_of(ECC_ACT_GELU_TANH, a[j]);
+    } else if (e.act == ECC_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            a[j] = act_of(ECC_ACT_SILU, a[j]);
+    }
+    if (e.residual) {
+        const uint64_t at = r0 * e.ldres + c;
+        if (e.res_type == ECC_F32)
+            add_rows<float>(e.residual, e.ldres, at, n, a);
+        else if (e.res_type == ECC_BF16)
+            add_rows<bf16>(e.residual, e.ldres, at, n, a);
+        else
+            add_rows<__half>(e.residual, e.ldres, at, n, a);
+    }
+    const uint64_t at = r0 * e.ldout + c;
+    if (e.out_type == ECC_F32)
+        store_rows<float>(e.out, e.ldout, at, n, a, 1.f);
+    else if (e.out_type == ECC_BF16)
+        store_rows<bf16>(e.out, e.ldout, at, n, a, 1.f);
+    else if (e.out_type == ECC_F16)
+        store_rows<__half>(e.out, e.ldout, at, n, a, 1.f);
+    else
+        store_rows<e4m3>(e.out, e.ldout, at, n, a, e.out_scale);
+}
+
+// ---------------------------------------------------------------- loads and products of a reduction block
+// rows [r0, r0 + n) of reduction block kb -> dst
+template <int CG, bool MN, bool F8>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, uint64_t r0, uint32_t n, uint32_t kb,
+                                             uint32_t bar)
+{
+    constexpr int per = F8 ? 128 : 64; // reduction indices of a block
+    if constexpr (MN) {
+        for (uint32_t c = 0; c < n; c += 64)
+            tma_load<CG>(dst + c * kTileBytes, map, (int)(r0 + c), (int)(kb * 64), bar);
+    } else {
+        tma_load<CG>(dst, map, (int)(kb * per), (int)r0, bar);
+    }
+}
+
+template <int CG, bool PMN, bool QMN, bool F8>
+__device__ __forceinline__ void multiply_block(uint32_t d, uint32_t pa, uint32_t qa, uint32_t idesc, bool first)
+{
+    const uint64_t a = operand_desc<PMN>(pa, 64 * kTileBytes), b = operand_desc<QMN>(qa, 64 * kTileBytes);
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k)
+        tensor_product<CG, F8>(d, a + k * operand_step<PMN>(), b + k * operand_step<QMN>(), idesc, !first || k > 0);
+}
+
+// ---------------------------------------------------------------- pairs of CTAs, many tiles
+// Tiles in groups of 8 column tiles, a group row tile by row tile: the tiles
+// in work at a time form a block that shares its operands through L2.
+struct TilePos {
+    uint32_t p, q;
+};
+__device__ __forceinline__ TilePos tile_pos(uint32_t t, uint32_t ptiles, uint32_t qtiles)
+{
+    const uint32_t g = t / (8 * qtiles), p0 = g * 8, w = min(8u, ptiles - p0), r = t - g * 8 * qtiles;
+    return {p0 + r % w, r / w};
+}
+
+template <bool PMN, bool QMN, bool F8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+    gemm_pair_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ GemmArgs g)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ GemmBars s;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank();
+    const uint32_t stage0 = (smem_u32(smem_raw) + kSmemHead - 1) & ~(kSmemHead - 1);
+    const uint32_t qn = g.bn / 2, stage_bytes = kPBytes + qn * kTileBytes;
+    const uint32_t tiles = g.ptiles * g.qtiles, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    if (threadIdx.x == 0) {
+        if (g.clear_status && blockIdx.x == 0) // waits that give up do so a second from now at the earliest
+            *(volatile uint32_t *)g.status = ECC_OK;
+        for (uint32_t i = 0; i < g.stages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.tfull[i], 1);
+            mbar_init(&s.tempty[i], 8); // four epilogue warps of each CTA
+        }
+        fence_mbar_init();
+        prefetch_map(&pmap);
+        prefetch_map(&qmap);
+    }
+    if (warp == 1) {
+        tmem_alloc<2>(smem_u32(&s.tmem), 512);
+        tmem_fence_before();
+    }
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();
+    tmem_fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)&s.tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t st = 0, ph = 0, issued = 0;
+            bool ok = true;
+            for (uint32_t t = pair; t < tiles && ok; t += pairs) {
+                const TilePos pos = tile_pos(t, g.ptiles, g.qtiles);
+                const uint64_t p0 = (uint64_t)pos.p * 2 * kPTile + rank * kPTile, q0 = (uint64_t)pos.q * g.bn + rank * qn;
+                for (uint32_t kb = 0; kb < g.kblocks; ++kb) {
+                    if (!(ok = mbar_wait(&s.empty[st], ph ^ 1, g.limit_ns)))
+                        break;
+                    const uint32_t bar = cluster_addr(smem_u32(&s.full[st]), 0), at = stage0 + st * stage_bytes;
+                    if (rank == 0)
+                        mbar_expect_tx(&s.full[st], 2 * stage_bytes);
+                    load_operand<2, PMN, F8>(at, &pmap, p0, kPTile, kb, bar);
+                    load_operand<2, QMN, F8>(at + kPBytes, &qmap, q0, qn, kb, bar);
+                    ++issued;
+                    if (++st == g.stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok) { // give the copies in flight a last wait
+                set_status(g.status, ECC_ERR_TIMEOUT);
+                if (rank == 0)
+                    for (uint32_t i = 0; i < min(issued, g.stages); ++i) {
+                        if (st == 0) {
+                            st = g.stages;
+                            ph ^= 1;
+                        }
+                        --st;
+                        (void)mbar_wait(&s.full[st], ph, g.limit_ns);
+                    }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            uint32_t st = 0, ph = 0, acc = 0, aph = 0;
+            bool ok = true;
+            for (uint32_t t = pair; t < tiles && ok; t += pairs) {
+                if (!(ok = mbar_wait(&s.tempty[acc], aph ^ 1, g.limit_ns)))
+                    break;
+                tmem_fence_after();
+                for (uint32_t kb = 0; kb < g.kblocks; ++kb) {
+                    if (!(ok = mbar_wait(&s.full[st], ph, g.limit_ns))) {
+                        (void)mbar_wait(&s.full[st], ph, g.limit_ns);
+                        break;
+                    }
+                    tmem_fence_after();
+                    const uint32_t at = stage0 + st * stage_bytes;
+                    multiply_block<2, PMN, QMN, F8>(tmem + acc * g.bn, at, at + kPBytes, g.idesc, kb == 0);
+                    tensor_commit<2>(smem_u32(&s.empty[st]));
+                    if (++st == g.stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+                tensor_commit<2>(smem_u32(&s.tfull[acc]));
+                if (acc)
+                    aph ^= 1;
+                acc ^= 1;
+            }
+            if (!ok)
+                set_status(g.status, ECC_ERR_TIMEOUT);
+        }
+    } else {
+        const uint32_t quad = warp & 3; // a warp reads the lanes of its number modulo 4
+        uint32_t acc = 0, aph = 0;
+        for (uint32_t t = pair; t < tiles; t += pairs) {
+            const TilePos pos = tile_pos(t, g.ptiles, g.qtiles);
+            const uint64_t c = (uint64_t)pos.p * 2 * kPTile + rank * kPTile + quad * 32 + lane, r0 = (uint64_t)pos.q * g.bn;
+            const bool col_ok = c < g.cols;
+            const float bias = g.e.bias && col_ok ? load_any(g.e.bias, c, g.e.bias_type) : 0.f;
+            if (!__all_sync(~0u, mbar_wait(&s.tfull[acc], aph, g.limit_ns))) {
+                if (lane == 0)
+                    set_status(g.status, ECC_ERR_TIMEOUT);
+                break;
+            }
+            tmem_fence_after();
+            const uint64_t left = g.rows - r0;
+            for (uint32_t j = 0; j < g.bn; j += 32) {
+                float a[32];
+                tmem_load32(tmem + (quad * 32 << 16) + acc * g.bn + j, a);
+                if (j + 32 == g.bn) { // the accumulator is read: products may fill it again
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        cluster_arrive(cluster_addr(smem_u32(&s.tempty[acc]), 0));
+                }
+                if (col_ok && j < left)
+                    finish(g.e, a, r0 + j, (uint32_t)min((uint64_t)32, left - j), c, bias);
+            }
+            if (acc)
+                aph ^= 1;
+            acc ^= 1;
+        }
+    }
+    __syncthreads();
+    __syncwarp();
+    tmem_fence_before();
+    cluster_sync(); // both CTAs are done with each other's barriers and tensor memory
+    tmem_fence_after();
+    if (warp == 1)
+        tmem_free<2>(tmem, 512);
+}
+
+// ---------------------------------------------------------------- clusters that share a tile's reduction
+template <int W>
+__device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, uint32_t quad, uint32_t lane, uint64_t c,
+                                              uint64_t r0, bool col_ok, float bias, bool direct, float *part)
+{
+    const uint64_t left = g.rows - r0;
+    for (uint32_t j = 0; j < g.bn && j < left; j += W) {
+        float a[W];
+        if (g.kblocks) {
+            if constexpr (W == 32)
+                tmem_load32(tmem + (quad * 32 << 16) + j, a);
+            else
+                tmem_load16(tmem + (quad * 32 << 16) + j, a);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                a[i] = 0.f;
+        }
+        if (direct) {
+            if (col_ok)
+                finish(g.e, a, r0 + j, (uint32_t)min((uint64_t)W, left - j), c, bias);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                part[(j + i) * kPTile + quad * 32 + lane] = a[i];
+        }
+    }
+}
+
+template <bool PMN, bool QMN, bool F8>
+__global__ void __launch_bounds__(kGemmThreads, 2)
+    gemm_split_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ GemmArgs g)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ GemmBars s;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = g.split > 1 ? cluster_rank() : 0;
+    const uint32_t off = (kSmemHead - (smem_u32(smem_raw) & (kSmemHead - 1))) & (kSmemHead - 1);
+    const uint32_t stage0 = smem_u32(smem_raw) + off;
+    const uint32_t stage_bytes = kPBytes + g.bn * kTileBytes;
+    const uint32_t tile = blockIdx.x / g.split;
+    const uint64_t p0 = (uint64_t)(tile % g.ptiles) * kPTile, q0 = (uint64_t)(tile / g.ptiles) * g.bn;
+    const uint32_t kb0 = (uint32_t)((uint64_t)g.kblocks * rank / g.split);
+    const uint32_t kb1 = (uint32_t)((uint64_t)g.kblocks * (rank + 1) / g.split);
+    const uint32_t tcols = g.bn < 32 ? 32 : g.bn;
+    if (threadIdx.x == 0) {
+        if (g.clear_status && blockIdx.x == 0)
+            *(volatile uint32_t *)g.status = ECC_OK;
+        for (uint32_t i = 0; i < g.stages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        mbar_init(&s.tfull[0], 1);
+        fence_mbar_init();
+        fence_proxy_async();
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(smem_u32(&s.tmem), tcols);
+        tmem_fence_before();
+    }
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)&s.tmem;
+
+    const uint32_t quad = warp & 3;
+    const uint64_t c = p0 + quad * 32 + lane;
+    const bool col_ok = c < g.cols;
+    float bias = 0.f;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t st = 0, ph = 0;
+            for (uint32_t kb = kb0; kb < kb1; ++kb) {
+                if (!(ok = mbar_wait(&s.empty[st], ph ^ 1, g.limit_ns)))
+                    break;
+                const uint32_t at = stage0 + st * stage_bytes;
+                mbar_expect_tx(&s.full[st], stage_bytes);
+                load_operand<1, PMN, F8>(at, &pmap, p0, kPTile, kb, smem_u32(&s.full[st]));
+                load_operand<1, QMN, F8>(at + kPBytes, &qmap, q0, g.bn, kb, smem_u32(&s.full[st]));
+                if (++st == g.stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (!ok) {
+                set_status(g.status, ECC_ERR_TIMEOUT);
+                for (uint32_t i = 0; i < g.stages; ++i) { // the copies in flight: a last wait each
+                    if (st == 0) {
+                        st = g.stages;
+                        ph ^= 1;
+                    }
+                    --st;
+                    (void)mbar_wait(&s.full[st], ph, g.limit_ns);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && kb1 > kb0) {
+            uint32_t st = 0, ph = 0;
+            for (uint32_t kb = kb0; kb < kb1; ++kb) {
+                if (!(ok = mbar_wait(&s.full[st], ph, g.limit_ns))) {
+                    (void)mbar_wait(&s.full[st], ph, g.limit_ns);
+                    break;
+                }
+                tmem_fence_after();
+                const uint32_t at = stage0 + st * stage_bytes;
+                multiply_block<1, PMN, QMN, F8>(tmem, at, at + kPBytes, g.idesc, kb == kb0);
+                tensor_commit<1>(smem_u32(&s.empty[st]));
+                if (++st == g.stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            tensor_commit<1>(smem_u32(&s.tfull[0]));
+            if (!ok)
+                set_status(g.status, ECC_ERR_TIMEOUT);
+        }
+    } else {
+        if (g.e.bias && col_ok)
+            bias = load_any(g.e.bias, c, g.e.bias_type);
+        if (kb1 > kb0) {
+            ok = __all_sync(~0u, mbar_wait(&s.tfull[0], 0, g.limit_ns));
+            if (!ok && lane == 0)
+                set_status(g.status, ECC_ERR_TIMEOUT);
+            tmem_fence_after();
+        }
+        // every product of this CTA is complete: the stages' memory holds its part from here on
+        float *part = reinterpret_cast<float *>(smem_raw + off);
+        if (ok) {
+            if (g.bn == 16)
+                split_columns<16>(g, tmem, quad, lane, c, q0, col_ok, bias, g.split == 1, part);
+            else
+                split_columns<32>(g, tmem, quad, lane, c, q0, col_ok, bias, g.split == 1, part);
+        }
+        tmem_fence_before();
+    }
+    __syncwarp();
+    if (g.split > 1) {
+        cluster_sync(); // all parts are written
+        if (warp >= 2) {
+            const uint32_t n = (uint32_t)min((uint64_t)g.bn, g.rows - q0);
+            const uint32_t base = stage0 + (quad * 32 + lane) * 4;
+            for (uint32_t j = rank; j < n; j += g.split) {
+                float a[1] = {0.f};
+                for (uint32_t k = 0; k < g.split; ++k)
+                    a[0] += cluster_load(cluster_addr(base + j * kPTile * 4, k));
+                if (col_ok)
+                    finish(g.e, a, q0 + j, 1, c, bias);
+            }
+        }
+        __syncwarp();
+        cluster_sync(); // nobody reads this CTA's part any more
+    } else {
+        __syncthreads();
+        __syncwarp();
+    }
+    tmem_fence_after();
+    if (warp == 1)
+        tmem_free<1>(tmem, tcols);
+}
+
+// ---------------------------------------------------------------- host side
+namespace {
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+EncodeTiled encode_tiled()
+{
+    static EncodeTiled fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            f = nullptr;
+        }
+        return (EncodeTiled)f;
+    }();
+    return fn;
+}
+
+// map of an operand: boxes of 128 bytes x `box_rows`
+bool make_map(CUtensorMap *map, const Operand &o, uint64_t rows, uint64_t K, uint32_t type, uint32_t box_rows)
+{
+    const uint32_t size = type_bytes(type);
+    const uint64_t inner = o.mn ? rows : K, outer = o.mn ? K : rows;
+    const cuuint64_t dims[2] = {inner, outer};
+    // the stride of a single row is never used, but has to be a multiple of 16 bytes
+    const cuuint64_t stride[1] = {outer > 1 ? o.ld * size : (inner * size + 15) / 16 * 16};
+    const cuuint32_t box[2] = {kTileBytes / size, box_rows}, one[2] = {1, 1};
+    const CUtensorMapDataType dt = type == ECC_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : type == ECC_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return encode_tiled()(map, dt, 2, const_cast<void *>(o.p), dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool PMN, bool QMN, bool F8>
+ecc_status gemm_launch(const Operand &P, const Operand &Q, uint64_t K, uint32_t type, GemmArgs g, bool pair, int sms,
+                       cudaStream_t st)
+{
+    CUtensorMap pm{}, qm{};
+    const uint32_t qn = pair ? g.bn / 2 : g.bn;
+    if (K && (!encode_tiled() || !make_map(&pm, P, g.cols, K, type, PMN ? 64 : kPTile) ||
+              !make_map(&qm, Q, g.rows, K, type, QMN ? 64 : qn)))
+        return ECC_ERR_CUDA;
+    const uint32_t stage_bytes = kPBytes + qn * kTileBytes;
+    const uint32_t budget = (pair ? kPairSmem : kSplitSmem) - kSmemHead - (uint32_t)sizeof(GemmBars);
+    g.stages = std::min(kMaxStages, budget / stage_bytes);
+    const size_t smem = kSmemHead + (size_t)g.stages * stage_bytes;
+    const void *f = pair ? (const void *)gemm_pair_kernel<PMN, QMN, F8> : (const void *)gemm_split_kernel<PMN, QMN, F8>;
+    if (occupancy(f, kGemmThreads, smem) <= 0)
+        return ECC_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    if (pair) {
+        cfg.gridDim = dim3(2 * (unsigned)std::min<uint64_t>((uint64_t)g.ptiles * g.qtiles, sms / 2));
+    } else {
+        cfg.gridDim = dim3(g.ptiles * g.qtiles * g.split);
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = g.split;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    void *args[] = {&pm, &qm, &g};
+    return launch_status(cudaLaunchKernelExC(&cfg, f, args));
+}
+
+} // namespace
+
+bool tma_rows(const void *p, uint64_t ld, uint32_t type, uint64_t rows)
+{
+    const uint64_t bytes = ld * type_bytes(type);
+    return ((uintptr_t)p & 15) == 0 && (rows <= 1 || ((bytes & 15) == 0 && bytes < (1ull << 40)));
+}
+
+ecc_status gemm(const Operand &P, const Operand &Q, uint64_t rows, uint64_t cols, uint64_t K, uint32_t type,
+                const Epilogue &e, uint32_t *status, bool clear_status, cudaStream_t st)
+{
+    const int sms = sm_count();
+    if (sms <= 0)
+        return ECC_ERR_CUDA;
+    const bool f8 = type == ECC_E4M3;
+    const uint32_t per = f8 ? 128 : 64;
+    GemmArgs g{};
+    g.e = e;
+    g.rows = rows;
+    g.cols = cols;
+    g.kblocks = (uint32_t)((K + per - 1) / per);
+    g.status = status;
+    g.clear_status = clear_status;
+    g.limit_ns = kWaitLimitNs + 1000ull * g.kblocks; // an epilogue waits for a whole reduction
+    const uint64_t ptiles = (cols + kPTile - 1) / kPTile;
+    auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
+    // pairs of CTAs where their 256 x 256 tiles fill the GPU, else one tile a cluster
+    const bool pair = g.kblocks && up(cols, 256) * up(rows, 256) * 2 >= (uint64_t)sms;
+    uint64_t tiles;
+    if (pair) {
+        g.bn = 256;
+        g.ptiles = (uint32_t)up(cols, 256);
+        tiles = g.ptiles * up(rows, 256);
+        g.qtiles = (uint32_t)up(rows, 256);
+        g.split = 1;
+    } else {
+        g.bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+        if (Q.mn && g.bn < 64)
+            g.bn = 64;
+        g.ptiles = (uint32_t)ptiles;
+        g.qtiles = (uint32_t)up(rows, g.bn);
+        tiles = ptiles * up(rows, g.bn);
+        g.split = 1;
+        while (g.split < 8 && tiles * g.split * 2 <= 2ull * sms && g.kblocks >= 8 * g.split)
+            g.split *= 2;
+    }
+    if (tiles >= (1u << 30))
+        return ECC_ERR_ARG;
+    g.idesc = product_desc(type, P.mn, Q.mn, pair ? 256 : 128, g.bn);
+    if (f8)
+        return gemm_launch<false, false, true>(P, Q, K, type, g, pair, sms, st);
+    if (P.mn && Q.mn)
+        return gemm_launch<true, true, false>(P, Q, K, type, g, pair, sms, st);
+    if (P.mn)
+        return gemm_launch<true, false, false>(P, Q, K, type, g, pair, sms, st);
+    return gemm_launch<false, false, false>(P, Q, K, type, g, pair, sms, st);
+}
+
+} // namespace ecc

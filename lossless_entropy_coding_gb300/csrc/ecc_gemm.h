@@ -1,0 +1,36 @@
+// ecc_gemm.h -- the matrix product the linear operators are made of.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/ecc_lm.h"
+
+namespace ecc {
+
+// out[r, c] = act(scale * sum over k of Q[r, k] P[c, k] + bias[c]) + residual[r, c]
+struct Epilogue {
+    const void *bias, *residual;
+    void *out, *pre;
+    uint64_t ldres, ldout, ldpre;
+    float scale, out_scale;
+    uint32_t bias_type, res_type, out_type, pre_type, act;
+};
+
+// An operand: `rows` x K values, either stored a matrix row after the other
+// (mn = false: the reduction is contiguous) or a reduction index after the
+// other (mn = true).  16-byte aligned rows.
+struct Operand {
+    const void *p;
+    uint64_t ld;
+    bool mn;
+};
+
+// whether an array of `rows` rows can be read by tiled TMA as it is
+bool tma_rows(const void *p, uint64_t ld, uint32_t type, uint64_t rows);
+// P holds the output's columns, Q its rows; clear_status: the launch's first
+// act is to set *status to ECC_OK
+ecc_status gemm(const Operand &P, const Operand &Q, uint64_t rows, uint64_t cols, uint64_t K, uint32_t type,
+                const Epilogue &e, uint32_t *status, bool clear_status, cudaStream_t st);
+
+} // namespace ecc
