@@ -141,7 +141,7 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
  *   logits  [rows, vocab] of `type` (F32, BF16, F16), leading dimension ld.
  *   tokens  int64[rows], or NULL.  A negative token means none: its log
  *           probability is 0.  A token >= vocab gets NaN.
- *   scale   > 0, finite (the reciprocal of a temperature).
+ *   scale   > 0, below 2^127 (the reciprocal of a temperature).
  *   logprob, entropy, lse  float32[rows]; logprob is not written without
  *           tokens; each may be NULL.
  *   top     0..32 and at most vocab; top_logprob float32[rows, top],
@@ -167,7 +167,7 @@ ecc_status ecc_token_logprob(const void *logits, uint64_t ld, uint32_t type, con
  *           scale; entropy may be NULL if dentropy is.
  *   dlogprob, dentropy  float32[rows]; NULL = zeros.  Rows whose token is
  *           negative or >= vocab take no part in dlogprob; a row of -infinity
- *           only has gradient 0.
+ *           only has gradient 0, one with a NaN or +infinity has gradient NaN.
  *   dlogits [rows, vocab] of `type`, leading dimension ldd; may be logits
  *           itself (ldd = ld).
  * Errors: ECC_ERR_ARG, ECC_ERR_CUDA.
