@@ -552,30 +552,37 @@ F32, BF16, F16, E4M3 = range(4)
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 MAX_TOP = 32
 
-_types = {}
+_types = {}  # torch element type -> C code, filled by _bind
+_empty = _raw_stream = _current_device = _f32 = _i32 = _i64 = _u8t = None
+
+
+def _bind():
+    """Look up once what every call below needs."""
+    global _empty, _raw_stream, _current_device, _f32, _i32, _i64, _u8t
+    torch = _torch()
+    _types.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3,
+                   torch.uint8: E4M3})
+    _empty, _f32, _i32, _i64, _u8t = torch.empty, torch.float32, torch.int32, torch.int64, torch.uint8
+    torch.cuda.init()
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _load()
+
+
+def _refuse(what: str):
+    raise EccError(ERR_ARG, what)
 
 
 def _type(t, what: str) -> int:
-    if not _types:
-        torch = _torch()
-        _types.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3,
-                       torch.uint8: E4M3})
     code = _types.get(t)
-    if code is None:
-        raise EccError(ERR_ARG, f"{what}: element type {t}")
-    return code
-
-
-def _refuse(ok: bool, what: str):
-    if not ok:
-        raise EccError(ERR_ARG, what)
+    return _refuse(what + ": element type") if code is None else code
 
 
 def _matrix(t, what: str):
     """(rows, columns, leading dimension) of a tensor of rows."""
     shape, stride = t.shape, t.stride()
     n = len(shape)
-    _refuse(n >= 1 and (shape[-1] <= 1 or stride[-1] == 1), f"{what}: rows are not contiguous")
+    if n == 0 or (stride[-1] != 1 and shape[-1] > 1):
+        _refuse(what + ": rows are not contiguous")
     cols = shape[-1]
     if n == 2:
         rows = shape[0]
@@ -586,8 +593,8 @@ def _matrix(t, what: str):
             continue
         if rows == 1:
             ld = stride[i]
-        else:
-            _refuse(shape[i] == 0 or stride[i] == rows * ld, f"{what}: leading dimensions do not collapse")
+        elif shape[i] and stride[i] != rows * ld:
+            _refuse(what + ": leading dimensions do not collapse")
         rows *= shape[i]
     return rows, cols, ld
 
@@ -596,7 +603,8 @@ def _vector(t, n: int, dev: int, what: str, dtype=None):
     """Pointer of a contiguous tensor of n elements (0 for None)."""
     if t is None:
         return 0
-    _refuse(t.numel() == n and t.is_contiguous() and t.get_device() == dev and (dtype is None or t.dtype == dtype), what)
+    if t.numel() != n or not t.is_contiguous() or t.get_device() != dev or (dtype is not None and t.dtype != dtype):
+        _refuse(what)
     return t.data_ptr()
 
 
@@ -606,11 +614,14 @@ def _on_stream(f):
     f gets the stream's handle."""
     @functools.wraps(f)
     def call(x, *args, stream=None, **kw):
-        torch = _torch()
-        _refuse(isinstance(x, torch.Tensor) and x.is_cuda, f"{f.__name__}: needs CUDA tensors")
+        if _empty is None:
+            _bind()
         dev = x.get_device()
-        if stream is None and dev == torch.cuda.current_device():
-            return f(x, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+        if dev < 0:
+            _refuse(f.__name__ + ": needs CUDA tensors")
+        if stream is None and dev == _current_device():
+            return f(x, *args, stream=_raw_stream(dev), **kw)
+        torch = _torch()
         with torch.cuda.device(dev):
             s = torch.cuda.current_stream() if stream is None else stream
             with torch.cuda.stream(s):
@@ -624,24 +635,24 @@ def ecc_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, out_d
     """Layer norm over the last dimension of device tensor x; returns (out,
     mean, rstd).  out_dtype: x's type (default), or uint8 / float8_e4m3fn for
     e4m3 values of out * out_scale.  weight, bias: of x's type or float32."""
-    torch = _torch()
     dev = x.get_device()
     rows, cols, ldx = _matrix(x, "ecc_layer_norm: x")
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    _refuse(out.shape == x.shape and out.get_device() == dev, "ecc_layer_norm: out")
+        out = _empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape or out.get_device() != dev:
+        _refuse("ecc_layer_norm: out")
     _, _, ldy = _matrix(out, "ecc_layer_norm: out")
     if mean is None:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        mean = _empty(x.shape[:-1], dtype=_f32, device=x.device)
     if rstd is None:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = _empty(x.shape[:-1], dtype=_f32, device=x.device)
     p_dtype = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
-    _check(_load().ecc_layer_norm(
+    _check(_lib.ecc_layer_norm(
         x.data_ptr(), ldx, _type(x.dtype, "ecc_layer_norm"),
         _vector(weight, cols, dev, "ecc_layer_norm: weight"), _vector(bias, cols, dev, "ecc_layer_norm: bias", p_dtype),
         _type(p_dtype, "ecc_layer_norm"), rows, cols, eps, out.data_ptr(), ldy, _type(out.dtype, "ecc_layer_norm"),
-        out_scale, _vector(mean, rows, dev, "ecc_layer_norm: mean", torch.float32),
-        _vector(rstd, rows, dev, "ecc_layer_norm: rstd", torch.float32), stream), "ecc_layer_norm")
+        out_scale, _vector(mean, rows, dev, "ecc_layer_norm: mean", _f32),
+        _vector(rstd, rows, dev, "ecc_layer_norm: rstd", _f32), stream), "ecc_layer_norm")
     return out, mean, rstd
 
 
@@ -653,31 +664,33 @@ def layer_norm_grad_workspace_bytes(rows: int, cols: int) -> int:
 def ecc_layer_norm_grad(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, ws=None, stream=None):
     """Backward pass of ecc_layer_norm; returns (dx, dweight, dbias), the last
     two float32.  weight None: ones (dweight and dbias are still summed)."""
-    torch = _torch()
     dev = dy.get_device()
     rows, cols, ldx = _matrix(x, "ecc_layer_norm_grad: x")
-    _refuse(x.shape == dy.shape and x.dtype == dy.dtype and x.get_device() == dev, "ecc_layer_norm_grad: x")
+    if x.shape != dy.shape or x.dtype != dy.dtype or x.get_device() != dev:
+        _refuse("ecc_layer_norm_grad: x")
     _, _, lddy = _matrix(dy, "ecc_layer_norm_grad: dy")
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _refuse(dx.shape == x.shape and dx.dtype == x.dtype and dx.get_device() == dev, "ecc_layer_norm_grad: dx")
+        dx = _empty(x.shape, dtype=x.dtype, device=x.device)
+    elif dx.shape != x.shape or dx.dtype != x.dtype or dx.get_device() != dev:
+        _refuse("ecc_layer_norm_grad: dx")
     _, _, lddx = _matrix(dx, "ecc_layer_norm_grad: dx")
     if dweight is None:
-        dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
+        dweight = _empty(cols, dtype=_f32, device=x.device)
     if dbias is None:
-        dbias = torch.empty(cols, dtype=torch.float32, device=x.device)
-    lib = _load()
+        dbias = _empty(cols, dtype=_f32, device=x.device)
+    lib = _lib
     if ws is None:
-        ws = torch.empty(lib.ecc_layer_norm_grad_workspace_bytes(rows, cols), dtype=torch.uint8, device=x.device)
-    _refuse(mean is not None and rstd is not None, "ecc_layer_norm_grad: mean and rstd")
+        ws = _empty(lib.ecc_layer_norm_grad_workspace_bytes(rows, cols), dtype=_u8t, device=x.device)
+    if mean is None or rstd is None:
+        _refuse("ecc_layer_norm_grad: mean and rstd")
     _check(lib.ecc_layer_norm_grad(
         dy.data_ptr(), lddy, x.data_ptr(), ldx, _type(x.dtype, "ecc_layer_norm_grad"),
         _vector(weight, cols, dev, "ecc_layer_norm_grad: weight"),
         _type(x.dtype if weight is None else weight.dtype, "ecc_layer_norm_grad"),
-        _vector(mean, rows, dev, "ecc_layer_norm_grad: mean", torch.float32),
-        _vector(rstd, rows, dev, "ecc_layer_norm_grad: rstd", torch.float32), rows, cols, dx.data_ptr(), lddx,
-        _vector(dweight, cols, dev, "ecc_layer_norm_grad: dweight", torch.float32),
-        _vector(dbias, cols, dev, "ecc_layer_norm_grad: dbias", torch.float32), ws.data_ptr(), ws.numel(), stream),
+        _vector(mean, rows, dev, "ecc_layer_norm_grad: mean", _f32),
+        _vector(rstd, rows, dev, "ecc_layer_norm_grad: rstd", _f32), rows, cols, dx.data_ptr(), lddx,
+        _vector(dweight, cols, dev, "ecc_layer_norm_grad: dweight", _f32),
+        _vector(dbias, cols, dev, "ecc_layer_norm_grad: dbias", _f32), ws.data_ptr(), ws.numel(), stream),
         "ecc_layer_norm_grad")
     return dx, dweight, dbias
 
@@ -687,8 +700,8 @@ _LINEAR_GRAD_JOB = struct.Struct("@7P9Qf5I")    # ecc_linear_grad_job
 
 
 def _activation(act: str, what: str) -> int:
-    _refuse(act in ACTIVATIONS, f"{what}: activation {act!r}")
-    return ACTIVATIONS[act]
+    code = ACTIVATIONS.get(act)
+    return _refuse(what + ": activation") if code is None else code
 
 
 def _operand(t, rows: int, cols: int, dev: int, what: str):
@@ -696,7 +709,8 @@ def _operand(t, rows: int, cols: int, dev: int, what: str):
     if t is None:
         return 0, 0, 0
     r, c, ld = _matrix(t, what)
-    _refuse(r == rows and c == cols and t.get_device() == dev, f"{what}: shape or device")
+    if r != rows or c != cols or t.get_device() != dev:
+        _refuse(what + ": shape or device")
     return t.data_ptr(), ld, _type(t.dtype, what)
 
 
@@ -708,19 +722,20 @@ def ecc_linear(x, w, bias=None, residual=None, act: str = "none", scale: float =
     out_dtype: x's type by default, bfloat16 for e4m3 operands; uint8 or
     float8_e4m3fn: e4m3 values of out * out_scale.  pre: a tensor [..., N]
     that receives the activation's argument, for ecc_linear_grad."""
-    torch = _torch()
     dev = x.get_device()
     M, K, ldx = _matrix(x, "ecc_linear: x")
     in_type = _type(x.dtype, "ecc_linear: x")
-    _refuse(w.dim() == 2, "ecc_linear: w")
+    if w.dim() != 2:
+        _refuse("ecc_linear: w")
     N = w.shape[0]
     pw, ldw, w_type = _operand(w, N, K, dev, "ecc_linear: w")
-    _refuse(w_type == in_type, "ecc_linear: x and w of different types")
+    if w_type != in_type:
+        _refuse("ecc_linear: x and w of different types")
     if out is None:
-        out = torch.empty((*x.shape[:-1], N), device=x.device,
-                          dtype=out_dtype or (torch.bfloat16 if in_type == E4M3 else x.dtype))
+        out = _empty((*x.shape[:-1], N), device=x.device,
+                          dtype=out_dtype or (_torch().bfloat16 if in_type == E4M3 else x.dtype))
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=x.device)
+        status = _empty(1, dtype=_i32, device=x.device)
     pout, ldout, out_type = _operand(out, M, N, dev, "ecc_linear: out")
     pres, ldres, res_type = _operand(residual, M, N, dev, "ecc_linear: residual")
     ppre, ldpre, pre_type = _operand(pre, M, N, dev, "ecc_linear: pre")
@@ -728,12 +743,12 @@ def ecc_linear(x, w, bias=None, residual=None, act: str = "none", scale: float =
                            ldw, ldres, ldout, ldpre, scale, out_scale, in_type,
                            0 if bias is None else _type(bias.dtype, "ecc_linear: bias"), res_type, out_type, pre_type,
                            _activation(act, "ecc_linear"))
-    lib = _load()
+    lib = _lib
     if ws is None:
         need = lib.ecc_linear_workspace_bytes(job)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        ws = _empty(need, dtype=_u8t, device=x.device) if need else None
     _check(lib.ecc_linear(job, 0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                          _vector(status, 1, dev, "ecc_linear: status", torch.int32), stream), "ecc_linear")
+                          _vector(status, 1, dev, "ecc_linear: status", _i32), stream), "ecc_linear")
     return out, status
 
 
@@ -744,36 +759,37 @@ def ecc_linear_grad(dy, x, w, pre=None, act: str = "none", scale: float = 1.0, d
     None for what `want` leaves out.  pre: the activation's argument (needed
     unless act is "none").  dw_dtype: x's type (default) or float32; dbias is
     float32."""
-    torch = _torch()
     dev = dy.get_device()
     M, N, lddy = _matrix(dy, "ecc_linear_grad: dy")
     in_type = _type(dy.dtype, "ecc_linear_grad: dy")
     K = x.shape[-1]
     px, ldx, x_type = _operand(x, M, K, dev, "ecc_linear_grad: x")
     pw, ldw, w_type = _operand(w, N, K, dev, "ecc_linear_grad: w")
-    _refuse(x_type == in_type and w_type == in_type, "ecc_linear_grad: dy, x and w of different types")
+    if x_type != in_type or w_type != in_type:
+        _refuse("ecc_linear_grad: dy, x and w of different types")
     ppre, ldpre, pre_type = _operand(pre, M, N, dev, "ecc_linear_grad: pre")
     if dx is None and "dx" in want:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = _empty(x.shape, dtype=x.dtype, device=x.device)
     if dw is None and "dw" in want:
-        dw = torch.empty((N, K), dtype=dw_dtype or x.dtype, device=x.device)
+        dw = _empty((N, K), dtype=dw_dtype or x.dtype, device=x.device)
     if dbias is None and "dbias" in want:
-        dbias = torch.empty(N, dtype=torch.float32, device=x.device)
+        dbias = _empty(N, dtype=_f32, device=x.device)
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=x.device)
+        status = _empty(1, dtype=_i32, device=x.device)
     pdx, lddx, dx_type = _operand(dx, M, K, dev, "ecc_linear_grad: dx")
-    _refuse(dx is None or dx_type == in_type, "ecc_linear_grad: dx")
+    if dx is not None and dx_type != in_type:
+        _refuse("ecc_linear_grad: dx")
     pdw, lddw, dw_type = _operand(dw, N, K, dev, "ecc_linear_grad: dw")
     job = _LINEAR_GRAD_JOB.pack(dy.data_ptr(), px, pw, ppre, pdx, pdw,
-                                _vector(dbias, N, dev, "ecc_linear_grad: dbias", torch.float32), M, N, K, lddy, ldx,
+                                _vector(dbias, N, dev, "ecc_linear_grad: dbias", _f32), M, N, K, lddy, ldx,
                                 ldw, ldpre, lddx, lddw, scale, in_type, pre_type, dw_type,
                                 _activation(act, "ecc_linear_grad"), 0)
-    lib = _load()
+    lib = _lib
     if ws is None:
         need = lib.ecc_linear_grad_workspace_bytes(job)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        ws = _empty(need, dtype=_u8t, device=x.device) if need else None
     _check(lib.ecc_linear_grad(job, 0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                               _vector(status, 1, dev, "ecc_linear_grad: status", torch.int32), stream),
+                               _vector(status, 1, dev, "ecc_linear_grad: status", _i32), stream),
            "ecc_linear_grad")
     return dx, dw, dbias, status
 
@@ -793,23 +809,24 @@ def ecc_token_logprob(logits, tokens=None, top: int = 0, scale: float = 1.0, str
     """Log probabilities of tokens (int64 [...], negative: none) under softmax
     of scale * logits [..., vocab], with each row's entropy, log partition and
     `top` most probable tokens (at most 32)."""
-    torch = _torch()
     dev = logits.get_device()
     rows, vocab, ld = _matrix(logits, "ecc_token_logprob: logits")
     lead = logits.shape[:-1]
-    _refuse(0 <= top <= MAX_TOP, "ecc_token_logprob: top")
-    ptok = _vector(tokens, rows, dev, "ecc_token_logprob: tokens", torch.int64)
-    stat = torch.empty((3, *lead), dtype=torch.float32, device=logits.device)
-    logprob, entropy, lse = stat.unbind(0)
+    if not 0 <= top <= MAX_TOP:
+        _refuse("ecc_token_logprob: top")
+    ptok = _vector(tokens, rows, dev, "ecc_token_logprob: tokens", _i64)
+    logprob = _empty(lead, dtype=_f32, device=logits.device) if tokens is not None else None
+    entropy = _empty(lead, dtype=_f32, device=logits.device)
+    lse = _empty(lead, dtype=_f32, device=logits.device)
     top_logprob = top_index = None
     if top:
-        top_logprob = torch.empty((*lead, top), dtype=torch.float32, device=logits.device)
-        top_index = torch.empty((*lead, top), dtype=torch.int32, device=logits.device)
-    _check(_load().ecc_token_logprob(
+        top_logprob = _empty((*lead, top), dtype=_f32, device=logits.device)
+        top_index = _empty((*lead, top), dtype=_i32, device=logits.device)
+    _check(_lib.ecc_token_logprob(
         logits.data_ptr(), ld, _type(logits.dtype, "ecc_token_logprob"), ptok, rows, vocab, scale, top,
-        logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logprob.data_ptr() if top else 0,
+        0 if logprob is None else logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logprob.data_ptr() if top else 0,
         top_index.data_ptr() if top else 0, stream), "ecc_token_logprob")
-    return TokenLogprob(logprob if tokens is not None else None, entropy, lse, top_logprob, top_index)
+    return TokenLogprob(logprob, entropy, lse, top_logprob, top_index)
 
 
 @_on_stream
@@ -818,18 +835,17 @@ def ecc_token_logprob_grad(logits, tokens, lse, entropy=None, dlogprob=None, den
     """Gradient with respect to the logits of sum(dlogprob * logprob +
     dentropy * entropy); returns dlogits (which may be given as logits
     itself)."""
-    torch = _torch()
     dev = logits.get_device()
     rows, vocab, ld = _matrix(logits, "ecc_token_logprob_grad: logits")
     if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    _refuse(dlogits.shape == logits.shape and dlogits.dtype == logits.dtype and dlogits.get_device() == dev,
-            "ecc_token_logprob_grad: dlogits")
+        dlogits = _empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    elif dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or dlogits.get_device() != dev:
+        _refuse("ecc_token_logprob_grad: dlogits")
     _, _, ldd = _matrix(dlogits, "ecc_token_logprob_grad: dlogits")
-    f = torch.float32
-    _check(_load().ecc_token_logprob_grad(
+    f = _f32
+    _check(_lib.ecc_token_logprob_grad(
         logits.data_ptr(), ld, _type(logits.dtype, "ecc_token_logprob_grad"),
-        _vector(tokens, rows, dev, "ecc_token_logprob_grad: tokens", torch.int64), rows, vocab, scale,
+        _vector(tokens, rows, dev, "ecc_token_logprob_grad: tokens", _i64), rows, vocab, scale,
         _vector(lse, rows, dev, "ecc_token_logprob_grad: lse", f),
         _vector(entropy, rows, dev, "ecc_token_logprob_grad: entropy", f),
         _vector(dlogprob, rows, dev, "ecc_token_logprob_grad: dlogprob", f),

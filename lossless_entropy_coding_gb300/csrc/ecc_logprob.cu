@@ -83,7 +83,8 @@ constexpr float kLseMost = 256.f;
 // A row of logits as `head` single values, `vecs` 16-byte aligned vectors and
 // `tail` single values.
 template <typename T> struct RowView {
-    static constexpr uint32_t V = 16 / sizeof(T);
+    static constexpr uint32_t V = 16 / sizeof(T); // values of a vector
+    static constexpr uint32_t U = 32 / V;         // vectors of a group: a thread takes 32 values at a time
     const T *x;
     uint32_t head, tail;
     uint64_t vecs;
@@ -99,38 +100,16 @@ template <typename T> struct RowView {
     __device__ __forceinline__ uint64_t single(uint32_t k) const { return k < head ? k : vecs * V + k; }
 };
 
-template <typename T> __device__ __forceinline__ void unpack(const uint4 &v, float *f);
-template <> __device__ __forceinline__ void unpack<float>(const uint4 &v, float *f)
-{
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
-}
-template <> __device__ __forceinline__ void unpack<bf16>(const uint4 &v, float *f)
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-template <> __device__ __forceinline__ void unpack<__half>(const uint4 &v, float *f)
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        f[2 * i] = g.x;
-        f[2 * i + 1] = g.y;
-    }
-}
-
 __device__ __forceinline__ float max_nan(float a, float b) // NaN if either is
 {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 __device__ __forceinline__ float exp2_fast(float x)
@@ -175,268 +154,259 @@ struct Softmax {
 };
 
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr uint32_t kUnroll = 4;    // vectors a thread loads at a time: a group
-constexpr uint32_t kGroupMax = 16; // group maxima kept for each thread
-constexpr uint32_t kCandidates = 1024;
+constexpr uint32_t kSlots = 16;    // group maxima kept for each column
+constexpr int kSelThreads = 128;   // selecting threads of a block
+constexpr uint32_t kStages = 4;    // stages of a block's ring
+constexpr uint32_t kStageVecs = 4 * kLpThreads;
+constexpr uint32_t kStageBytes = kStageVecs * 16;
 
-struct LogprobShared {
-    float gmax[kGroupMax][kLpThreads]; // largest logit of the groups of a slot
-    unsigned long long key[kCandidates];
-    uint32_t pair[kLpThreads * kGroupMax];
-    unsigned long long best[ECC_MAX_TOP]; // the CTA's alternatives, in order
+// A team of N threads (a warp, or a block's four selecting warps) finds a row's
+// alternatives from the group maxima of C columns of vectors: column t holds
+// the vectors t, t + C, ... of the team's share.
+template <int N, int C> struct Team {
+    static constexpr uint32_t threads = N, columns = C, keys = N == 32 ? 256 : 512; // keys: candidates that are ranked
+    unsigned long long key[keys];
+    unsigned long long best[ECC_MAX_TOP]; // the alternatives, in order
     unsigned long long largest;
-    float m[kLpWarps], s[kLpWarps], t[kLpWarps];
-    uint32_t low[kLpWarps];
-    float cta[3];
+    uint16_t pair[C * kSlots]; // slot << 8 | column
+    uint32_t low[N / 32];
+    float sum[3];
     uint32_t n_key, n_pair;
-};
 
-// The `top` largest keys of key[0, n) in order (a key's rank is the number
-// of larger ones; keys differ); missing ones are 0.
-__device__ __forceinline__ void rank_keys(LogprobShared &sh, uint32_t n, uint32_t top)
+    static __device__ __forceinline__ void sync()
+    {
+        if constexpr (N == 32)
+            __syncwarp();
+        else
+            asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+    }
+    static __device__ __forceinline__ uint32_t thread() { return threadIdx.x % N; }
+};
+using WarpTeam = Team<32, 32>;
+using BlockTeam = Team<kSelThreads, kLpThreads>;
+
+// The `top` largest of key[0, n) in order (a key's rank is the number of
+// larger ones; keys differ), four threads a key; missing ones are 0.
+template <typename Tm> __device__ __forceinline__ void rank_keys(Tm &sh, uint32_t n, uint32_t top)
 {
-    for (uint32_t i = threadIdx.x; i < n; i += kLpThreads) {
-        const unsigned long long k = sh.key[i];
+    const uint32_t tid = Tm::thread(), q = tid & 3;
+    for (uint32_t i0 = 0; i0 < n; i0 += Tm::threads / 4) {
+        const uint32_t i = i0 + tid / 4;
+        const unsigned long long k = i < n ? sh.key[i] : ~0ull;
         uint32_t rank = 0;
-        for (uint32_t j = 0; j < n; ++j)
+#pragma unroll 4
+        for (uint32_t j = q; j < n; j += 4)
             rank += sh.key[j] > k;
-        if (rank < top)
+        rank += __shfl_xor_sync(~0u, rank, 1);
+        rank += __shfl_xor_sync(~0u, rank, 2);
+        if (q == 0 && i < n && rank < top)
             sh.best[rank] = k;
     }
-    for (uint32_t i = n + threadIdx.x; i < top; i += kLpThreads)
+    for (uint32_t i = n + tid; i < top; i += Tm::threads)
         sh.best[i] = 0;
 }
 
-// A row by a cluster of `split` CTAs, each a share of its vectors (the first
-// also the single values at the ends): one pass over the row that keeps the
-// softmax sums, and for the alternatives the largest logit of each group of
-// vectors.  At least `top` threads' largest logits reach the bound
-// min over warps (r-th largest of the warp's threads), r = top / warps, so
-// every alternative does; only the groups that reach it are read again (a few
-// dozen, a lane a value, from L2), and the values that do are ranked.  Bound
-// by HBM: one read of the logits.
-template <typename T> __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobParams p, uint32_t split)
-{
-    extern __shared__ __align__(16) uint8_t raw[];
-    LogprobShared &sh = *reinterpret_cast<LogprobShared *>(raw);
-    constexpr uint32_t V = RowView<T>::V;
-    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = split > 1 ? cluster_rank() : 0;
-    const uint64_t r = blockIdx.x / split;
-    const T *x = static_cast<const T *>(p.logits) + r * p.ld;
-    const RowView<T> row(x, p.vocab);
-    const uint64_t v0 = row.vecs * rank / split, v1 = row.vecs * (rank + 1) / split;
-    const uint32_t singles = rank == 0 ? row.head + row.tail : 0;
-    const float c = p.scale * 1.44269504f;
-    const int64_t tok = p.tokens && tid == 0 && rank == 0 ? p.tokens[r] : -1;
-    const float xtok = tok >= 0 && tok < (int64_t)p.vocab ? to_f32(x[tok]) : 0.f;
+// A team's share of a row: vectors [v0, v1), and the single values at the
+// row's ends for the first share.
+template <typename T> struct Share {
+    RowView<T> row;
+    uint64_t v0, v1, n;
+    uint32_t singles;
+};
 
-    const uint64_t groups = (v1 - v0 + kUnroll * kLpThreads - 1) / (kUnroll * kLpThreads);
-    const uint32_t per_slot = (uint32_t)((groups + kGroupMax - 1) / kGroupMax);
-    Softmax sm;
-    float own = -INFINITY, slot_max = -INFINITY; // largest logit of this thread's vectors, of the slot's
-    uint32_t slot = 0, in_slot = 0;
-    for (uint64_t g = 0; g < groups; ++g) {
-        const uint64_t i0 = v0 + g * kUnroll * kLpThreads + tid;
-        uint4 q[kUnroll];
+// A group of a thread's values into the softmax; its largest.  Without the cut
+// of Softmax::add, two values at a time; where that meets 0 * infinity (a
+// masked value), again with the cut.
+template <int P> __device__ __forceinline__ float add_group(Softmax &sm, const float2 (&f)[P], float c)
+{
+    float big = max_nan(f[0].x, f[0].y), more = -INFINITY;
 #pragma unroll
-        for (uint32_t u = 0; u < kUnroll; ++u)
-            if (i0 + u * kLpThreads < v1)
-                q[u] = ld_stream16(row.vec(i0 + u * kLpThreads));
-        float f[kUnroll][V], big = -INFINITY;
+    for (int i = 1; i < P; ++i)
+        (i & 1 ? more : big) = max_nan(i & 1 ? more : big, f[i].x, f[i].y);
+    big = max_nan(big, more);
+    if (!(big <= sm.m))
+        sm.raise(max_nan(sm.m, big), c);
+    const float2 minus = both(sm.m == -INFINITY ? 0.f : -sm.m), c2 = both(c);
+    float2 s0 = both(0.f), s1 = s0, t0 = s0, t1 = s0;
 #pragma unroll
-        for (uint32_t u = 0; u < kUnroll; ++u) {
-            if (i0 + u * kLpThreads < v1) {
-                unpack<T>(q[u], f[u]);
-            } else {
+    for (int i = 0; i < P; ++i) {
+        const float2 d = mul2(add2(f[i], minus), c2), e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+        if (i & 1) {
+            s1 = add2(s1, e);
+            t1 = fma2(e, d, t1);
+        } else {
+            s0 = add2(s0, e);
+            t0 = fma2(e, d, t0);
+        }
+    }
+    s0 = add2(s0, s1);
+    t0 = add2(t0, t1);
+    const float t = t0.x + t0.y;
+    if (t == t) {
+        sm.s += s0.x + s0.y;
+        sm.t += t;
+    } else {
 #pragma unroll
-                for (uint32_t k = 0; k < V; ++k)
-                    f[u][k] = -INFINITY;
+        for (int i = 0; i < P; ++i) {
+            sm.add(f[i].x, c);
+            sm.add(f[i].y, c);
+        }
+    }
+    return big;
+}
+
+// The share's alternatives -> sh.best.  gmax[k][t] is the largest logit of
+// slot k (`per_slot` groups) of column t.  At least `top` columns reach the
+// bound min over the warps (r-th largest of its lanes' columns), r = top /
+// warps, so every alternative does; only the slots that reach it are read
+// again (a few dozen, a lane a value, from L2), and the values that do are
+// ranked.  `single` is the value of the row's ends that this thread holds.
+template <typename T, typename Tm>
+__device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::columns], const Share<T> &a, uint32_t top,
+                                           uint32_t slots, uint64_t groups, uint32_t per_slot, bool has_single,
+                                           float single, uint64_t single_at)
+{
+    constexpr uint32_t V = RowView<T>::V, U = RowView<T>::U, N = Tm::threads, C = Tm::columns;
+    const uint32_t tid = Tm::thread(), lane = tid & 31, warp = tid >> 5;
+    const T *x = a.row.x;
+    float own = -INFINITY;
+    for (uint32_t k = 0; k < slots; ++k)
+#pragma unroll
+        for (uint32_t t = 0; t < C; t += N)
+            own = max_nan(own, gmax[k][t + tid]);
+    // warps whose lanes all have a vector; with none, every value above -infinity is a candidate
+    const uint32_t full = (uint32_t)min((uint64_t)(N / 32), (a.v1 - a.v0) / 32);
+    const uint32_t take = full ? (top + full - 1) / full : 0;
+    uint32_t mine = order_bits(own), low = 0;
+    for (uint32_t i = 0; i < take; ++i) {
+        low = __reduce_max_sync(~0u, mine);
+        if (lane == __ffs(__ballot_sync(~0u, mine == low)) - 1)
+            mine = 0;
+    }
+    if (lane == 0)
+        sh.low[warp] = low;
+    if (tid == 0)
+        sh.n_key = sh.n_pair = 0;
+    Tm::sync();
+    uint32_t bound = order_bits(-INFINITY) + 1; // -infinity is no candidate
+    if (full) {
+        uint32_t b = 0xFFFFFFFFu;
+        for (uint32_t w = 0; w < full; ++w)
+            b = min(b, sh.low[w]);
+        bound = max(bound, b);
+    }
+    for (uint32_t k = 0; k < slots; ++k)
+#pragma unroll
+        for (uint32_t t = 0; t < C; t += N)
+            if (order_bits(gmax[k][t + tid]) >= bound)
+                sh.pair[atomicAdd(&sh.n_pair, 1u)] = (uint16_t)(k << 8 | (t + tid));
+    if (has_single && order_bits(single) >= bound)
+        sh.key[atomicAdd(&sh.n_key, 1u)] = order_key(single, (uint32_t)single_at); // at most 14
+    Tm::sync();
+    const uint32_t pairs = sh.n_pair;
+    auto keep = [&](float f, uint64_t at) {
+        if (order_bits(f) >= bound) {
+            const uint32_t n = atomicAdd(&sh.n_key, 1u);
+            if (n < Tm::keys)
+                sh.key[n] = order_key(f, (uint32_t)at);
+        }
+    };
+    auto place = [&](uint32_t pair, uint64_t e) { // value e of a pair's slot: its vector
+        return a.v0 + ((uint64_t)(pair >> 8) * per_slot * U + e / V) * C + (pair & 0xFFu);
+    };
+    if (per_slot == 1) { // a lane a value; eight pairs' loads at a time
+        for (uint32_t i0 = warp; i0 < pairs; i0 += 8 * (N / 32)) {
+            T q[8];
+            uint64_t at[8];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                const uint32_t i = i0 + j * (N / 32);
+                const uint64_t v = i < pairs ? place(sh.pair[i], lane) : a.v1;
+                at[j] = v < a.v1 ? a.row.head + v * V + lane % V : ~0ull;
+                if (at[j] != ~0ull)
+                    q[j] = x[at[j]];
             }
 #pragma unroll
-            for (uint32_t k = 0; k < V; ++k)
-                big = max_nan(big, f[u][k]);
+            for (uint32_t j = 0; j < 8; ++j)
+                if (at[j] != ~0ull)
+                    keep(to_f32(q[j]), at[j]);
         }
-        if (!(big <= sm.m))
-            sm.raise(max_nan(sm.m, big), c);
-#pragma unroll
-        for (uint32_t u = 0; u < kUnroll; ++u)
-#pragma unroll
-            for (uint32_t k = 0; k < V; ++k)
-                sm.add(f[u][k], c);
-        if (p.top) {
-            slot_max = max_nan(slot_max, big);
-            if (++in_slot == per_slot || g + 1 == groups) {
-                sh.gmax[slot][tid] = slot_max;
-                own = max_nan(own, slot_max);
-                slot_max = -INFINITY;
-                ++slot;
-                in_slot = 0;
+    } else {
+        for (uint32_t i = warp; i < pairs; i += N / 32) {
+            const uint64_t g0 = (uint64_t)(sh.pair[i] >> 8) * per_slot, g1 = min(groups, g0 + per_slot);
+            for (uint64_t e = lane; e < (g1 - g0) * 32; e += 32) {
+                const uint64_t v = place(sh.pair[i], e), at = a.row.head + v * V + e % V;
+                if (v < a.v1)
+                    keep(to_f32(x[at]), at);
             }
         }
     }
-    for (uint32_t k = tid; k < singles; k += kLpThreads) {
-        const float v = to_f32(x[row.single(k)]);
-        if (!(v <= sm.m))
-            sm.raise(max_nan(sm.m, v), c);
-        sm.add(v, c);
+    Tm::sync();
+    const uint32_t n = sh.n_key;
+    const uint64_t first = a.singles ? 0 : a.row.head + a.v0 * V, last = a.row.head + a.v1 * V;
+    if (n <= Tm::keys) {
+        rank_keys(sh, n, top);
+        Tm::sync();
+        if (n < top && warp == 0) { // fewer than asked for: tokens without probability, lowest index first
+            uint32_t have = n;
+            for (uint64_t i0 = first; have < top; i0 += 32) {
+                uint64_t i = i0 + lane;
+                bool in = i < last;
+                if (!in && a.singles) { // behind the vectors: the tail
+                    i = a.row.head + a.row.vecs * V + (i - last);
+                    in = i < a.n;
+                }
+                const bool hit = in && order_bits(to_f32(x[in ? i : 0])) < bound;
+                const uint32_t hits = __ballot_sync(~0u, hit), at = have + __popc(hits & ((1u << lane) - 1));
+                if (hit && at < top)
+                    sh.best[at] = order_key(-INFINITY, (uint32_t)i);
+                have += __popc(hits);
+                if (!__any_sync(~0u, in))
+                    break;
+            }
+        }
+    } else { // many equal values: one alternative a pass, the largest key below the last one
+        unsigned long long before = ~0ull;
+        for (uint32_t k = 0; k < top; ++k) {
+            if (tid == 0)
+                sh.largest = 0;
+            Tm::sync();
+            unsigned long long big = 0;
+            auto look = [&](uint64_t i) {
+                const unsigned long long key = order_key(to_f32(x[i]), (uint32_t)i);
+                if (key < before && key > big)
+                    big = key;
+            };
+            for (uint64_t i = a.row.head + a.v0 * V + tid; i < last; i += N)
+                look(i);
+            for (uint32_t i = tid; i < a.singles; i += N)
+                look(a.row.single(i));
+            atomicMax(&sh.largest, big);
+            Tm::sync();
+            before = sh.largest;
+            if (tid == 0)
+                sh.best[k] = before;
+            Tm::sync();
+        }
     }
-    // join lanes, warps (thread 0)
+    Tm::sync();
+}
+
+// a warp's sums, on every lane
+__device__ __forceinline__ void join_lanes(Softmax &sm, float c)
+{
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         sm.join(__shfl_xor_sync(~0u, sm.m, o), __shfl_xor_sync(~0u, sm.s, o), __shfl_xor_sync(~0u, sm.t, o), c);
-    if (lane == 0) {
-        sh.m[warp] = sm.m;
-        sh.s[warp] = sm.s;
-        sh.t[warp] = sm.t;
-    }
-    if (p.top) {
-        // warps whose threads all have a vector; with none, every finite value is ranked
-        const uint32_t full = (uint32_t)min((uint64_t)kLpWarps, (v1 - v0) / 32);
-        const uint32_t take = full ? (p.top + full - 1) / full : 0;
-        uint32_t mine = order_bits(own), low = 0;
-        for (uint32_t i = 0; i < min(take, 32u); ++i) {
-            low = __reduce_max_sync(~0u, mine);
-            const uint32_t at = __ffs(__ballot_sync(~0u, mine == low)) - 1;
-            if (lane == at)
-                mine = 0;
-        }
-        if (lane == 0)
-            sh.low[warp] = low;
-        if (tid == 0)
-            sh.n_key = sh.n_pair = 0;
-        __syncthreads();
-        uint32_t bound = order_bits(-INFINITY) + 1; // -infinity is no candidate
-        if (full) {
-            uint32_t b = 0xFFFFFFFFu;
-            for (uint32_t w = 0; w < full; ++w)
-                b = min(b, sh.low[w]);
-            bound = max(bound, b);
-        }
-        for (uint32_t k = 0; k < slot; ++k)
-            if (order_bits(sh.gmax[k][tid]) >= bound)
-                sh.pair[atomicAdd(&sh.n_pair, 1u)] = k << 16 | tid;
-        for (uint32_t k = tid; k < singles; k += kLpThreads) {
-            const uint64_t i = row.single(k);
-            const float v = to_f32(x[i]);
-            if (order_bits(v) >= bound)
-                sh.key[atomicAdd(&sh.n_key, 1u)] = order_key(v, (uint32_t)i); // at most 14
-        }
-        __syncthreads();
-        const uint32_t pairs = sh.n_pair;
-        for (uint32_t i = warp; i < pairs; i += kLpWarps) {
-            const uint32_t k = sh.pair[i] >> 16, t = sh.pair[i] & 0xFFFFu;
-            const uint64_t g0 = (uint64_t)k * per_slot, g1 = min(groups, g0 + per_slot);
-            for (uint64_t e = lane; e < (g1 - g0) * kUnroll * V; e += 32) {
-                const uint64_t v = v0 + (g0 * kUnroll + e / V) * kLpThreads + t;
-                if (v < v1) {
-                    const uint64_t at = row.head + v * V + e % V;
-                    const float f = to_f32(x[at]);
-                    if (order_bits(f) >= bound) {
-                        const uint32_t n = atomicAdd(&sh.n_key, 1u);
-                        if (n < kCandidates)
-                            sh.key[n] = order_key(f, (uint32_t)at);
-                    }
-                }
-            }
-        }
-        __syncthreads();
-        const uint32_t n = sh.n_key;
-        if (n <= kCandidates) {
-            rank_keys(sh, n, p.top);
-            __syncthreads();
-            if (n < p.top && warp == 0) { // fewer values than asked for: tokens without probability, lowest index first
-                uint32_t have = n;
-                // this CTA's values in index order: heads, vectors, tails
-                const uint64_t first = rank == 0 ? 0 : row.head + v0 * V;
-                const uint64_t last = row.head + v1 * V;
-                for (uint64_t i0 = first; have < p.top; i0 += 32) {
-                    // the vectors' range, then (first CTA) the tail
-                    uint64_t i = i0 + lane;
-                    bool in = i < last;
-                    if (!in && rank == 0) {
-                        i = row.head + row.vecs * V + (i - last);
-                        in = i < p.vocab;
-                    }
-                    const bool hit = in && order_bits(to_f32(x[in ? i : 0])) < bound;
-                    const uint32_t hits = __ballot_sync(~0u, hit), at = have + __popc(hits & ((1u << lane) - 1));
-                    if (hit && at < p.top)
-                        sh.best[at] = order_key(-INFINITY, (uint32_t)i);
-                    have += __popc(hits);
-                    if (!__any_sync(~0u, in))
-                        break;
-                }
-            }
-        } else { // many equal values: one alternative a pass, the largest key below the last one
-            unsigned long long before = ~0ull;
-            for (uint32_t k = 0; k < p.top; ++k) {
-                if (tid == 0)
-                    sh.largest = 0;
-                __syncthreads();
-                unsigned long long big = 0;
-                auto look = [&](uint64_t i) {
-                    const unsigned long long key = order_key(to_f32(x[i]), (uint32_t)i);
-                    if (key < before && key > big)
-                        big = key;
-                };
-                for (uint64_t i = row.head + v0 * V + tid; i < row.head + v1 * V; i += kLpThreads)
-                    look(i);
-                for (uint32_t i = tid; i < singles; i += kLpThreads)
-                    look(row.single(i));
-                atomicMax(&sh.largest, big);
-                __syncthreads();
-                before = sh.largest;
-                if (tid == 0)
-                    sh.best[k] = before;
-                __syncthreads();
-            }
-        }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        sm.m = sh.m[0];
-        sm.s = sh.s[0];
-        sm.t = sh.t[0];
-        for (int w = 1; w < kLpWarps; ++w)
-            sm.join(sh.m[w], sh.s[w], sh.t[w], c);
-        sh.cta[0] = sm.m;
-        sh.cta[1] = sm.s;
-        sh.cta[2] = sm.t;
-    }
-    __syncthreads();
-    if (split > 1) {
-        cluster_sync();
-        if (rank == 0) {
-            if (tid == 0) {
-                for (uint32_t q = 1; q < split; ++q) {
-                    const uint32_t a = cluster_addr(smem_u32(sh.cta), q);
-                    sm.join(cluster_load(a), cluster_load(a + 4), cluster_load(a + 8), c);
-                }
-                sh.cta[0] = sm.m;
-                sh.cta[1] = sm.s;
-                sh.cta[2] = sm.t;
-            }
-            const uint32_t n = split * p.top; // at most 256 keys; those of short shares are 0
-            if (tid == 0)
-                sh.n_key = 0;
-            __syncthreads();
-            for (uint32_t i = tid; i < n; i += kLpThreads) {
-                const uint32_t q = i / p.top, a = cluster_addr(smem_u32(sh.best + i % p.top), q);
-                const uint32_t lo = __float_as_uint(cluster_load(a)), hi = __float_as_uint(cluster_load(a + 4));
-                if (hi)
-                    sh.key[atomicAdd(&sh.n_key, 1u)] = (unsigned long long)hi << 32 | lo;
-            }
-            __syncthreads();
-            if (p.top)
-                rank_keys(sh, sh.n_key, p.top);
-            __syncthreads();
-        }
-        __syncwarp();
-        cluster_sync(); // the first CTA has read the others' results
-        if (rank)
-            return;
-    }
-    // t and log2 s are in units of log2(e)
-    const RowResult res(sh.cta[0], sh.cta[1], sh.cta[2] * 0.69314718f, p.scale);
+}
+
+// the row's outputs from sh.sum and sh.best; thread 0 knows the token and its logit
+template <typename Tm>
+__device__ __forceinline__ void write_row(const LogprobParams &p, const Tm &sh, uint64_t r, int64_t tok, float xtok)
+{
+    const uint32_t tid = Tm::thread();
+    // (t is in units of log2(e))
+    const RowResult res(sh.sum[0], sh.sum[1], sh.sum[2] * 0.69314718f, p.scale);
     if (tid == 0) {
         if (p.lse)
             p.lse[r] = res.lse;
@@ -452,6 +422,317 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads, 4) logprob_k
         p.top_index[r * p.top + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)k);
         p.top_logprob[r * p.top + tid] = res.logprob(v);
     }
+}
+
+// Short rows: a warp a row, four a block, no block barriers.
+template <typename T> __global__ void __launch_bounds__(128, 6) logprob_warp_kernel(LogprobParams p)
+{
+    __shared__ WarpTeam teams[4];
+    __shared__ float gmax[4][kSlots][32];
+    constexpr uint32_t V = RowView<T>::V, U = RowView<T>::U;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    WarpTeam &sh = teams[warp];
+    const uint64_t r = (uint64_t)blockIdx.x * 4 + warp;
+    if (r >= p.rows)
+        return;
+    const T *x = static_cast<const T *>(p.logits) + r * p.ld;
+    const RowView<T> row(x, p.vocab);
+    const Share<T> a{row, 0, row.vecs, p.vocab, row.head + row.tail};
+    const float c = p.scale * 1.44269504f;
+    const int64_t tok = p.tokens ? p.tokens[r] : -1;
+    const float xtok = tok >= 0 && tok < (int64_t)p.vocab ? to_f32(x[tok]) : 0.f;
+    const bool has_single = lane < a.singles;
+    const uint64_t single_at = has_single ? row.single(lane) : 0;
+    const float single = has_single ? to_f32(x[single_at]) : -INFINITY;
+    const uint64_t groups = (row.vecs + U * 32 - 1) / (U * 32);
+    const uint32_t per_slot = (uint32_t)((groups + kSlots - 1) / kSlots);
+    Softmax sm;
+    uint32_t slot = 0;
+    for (uint64_t g = 0; g < groups;) {
+        float slot_max = -INFINITY;
+        for (uint32_t k = 0; k < per_slot && g < groups; ++k, ++g) {
+            const uint64_t i0 = g * U * 32 + lane;
+            uint4 q[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u)
+                if (i0 + u * 32 < row.vecs)
+                    q[u] = ld_stream16(row.vec(i0 + u * 32));
+            float2 f[16];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u)
+                if (i0 + u * 32 < row.vecs) {
+                    unpack2<T>(q[u], f + u * V / 2);
+                } else {
+#pragma unroll
+                    for (uint32_t i = 0; i < V / 2; ++i)
+                        f[u * V / 2 + i] = both(-INFINITY);
+                }
+            slot_max = max_nan(slot_max, add_group(sm, f, c));
+        }
+        gmax[warp][slot][lane] = slot_max;
+        ++slot;
+    }
+    if (has_single) {
+        if (!(single <= sm.m))
+            sm.raise(max_nan(sm.m, single), c);
+        sm.add(single, c);
+    }
+    __syncwarp();
+    join_lanes(sm, c);
+    if (lane == 0) {
+        sh.sum[0] = sm.m;
+        sh.sum[1] = sm.s;
+        sh.sum[2] = sm.t;
+    }
+    __syncwarp();
+    if (p.top)
+        select_top<T>(sh, gmax[warp], a, p.top, slot, groups, per_slot, has_single, single, single_at);
+    write_row(p, sh, r, tok, xtok);
+}
+
+// Long rows.  A block walks the rows b, b + blocks, ... (split = 1), or a
+// cluster of `split` blocks shares one row and joins its parts through
+// distributed shared memory.  A copy warp streams the rows' vectors into a
+// ring (16 KB bulk copies, several in flight, on over the end of a row);
+// eight warps run the softmax and leave each row's sums and group maxima in
+// one of two buffers; four warps select the alternatives and write the row
+// meanwhile.  (With the eight warps selecting, the ring idled for most of a
+// row: 4096 rows of 50021 float32, top 20: 221 us.)  One pass over the logits,
+// bound by HBM.  If a bounded wait runs out, the block's remaining rows get
+// NaN.
+constexpr int kStreamThreads = kLpThreads + kSelThreads + 32;
+struct RowBuffer {
+    float gmax[kSlots][kLpThreads];
+    float m[kLpWarps], s[kLpWarps], t[kLpWarps];
+    uint32_t failed;
+};
+struct StreamShared {
+    RowBuffer row[2];
+    BlockTeam team;
+    uint64_t full[kStages], empty[kStages];
+};
+// hand a buffer over between the eight and the four warps (barriers 2 to 5)
+__device__ __forceinline__ void buffer_arrive(uint32_t id)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kLpThreads + kSelThreads) : "memory");
+}
+__device__ __forceinline__ void buffer_sync(uint32_t id)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kLpThreads + kSelThreads) : "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(LogprobParams p, uint32_t split)
+{
+    extern __shared__ __align__(128) uint8_t raw[];
+    constexpr uint32_t V = RowView<T>::V, U = RowView<T>::U;
+    uint8_t *ring = raw;
+    StreamShared &ss = *reinterpret_cast<StreamShared *>(raw + kStages * kStageBytes);
+    BlockTeam &sh = ss.team;
+    const uint32_t rank = split > 1 ? cluster_rank() : 0;
+    const uint64_t step = split > 1 ? p.rows : gridDim.x, r0 = blockIdx.x / split;
+    const float c = p.scale * 1.44269504f;
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < kStages; ++i) {
+            mbar_init(&ss.full[i], 1);
+            mbar_init(&ss.empty[i], kLpWarps);
+        }
+        fence_mbar_init();
+        fence_proxy_async();
+        ss.row[0].failed = ss.row[1].failed = 0;
+    }
+    __syncthreads();
+    auto share_of = [&](uint64_t r) {
+        const RowView<T> row(static_cast<const T *>(p.logits) + r * p.ld, p.vocab);
+        return Share<T>{row, row.vecs * rank / split, row.vecs * (rank + 1) / split, p.vocab,
+                        rank == 0 ? row.head + row.tail : 0};
+    };
+    auto groups_of = [&](const Share<T> &a) { return (a.v1 - a.v0 + U * kLpThreads - 1) / (U * kLpThreads); };
+    auto per_slot_of = [&](uint64_t groups) { return (uint32_t)((groups + kSlots - 1) / kSlots); };
+    if (threadIdx.x >= kLpThreads + kSelThreads) { // the copy warp
+        if (threadIdx.x == kLpThreads + kSelThreads) {
+            uint32_t st = 0, ph = 0, issued = 0;
+            bool ok = true;
+            for (uint64_t r = r0; r < p.rows && ok; r += step) {
+                const Share<T> a = share_of(r);
+                for (uint64_t v = a.v0; v < a.v1; v += kStageVecs) {
+                    if (!(ok = mbar_wait(&ss.empty[st], ph ^ 1, kWaitLimitNs)))
+                        break;
+                    const uint32_t bytes = (uint32_t)min((uint64_t)kStageVecs, a.v1 - v) * 16;
+                    mbar_expect_tx(&ss.full[st], bytes);
+                    bulk_g2s(ring + st * kStageBytes, a.row.vec(v), bytes, &ss.full[st]);
+                    ++issued;
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok) // the copies in flight: a last wait each
+                for (uint32_t i = 0; i < min(issued, kStages); ++i) {
+                    if (st == 0) {
+                        st = kStages;
+                        ph ^= 1;
+                    }
+                    --st;
+                    (void)mbar_wait(&ss.full[st], ph, kWaitLimitNs);
+                }
+        }
+    } else if (threadIdx.x < kLpThreads) { // the softmax
+        const uint32_t tid = threadIdx.x;
+        uint32_t st = 0, ph = 0, b = 0;
+        bool ok = true; // a wait that runs out ends the block's loads
+        for (uint64_t r = r0; r < p.rows; r += step, b ^= 1) {
+            RowBuffer &buf = ss.row[b];
+            if (r >= r0 + 2 * step)
+                buffer_sync(4 + b); // the row before last is written
+            const Share<T> a = share_of(r);
+            const uint64_t nv = a.v1 - a.v0, groups = groups_of(a);
+            const uint32_t per_slot = per_slot_of(groups);
+            Softmax sm;
+            uint32_t slot = 0;
+            for (uint64_t g = 0; g < groups && ok;) {
+                float slot_max = -INFINITY;
+                for (uint32_t k = 0; k < per_slot && g < groups; ++k, ++g) {
+                    float2 f[16];
+#pragma unroll
+                    for (uint32_t h = 0; h < U / 4; ++h) { // a group's stages
+                        const uint64_t done = g * U * kLpThreads + h * kStageVecs;
+                        const uint32_t count = done < nv ? (uint32_t)min((uint64_t)kStageVecs, nv - done) : 0;
+                        if (count && !(ok = ok && mbar_wait(&ss.full[st], ph, kWaitLimitNs)))
+                            ss.row[0].failed = ss.row[1].failed = 1;
+                        const uint4 *q = reinterpret_cast<const uint4 *>(ring + st * kStageBytes);
+                        if (count == kStageVecs) {
+#pragma unroll
+                            for (uint32_t u = 0; u < 4; ++u)
+                                unpack2<T>(q[tid + u * kLpThreads], f + (h * 4 + u) * V / 2);
+                        } else {
+#pragma unroll
+                            for (uint32_t u = 0; u < 4; ++u)
+                                if (tid + u * kLpThreads < count) {
+                                    unpack2<T>(q[tid + u * kLpThreads], f + (h * 4 + u) * V / 2);
+                                } else {
+#pragma unroll
+                                    for (uint32_t i = 0; i < V / 2; ++i)
+                                        f[(h * 4 + u) * V / 2 + i] = both(-INFINITY);
+                                }
+                        }
+                        if (count) {
+                            __syncwarp();
+                            if ((tid & 31) == 0) // the stage is in registers
+                                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&ss.empty[st])) : "memory");
+                            if (++st == kStages) {
+                                st = 0;
+                                ph ^= 1;
+                            }
+                        }
+                    }
+                    if (!ok)
+                        break;
+                    slot_max = max_nan(slot_max, add_group(sm, f, c));
+                }
+                if (ok && p.top)
+                    buf.gmax[slot++][tid] = slot_max;
+            }
+            __syncwarp();
+            join_lanes(sm, c);
+            if ((tid & 31) == 0) {
+                buf.m[tid >> 5] = sm.m;
+                buf.s[tid >> 5] = sm.s;
+                buf.t[tid >> 5] = sm.t;
+            }
+            buffer_arrive(2 + b);
+        }
+    } else { // the alternatives and the outputs
+        const uint32_t tid = BlockTeam::thread();
+        uint32_t b = 0;
+        for (uint64_t r = r0; r < p.rows; r += step, b ^= 1) {
+            RowBuffer &buf = ss.row[b];
+            const Share<T> a = share_of(r);
+            // asked for early: the token's logit, the values at the row's ends (lanes 8 to 21 of the first warp)
+            const int64_t tok = p.tokens && tid == 0 && rank == 0 ? p.tokens[r] : -1;
+            const float xtok = tok >= 0 && tok < (int64_t)p.vocab ? to_f32(a.row.x[tok]) : 0.f;
+            const bool has_single = tid >= 8 && tid - 8 < a.singles;
+            const uint64_t single_at = has_single ? a.row.single(tid - 8) : 0;
+            const float single = has_single ? to_f32(a.row.x[single_at]) : -INFINITY;
+            const uint64_t groups = groups_of(a);
+            const uint32_t per_slot = per_slot_of(groups);
+            buffer_sync(2 + b);
+            const bool failed = buf.failed;
+            if (tid < 32) {
+                Softmax sm;
+                if (tid < kLpWarps) {
+                    sm.m = failed ? NAN : buf.m[tid];
+                    sm.s = buf.s[tid];
+                    sm.t = buf.t[tid];
+                } else if (has_single) {
+                    sm.m = single;
+                    sm.add(single, c);
+                }
+                join_lanes(sm, c);
+                if (tid == 0) {
+                    sh.sum[0] = sm.m;
+                    sh.sum[1] = sm.s;
+                    sh.sum[2] = sm.t;
+                }
+            }
+            if (failed) {
+                for (uint32_t i = tid; i < p.top; i += kSelThreads)
+                    sh.best[i] = order_key(NAN, 0);
+            } else if (p.top) {
+                const uint32_t slots = per_slot ? (uint32_t)((groups + per_slot - 1) / per_slot) : 0;
+                select_top<T>(sh, buf.gmax, a, p.top, slots, groups, per_slot, has_single, single, single_at);
+            }
+            BlockTeam::sync();
+            if (r + 2 * step < p.rows)
+                buffer_arrive(4 + b);
+            if (split > 1)
+                break; // one row a cluster; its parts are joined below
+            write_row(p, sh, r, tok, xtok);
+            BlockTeam::sync(); // the next row writes what write_row reads
+        }
+    }
+    if (split == 1)
+        return;
+    __syncwarp();
+    cluster_sync(); // every part is there
+    if (rank == 0 && threadIdx.x >= kLpThreads && threadIdx.x < kLpThreads + kSelThreads) {
+        const uint32_t tid = BlockTeam::thread();
+        const int64_t tok = p.tokens && tid == 0 ? p.tokens[r0] : -1;
+        const T *x = static_cast<const T *>(p.logits) + r0 * p.ld;
+        const float xtok = tok >= 0 && tok < (int64_t)p.vocab ? to_f32(x[tok]) : 0.f;
+        if (tid < 32) {
+            Softmax sm;
+            if (tid < split) {
+                const uint32_t at = cluster_addr(smem_u32(sh.sum), tid);
+                sm.m = cluster_load(at);
+                sm.s = cluster_load(at + 4);
+                sm.t = cluster_load(at + 8);
+            }
+            join_lanes(sm, c);
+            if (tid == 0) {
+                sh.sum[0] = sm.m;
+                sh.sum[1] = sm.s;
+                sh.sum[2] = sm.t;
+                sh.n_key = 0;
+            }
+        }
+        BlockTeam::sync();
+        const uint32_t n = split * p.top; // at most 256 keys; a short share's missing ones are 0
+        for (uint32_t i = tid; i < n; i += kSelThreads) {
+            const uint32_t at = cluster_addr(smem_u32(sh.best + i % p.top), i / p.top);
+            const uint32_t lo = __float_as_uint(cluster_load(at)), hi = __float_as_uint(cluster_load(at + 4));
+            if (hi)
+                sh.key[atomicAdd(&sh.n_key, 1u)] = (unsigned long long)hi << 32 | lo;
+        }
+        BlockTeam::sync();
+        if (p.top)
+            rank_keys(sh, sh.n_key, p.top);
+        BlockTeam::sync();
+        write_row(p, sh, r0, tok, xtok);
+    }
+    __syncwarp();
+    cluster_sync(); // the first block has read the others' parts
 }
 
 // ---------------------------------------------------------------- gradient
@@ -474,14 +755,21 @@ __device__ __forceinline__ uint4 load_once(const uint4 *p)
 struct GradRow {
     float m, c, l, A, B, dlp, dent, ent, scale;
     int64_t tok;
+    __device__ __forceinline__ float log2p(float x) const { return fmaxf(fmaf(x - m, c, -l), -200.f); }
     __device__ __forceinline__ float value(float x) const
     {
-        const float g = fmaxf(fmaf(x - m, c, -l), -200.f);
+        const float g = log2p(x);
         return exp2_fast(g) * fmaf(B, g, A);
+    }
+    __device__ __forceinline__ float2 value2(float2 x) const
+    {
+        float2 g = fma2(add2(x, both(-m)), both(c), both(-l));
+        g = make_float2(fmaxf(g.x, -200.f), fmaxf(g.y, -200.f));
+        return mul2(make_float2(exp2_fast(g.x), exp2_fast(g.y)), fma2(both(B), g, both(A)));
     }
     __device__ __forceinline__ float token_value(float x) const
     {
-        const float g = fmaxf(fmaf(x - m, c, -l), -200.f);
+        const float g = log2p(x);
         const double q = exp2_fast(g), tail = q * ((double)g * 0.6931471805599453 + ent);
         return (float)(((double)dlp * (1.0 - q) - (double)dent * tail) * scale);
     }
@@ -502,32 +790,6 @@ template <typename Op> __device__ __forceinline__ float block_reduce(float v, Op
     for (int i = 1; i < kLpWarps; ++i)
         v = op(v, part[i]);
     return v;
-}
-
-template <typename T> __device__ __forceinline__ uint4 pack(const float *f);
-template <> __device__ __forceinline__ uint4 pack<float>(const float *f)
-{
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-}
-template <> __device__ __forceinline__ uint4 pack<bf16>(const float *f)
-{
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <> __device__ __forceinline__ uint4 pack<__half>(const float *f)
-{
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 b = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // A row by a cluster of `split` CTAs, each a share of it.
@@ -575,23 +837,34 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads) logprob_grad
     if ((((uintptr_t)x ^ (uintptr_t)d) & 15) == 0) { // both rows' vectors start at the same value
         const uint64_t v0 = view.vecs * part / split, v1 = view.vecs * (part + 1) / split;
         uint4 *out = reinterpret_cast<uint4 *>(d + view.head);
-        for (uint64_t i0 = v0 + tid; i0 < v1; i0 += kUnroll * kLpThreads) {
-            uint4 q[kUnroll];
+        // the token's vector, if it lies in one
+        const uint64_t tv = row.tok >= (int64_t)view.head ? (uint64_t)(row.tok - view.head) / V : ~0ull;
+        for (uint64_t i0 = v0 + tid; i0 < v1; i0 += 4 * kLpThreads) {
+            uint4 q[4];
 #pragma unroll
-            for (uint32_t u = 0; u < kUnroll; ++u)
+            for (uint32_t u = 0; u < 4; ++u)
                 if (i0 + u * kLpThreads < v1)
                     q[u] = load_once(view.vec(i0 + u * kLpThreads));
 #pragma unroll
-            for (uint32_t u = 0; u < kUnroll; ++u) {
+            for (uint32_t u = 0; u < 4; ++u) {
                 const uint64_t i = i0 + u * kLpThreads;
                 if (i < v1) {
-                    float f[V];
-                    unpack<T>(q[u], f);
-                    const uint64_t at = (uint64_t)row.tok - (view.head + i * V);
+                    float2 f[V / 2], o[V / 2];
+                    unpack2<T>(q[u], f);
 #pragma unroll
-                    for (uint32_t k = 0; k < V; ++k)
-                        f[k] = at == k ? row.token_value(f[k]) : row.value(f[k]);
-                    st_stream16(out + i, pack<T>(f));
+                    for (uint32_t k = 0; k < V / 2; ++k)
+                        o[k] = row.value2(f[k]);
+                    if (i == tv) {
+                        const uint32_t at = (uint32_t)(row.tok - view.head) % V;
+#pragma unroll
+                        for (uint32_t k = 0; k < V / 2; ++k) {
+                            if (at == 2 * k)
+                                o[k].x = row.token_value(f[k].x);
+                            if (at == 2 * k + 1)
+                                o[k].y = row.token_value(f[k].y);
+                        }
+                    }
+                    st_stream16(out + i, pack2<T>(o));
                 }
             }
         }
@@ -633,11 +906,11 @@ uint32_t row_split(uint64_t rows, uint64_t vocab, uint64_t ctas, uint64_t least)
     return s;
 }
 
-cudaLaunchConfig_t row_config(uint64_t rows, uint32_t split, size_t smem, cudaLaunchAttribute *at, cudaStream_t st)
+cudaLaunchConfig_t row_config(uint64_t rows, uint32_t split, int threads, size_t smem, cudaLaunchAttribute *at, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(rows * split));
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     at->id = cudaLaunchAttributeClusterDimension;
@@ -651,15 +924,24 @@ cudaLaunchConfig_t row_config(uint64_t rows, uint32_t split, size_t smem, cudaLa
 template <typename T> ecc_status logprob_launch(const LogprobParams &p, cudaStream_t st)
 {
     const int sms = sm_count();
-    const size_t smem = sizeof(LogprobShared);
-    if (sms <= 0 || occupancy((const void *)logprob_kernel<T>, kLpThreads, smem) <= 0)
+    if (sms <= 0)
         return ECC_ERR_CUDA;
-    const uint32_t split = row_split(p.rows, p.vocab, 2ull * sms, 2048);
-    if (p.rows >= (1ull << 31) / split)
-        return ECC_ERR_ARG;
+    // a warp a row where that fills the GPU, or where a block would have
+    // fewer than eight values a thread
+    if (p.vocab <= 2048 || (p.vocab <= 8192 && p.rows >= 8ull * sms)) {
+        if (p.rows > (1ull << 32))
+            return ECC_ERR_ARG;
+        logprob_warp_kernel<T><<<(unsigned)((p.rows + 3) / 4), 128, 0, st>>>(p);
+        return launch_status(cudaGetLastError());
+    }
+    const size_t smem = kStages * kStageBytes + sizeof(StreamShared);
+    if (occupancy((const void *)logprob_stream_kernel<T>, kStreamThreads, smem) <= 0)
+        return ECC_ERR_CUDA;
+    const uint32_t split = row_split(p.rows, p.vocab, 2ull * sms, 4096);
+    const uint64_t rows = split > 1 ? p.rows : std::min<uint64_t>(p.rows, 2ull * sms);
     cudaLaunchAttribute at;
-    const cudaLaunchConfig_t cfg = row_config(p.rows, split, smem, &at, st);
-    return launch_status(cudaLaunchKernelEx(&cfg, logprob_kernel<T>, p, split));
+    const cudaLaunchConfig_t cfg = row_config(rows, split, kStreamThreads, smem, &at, st);
+    return launch_status(cudaLaunchKernelEx(&cfg, logprob_stream_kernel<T>, p, split));
 }
 
 template <typename T> ecc_status logprob_grad_launch(const LogprobGradParams &p, cudaStream_t st)
@@ -671,7 +953,7 @@ template <typename T> ecc_status logprob_grad_launch(const LogprobGradParams &p,
     if (p.rows >= (1ull << 31) / split)
         return ECC_ERR_ARG;
     cudaLaunchAttribute at;
-    const cudaLaunchConfig_t cfg = row_config(p.rows, split, 0, &at, st);
+    const cudaLaunchConfig_t cfg = row_config(p.rows, split, kLpThreads, 0, &at, st);
     return launch_status(cudaLaunchKernelEx(&cfg, logprob_grad_kernel<T>, p, split));
 }
 

@@ -160,57 +160,66 @@ __global__ void __launch_bounds__(kNormThreads) norm_parts_kernel(const float *p
 }
 
 // ---------------------------------------------------------------- rows in registers
-// V consecutive elements as one memory access
-template <typename T, int V> struct alignas(V * sizeof(T)) Pack {
-    T v[V];
-};
-// not through the read-only path: the output may be the input
-template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T *p)
+// A thread holds E values of a row, in pairs: E / V accesses of V values
+// (V = 16 / sizeof(T), rows on 16-byte boundaries; V = 1, rows anywhere),
+// access k at columns (t + k * width) V; values past the row's end are 0.
+// (Loads are not through the read-only path: the output may be the input.)
+template <typename T, int V, int E>
+__device__ __forceinline__ void load_row(const T *row, uint32_t t, uint32_t width, uint32_t n, float2 (&f)[E / 2])
 {
-    return *reinterpret_cast<const Pack<T, V> *>(p);
-}
-template <typename T, int V> __device__ __forceinline__ void store_pack(T *p, const float (&f)[V])
-{
-    Pack<T, V> o;
+    if constexpr (V == 1) {
+        T q[E];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        o.v[i] = from_f32<T>(f[i]);
-    *reinterpret_cast<Pack<T, V> *>(p) = o;
-}
-template <int V> __device__ __forceinline__ void store_pack(e4m3 *p, const float (&f)[V])
-{
-    if constexpr (V % 2 == 0) {
-        Pack<uint16_t, V / 2> o;
+        for (int k = 0; k < E; ++k)
+            q[k] = t + k * width < n ? row[t + k * width] : T(0.f);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i)
-            o.v[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-        *reinterpret_cast<Pack<uint16_t, V / 2> *>(p) = o;
+        for (int k = 0; k < E; k += 2)
+            f[k / 2] = make_float2(to_f32(q[k]), to_f32(q[k + 1]));
     } else {
+        uint4 q[E / V];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            p[i] = from_f32<e4m3>(f[i]);
+        for (int k = 0; k < E / V; ++k)
+            q[k] = t + k * width < n ? *reinterpret_cast<const uint4 *>(row + (uint64_t)(t + k * width) * V)
+                                     : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < E / V; ++k)
+            unpack2<T>(q[k], f + k * V / 2);
     }
 }
-// V parameters from column c: of the rows' type in one access, or float32
-template <typename T, int V> __device__ __forceinline__ void load_params(const void *p, uint64_t c, uint32_t type, float (&f)[V])
+// access k of a parameter vector (of the rows' type, or float32)
+template <typename T, int V>
+__device__ __forceinline__ void load_params(const void *p, uint32_t at, uint32_t type, float2 (&f)[V / 2])
 {
     if (type == TypeCode<T>::value) {
-        const Pack<T, V> q = load_pack<T, V>(static_cast<const T *>(p) + c);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            f[i] = to_f32(q.v[i]);
+        unpack2<T>(*reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + (uint64_t)at * V), f);
     } else {
+        const float *q = static_cast<const float *>(p) + (uint64_t)at * V;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            f[i] = static_cast<const float *>(p)[c + i];
+        for (int i = 0; i < V / 2; ++i)
+            f[i] = make_float2(q[2 * i], q[2 * i + 1]);
+    }
+}
+template <typename T, int V> __device__ __forceinline__ void store_values(T *p, const float2 *f)
+{
+    if constexpr (sizeof(T) == 1) {
+        uint32_t w[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            w[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(f[2 * i], __NV_SATFINITE, __NV_E4M3) |
+                   (uint32_t)__nv_cvt_float2_to_fp8x2(f[2 * i + 1], __NV_SATFINITE, __NV_E4M3) << 16;
+        if constexpr (V == 8)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t *>(p) = w[0];
+    } else {
+        *reinterpret_cast<uint4 *>(p) = pack2<T>(f);
     }
 }
 
-// A row by `warps` warps, PER accesses of V elements a thread: the row is
-// read once and both passes over it (the mean, the squared deviations) run
-// on registers.  Blocks of one warp a row hold four rows.  Bound by HBM: the
-// row read, the output written.
-template <typename T, typename TO, int V, int PER>
+// A row by `warps` warps: it is read once and both passes over it (the mean,
+// the squared deviations) run on registers.  Blocks of one warp a row hold
+// four rows.  Bound by HBM: the row read, the output written.
+template <typename T, typename TO, int V, int E>
 __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, uint32_t warps)
 {
     __shared__ float part[2][32];
@@ -219,12 +228,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, uint32_t warps
     if (r >= p.rows)
         return; // (whole warps of a block of one warp a row)
     const uint32_t t = warps == 1 ? lane : threadIdx.x, n = (uint32_t)(p.cols / V);
-    const T *x = static_cast<const T *>(p.x) + r * p.ldx;
-    Pack<T, V> q[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k)
-        if (t + k * width < n)
-            q[k] = load_pack<T, V>(x + (uint64_t)(t + k * width) * V);
+    float2 f[E / 2];
+    load_row<T, V, E>(static_cast<const T *>(p.x) + r * p.ldx, t, width, n, f);
     auto total = [&](float s, int which) {
         s = warp_sum(s);
         if (warps == 1)
@@ -236,50 +241,70 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, uint32_t warps
         return warp_sum(s);
     };
     const float inv = 1.f / (float)p.cols;
-    float s = 0.f;
+    float2 s = both(0.f);
 #pragma unroll
-    for (int k = 0; k < PER; ++k)
-        if (t + k * width < n) {
+    for (int i = 0; i < E / 2; ++i)
+        s = add2(s, f[i]);
+    const float mean = total(s.x + s.y, 0) * inv;
+    s = both(0.f);
+    const float2 minus = both(-mean);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                s += to_f32(q[k].v[i]);
+    for (int i = 0; i < E / 2; ++i) {
+        f[i] = add2(f[i], minus);
+        if constexpr (V == 1) { // past the end: no deviation
+            if (t + 2 * i * width >= n)
+                f[i].x = 0.f;
+            if (t + (2 * i + 1) * width >= n)
+                f[i].y = 0.f;
+        } else if (t + (2 * i / V) * width >= n) {
+            f[i] = both(0.f);
         }
-    const float mean = total(s, 0) * inv;
-    s = 0.f;
-#pragma unroll
-    for (int k = 0; k < PER; ++k)
-        if (t + k * width < n) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = to_f32(q[k].v[i]) - mean;
-                s += d * d;
-            }
-        }
-    const float rstd = 1.f / sqrtf(total(s, 1) * inv + p.eps);
+        s = fma2(f[i], f[i], s);
+    }
+    const float rstd = 1.f / sqrtf(total(s.x + s.y, 1) * inv + p.eps);
     TO *y = static_cast<TO *>(p.y) + r * p.ldy;
+    const float2 r2 = both(rstd), scale = both(p.y_scale);
+    if constexpr (V == 1) {
 #pragma unroll
-    for (int k = 0; k < PER; ++k)
-        if (t + k * width < n) {
-            const uint64_t c = (uint64_t)(t + k * width) * V;
-            float f[V], w[V], b[V];
-            if (p.weight)
-                load_params<T, V>(p.weight, c, p.p_type, w);
-            if (p.bias)
-                load_params<T, V>(p.bias, c, p.p_type, b);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                f[i] = (to_f32(q[k].v[i]) - mean) * rstd;
+        for (int k = 0; k < E; ++k) {
+            const uint32_t c = t + k * width;
+            if (c < n) {
+                float v = (k & 1 ? f[k / 2].y : f[k / 2].x) * rstd;
                 if (p.weight)
-                    f[i] *= w[i];
+                    v *= load_any(p.weight, c, p.p_type);
                 if (p.bias)
-                    f[i] += b[i];
-                f[i] *= p.y_scale;
+                    v += load_any(p.bias, c, p.p_type);
+                y[c] = from_f32<TO>(v * p.y_scale);
             }
-            if constexpr (sizeof(TO) == 1)
-                store_pack<V>(y + c, f);
-            else
-                store_pack<TO, V>(y + c, f);
         }
+    } else {
+#pragma unroll
+        for (int k = 0; k < E / V; ++k)
+            if (t + k * width < n) {
+                float2 *v = f + k * V / 2, q[V / 2];
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i)
+                    v[i] = mul2(v[i], r2);
+                if (p.weight) {
+                    load_params<T, V>(p.weight, t + k * width, p.p_type, q);
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i)
+                        v[i] = mul2(v[i], q[i]);
+                }
+                if (p.bias) {
+                    load_params<T, V>(p.bias, t + k * width, p.p_type, q);
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i)
+                        v[i] = add2(v[i], q[i]);
+                }
+                if constexpr (sizeof(TO) == 1) {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i)
+                        v[i] = mul2(v[i], scale);
+                }
+                store_values<TO, V>(y + (uint64_t)(t + k * width) * V, v);
+            }
+    }
     if (t == 0) {
         if (p.mean)
             p.mean[r] = mean;
@@ -289,17 +314,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, uint32_t warps
 }
 
 // ---------------------------------------------------------------- backward, rows in registers
-constexpr int kGradThreads = 1024; // a block an SM; groups of `width` threads take a row each
-constexpr int kGradWarps = kGradThreads / 32;
-
-// groups of a block; each of several warps has a barrier of its own (1 to 15)
-__host__ __device__ inline uint32_t grad_groups(uint32_t width)
-{
-    const uint32_t g = kGradThreads / width;
-    return width > 32 && g > 15 ? 15 : g;
-}
-
-__device__ __forceinline__ void group_barrier(uint32_t id, uint32_t threads)
+__device__ __forceinline__ void group_barrier(uint32_t id, uint32_t threads) // id below 15
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
 }
@@ -309,54 +324,118 @@ __device__ __forceinline__ void copy_async16(uint32_t dst, const void *src)
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 load_shared16(uint32_t at)
+{
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
+    return q;
+}
 
-// Persistent: a group of `width` threads walks the rows g, g + groups, ...;
-// each thread keeps its columns' sums of dy * xh and dy in registers, so x
-// and dy are read once for all three gradients.  With RING > 0 a thread
-// copies its 16-byte pieces of the next RING - 1 rows ahead into its own
-// part of shared memory (nobody else reads it: no barrier); otherwise
-// (elements on other boundaries) it loads as it goes.  One barrier a row joins the
-// warps' sums.  The groups' column sums are added in shared memory and the
-// blocks' in norm_parts_kernel, both in a fixed order.  Bound by HBM.
-template <typename T, int V, int PER, int RING>
-__global__ void __launch_bounds__(kGradThreads, 1) norm_grad_kernel(NormGradParams p, uint32_t width)
+// The sums over a group's threads of 2 ROWS values each, known to all of them
+// on return: within a warp the values are halved over the lanes (each lane
+// ends with one value), the warps' sums go through shared memory.
+template <int ROWS>
+__device__ __forceinline__ void group_sums(float (&v)[2 * ROWS], float (*part)[2 * ROWS], uint32_t group, uint32_t width,
+                                           uint32_t warp0)
+{
+    constexpr int NV = 2 * ROWS, SPAN = 32 / NV; // lanes that hold one value's parts in the end
+    const uint32_t lane = threadIdx.x & 31, warps = width / 32;
+    int n = NV;
+#pragma unroll
+    for (int o = 16; o >= SPAN; o >>= 1) {
+        n /= 2;
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(~0u, send, o);
+        }
+    }
+    float s = v[0]; // value lane / SPAN
+#pragma unroll
+    for (int o = SPAN / 2; o; o >>= 1)
+        s += __shfl_xor_sync(~0u, s, o);
+    if (warps > 1) {
+        if (lane % SPAN == 0)
+            part[threadIdx.x >> 5][lane / SPAN] = s;
+        group_barrier(group, width);
+        s = 0.f;
+        for (uint32_t w = lane % SPAN; w < warps; w += SPAN)
+            s += part[warp0 + w][lane / SPAN];
+#pragma unroll
+        for (int o = SPAN / 2; o; o >>= 1)
+            s += __shfl_xor_sync(~0u, s, o);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        v[i] = __shfl_sync(~0u, s, i * SPAN);
+}
+
+// Persistent, a block an SM: groups of `width` of its NT threads walk their
+// rows ROWS at a time; each thread keeps its columns' sums of dy * xh and dy
+// in registers, so x and dy are read once for all three gradients.  With
+// RING > 0 a thread copies its 16-byte pieces of the next RING - 1 steps
+// ahead into its own part of shared memory (nobody else reads it: no
+// barrier); otherwise (V = 1) it loads as it goes.  One barrier a step joins
+// the warps' sums.  The groups' column sums are added in shared memory and
+// the blocks' in norm_parts_kernel, both in a fixed order.  Bound by HBM.
+template <typename T, int NT, int V, int E, int RING, int ROWS>
+__global__ void __launch_bounds__(NT, 1) norm_grad_kernel(NormGradParams p, uint32_t width)
 {
     extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ float2 part[2][kGradWarps];
-    const uint32_t tid = threadIdx.x, lane = tid & 31, group = tid / width, t = tid - group * width;
-    const uint32_t groups = grad_groups(width), warps = width / 32, warp0 = group * warps, warp = tid >> 5;
+    __shared__ float part[2][NT / 32][2 * ROWS];
+    constexpr int PER = E / V;
+    const uint32_t tid = threadIdx.x, group = tid / width, t = tid - group * width;
+    const uint32_t groups = NT / width, warp0 = group * (width / 32);
     const uint32_t n = (uint32_t)(p.cols / V);
-    const uint64_t step = (uint64_t)gridDim.x * groups;
+    const uint64_t step = (uint64_t)gridDim.x * groups * ROWS;
     const float inv = 1.f / (float)p.cols;
-    float w[PER][V], aw[PER][V], ab[PER][V];
+    float2 w[E / 2], aw[E / 2], ab[E / 2];
 #pragma unroll
-    for (int k = 0; k < PER; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            w[k][i] = 1.f;
-            aw[k][i] = ab[k][i] = 0.f;
-        }
+    for (int i = 0; i < E / 2; ++i) {
+        w[i] = both(1.f);
+        aw[i] = ab[i] = both(0.f);
+    }
     const bool works = group < groups; // threads past the last whole group only join the barriers of the end
     const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
     T *dx = static_cast<T *>(p.dx);
     if (works) {
-        if (p.weight)
+        if (p.weight) {
+            if constexpr (V == 1) {
 #pragma unroll
-            for (int k = 0; k < PER; ++k)
-                if (t + k * width < n)
-                    load_params<T, V>(p.weight, (uint64_t)(t + k * width) * V, p.p_type, w[k]);
-        const uint64_t r0 = (uint64_t)blockIdx.x * groups + group;
-        const uint32_t slots = smem_u32(raw) + tid * 16; // piece s of a row's 2 PER at s * kGradThreads * 16
+                for (int k = 0; k < E; ++k)
+                    if (t + k * width < n)
+                        (k & 1 ? w[k / 2].y : w[k / 2].x) = load_any(p.weight, t + k * width, p.p_type);
+            } else {
+#pragma unroll
+                for (int k = 0; k < PER; ++k)
+                    if (t + k * width < n) {
+                        float2 q[V / 2];
+                        load_params<T, V>(p.weight, t + k * width, p.p_type, q);
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i)
+                            w[k * V / 2 + i] = q[i];
+                    }
+            }
+        }
+        const uint64_t r0 = ((uint64_t)blockIdx.x * groups + group) * ROWS;
+        // piece i of a step (row, access, x or dy) at i * NT * 16
+        const uint32_t slots = smem_u32(raw) + tid * 16;
+        constexpr uint32_t pieces = ROWS * PER * 2;
         auto fetch = [&](uint64_t r, uint32_t at) {
             if constexpr (RING > 0) {
-                if (r < p.rows)
 #pragma unroll
-                    for (int k = 0; k < PER; ++k)
-                        if (t + k * width < n) {
-                            const uint64_t c = (uint64_t)(t + k * width) * V;
-                            copy_async16(slots + (at * 2 * PER + 2 * k) * kGradThreads * 16, x + r * p.ldx + c);
-                            copy_async16(slots + (at * 2 * PER + 2 * k + 1) * kGradThreads * 16, dy + r * p.lddy + c);
-                        }
+                for (int j = 0; j < ROWS; ++j)
+                    if (r + j < p.rows) {
+#pragma unroll
+                        for (int k = 0; k < PER; ++k)
+                            if (t + k * width < n) {
+                                const uint64_t c = (uint64_t)(t + k * width) * V;
+                                const uint32_t to = slots + (at * pieces + (j * PER + k) * 2) * NT * 16;
+                                copy_async16(to, x + (r + j) * p.ldx + c);
+                                copy_async16(to + NT * 16, dy + (r + j) * p.lddy + c);
+                            }
+                    }
                 copy_async_commit();
             }
         };
@@ -364,65 +443,77 @@ __global__ void __launch_bounds__(kGradThreads, 1) norm_grad_kernel(NormGradPara
         for (int k = 0; k + 1 < RING; ++k)
             fetch(r0 + k * step, k);
         uint32_t at = 0, flip = 0;
+        float mean[ROWS], rstd[ROWS];
+        auto stats = [&](uint64_t r) {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+                mean[j] = r + j < p.rows ? p.mean[r + j] : 0.f;
+                rstd[j] = r + j < p.rows ? p.rstd[r + j] : 0.f;
+            }
+        };
+        stats(r0);
         for (uint64_t r = r0; r < p.rows; r += step) {
-            Pack<T, V> xq[PER], dq[PER];
-            const float mean = p.mean[r], rstd = p.rstd[r];
             if constexpr (RING > 0) {
                 fetch(r + (RING - 1) * step, at ? at - 1 : RING - 1);
                 copy_async_wait<RING - 1>();
-#pragma unroll
-                for (int k = 0; k < PER; ++k) {
-                    xq[k] = *reinterpret_cast<const Pack<T, V> *>(raw + ((at * 2 * PER + 2 * k) * kGradThreads + tid) * 16);
-                    dq[k] = *reinterpret_cast<const Pack<T, V> *>(raw + ((at * 2 * PER + 2 * k + 1) * kGradThreads + tid) * 16);
-                }
-                at = at + 1 == RING ? 0 : at + 1;
-            } else {
-#pragma unroll
-                for (int k = 0; k < PER; ++k)
-                    if (t + k * width < n) {
-                        xq[k] = load_pack<T, V>(x + r * p.ldx + (uint64_t)(t + k * width) * V);
-                        dq[k] = load_pack<T, V>(dy + r * p.lddy + (uint64_t)(t + k * width) * V);
-                    }
             }
-            float s = 0.f, q = 0.f;
+            float2 g[ROWS][E / 2], xh[ROWS][E / 2];
+            float v[2 * ROWS], rs[ROWS];
 #pragma unroll
-            for (int k = 0; k < PER; ++k)
-                if (t + k * width < n) {
+            for (int j = 0; j < ROWS; ++j) {
+                if constexpr (RING > 0) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float d = to_f32(dq[k].v[i]), xh = (to_f32(xq[k].v[i]) - mean) * rstd, g = d * w[k][i];
-                        s += g;
-                        q += g * xh;
-                        aw[k][i] += d * xh;
-                        ab[k][i] += d;
+                    for (int k = 0; k < PER; ++k) {
+                        const uint32_t s0 = slots + (at * pieces + (j * PER + k) * 2) * NT * 16;
+                        const bool in = r + j < p.rows && t + k * width < n;
+                        const uint4 zero = make_uint4(0, 0, 0, 0);
+                        unpack2<T>(in ? load_shared16(s0) : zero, xh[j] + k * V / 2);
+                        unpack2<T>(in ? load_shared16(s0 + NT * 16) : zero, g[j] + k * V / 2);
                     }
+                } else {
+                    const uint32_t m = r + j < p.rows ? n : 0;
+                    load_row<T, V, E>(x + (r + j) * p.ldx, t, width, m, xh[j]);
+                    load_row<T, V, E>(dy + (r + j) * p.lddy, t, width, m, g[j]);
                 }
-            if (!p.dx)
-                continue;
-            s = warp_sum(s);
-            q = warp_sum(q);
-            if (warps > 1) {
-                if (lane == 0)
-                    part[flip][warp] = make_float2(s, q);
-                group_barrier(group, width);
-                const float2 o = lane < warps ? part[flip][warp0 + lane] : make_float2(0.f, 0.f);
-                s = warp_sum(o.x);
-                q = warp_sum(o.y);
+                const float2 minus = both(-mean[j]), r2 = both(rstd[j]);
+                float2 s = both(0.f), q = both(0.f);
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    const float2 d = g[j][i];
+                    xh[j][i] = mul2(add2(xh[j][i], minus), r2);
+                    g[j][i] = mul2(d, w[i]);
+                    s = add2(s, g[j][i]);
+                    q = fma2(g[j][i], xh[j][i], q);
+                    aw[i] = fma2(d, xh[j][i], aw[i]);
+                    ab[i] = add2(ab[i], d);
+                }
+                v[2 * j] = s.x + s.y;
+                v[2 * j + 1] = q.x + q.y;
+                rs[j] = rstd[j];
+            }
+            stats(r + step); // a step ahead: they would be waited for
+            if (p.dx) {
+                group_sums<ROWS>(v, part[flip], group, width, warp0);
                 flip ^= 1;
-            }
-            s *= inv;
-            q *= inv;
 #pragma unroll
-            for (int k = 0; k < PER; ++k)
-                if (t + k * width < n) {
-                    float f[V];
+                for (int j = 0; j < ROWS; ++j)
+                    if (r + j < p.rows) {
+                        const float2 s = both(-v[2 * j] * inv), q = both(-v[2 * j + 1] * inv), r2 = both(rs[j]);
+                        T *o = dx + (r + j) * p.lddx;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float xh = (to_f32(xq[k].v[i]) - mean) * rstd;
-                        f[i] = rstd * (to_f32(dq[k].v[i]) * w[k][i] - s - xh * q);
+                        for (int i = 0; i < E / 2; ++i)
+                            g[j][i] = mul2(fma2(xh[j][i], q, add2(g[j][i], s)), r2);
+#pragma unroll
+                        for (int k = 0; k < PER; ++k)
+                            if (t + k * width < n) {
+                                if constexpr (V == 1)
+                                    o[t + k * width] = from_f32<T>(k & 1 ? g[j][k / 2].y : g[j][k / 2].x);
+                                else
+                                    store_values<T, V>(o + (uint64_t)(t + k * width) * V, g[j] + k * V / 2);
+                            }
                     }
-                    store_pack<T, V>(dx + r * p.lddx + (uint64_t)(t + k * width) * V, f);
-                }
+            }
+            at = at + 1 == RING ? 0 : at + 1;
         }
         if constexpr (RING > 0)
             copy_async_wait<0>();
@@ -431,23 +522,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) norm_grad_kernel(NormGradPara
         return;
     // the groups' sums, one group after the other
     float *sums = reinterpret_cast<float *>(raw); // [2][cols]
-    for (uint32_t g = 0; g < groups; ++g) {
+    for (uint32_t k = 0; k < groups; ++k) {
         __syncthreads();
-        if (works && group == g)
+        if (works && group == k) {
 #pragma unroll
-            for (int k = 0; k < PER; ++k)
-                if (t + k * width < n) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const uint32_t c = (t + k * width) * V + i;
-                        const float a = aw[k][i], b = ab[k][i];
-                        sums[c] = g ? sums[c] + a : a;
-                        sums[p.cols + c] = g ? sums[p.cols + c] + b : b;
-                    }
+            for (int i = 0; i < E; ++i)
+                if (t + (i / V) * width < n) {
+                    const uint32_t c = (t + (i / V) * width) * V + i % V;
+                    const float a = i & 1 ? aw[i / 2].y : aw[i / 2].x, b = i & 1 ? ab[i / 2].y : ab[i / 2].x;
+                    sums[c] = k ? sums[c] + a : a;
+                    sums[p.cols + c] = k ? sums[p.cols + c] + b : b;
                 }
+        }
     }
     __syncthreads();
-    for (uint32_t c = tid; c < p.cols; c += kGradThreads) {
+    for (uint32_t c = tid; c < p.cols; c += NT) {
         p.part[(uint64_t)blockIdx.x * p.cols + c] = sums[c];
         p.part[(uint64_t)(p.parts + blockIdx.x) * p.cols + c] = sums[p.cols + c];
     }
@@ -461,26 +550,24 @@ unsigned row_grid(uint64_t rows) { return (unsigned)std::min<uint64_t>(rows, 1u 
 
 template <typename T, typename TO, int V> bool norm_registers(const NormParams &p, int sms, cudaStream_t st)
 {
-    // few rows: spread a row over more warps (its latency counts); many: a
-    // warp a row while 16 accesses a thread hold it (no barriers)
+    // Values a thread.  Few rows: 8, a row over as many warps as it takes (its
+    // latency counts); many: 32 of aligned rows or 16, fewer warps to join.
     const uint64_t n = p.cols / V;
-    const uint64_t per = p.rows < 4ull * sms ? 1 : n <= 32 * 4 ? 4 : 16;
-    uint64_t warps = 1;
-    while (warps < 32 && warps * 32 * per < n)
-        warps *= 2;
-    const uint64_t need = (n + warps * 32 - 1) / (warps * 32);
-    if (need > 16)
+    constexpr uint64_t few = 8 / V, many = (V == 1 ? 16 : 32) / V;
+    const uint64_t per = p.rows < 4ull * sms && n <= 1024 * few ? few : many;
+    if (n > 1024 * many)
         return false;
+    uint64_t warps = 1;
+    while (warps * 32 * per < n)
+        warps *= 2;
     const uint64_t blocks = warps == 1 ? (p.rows + 3) / 4 : p.rows;
     if (blocks >= (1ull << 31))
         return false;
     const unsigned threads = warps == 1 ? 128 : (unsigned)warps * 32;
-    if (need == 1)
-        norm_kernel<T, TO, V, 1><<<(unsigned)blocks, threads, 0, st>>>(p, (uint32_t)warps);
-    else if (need <= 4)
-        norm_kernel<T, TO, V, 4><<<(unsigned)blocks, threads, 0, st>>>(p, (uint32_t)warps);
+    if (per == few)
+        norm_kernel<T, TO, V, few * V><<<(unsigned)blocks, threads, 0, st>>>(p, (uint32_t)warps);
     else
-        norm_kernel<T, TO, V, 16><<<(unsigned)blocks, threads, 0, st>>>(p, (uint32_t)warps);
+        norm_kernel<T, TO, V, many * V><<<(unsigned)blocks, threads, 0, st>>>(p, (uint32_t)warps);
     return true;
 }
 
@@ -504,14 +591,17 @@ template <typename T> ecc_status norm_launch(const NormParams &p, uint32_t y_typ
     return y_type == ECC_E4M3 ? norm_launch_to<T, e4m3>(p, st) : norm_launch_to<T, T>(p, st);
 }
 
-template <typename T, int V, int PER, int RING>
-bool norm_grad_registers(const NormGradParams &p, unsigned grid, uint32_t width, cudaStream_t st)
+template <typename T, int NT, int V, int E, int RING, int ROWS>
+bool norm_grad_registers(NormGradParams &p, cudaStream_t st)
 {
-    const size_t smem = std::max<size_t>((size_t)RING * 2 * PER * kGradThreads * 16, p.part ? p.cols * 8 : 0);
-    const void *f = (const void *)norm_grad_kernel<T, V, PER, RING>;
-    if (smem > kMaxDynSmem - 1024 || occupancy(f, kGradThreads, smem) <= 0)
+    const uint64_t n = p.cols / V, width = (n * V + E * 32 - 1) / (E * 32) * 32;
+    const size_t smem = std::max<size_t>((size_t)RING * ROWS * 2 * (E / V) * NT * 16, p.part ? p.cols * 8 : 0);
+    const void *f = (const void *)norm_grad_kernel<T, NT, V, E, RING, ROWS>;
+    if (width > NT || smem > kMaxDynSmem - 2048 || occupancy(f, NT, smem) <= 0)
         return false;
-    norm_grad_kernel<T, V, PER, RING><<<grid, kGradThreads, smem, st>>>(p, width);
+    const uint64_t steps = (p.rows + ROWS - 1) / ROWS, groups = NT / width;
+    p.parts = (uint32_t)std::min<uint64_t>((steps + groups - 1) / groups, p.parts);
+    norm_grad_kernel<T, NT, V, E, RING, ROWS><<<p.parts, NT, smem, st>>>(p, (uint32_t)width);
     return true;
 }
 
@@ -531,16 +621,14 @@ template <typename T> ecc_status norm_grad_launch(NormGradParams p, cudaStream_t
         const bool vec = p.cols % V == 0 && whole(p.x, p.ldx, sizeof(T)) && whole(p.dy, p.lddy, sizeof(T)) &&
                          (!p.dx || whole(p.dx, p.lddx, sizeof(T))) &&
                          (p.p_type != TypeCode<T>::value || whole(p.weight, 0, 1));
-        const uint64_t n = vec ? p.cols / V : p.cols;
-        const uint64_t per = vec ? (n > kGradThreads ? 2 : 1) : 8; // accesses a thread
-        const uint64_t width = (n + per * 32 - 1) / (per * 32) * 32;
-        if (width <= kGradThreads) {
-            const uint32_t w = (uint32_t)width, g = grad_groups(w);
-            p.parts = (uint32_t)std::min<uint64_t>((p.rows + g - 1) / g, p.parts);
-            done = !vec       ? norm_grad_registers<T, 1, 8, 0>(p, p.parts, w, st)
-                   : per == 1 ? norm_grad_registers<T, V, 1, 4>(p, p.parts, w, st)
-                              : norm_grad_registers<T, V, 2, 3>(p, p.parts, w, st);
-        }
+        // the fewest values a thread that let a block of 512 threads hold a
+        // row (its threads' sums take 128 registers), at last 1024 threads
+        if (vec)
+            done = norm_grad_registers<T, 512, V, 8, 4, 2>(p, st) || norm_grad_registers<T, 512, V, 16, 4, 1>(p, st) ||
+                   norm_grad_registers<T, 1024, V, 16, 3, 1>(p, st);
+        else
+            done = norm_grad_registers<T, 512, 1, 8, 0, 2>(p, st) || norm_grad_registers<T, 512, 1, 16, 0, 1>(p, st) ||
+                   norm_grad_registers<T, 1024, 1, 16, 0, 1>(p, st);
     }
     if (!done) { // longer rows
         if (sums) // before dx, which may overwrite dy or x
