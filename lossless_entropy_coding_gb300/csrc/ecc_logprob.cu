@@ -81,23 +81,21 @@ constexpr float kLseMost = 256.f;
 
 // ---------------------------------------------------------------- rows in vectors
 // A row of logits as `head` single values, `vecs` 16-byte aligned vectors and
-// `tail` single values.
+// `tail` single values (fewer than 2^31 values in all).
 template <typename T> struct RowView {
     static constexpr uint32_t V = 16 / sizeof(T); // values of a vector
     static constexpr uint32_t U = 32 / V;         // vectors of a group: a thread takes 32 values at a time
     const T *x;
-    uint32_t head, tail;
-    uint64_t vecs;
+    uint32_t head, tail, vecs;
     __device__ __forceinline__ RowView(const T *row, uint64_t n) : x(row)
     {
-        const uint64_t h = ((16 - ((uintptr_t)row & 15)) & 15) / sizeof(T);
-        head = (uint32_t)min(h, n);
-        vecs = (n - head) / V;
-        tail = (uint32_t)((n - head) % V);
+        head = min((16u - ((uint32_t)(uintptr_t)row & 15u) & 15u) / (uint32_t)sizeof(T), (uint32_t)n);
+        vecs = ((uint32_t)n - head) / V;
+        tail = ((uint32_t)n - head) % V;
     }
-    __device__ __forceinline__ const uint4 *vec(uint64_t i) const { return reinterpret_cast<const uint4 *>(x + head) + i; }
+    __device__ __forceinline__ const uint4 *vec(uint32_t i) const { return reinterpret_cast<const uint4 *>(x + head) + i; }
     // the k-th of the head and tail values (k < head + tail): its index
-    __device__ __forceinline__ uint64_t single(uint32_t k) const { return k < head ? k : vecs * V + k; }
+    __device__ __forceinline__ uint32_t single(uint32_t k) const { return k < head ? k : vecs * V + k; }
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) // NaN if either is
@@ -210,8 +208,7 @@ template <typename Tm> __device__ __forceinline__ void rank_keys(Tm &sh, uint32_
 // row's ends for the first share.
 template <typename T> struct Share {
     RowView<T> row;
-    uint64_t v0, v1, n;
-    uint32_t singles;
+    uint32_t v0, v1, n, singles;
 };
 
 // A group of a thread's values into the softmax; its largest.  Without the cut
@@ -263,8 +260,8 @@ template <int P> __device__ __forceinline__ float add_group(Softmax &sm, const f
 // ranked.  `single` is the value of the row's ends that this thread holds.
 template <typename T, typename Tm>
 __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::columns], const Share<T> &a, uint32_t top,
-                                           uint32_t slots, uint64_t groups, uint32_t per_slot, bool has_single,
-                                           float single, uint64_t single_at)
+                                           uint32_t slots, uint32_t groups, uint32_t per_slot, bool has_single,
+                                           float single, uint32_t single_at)
 {
     constexpr uint32_t V = RowView<T>::V, U = RowView<T>::U, N = Tm::threads, C = Tm::columns;
     const uint32_t tid = Tm::thread(), lane = tid & 31, warp = tid >> 5;
@@ -275,7 +272,7 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
         for (uint32_t t = 0; t < C; t += N)
             own = max_nan(own, gmax[k][t + tid]);
     // warps whose lanes all have a vector; with none, every value above -infinity is a candidate
-    const uint32_t full = (uint32_t)min((uint64_t)(N / 32), (a.v1 - a.v0) / 32);
+    const uint32_t full = min(N / 32, (a.v1 - a.v0) / 32);
     const uint32_t take = full ? (top + full - 1) / full : 0;
     uint32_t mine = order_bits(own), low = 0;
     for (uint32_t i = 0; i < take; ++i) {
@@ -301,41 +298,41 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
             if (order_bits(gmax[k][t + tid]) >= bound)
                 sh.pair[atomicAdd(&sh.n_pair, 1u)] = (uint16_t)(k << 8 | (t + tid));
     if (has_single && order_bits(single) >= bound)
-        sh.key[atomicAdd(&sh.n_key, 1u)] = order_key(single, (uint32_t)single_at); // at most 14
+        sh.key[atomicAdd(&sh.n_key, 1u)] = order_key(single, single_at); // at most 14
     Tm::sync();
     const uint32_t pairs = sh.n_pair;
-    auto keep = [&](float f, uint64_t at) {
+    auto keep = [&](float f, uint32_t at) {
         if (order_bits(f) >= bound) {
             const uint32_t n = atomicAdd(&sh.n_key, 1u);
             if (n < Tm::keys)
-                sh.key[n] = order_key(f, (uint32_t)at);
+                sh.key[n] = order_key(f, at);
         }
     };
-    auto place = [&](uint32_t pair, uint64_t e) { // value e of a pair's slot: its vector
-        return a.v0 + ((uint64_t)(pair >> 8) * per_slot * U + e / V) * C + (pair & 0xFFu);
+    auto place = [&](uint32_t pair, uint32_t e) { // value e of a pair's slot: its vector
+        return a.v0 + ((pair >> 8) * per_slot * U + e / V) * C + (pair & 0xFFu);
     };
     if (per_slot == 1) { // a lane a value; eight pairs' loads at a time
         for (uint32_t i0 = warp; i0 < pairs; i0 += 8 * (N / 32)) {
             T q[8];
-            uint64_t at[8];
+            uint32_t at[8];
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j) {
                 const uint32_t i = i0 + j * (N / 32);
-                const uint64_t v = i < pairs ? place(sh.pair[i], lane) : a.v1;
-                at[j] = v < a.v1 ? a.row.head + v * V + lane % V : ~0ull;
-                if (at[j] != ~0ull)
+                const uint32_t v = i < pairs ? place(sh.pair[i], lane) : a.v1;
+                at[j] = v < a.v1 ? a.row.head + v * V + lane % V : ~0u;
+                if (at[j] != ~0u)
                     q[j] = x[at[j]];
             }
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j)
-                if (at[j] != ~0ull)
+                if (at[j] != ~0u)
                     keep(to_f32(q[j]), at[j]);
         }
     } else {
         for (uint32_t i = warp; i < pairs; i += N / 32) {
-            const uint64_t g0 = (uint64_t)(sh.pair[i] >> 8) * per_slot, g1 = min(groups, g0 + per_slot);
-            for (uint64_t e = lane; e < (g1 - g0) * 32; e += 32) {
-                const uint64_t v = place(sh.pair[i], e), at = a.row.head + v * V + e % V;
+            const uint32_t g0 = (sh.pair[i] >> 8) * per_slot, g1 = min(groups, g0 + per_slot);
+            for (uint32_t e = lane; e < (g1 - g0) * 32; e += 32) {
+                const uint32_t v = place(sh.pair[i], e), at = a.row.head + v * V + e % V;
                 if (v < a.v1)
                     keep(to_f32(x[at]), at);
             }
@@ -343,14 +340,14 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
     }
     Tm::sync();
     const uint32_t n = sh.n_key;
-    const uint64_t first = a.singles ? 0 : a.row.head + a.v0 * V, last = a.row.head + a.v1 * V;
+    const uint32_t first = a.singles ? 0 : a.row.head + a.v0 * V, last = a.row.head + a.v1 * V;
     if (n <= Tm::keys) {
         rank_keys(sh, n, top);
         Tm::sync();
         if (n < top && warp == 0) { // fewer than asked for: tokens without probability, lowest index first
             uint32_t have = n;
-            for (uint64_t i0 = first; have < top; i0 += 32) {
-                uint64_t i = i0 + lane;
+            for (uint32_t i0 = first; have < top; i0 += 32) {
+                uint32_t i = i0 + lane;
                 bool in = i < last;
                 if (!in && a.singles) { // behind the vectors: the tail
                     i = a.row.head + a.row.vecs * V + (i - last);
@@ -359,7 +356,7 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
                 const bool hit = in && order_bits(to_f32(x[in ? i : 0])) < bound;
                 const uint32_t hits = __ballot_sync(~0u, hit), at = have + __popc(hits & ((1u << lane) - 1));
                 if (hit && at < top)
-                    sh.best[at] = order_key(-INFINITY, (uint32_t)i);
+                    sh.best[at] = order_key(-INFINITY, i);
                 have += __popc(hits);
                 if (!__any_sync(~0u, in))
                     break;
@@ -372,12 +369,12 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
                 sh.largest = 0;
             Tm::sync();
             unsigned long long big = 0;
-            auto look = [&](uint64_t i) {
-                const unsigned long long key = order_key(to_f32(x[i]), (uint32_t)i);
+            auto look = [&](uint32_t i) {
+                const unsigned long long key = order_key(to_f32(x[i]), i);
                 if (key < before && key > big)
                     big = key;
             };
-            for (uint64_t i = a.row.head + a.v0 * V + tid; i < last; i += N)
+            for (uint32_t i = a.row.head + a.v0 * V + tid; i < last; i += N)
                 look(i);
             for (uint32_t i = tid; i < a.singles; i += N)
                 look(a.row.single(i));
@@ -437,21 +434,21 @@ template <typename T> __global__ void __launch_bounds__(128, 6) logprob_warp_ker
         return;
     const T *x = static_cast<const T *>(p.logits) + r * p.ld;
     const RowView<T> row(x, p.vocab);
-    const Share<T> a{row, 0, row.vecs, p.vocab, row.head + row.tail};
+    const Share<T> a{row, 0, row.vecs, (uint32_t)p.vocab, row.head + row.tail};
     const float c = p.scale * 1.44269504f;
     const int64_t tok = p.tokens ? p.tokens[r] : -1;
     const float xtok = tok >= 0 && tok < (int64_t)p.vocab ? to_f32(x[tok]) : 0.f;
     const bool has_single = lane < a.singles;
-    const uint64_t single_at = has_single ? row.single(lane) : 0;
+    const uint32_t single_at = has_single ? row.single(lane) : 0;
     const float single = has_single ? to_f32(x[single_at]) : -INFINITY;
-    const uint64_t groups = (row.vecs + U * 32 - 1) / (U * 32);
-    const uint32_t per_slot = (uint32_t)((groups + kSlots - 1) / kSlots);
+    const uint32_t groups = (row.vecs + U * 32 - 1) / (U * 32);
+    const uint32_t per_slot = (groups + kSlots - 1) / kSlots;
     Softmax sm;
     uint32_t slot = 0;
-    for (uint64_t g = 0; g < groups;) {
+    for (uint32_t g = 0; g < groups;) {
         float slot_max = -INFINITY;
         for (uint32_t k = 0; k < per_slot && g < groups; ++k, ++g) {
-            const uint64_t i0 = g * U * 32 + lane;
+            const uint32_t i0 = g * U * 32 + lane;
             uint4 q[U];
 #pragma unroll
             for (uint32_t u = 0; u < U; ++u)
@@ -544,21 +541,23 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
     __syncthreads();
     auto share_of = [&](uint64_t r) {
         const RowView<T> row(static_cast<const T *>(p.logits) + r * p.ld, p.vocab);
-        return Share<T>{row, row.vecs * rank / split, row.vecs * (rank + 1) / split, p.vocab,
-                        rank == 0 ? row.head + row.tail : 0};
+        // (split is a power of two)
+        const uint32_t shift = 31 - __clz(split);
+        return Share<T>{row, (uint32_t)((uint64_t)row.vecs * rank >> shift), (uint32_t)((uint64_t)row.vecs * (rank + 1) >> shift),
+                        (uint32_t)p.vocab, rank == 0 ? row.head + row.tail : 0};
     };
     auto groups_of = [&](const Share<T> &a) { return (a.v1 - a.v0 + U * kLpThreads - 1) / (U * kLpThreads); };
-    auto per_slot_of = [&](uint64_t groups) { return (uint32_t)((groups + kSlots - 1) / kSlots); };
+    auto per_slot_of = [&](uint32_t groups) { return (groups + kSlots - 1) / kSlots; };
     if (threadIdx.x >= kLpThreads + kSelThreads) { // the copy warp
         if (threadIdx.x == kLpThreads + kSelThreads) {
             uint32_t st = 0, ph = 0, issued = 0;
             bool ok = true;
             for (uint64_t r = r0; r < p.rows && ok; r += step) {
                 const Share<T> a = share_of(r);
-                for (uint64_t v = a.v0; v < a.v1; v += kStageVecs) {
+                for (uint32_t v = a.v0; v < a.v1; v += kStageVecs) {
                     if (!(ok = mbar_wait(&ss.empty[st], ph ^ 1, kWaitLimitNs)))
                         break;
-                    const uint32_t bytes = (uint32_t)min((uint64_t)kStageVecs, a.v1 - v) * 16;
+                    const uint32_t bytes = min(kStageVecs, a.v1 - v) * 16;
                     mbar_expect_tx(&ss.full[st], bytes);
                     bulk_g2s(ring + st * kStageBytes, a.row.vec(v), bytes, &ss.full[st]);
                     ++issued;
@@ -587,52 +586,61 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
             if (r >= r0 + 2 * step)
                 buffer_sync(4 + b); // the row before last is written
             const Share<T> a = share_of(r);
-            const uint64_t nv = a.v1 - a.v0, groups = groups_of(a);
+            const uint32_t nv = a.v1 - a.v0, groups = groups_of(a), whole = nv / (U * kLpThreads);
             const uint32_t per_slot = per_slot_of(groups);
             Softmax sm;
             uint32_t slot = 0;
-            for (uint64_t g = 0; g < groups && ok;) {
-                float slot_max = -INFINITY;
-                for (uint32_t k = 0; k < per_slot && g < groups; ++k, ++g) {
-                    float2 f[16];
+            float slot_max = -INFINITY;
+            uint32_t left = per_slot; // groups left of the slot
+            for (uint32_t g = 0; g < groups; ++g) {
+                float2 f[16];
 #pragma unroll
-                    for (uint32_t h = 0; h < U / 4; ++h) { // a group's stages
-                        const uint64_t done = g * U * kLpThreads + h * kStageVecs;
-                        const uint32_t count = done < nv ? (uint32_t)min((uint64_t)kStageVecs, nv - done) : 0;
-                        if (count && !(ok = ok && mbar_wait(&ss.full[st], ph, kWaitLimitNs)))
-                            ss.row[0].failed = ss.row[1].failed = 1;
-                        const uint4 *q = reinterpret_cast<const uint4 *>(ring + st * kStageBytes);
-                        if (count == kStageVecs) {
+                for (uint32_t h = 0; h < U / 4; ++h) { // a group's stages
+                    uint32_t count = kStageVecs;
+                    if (g == whole) {
+                        const uint32_t done = g * U * kLpThreads + h * kStageVecs;
+                        count = done < nv ? min(kStageVecs, nv - done) : 0;
+                    }
+                    if (count && !(ok = ok && mbar_wait(&ss.full[st], ph, kWaitLimitNs)))
+                        break;
+                    const uint4 *q = reinterpret_cast<const uint4 *>(ring + st * kStageBytes) + tid;
+                    if (count == kStageVecs) {
 #pragma unroll
-                            for (uint32_t u = 0; u < 4; ++u)
-                                unpack2<T>(q[tid + u * kLpThreads], f + (h * 4 + u) * V / 2);
-                        } else {
+                        for (uint32_t u = 0; u < 4; ++u)
+                            unpack2<T>(q[u * kLpThreads], f + (h * 4 + u) * V / 2);
+                    } else {
 #pragma unroll
-                            for (uint32_t u = 0; u < 4; ++u)
-                                if (tid + u * kLpThreads < count) {
-                                    unpack2<T>(q[tid + u * kLpThreads], f + (h * 4 + u) * V / 2);
-                                } else {
+                        for (uint32_t u = 0; u < 4; ++u)
+                            if (tid + u * kLpThreads < count) {
+                                unpack2<T>(q[u * kLpThreads], f + (h * 4 + u) * V / 2);
+                            } else {
 #pragma unroll
-                                    for (uint32_t i = 0; i < V / 2; ++i)
-                                        f[(h * 4 + u) * V / 2 + i] = both(-INFINITY);
-                                }
-                        }
-                        if (count) {
-                            __syncwarp();
-                            if ((tid & 31) == 0) // the stage is in registers
-                                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&ss.empty[st])) : "memory");
-                            if (++st == kStages) {
-                                st = 0;
-                                ph ^= 1;
+                                for (uint32_t i = 0; i < V / 2; ++i)
+                                    f[(h * 4 + u) * V / 2 + i] = both(-INFINITY);
                             }
+                    }
+                    if (count) {
+                        __syncwarp();
+                        if ((tid & 31) == 0) // the stage is in registers
+                            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&ss.empty[st])) : "memory");
+                        if (++st == kStages) {
+                            st = 0;
+                            ph ^= 1;
                         }
                     }
-                    if (!ok)
-                        break;
-                    slot_max = max_nan(slot_max, add_group(sm, f, c));
                 }
-                if (ok && p.top)
-                    buf.gmax[slot++][tid] = slot_max;
+                if (!ok) {
+                    ss.row[0].failed = ss.row[1].failed = 1;
+                    break;
+                }
+                slot_max = max_nan(slot_max, add_group(sm, f, c));
+                if (--left == 0 || g + 1 == groups) {
+                    if (p.top)
+                        buf.gmax[slot][tid] = slot_max;
+                    ++slot;
+                    left = per_slot;
+                    slot_max = -INFINITY;
+                }
             }
             __syncwarp();
             join_lanes(sm, c);
@@ -653,9 +661,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
             const int64_t tok = p.tokens && tid == 0 && rank == 0 ? p.tokens[r] : -1;
             const float xtok = tok >= 0 && tok < (int64_t)p.vocab ? to_f32(a.row.x[tok]) : 0.f;
             const bool has_single = tid >= 8 && tid - 8 < a.singles;
-            const uint64_t single_at = has_single ? a.row.single(tid - 8) : 0;
+            const uint32_t single_at = has_single ? a.row.single(tid - 8) : 0;
             const float single = has_single ? to_f32(a.row.x[single_at]) : -INFINITY;
-            const uint64_t groups = groups_of(a);
+            const uint32_t groups = groups_of(a);
             const uint32_t per_slot = per_slot_of(groups);
             buffer_sync(2 + b);
             const bool failed = buf.failed;
@@ -680,7 +688,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
                 for (uint32_t i = tid; i < p.top; i += kSelThreads)
                     sh.best[i] = order_key(NAN, 0);
             } else if (p.top) {
-                const uint32_t slots = per_slot ? (uint32_t)((groups + per_slot - 1) / per_slot) : 0;
+                const uint32_t slots = per_slot ? (groups + per_slot - 1) / per_slot : 0;
                 select_top<T>(sh, buf.gmax, a, p.top, slots, groups, per_slot, has_single, single, single_at);
             }
             BlockTeam::sync();
@@ -835,11 +843,11 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads) logprob_grad
     }
     const RowView<T> view(x, p.vocab);
     if ((((uintptr_t)x ^ (uintptr_t)d) & 15) == 0) { // both rows' vectors start at the same value
-        const uint64_t v0 = view.vecs * part / split, v1 = view.vecs * (part + 1) / split;
+        const uint32_t v0 = (uint64_t)view.vecs * part / split, v1 = (uint64_t)view.vecs * (part + 1) / split;
         uint4 *out = reinterpret_cast<uint4 *>(d + view.head);
         // the token's vector, if it lies in one
         const uint64_t tv = row.tok >= (int64_t)view.head ? (uint64_t)(row.tok - view.head) / V : ~0ull;
-        for (uint64_t i0 = v0 + tid; i0 < v1; i0 += 4 * kLpThreads) {
+        for (uint32_t i0 = v0 + tid; i0 < v1; i0 += 4 * kLpThreads) {
             uint4 q[4];
 #pragma unroll
             for (uint32_t u = 0; u < 4; ++u)
@@ -847,7 +855,7 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads) logprob_grad
                     q[u] = load_once(view.vec(i0 + u * kLpThreads));
 #pragma unroll
             for (uint32_t u = 0; u < 4; ++u) {
-                const uint64_t i = i0 + u * kLpThreads;
+                const uint32_t i = i0 + u * kLpThreads;
                 if (i < v1) {
                     float2 f[V / 2], o[V / 2];
                     unpack2<T>(q[u], f);
@@ -870,7 +878,7 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads) logprob_grad
         }
         if (part == 0)
             for (uint32_t k = tid; k < view.head + view.tail; k += kLpThreads) {
-                const uint64_t i = view.single(k);
+                const uint32_t i = view.single(k);
                 const float f = to_f32(x[i]);
                 d[i] = from_f32<T>((uint64_t)row.tok == i ? row.token_value(f) : row.value(f));
             }
