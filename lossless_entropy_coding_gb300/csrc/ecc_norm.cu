@@ -199,6 +199,28 @@ __device__ __forceinline__ void load_params(const void *p, uint32_t at, uint32_t
             f[i] = make_float2(q[2 * i], q[2 * i + 1]);
     }
 }
+// a thread's single parameters (`none` where there is no such vector)
+template <typename T, int E>
+__device__ __forceinline__ void load_singles(const void *p, uint32_t type, uint32_t t, uint32_t width, uint32_t n,
+                                             float none, float (&f)[E])
+{
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+        f[k] = none;
+    if (!p)
+        return;
+    if (type == TypeCode<T>::value) {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            if (t + k * width < n)
+                f[k] = to_f32(static_cast<const T *>(p)[t + k * width]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            if (t + k * width < n)
+                f[k] = static_cast<const float *>(p)[t + k * width];
+    }
+}
 template <typename T, int V> __device__ __forceinline__ void store_values(T *p, const float2 *f)
 {
     if constexpr (sizeof(T) == 1) {
@@ -216,108 +238,6 @@ template <typename T, int V> __device__ __forceinline__ void store_values(T *p, 
     }
 }
 
-// A row by `warps` warps: it is read once and both passes over it (the mean,
-// the squared deviations) run on registers.  Blocks of one warp a row hold
-// four rows.  Bound by HBM: the row read, the output written.
-template <typename T, typename TO, int V, int E>
-__global__ void __launch_bounds__(1024) norm_kernel(NormParams p, uint32_t warps)
-{
-    __shared__ float part[2][32];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, width = warps * 32;
-    const uint64_t r = warps == 1 ? (uint64_t)blockIdx.x * (blockDim.x / 32) + warp : blockIdx.x;
-    if (r >= p.rows)
-        return; // (whole warps of a block of one warp a row)
-    const uint32_t t = warps == 1 ? lane : threadIdx.x, n = (uint32_t)(p.cols / V);
-    float2 f[E / 2];
-    load_row<T, V, E>(static_cast<const T *>(p.x) + r * p.ldx, t, width, n, f);
-    auto total = [&](float s, int which) {
-        s = warp_sum(s);
-        if (warps == 1)
-            return s;
-        if (lane == 0)
-            part[which][warp] = s;
-        __syncthreads();
-        s = lane < warps ? part[which][lane] : 0.f;
-        return warp_sum(s);
-    };
-    const float inv = 1.f / (float)p.cols;
-    float2 s = both(0.f);
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i)
-        s = add2(s, f[i]);
-    const float mean = total(s.x + s.y, 0) * inv;
-    s = both(0.f);
-    const float2 minus = both(-mean);
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-        f[i] = add2(f[i], minus);
-        if constexpr (V == 1) { // past the end: no deviation
-            if (t + 2 * i * width >= n)
-                f[i].x = 0.f;
-            if (t + (2 * i + 1) * width >= n)
-                f[i].y = 0.f;
-        } else if (t + (2 * i / V) * width >= n) {
-            f[i] = both(0.f);
-        }
-        s = fma2(f[i], f[i], s);
-    }
-    const float rstd = 1.f / sqrtf(total(s.x + s.y, 1) * inv + p.eps);
-    TO *y = static_cast<TO *>(p.y) + r * p.ldy;
-    const float2 r2 = both(rstd), scale = both(p.y_scale);
-    if constexpr (V == 1) {
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-            const uint32_t c = t + k * width;
-            if (c < n) {
-                float v = (k & 1 ? f[k / 2].y : f[k / 2].x) * rstd;
-                if (p.weight)
-                    v *= load_any(p.weight, c, p.p_type);
-                if (p.bias)
-                    v += load_any(p.bias, c, p.p_type);
-                y[c] = from_f32<TO>(v * p.y_scale);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < E / V; ++k)
-            if (t + k * width < n) {
-                float2 *v = f + k * V / 2, q[V / 2];
-#pragma unroll
-                for (int i = 0; i < V / 2; ++i)
-                    v[i] = mul2(v[i], r2);
-                if (p.weight) {
-                    load_params<T, V>(p.weight, t + k * width, p.p_type, q);
-#pragma unroll
-                    for (int i = 0; i < V / 2; ++i)
-                        v[i] = mul2(v[i], q[i]);
-                }
-                if (p.bias) {
-                    load_params<T, V>(p.bias, t + k * width, p.p_type, q);
-#pragma unroll
-                    for (int i = 0; i < V / 2; ++i)
-                        v[i] = add2(v[i], q[i]);
-                }
-                if constexpr (sizeof(TO) == 1) {
-#pragma unroll
-                    for (int i = 0; i < V / 2; ++i)
-                        v[i] = mul2(v[i], scale);
-                }
-                store_values<TO, V>(y + (uint64_t)(t + k * width) * V, v);
-            }
-    }
-    if (t == 0) {
-        if (p.mean)
-            p.mean[r] = mean;
-        if (p.rstd)
-            p.rstd[r] = rstd;
-    }
-}
-
-// ---------------------------------------------------------------- backward, rows in registers
-__device__ __forceinline__ void group_barrier(uint32_t id, uint32_t threads) // id below 15
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
-}
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -331,6 +251,153 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t at)
     return q;
 }
 
+// ROWS rows by `warps` warps: they are read once and both passes over them
+// (the mean, the squared deviations) run on registers.  Blocks of one warp a
+// row hold four warps.  Two rows at a time share the parameters (read for each
+// row they cost twice the row's own L1 traffic), the barriers and the
+// shuffles' latency.  Bound by HBM: the rows read, the output written.
+template <typename T, typename TO, int V, int E, int ROWS>
+__global__ void __launch_bounds__(ROWS > 1 ? 128 : 1024, ROWS > 1 ? 5 : 1) norm_kernel(NormParams p, uint32_t warps)
+{
+    __shared__ float part[2][ROWS][32];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, width = warps * 32;
+    const uint64_t r = (warps == 1 ? (uint64_t)blockIdx.x * (blockDim.x / 32) + warp : blockIdx.x) * ROWS;
+    if (r >= p.rows)
+        return; // (whole warps of a block of one warp a row)
+    const uint32_t t = warps == 1 ? lane : threadIdx.x, n = (uint32_t)(p.cols / V);
+    float2 f[ROWS][E / 2];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j)
+        load_row<T, V, E>(static_cast<const T *>(p.x) + (r + j) * p.ldx, t, width, r + j < p.rows ? n : 0, f[j]);
+    auto total = [&](float (&s)[ROWS], int which) {
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j)
+            s[j] = warp_sum(s[j]);
+        if (warps == 1)
+            return;
+        if (lane == 0) {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+                part[which][j][warp] = s[j];
+        }
+        __syncthreads();
+        if (warps <= 4) {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+                s[j] = part[which][j][0];
+                for (uint32_t i = 1; i < warps; ++i)
+                    s[j] += part[which][j][i];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+                s[j] = warp_sum(lane < warps ? part[which][j][lane] : 0.f);
+        }
+    };
+    const float inv = 1.f / (float)p.cols;
+    float mean[ROWS], rstd[ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+        float2 s = both(0.f);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            s = add2(s, f[j][i]);
+        mean[j] = s.x + s.y;
+    }
+    total(mean, 0);
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+        mean[j] *= inv;
+        const float2 minus = both(-mean[j]);
+        float2 s = both(0.f);
+        if (n == width * (E / V)) {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                f[j][i] = add2(f[j][i], minus);
+                s = fma2(f[j][i], f[j][i], s);
+            }
+        } else { // past the end: no deviation
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                f[j][i] = add2(f[j][i], minus);
+                f[j][i].x = t + (2 * i / V) * width < n ? f[j][i].x : 0.f;
+                f[j][i].y = t + ((2 * i + 1) / V) * width < n ? f[j][i].y : 0.f;
+                s = fma2(f[j][i], f[j][i], s);
+            }
+        }
+        rstd[j] = s.x + s.y;
+    }
+    total(rstd, 1);
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j)
+        rstd[j] = 1.f / sqrtf(rstd[j] * inv + p.eps);
+    TO *y = static_cast<TO *>(p.y) + r * p.ldy;
+    if constexpr (V == 1) {
+#pragma unroll
+        for (int k0 = 0; k0 < E; k0 += 4) {
+            const uint32_t t0 = t + k0 * width;
+            float w[4], b[4];
+            load_singles<T, 4>(p.weight, p.p_type, t0, width, n, 1.f, w);
+            load_singles<T, 4>(p.bias, p.p_type, t0, width, n, 0.f, b);
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (t0 + k * width < n && r + j < p.rows) {
+                        const float2 q = f[j][(k0 + k) / 2];
+                        float v = fmaf((k & 1 ? q.y : q.x) * rstd[j], w[k], b[k]);
+                        if constexpr (sizeof(TO) == 1)
+                            v *= p.y_scale;
+                        y[j * p.ldy + t0 + k * width] = from_f32<TO>(v);
+                    }
+        }
+    } else {
+        const float2 scale = both(p.y_scale);
+#pragma unroll
+        for (int k = 0; k < E / V; ++k)
+            if (t + k * width < n) {
+                float2 w[V / 2], b[V / 2];
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    w[i] = both(1.f);
+                    b[i] = both(0.f);
+                }
+                if (p.weight)
+                    load_params<T, V>(p.weight, t + k * width, p.p_type, w);
+                if (p.bias)
+                    load_params<T, V>(p.bias, t + k * width, p.p_type, b);
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j) {
+                    float2 *v = f[j] + k * V / 2;
+                    const float2 r2 = both(rstd[j]);
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        v[i] = fma2(mul2(v[i], r2), w[i], b[i]);
+                        if constexpr (sizeof(TO) == 1)
+                            v[i] = mul2(v[i], scale);
+                    }
+                    if (r + j < p.rows)
+                        store_values<TO, V>(y + j * p.ldy + (uint64_t)(t + k * width) * V, v);
+                }
+            }
+    }
+    if (t == 0) {
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j)
+            if (r + j < p.rows) {
+                if (p.mean)
+                    p.mean[r + j] = mean[j];
+                if (p.rstd)
+                    p.rstd[r + j] = rstd[j];
+            }
+    }
+}
+
+// ---------------------------------------------------------------- backward, rows in registers
+__device__ __forceinline__ void group_barrier(uint32_t id, uint32_t threads) // id below 15
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+}
 // The sums over a group's threads of 2 ROWS values each, known to all of them
 // on return: within a warp the values are halved over the lanes (each lane
 // ends with one value), the warps' sums go through shared memory.
@@ -402,10 +469,11 @@ __global__ void __launch_bounds__(NT, 1) norm_grad_kernel(NormGradParams p, uint
     if (works) {
         if (p.weight) {
             if constexpr (V == 1) {
+                float q[E];
+                load_singles<T, E>(p.weight, p.p_type, t, width, n, 1.f, q);
 #pragma unroll
-                for (int k = 0; k < E; ++k)
-                    if (t + k * width < n)
-                        (k & 1 ? w[k / 2].y : w[k / 2].x) = load_any(p.weight, t + k * width, p.p_type);
+                for (int k = 0; k < E / 2; ++k)
+                    w[k] = make_float2(q[2 * k], q[2 * k + 1]);
             } else {
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
@@ -520,25 +588,25 @@ __global__ void __launch_bounds__(NT, 1) norm_grad_kernel(NormGradParams p, uint
     }
     if (!p.part)
         return;
-    // the groups' sums, one group after the other
-    float *sums = reinterpret_cast<float *>(raw); // [2][cols]
-    for (uint32_t k = 0; k < groups; ++k) {
-        __syncthreads();
-        if (works && group == k) {
+    // the groups' sums, then their sum in the groups' order
+    float *sums = reinterpret_cast<float *>(raw); // [groups][2][cols]
+    __syncthreads();
+    if (works) {
+        float *mine = sums + (uint64_t)group * 2 * p.cols;
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (t + (i / V) * width < n) {
-                    const uint32_t c = (t + (i / V) * width) * V + i % V;
-                    const float a = i & 1 ? aw[i / 2].y : aw[i / 2].x, b = i & 1 ? ab[i / 2].y : ab[i / 2].x;
-                    sums[c] = k ? sums[c] + a : a;
-                    sums[p.cols + c] = k ? sums[p.cols + c] + b : b;
-                }
-        }
+        for (int i = 0; i < E; ++i)
+            if (t + (i / V) * width < n) {
+                const uint32_t c = (t + (i / V) * width) * V + i % V;
+                mine[c] = i & 1 ? aw[i / 2].y : aw[i / 2].x;
+                mine[p.cols + c] = i & 1 ? ab[i / 2].y : ab[i / 2].x;
+            }
     }
     __syncthreads();
-    for (uint32_t c = tid; c < p.cols; c += NT) {
-        p.part[(uint64_t)blockIdx.x * p.cols + c] = sums[c];
-        p.part[(uint64_t)(p.parts + blockIdx.x) * p.cols + c] = sums[p.cols + c];
+    for (uint32_t c = tid; c < 2 * p.cols; c += NT) {
+        float s = 0.f;
+        for (uint32_t k = 0; k < groups; ++k)
+            s += sums[k * 2 * p.cols + c];
+        p.part[c < p.cols ? (uint64_t)blockIdx.x * p.cols + c : (uint64_t)(p.parts + blockIdx.x) * p.cols + (c - p.cols)] = s;
     }
 }
 
@@ -550,24 +618,26 @@ unsigned row_grid(uint64_t rows) { return (unsigned)std::min<uint64_t>(rows, 1u 
 
 template <typename T, typename TO, int V> bool norm_registers(const NormParams &p, int sms, cudaStream_t st)
 {
-    // Values a thread.  Few rows: 8, a row over as many warps as it takes (its
-    // latency counts); many: 32 of aligned rows or 16, fewer warps to join.
+    // Accesses a thread.  Few rows: 8 values, a row over as many warps as it
+    // takes (its latency counts); many: four accesses of aligned rows or 16
+    // values, fewer warps to join.
     const uint64_t n = p.cols / V;
-    constexpr uint64_t few = 8 / V, many = (V == 1 ? 16 : 32) / V;
-    const uint64_t per = p.rows < 4ull * sms && n <= 1024 * few ? few : many;
+    constexpr uint64_t few = 8 / V, many = V == 1 ? 16 : 4;
+    const bool plenty = p.rows >= 16ull * sms;
+    const uint64_t per = (p.rows < 4ull * sms && n <= 1024 * few) || (plenty && n <= 32 * few) ? few : many;
     if (n > 1024 * many)
         return false;
-    uint64_t warps = 1;
-    while (warps * 32 * per < n)
-        warps *= 2;
-    const uint64_t blocks = warps == 1 ? (p.rows + 3) / 4 : p.rows;
+    const uint64_t warps = (n + 32 * per - 1) / (32 * per);
+    // several rows a team where blocks of four warps hold them and there are plenty
+    const uint64_t rows = !plenty || warps > 4 ? 1 : per == few ? 4 : 2;
+    const uint64_t teams = (p.rows + rows - 1) / rows, blocks = warps == 1 ? (teams + 3) / 4 : teams;
     if (blocks >= (1ull << 31))
         return false;
     const unsigned threads = warps == 1 ? 128 : (unsigned)warps * 32;
-    if (per == few)
-        norm_kernel<T, TO, V, few * V><<<(unsigned)blocks, threads, 0, st>>>(p, (uint32_t)warps);
-    else
-        norm_kernel<T, TO, V, many * V><<<(unsigned)blocks, threads, 0, st>>>(p, (uint32_t)warps);
+    const auto f = per == few  ? (rows == 1 ? norm_kernel<T, TO, V, few * V, 1> : norm_kernel<T, TO, V, few * V, 4>)
+                   : rows == 1 ? norm_kernel<T, TO, V, many * V, 1>
+                               : norm_kernel<T, TO, V, many * V, 2>;
+    f<<<(unsigned)blocks, threads, 0, st>>>(p, (uint32_t)warps);
     return true;
 }
 
@@ -595,9 +665,11 @@ template <typename T, int NT, int V, int E, int RING, int ROWS>
 bool norm_grad_registers(NormGradParams &p, cudaStream_t st)
 {
     const uint64_t n = p.cols / V, width = (n * V + E * 32 - 1) / (E * 32) * 32;
-    const size_t smem = std::max<size_t>((size_t)RING * ROWS * 2 * (E / V) * NT * 16, p.part ? p.cols * 8 : 0);
+    if (width > NT)
+        return false;
+    const size_t smem = std::max<size_t>((size_t)RING * ROWS * 2 * (E / V) * NT * 16, p.part ? NT / width * p.cols * 8 : 0);
     const void *f = (const void *)norm_grad_kernel<T, NT, V, E, RING, ROWS>;
-    if (width > NT || smem > kMaxDynSmem - 2048 || occupancy(f, NT, smem) <= 0)
+    if (smem > kMaxDynSmem - 2048 || occupancy(f, NT, smem) <= 0)
         return false;
     const uint64_t steps = (p.rows + ROWS - 1) / ROWS, groups = NT / width;
     p.parts = (uint32_t)std::min<uint64_t>((steps + groups - 1) / groups, p.parts);
@@ -623,9 +695,10 @@ template <typename T> ecc_status norm_grad_launch(NormGradParams p, cudaStream_t
                          (p.p_type != TypeCode<T>::value || whole(p.weight, 0, 1));
         // the fewest values a thread that let a block of 512 threads hold a
         // row (its threads' sums take 128 registers), at last 1024 threads
+        constexpr int ring = sizeof(T) == 4 ? 3 : 4;
         if (vec)
-            done = norm_grad_registers<T, 512, V, 8, 4, 2>(p, st) || norm_grad_registers<T, 512, V, 16, 4, 1>(p, st) ||
-                   norm_grad_registers<T, 1024, V, 16, 3, 1>(p, st);
+            done = norm_grad_registers<T, 512, V, 8, ring, 2>(p, st) || norm_grad_registers<T, 512, V, 16, ring, 1>(p, st) ||
+                   (sizeof(T) == 2 && norm_grad_registers<T, 1024, V, 16, 3, 1>(p, st));
         else
             done = norm_grad_registers<T, 512, 1, 8, 0, 2>(p, st) || norm_grad_registers<T, 512, 1, 16, 0, 1>(p, st) ||
                    norm_grad_registers<T, 1024, 1, 16, 0, 1>(p, st);
