@@ -9,15 +9,17 @@
 // thread needs one bias value a tile.  The other side, Q, gives the tile's
 // width: 16 for a few tokens up to 256 for a training batch.
 //
-// gemm_pair_kernel: for many tiles.  Persistent pairs of CTAs (tcgen05
-// cta_group::2, 256 x `bn` a pair); per CTA a TMA warp, a product warp (of
-// the pair's first CTA) and four epilogue warps, which work on one
-// accumulator while the products fill the other.
-// gemm_split_kernel: for few tiles.  One 128 x `bn` tile a cluster of up to 8
-// CTAs that share its reduction; the parts are joined through distributed
-// shared memory in the order of the CTAs' ranks.  Two CTAs an SM.
+// gemm_pair_kernel: pairs of CTAs (tcgen05 cta_group::2) on 256 x `bn` tiles;
+// per CTA a TMA warp, a product warp (of the pair's first CTA) and four
+// epilogue warps.  The pairs are persistent, and the epilogue works on one
+// accumulator while the products fill the other.  For many tiles.
+// gemm_split_kernel: one 128 x `bn` tile a cluster of up to 8 CTAs that share
+// its reduction, for few tiles: the parts are joined through distributed
+// shared memory, in the order of the CTAs' ranks.  Two CTAs an SM, or one
+// with twice the stages where there are no more CTAs than SMs.
 
 #include <algorithm>
+#include <cmath>
 
 #include "ecc_gemm.h"
 #include "ecc_tensor.cuh"
@@ -28,7 +30,7 @@ constexpr int kGemmThreads = 192; // TMA warp, product warp, 4 epilogue warps
 constexpr uint32_t kPTile = 128;  // P rows of a CTA
 constexpr uint32_t kMaxStages = 12;
 constexpr uint32_t kPBytes = kPTile * kTileBytes;
-constexpr uint32_t kPairSmem = 226 * 1024, kSplitSmem = 112 * 1024;
+constexpr uint32_t kAloneSmem = 226 * 1024, kSharedSmem = 112 * 1024; // of a CTA that has an SM to itself, or half of it
 constexpr uint32_t kSmemHead = 1024; // room to align the stages to 1024 bytes
 
 struct GemmArgs {
@@ -140,6 +142,36 @@ __device__ __forceinline__ void finish(const Epilogue &e, float (&a)[W], uint64_
         store_rows<e4m3>(e.out, e.ldout, at, n, a, e.out_scale);
 }
 
+// This CTA's part of a tile, [column of tensor memory][lane], for the join.
+template <int W> __device__ __forceinline__ void keep_part(float *parts, const float (&a)[W], uint32_t j, uint32_t row)
+{
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        parts[(j + i) * kPTile + row] = a[i];
+}
+// Share `share` of a tile's rows [r0, ...): the sum of the g.split CTAs'
+// parts, eight rows at a time so that their loads are in flight together,
+// then the epilogue.  `at`: this lane's first value in its CTA's part.
+__device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint32_t share, uint64_t r0, uint64_t c)
+{
+    const uint32_t n = (uint32_t)min((uint64_t)g.bn, g.rows - r0), per = (n + g.split - 1) / g.split;
+    const uint32_t j0 = share * per, j1 = min(n, j0 + per);
+    if (c >= g.cols)
+        return;
+    const float bias = g.e.bias ? load_any(g.e.bias, c, g.e.bias_type) : 0.f;
+    for (uint32_t j = j0; j < j1; j += 8) {
+        float a[8] = {};
+        for (uint32_t k = 0; k < g.split; ++k) {
+            const uint32_t from = cluster_addr(at + j * kPTile * 4, k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (j + i < j1)
+                    a[i] += cluster_load(from + i * kPTile * 4);
+        }
+        finish(g.e, a, r0 + j, min(8u, j1 - j), c, bias);
+    }
+}
+
 // ---------------------------------------------------------------- loads and products of a reduction block
 // rows [r0, r0 + n) of reduction block kb -> dst
 template <int CG, bool MN, bool F8>
@@ -177,13 +209,14 @@ __device__ __forceinline__ TilePos tile_pos(uint32_t t, uint32_t ptiles, uint32_
 }
 
 template <bool PMN, bool QMN, bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ GemmArgs g)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ GemmBars s;
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank();
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
     const uint32_t stage0 = (smem_u32(smem_raw) + kSmemHead - 1) & ~(kSmemHead - 1);
     const uint32_t qn = g.bn / 2, stage_bytes = kPBytes + qn * kTileBytes;
     const uint32_t tiles = g.ptiles * g.qtiles, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
@@ -199,9 +232,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             mbar_init(&s.tempty[i], 8); // four epilogue warps of each CTA
         }
         fence_mbar_init();
+    }
+    if (threadIdx.x == 32) {
         prefetch_map(&pmap);
         prefetch_map(&qmap);
     }
+    __syncwarp();
     if (warp == 1) {
         tmem_alloc<2>(smem_u32(&s.tmem), 512);
         tmem_fence_before();
@@ -340,9 +376,7 @@ __device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, 
             if (col_ok)
                 finish(g.e, a, r0 + j, (uint32_t)min((uint64_t)W, left - j), c, bias);
         } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                part[(j + i) * kPTile + quad * 32 + lane] = a[i];
+            keep_part(part, a, j, quad * 32 + lane);
         }
     }
 }
@@ -374,6 +408,11 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
         fence_mbar_init();
         fence_proxy_async();
     }
+    if (threadIdx.x == 32 && g.kblocks) {
+        prefetch_map(&pmap);
+        prefetch_map(&qmap);
+    }
+    __syncwarp();
     if (warp == 1) {
         tmem_alloc<1>(smem_u32(&s.tmem), tcols);
         tmem_fence_before();
@@ -457,17 +496,8 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
     __syncwarp();
     if (g.split > 1) {
         cluster_sync(); // all parts are written
-        if (warp >= 2) {
-            const uint32_t n = (uint32_t)min((uint64_t)g.bn, g.rows - q0);
-            const uint32_t base = stage0 + (quad * 32 + lane) * 4;
-            for (uint32_t j = rank; j < n; j += g.split) {
-                float a[1] = {0.f};
-                for (uint32_t k = 0; k < g.split; ++k)
-                    a[0] += cluster_load(cluster_addr(base + j * kPTile * 4, k));
-                if (col_ok)
-                    finish(g.e, a, q0 + j, 1, c, bias);
-            }
-        }
+        if (warp >= 2)
+            join_parts(g, stage0 + (quad * 32 + lane) * 4, rank, q0, c);
         __syncwarp();
         cluster_sync(); // nobody reads this CTA's part any more
     } else {
@@ -516,6 +546,63 @@ bool make_map(CUtensorMap *map, const Operand &o, uint64_t rows, uint64_t K, uin
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+uint64_t up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+struct Shape {
+    bool pair;
+    uint32_t bn, split;
+};
+
+// The launch shape with the least estimated time, in SM cycles.  What the
+// estimate is made of was fitted to 48 products of 1 to 8192 rows, 100 to
+// 16384 columns and reductions of 256 to 16384, bf16 and e4m3, each in every
+// shape; the chosen shape was within 8% of the best of its product for 46.
+// - a reduction block costs its products (128 bn 64 multiply-adds at 4096 a
+//   cycle, 8-bit operands twice that) or its loads, whichever is more: 49
+//   bytes a cycle for pairs, for single CTAs 70 on a full GPU, 62 below, 48
+//   where the operands are streamed once (few rows);
+// - a wave is one CTA an SM (two of the single ones share an SM's time), and
+//   the operands cannot arrive faster than HBM gives them;
+// - an epilogue, and joining a shared reduction.
+// So 1 x 16384 x 4096 takes 26.7 us in 16-row tiles (28 in 64-row ones), 128
+// x 4096 x 4096 15.5 us as 64-row tiles of four CTAs each (25 as pairs, 18 as
+// 64-row tiles of two), 1024 x 4096 x 4096 28.5 us as pairs (32 as 128-row
+// tiles).
+Shape choose_shape(uint64_t rows, uint64_t cols, uint64_t K, uint32_t kblocks, bool q_mn, bool f8, int sms)
+{
+    Shape best{false, rows <= 16 && !q_mn ? 16u : 64u, 1};
+    if (!kblocks)
+        return best;
+    const double hbm = (double)(rows + cols) * K * (f8 ? 1 : 2) / 3500;
+    double least = 1e30;
+    auto consider = [&](bool pair, uint32_t bn, uint32_t split, double t) {
+        if (t < least) {
+            least = t;
+            best = {pair, bn, split};
+        }
+    };
+    for (uint32_t bn : {256u, 128u}) {
+        const double waves = std::ceil(2.0 * up(cols, 256) * up(rows, bn) / sms), bytes = kPBytes + bn / 2 * kTileBytes;
+        const double work = waves * kblocks * std::max(bytes / 49, bn * 2.0);
+        consider(true, bn, 1, std::max(work, hbm) + 5500 + 12 * bn + 0.01 * work);
+    }
+    for (uint32_t bn : {128u, 64u, 32u, 16u}) {
+        if ((bn < 128 && rows > 4 * bn) || (bn > 16 && 2 * rows <= bn) || (q_mn && bn < 64))
+            continue;
+        for (uint32_t split = 1; split <= 8; split *= 2) {
+            const double ctas = (double)up(cols, 128) * up(rows, bn) * split, bytes = kPBytes + bn * kTileBytes;
+            if (split > 1 && (ctas > 2.0 * sms || kblocks < 2 * split))
+                break;
+            const double waves = ctas <= 2.0 * sms ? std::max(1.0, ctas / sms) : std::ceil(ctas / sms);
+            const double rate = ctas > sms ? 70 : rows <= 128 ? 48 : 62;
+            const double work = (double)up(kblocks, split) * waves * std::max(bytes / rate, bn * 2.0);
+            const double join = split > 1 ? 2500 + 25.0 * bn * waves : 0;
+            consider(false, bn, split, std::max(work, hbm) + 3000 + 12 * bn * waves + join + 0.01 * work);
+        }
+    }
+    return best;
+}
+
 template <bool PMN, bool QMN, bool F8>
 ecc_status gemm_launch(const Operand &P, const Operand &Q, uint64_t K, uint32_t type, GemmArgs g, bool pair, int sms,
                        cudaStream_t st)
@@ -526,7 +613,9 @@ ecc_status gemm_launch(const Operand &P, const Operand &Q, uint64_t K, uint32_t 
               !make_map(&qm, Q, g.rows, K, type, QMN ? 64 : qn)))
         return ECC_ERR_CUDA;
     const uint32_t stage_bytes = kPBytes + qn * kTileBytes;
-    const uint32_t budget = (pair ? kPairSmem : kSplitSmem) - kSmemHead - (uint32_t)sizeof(GemmBars);
+    const uint32_t tiles = g.ptiles * g.qtiles;
+    const bool alone = pair || tiles * g.split <= (uint32_t)sms; // one CTA an SM
+    const uint32_t budget = (alone ? kAloneSmem : kSharedSmem) - kSmemHead - (uint32_t)sizeof(GemmBars);
     g.stages = std::min(kMaxStages, budget / stage_bytes);
     const size_t smem = kSmemHead + (size_t)g.stages * stage_bytes;
     const void *f = pair ? (const void *)gemm_pair_kernel<PMN, QMN, F8> : (const void *)gemm_split_kernel<PMN, QMN, F8>;
@@ -536,17 +625,13 @@ ecc_status gemm_launch(const Operand &P, const Operand &Q, uint64_t K, uint32_t 
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
+    cfg.gridDim = dim3(pair ? 2 * std::min<uint32_t>(tiles, sms / 2) : tiles * g.split);
     cudaLaunchAttribute at[1];
-    if (pair) {
-        cfg.gridDim = dim3(2 * (unsigned)std::min<uint64_t>((uint64_t)g.ptiles * g.qtiles, sms / 2));
-    } else {
-        cfg.gridDim = dim3(g.ptiles * g.qtiles * g.split);
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = g.split;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-    }
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = pair ? 2 : g.split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     void *args[] = {&pm, &qm, &g};
     return launch_status(cudaLaunchKernelExC(&cfg, f, args));
 }
@@ -575,30 +660,15 @@ ecc_status gemm(const Operand &P, const Operand &Q, uint64_t rows, uint64_t cols
     g.status = status;
     g.clear_status = clear_status;
     g.limit_ns = kWaitLimitNs + 1000ull * g.kblocks; // an epilogue waits for a whole reduction
-    const uint64_t ptiles = (cols + kPTile - 1) / kPTile;
-    auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
-    // pairs of CTAs where their 256 x 256 tiles fill the GPU, else one tile a cluster
-    const bool pair = g.kblocks && up(cols, 256) * up(rows, 256) * 2 >= (uint64_t)sms;
-    uint64_t tiles;
-    if (pair) {
-        g.bn = 256;
-        g.ptiles = (uint32_t)up(cols, 256);
-        tiles = g.ptiles * up(rows, 256);
-        g.qtiles = (uint32_t)up(rows, 256);
-        g.split = 1;
-    } else {
-        g.bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-        if (Q.mn && g.bn < 64)
-            g.bn = 64;
-        g.ptiles = (uint32_t)ptiles;
-        g.qtiles = (uint32_t)up(rows, g.bn);
-        tiles = ptiles * up(rows, g.bn);
-        g.split = 1;
-        while (g.split < 8 && tiles * g.split * 2 <= 2ull * sms && g.kblocks >= 8 * g.split)
-            g.split *= 2;
-    }
-    if (tiles >= (1u << 30))
+    const Shape shape = choose_shape(rows, cols, K, g.kblocks, Q.mn, f8, sms);
+    const uint64_t ptiles = up(cols, shape.pair ? 2 * kPTile : kPTile), qtiles = up(rows, shape.bn);
+    if (ptiles * qtiles >= (1u << 27))
         return ECC_ERR_ARG;
+    g.bn = shape.bn;
+    g.split = shape.split;
+    g.ptiles = (uint32_t)ptiles;
+    g.qtiles = (uint32_t)qtiles;
+    const bool pair = shape.pair;
     g.idesc = product_desc(type, P.mn, Q.mn, pair ? 256 : 128, g.bn);
     if (f8)
         return gemm_launch<false, false, true>(P, Q, K, type, g, pair, sms, st);
