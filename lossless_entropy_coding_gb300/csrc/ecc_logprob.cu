@@ -152,7 +152,8 @@ struct Softmax {
 };
 
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr uint32_t kSlots = 16;    // group maxima kept for each column
+constexpr uint32_t kSlots = 16;    // slot maxima kept for each column of a block, and of a warp
+constexpr uint32_t kWarpSlots = 8;
 constexpr int kSelThreads = 128;   // selecting threads of a block
 constexpr uint32_t kStages = 4;    // stages of a block's ring
 constexpr uint32_t kStageVecs = 4 * kLpThreads;
@@ -166,10 +167,11 @@ template <int N, int C> struct Team {
     unsigned long long key[keys];
     unsigned long long best[ECC_MAX_TOP]; // the alternatives, in order
     unsigned long long largest;
-    uint16_t pair[C * kSlots]; // slot << 8 | column
+    uint16_t pair[C * (N == 32 ? kWarpSlots : kSlots)]; // slot << 8 | column
     uint32_t low[N / 32];
     float sum[3];
-    uint32_t n_key, n_pair;
+    uint16_t kept[N == 32 ? 1 : keys];
+    uint32_t n_key, n_pair, n_kept;
 
     static __device__ __forceinline__ void sync()
     {
@@ -211,16 +213,19 @@ template <typename T> struct Share {
     uint32_t v0, v1, n, singles;
 };
 
-// A group of a thread's values into the softmax; its largest.  Without the cut
+// A group of a thread's values, `big` the largest, into the softmax.  Without the cut
 // of Softmax::add, two values at a time; where that meets 0 * infinity (a
 // masked value), again with the cut.
-template <int P> __device__ __forceinline__ float add_group(Softmax &sm, const float2 (&f)[P], float c)
+template <int P> __device__ __forceinline__ float largest_of(const float2 *f)
 {
     float big = max_nan(f[0].x, f[0].y), more = -INFINITY;
 #pragma unroll
     for (int i = 1; i < P; ++i)
         (i & 1 ? more : big) = max_nan(i & 1 ? more : big, f[i].x, f[i].y);
-    big = max_nan(big, more);
+    return max_nan(big, more);
+}
+template <int P> __device__ __forceinline__ void add_group(Softmax &sm, const float2 (&f)[P], float big, float c)
+{
     if (!(big <= sm.m))
         sm.raise(max_nan(sm.m, big), c);
     const float2 minus = both(sm.m == -INFINITY ? 0.f : -sm.m), c2 = both(c);
@@ -249,94 +254,126 @@ template <int P> __device__ __forceinline__ float add_group(Softmax &sm, const f
             sm.add(f[i].y, c);
         }
     }
-    return big;
 }
 
 // The share's alternatives -> sh.best.  gmax[k][t] is the largest logit of
-// slot k (`per_slot` groups) of column t.  At least `top` columns reach the
-// bound min over the warps (r-th largest of its lanes' columns), r = top /
-// warps, so every alternative does; only the slots that reach it are read
-// again (a few dozen, a lane a value, from L2), and the values that do are
-// ranked.  `single` is the value of the row's ends that this thread holds.
+// slot k of column t: its vectors [k << shift, (k + 1) << shift).  A bound
+// that at least `top` slots reach is a bound that every alternative reaches;
+// only the slots that reach it are read again (a few dozen, a lane a value,
+// from L2), and the values that do are ranked.  For a warp the bound is the
+// top-th largest slot, to 24 bits, found bit by bit; for a block first the
+// minimum over its warps of the r-th largest of the lanes' columns, r = top /
+// warps, then the top-th largest of the slots that reach it (two or three
+// times `top`: reading all those again took longer than a row's softmax).
+// `single` is the value of the row's ends that this thread holds.
 template <typename T, typename Tm>
 __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::columns], const Share<T> &a, uint32_t top,
-                                           uint32_t slots, uint32_t groups, uint32_t per_slot, bool has_single,
-                                           float single, uint32_t single_at)
+                                           uint32_t slots, uint32_t shift, bool has_single, float single,
+                                           uint32_t single_at)
 {
-    constexpr uint32_t V = RowView<T>::V, U = RowView<T>::U, N = Tm::threads, C = Tm::columns;
+    constexpr uint32_t V = RowView<T>::V, N = Tm::threads, C = Tm::columns;
     const uint32_t tid = Tm::thread(), lane = tid & 31, warp = tid >> 5;
     const T *x = a.row.x;
-    float own = -INFINITY;
-    for (uint32_t k = 0; k < slots; ++k)
-#pragma unroll
-        for (uint32_t t = 0; t < C; t += N)
-            own = max_nan(own, gmax[k][t + tid]);
-    // warps whose lanes all have a vector; with none, every value above -infinity is a candidate
-    const uint32_t full = min(N / 32, (a.v1 - a.v0) / 32);
-    const uint32_t take = full ? (top + full - 1) / full : 0;
-    uint32_t mine = order_bits(own), low = 0;
-    for (uint32_t i = 0; i < take; ++i) {
-        low = __reduce_max_sync(~0u, mine);
-        if (lane == __ffs(__ballot_sync(~0u, mine == low)) - 1)
-            mine = 0;
-    }
-    if (lane == 0)
-        sh.low[warp] = low;
-    if (tid == 0)
-        sh.n_key = sh.n_pair = 0;
-    Tm::sync();
     uint32_t bound = order_bits(-INFINITY) + 1; // -infinity is no candidate
-    if (full) {
-        uint32_t b = 0xFFFFFFFFu;
-        for (uint32_t w = 0; w < full; ++w)
-            b = min(b, sh.low[w]);
-        bound = max(bound, b);
+    if (tid == 0)
+        sh.n_key = sh.n_pair = sh.n_kept = 0;
+    if constexpr (N == 32) {
+        uint32_t key[kWarpSlots], low = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kWarpSlots; ++k)
+            key[k] = k < slots ? order_bits(gmax[k][lane]) : 0;
+        for (uint32_t bit = 0x80000000u; bit >= 0x100u; bit >>= 1) {
+            uint32_t n = 0;
+#pragma unroll
+            for (uint32_t k = 0; k < kWarpSlots; ++k)
+                n += key[k] >= (low | bit);
+            if (__reduce_add_sync(~0u, n) >= top)
+                low |= bit;
+        }
+        bound = max(bound, low);
+        Tm::sync();
+    } else {
+        float own = -INFINITY;
+        for (uint32_t k = 0; k < slots; ++k)
+#pragma unroll
+            for (uint32_t t = 0; t < C; t += N)
+                own = max_nan(own, gmax[k][t + tid]);
+        // warps whose lanes all have a vector; with none, every value above -infinity is a candidate
+        const uint32_t full = min(N / 32, (a.v1 - a.v0) / 32), take = full ? (top + full - 1) / full : 0;
+        uint32_t mine = order_bits(own), low = 0;
+        for (uint32_t i = 0; i < take; ++i) {
+            low = __reduce_max_sync(~0u, mine);
+            if (lane == __ffs(__ballot_sync(~0u, mine == low)) - 1)
+                mine = 0;
+        }
+        if (lane == 0)
+            sh.low[warp] = low;
+        Tm::sync();
+        if (full) {
+            uint32_t b = 0xFFFFFFFFu;
+            for (uint32_t w = 0; w < full; ++w)
+                b = min(b, sh.low[w]);
+            bound = max(bound, b);
+        }
     }
     for (uint32_t k = 0; k < slots; ++k)
 #pragma unroll
-        for (uint32_t t = 0; t < C; t += N)
-            if (order_bits(gmax[k][t + tid]) >= bound)
-                sh.pair[atomicAdd(&sh.n_pair, 1u)] = (uint16_t)(k << 8 | (t + tid));
+        for (uint32_t t = 0; t < C; t += N) {
+            const uint32_t bits = order_bits(gmax[k][t + tid]);
+            if (bits >= bound) {
+                const uint32_t n = atomicAdd(&sh.n_pair, 1u);
+                sh.pair[n] = (uint16_t)(k << 8 | (t + tid));
+                if (n < Tm::keys)
+                    sh.key[n] = (unsigned long long)bits << 32 | n;
+            }
+        }
+    Tm::sync();
+    const uint16_t *pair = sh.pair;
+    uint32_t pairs = sh.n_pair;
+    if constexpr (N > 32) {
+        if (pairs > top && pairs <= Tm::keys) {
+            rank_keys(sh, pairs, top);
+            Tm::sync();
+            bound = (uint32_t)(sh.best[top - 1] >> 32);
+            for (uint32_t i = tid; i < pairs; i += N)
+                if ((uint32_t)(sh.key[i] >> 32) >= bound)
+                    sh.kept[atomicAdd(&sh.n_kept, 1u)] = sh.pair[i];
+            Tm::sync();
+            pair = sh.kept;
+            pairs = sh.n_kept;
+        }
+    }
     if (has_single && order_bits(single) >= bound)
         sh.key[atomicAdd(&sh.n_key, 1u)] = order_key(single, single_at); // at most 14
     Tm::sync();
-    const uint32_t pairs = sh.n_pair;
-    auto keep = [&](float f, uint32_t at) {
-        if (order_bits(f) >= bound) {
-            const uint32_t n = atomicAdd(&sh.n_key, 1u);
-            if (n < Tm::keys)
-                sh.key[n] = order_key(f, at);
-        }
-    };
-    auto place = [&](uint32_t pair, uint32_t e) { // value e of a pair's slot: its vector
-        return a.v0 + ((pair >> 8) * per_slot * U + e / V) * C + (pair & 0xFFu);
-    };
-    if (per_slot == 1) { // a lane a value; eight pairs' loads at a time
-        for (uint32_t i0 = warp; i0 < pairs; i0 += 8 * (N / 32)) {
-            T q[8];
-            uint32_t at[8];
+    // the slots' values, eight loads a thread at a time
+    const uint32_t log_v = sizeof(T) == 4 ? 2 : 3, log_slot = shift + log_v, items = pairs << log_slot;
+    for (uint32_t i0 = tid; i0 < items; i0 += 8 * N) {
+        T q[8];
+        uint32_t at[8];
 #pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) {
-                const uint32_t i = i0 + j * (N / 32);
-                const uint32_t v = i < pairs ? place(sh.pair[i], lane) : a.v1;
-                at[j] = v < a.v1 ? a.row.head + v * V + lane % V : ~0u;
-                if (at[j] != ~0u)
+        for (uint32_t j = 0; j < 8; ++j) {
+            const uint32_t i = i0 + j * N;
+            at[j] = ~0u;
+            if (i < items) {
+                const uint32_t slot = pair[i >> log_slot], e = i & ((1u << log_slot) - 1);
+                const uint32_t v = a.v0 + (((slot >> 8) << shift) + (e >> log_v)) * C + (slot & 0xFFu);
+                if (v < a.v1) {
+                    at[j] = a.row.head + v * V + (e & (V - 1));
                     q[j] = x[at[j]];
+                }
             }
+        }
 #pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-                if (at[j] != ~0u)
-                    keep(to_f32(q[j]), at[j]);
-        }
-    } else {
-        for (uint32_t i = warp; i < pairs; i += N / 32) {
-            const uint32_t g0 = (sh.pair[i] >> 8) * per_slot, g1 = min(groups, g0 + per_slot);
-            for (uint32_t e = lane; e < (g1 - g0) * 32; e += 32) {
-                const uint32_t v = place(sh.pair[i], e), at = a.row.head + v * V + e % V;
-                if (v < a.v1)
-                    keep(to_f32(x[at]), at);
+        for (uint32_t j = 0; j < 8; ++j)
+            if (at[j] != ~0u) {
+                const float f = to_f32(q[j]);
+                if (order_bits(f) >= bound) {
+                    const uint32_t n = atomicAdd(&sh.n_key, 1u);
+                    if (n < Tm::keys)
+                        sh.key[n] = order_key(f, at[j]);
+                }
             }
-        }
     }
     Tm::sync();
     const uint32_t n = sh.n_key;
@@ -425,7 +462,7 @@ __device__ __forceinline__ void write_row(const LogprobParams &p, const Tm &sh, 
 template <typename T> __global__ void __launch_bounds__(128, 6) logprob_warp_kernel(LogprobParams p)
 {
     __shared__ WarpTeam teams[4];
-    __shared__ float gmax[4][kSlots][32];
+    __shared__ float gmax[4][kWarpSlots][32];
     constexpr uint32_t V = RowView<T>::V, U = RowView<T>::U;
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     WarpTeam &sh = teams[warp];
@@ -442,32 +479,41 @@ template <typename T> __global__ void __launch_bounds__(128, 6) logprob_warp_ker
     const uint32_t single_at = has_single ? row.single(lane) : 0;
     const float single = has_single ? to_f32(x[single_at]) : -INFINITY;
     const uint32_t groups = (row.vecs + U * 32 - 1) / (U * 32);
-    const uint32_t per_slot = (groups + kSlots - 1) / kSlots;
+    uint32_t shift = 0; // vectors of a slot: a power of two
+    while ((kWarpSlots * 32u << shift) < row.vecs)
+        ++shift;
     Softmax sm;
-    uint32_t slot = 0;
-    for (uint32_t g = 0; g < groups;) {
-        float slot_max = -INFINITY;
-        for (uint32_t k = 0; k < per_slot && g < groups; ++k, ++g) {
-            const uint32_t i0 = g * U * 32 + lane;
-            uint4 q[U];
+    float slot_max = -INFINITY;
+    for (uint32_t g = 0; g < groups; ++g) {
+        const uint32_t i0 = g * U * 32 + lane;
+        uint4 q[U];
 #pragma unroll
-            for (uint32_t u = 0; u < U; ++u)
-                if (i0 + u * 32 < row.vecs)
-                    q[u] = ld_stream16(row.vec(i0 + u * 32));
-            float2 f[16];
+        for (uint32_t u = 0; u < U; ++u)
+            if (i0 + u * 32 < row.vecs)
+                q[u] = ld_stream16(row.vec(i0 + u * 32));
+        float2 f[16];
+        float big = -INFINITY;
 #pragma unroll
-            for (uint32_t u = 0; u < U; ++u)
-                if (i0 + u * 32 < row.vecs) {
-                    unpack2<T>(q[u], f + u * V / 2);
-                } else {
+        for (uint32_t u = 0; u < U; ++u) {
+            if (i0 + u * 32 < row.vecs) {
+                unpack2<T>(q[u], f + u * V / 2);
+            } else {
 #pragma unroll
-                    for (uint32_t i = 0; i < V / 2; ++i)
-                        f[u * V / 2 + i] = both(-INFINITY);
-                }
-            slot_max = max_nan(slot_max, add_group(sm, f, c));
+                for (uint32_t i = 0; i < V / 2; ++i)
+                    f[u * V / 2 + i] = both(-INFINITY);
+            }
+            const float m = largest_of<V / 2>(f + u * V / 2);
+            big = max_nan(big, m);
+            slot_max = max_nan(slot_max, m);
+            const uint32_t next = g * U + u + 1; // vectors of this lane so far
+            if (p.top && ((next & ((1u << shift) - 1)) == 0 || next == groups * U)) {
+                const uint32_t k = (next - 1) >> shift;
+                if (k < kWarpSlots)
+                    gmax[warp][k][lane] = slot_max;
+                slot_max = -INFINITY;
+            }
         }
-        gmax[warp][slot][lane] = slot_max;
-        ++slot;
+        add_group(sm, f, big, c);
     }
     if (has_single) {
         if (!(single <= sm.m))
@@ -483,7 +529,8 @@ template <typename T> __global__ void __launch_bounds__(128, 6) logprob_warp_ker
     }
     __syncwarp();
     if (p.top)
-        select_top<T>(sh, gmax[warp], a, p.top, slot, groups, per_slot, has_single, single, single_at);
+        select_top<T>(sh, gmax[warp], a, p.top, min(kWarpSlots, (groups * U + (1u << shift) - 1) >> shift), shift,
+                      has_single, single, single_at);
     write_row(p, sh, r, tok, xtok);
 }
 
@@ -547,7 +594,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
                         (uint32_t)p.vocab, rank == 0 ? row.head + row.tail : 0};
     };
     auto groups_of = [&](const Share<T> &a) { return (a.v1 - a.v0 + U * kLpThreads - 1) / (U * kLpThreads); };
-    auto per_slot_of = [&](uint32_t groups) { return (groups + kSlots - 1) / kSlots; };
+    auto per_slot_of = [&](uint32_t groups) { // a power of two
+        uint32_t n = 1;
+        while (n * kSlots < groups)
+            n *= 2;
+        return n;
+    };
     if (threadIdx.x >= kLpThreads + kSelThreads) { // the copy warp
         if (threadIdx.x == kLpThreads + kSelThreads) {
             uint32_t st = 0, ph = 0, issued = 0;
@@ -633,7 +685,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
                     ss.row[0].failed = ss.row[1].failed = 1;
                     break;
                 }
-                slot_max = max_nan(slot_max, add_group(sm, f, c));
+                const float big = largest_of<16>(f);
+                add_group(sm, f, big, c);
+                slot_max = max_nan(slot_max, big);
                 if (--left == 0 || g + 1 == groups) {
                     if (p.top)
                         buf.gmax[slot][tid] = slot_max;
@@ -653,16 +707,34 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
         }
     } else { // the alternatives and the outputs
         const uint32_t tid = BlockTeam::thread();
+        // asked for a row ahead: the token, its logit, the values at the row's ends (threads 8 to 21)
+        struct {
+            int64_t tok;
+            T logit, single;
+        } next;
+        auto token_of = [&](uint64_t r) { return r < p.rows && p.tokens && tid == 0 && rank == 0 ? p.tokens[r] : (int64_t)-1; };
+        auto ask = [&](uint64_t r) {
+            if (r >= p.rows)
+                return;
+            const Share<T> a = share_of(r);
+            if (next.tok >= 0 && next.tok < (int64_t)p.vocab)
+                next.logit = a.row.x[next.tok];
+            if (tid >= 8 && tid - 8 < a.singles)
+                next.single = a.row.x[a.row.single(tid - 8)];
+        };
+        next.tok = token_of(r0);
+        next.logit = next.single = T(0.f);
+        ask(r0);
         uint32_t b = 0;
         for (uint64_t r = r0; r < p.rows; r += step, b ^= 1) {
             RowBuffer &buf = ss.row[b];
             const Share<T> a = share_of(r);
-            // asked for early: the token's logit, the values at the row's ends (lanes 8 to 21 of the first warp)
-            const int64_t tok = p.tokens && tid == 0 && rank == 0 ? p.tokens[r] : -1;
-            const float xtok = tok >= 0 && tok < (int64_t)p.vocab ? to_f32(a.row.x[tok]) : 0.f;
+            const int64_t tok = next.tok;
+            const float xtok = to_f32(next.logit);
             const bool has_single = tid >= 8 && tid - 8 < a.singles;
             const uint32_t single_at = has_single ? a.row.single(tid - 8) : 0;
-            const float single = has_single ? to_f32(a.row.x[single_at]) : -INFINITY;
+            const float single = has_single ? to_f32(next.single) : -INFINITY;
+            next.tok = token_of(r + step);
             const uint32_t groups = groups_of(a);
             const uint32_t per_slot = per_slot_of(groups);
             buffer_sync(2 + b);
@@ -688,14 +760,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
                 for (uint32_t i = tid; i < p.top; i += kSelThreads)
                     sh.best[i] = order_key(NAN, 0);
             } else if (p.top) {
-                const uint32_t slots = per_slot ? (groups + per_slot - 1) / per_slot : 0;
-                select_top<T>(sh, buf.gmax, a, p.top, slots, groups, per_slot, has_single, single, single_at);
+                select_top<T>(sh, buf.gmax, a, p.top, (groups + per_slot - 1) / per_slot, 31 - __clz(per_slot * U),
+                              has_single, single, single_at);
             }
             BlockTeam::sync();
             if (r + 2 * step < p.rows)
                 buffer_arrive(4 + b);
             if (split > 1)
                 break; // one row a cluster; its parts are joined below
+            ask(r + step);
             write_row(p, sh, r, tok, xtok);
             BlockTeam::sync(); // the next row writes what write_row reads
         }
