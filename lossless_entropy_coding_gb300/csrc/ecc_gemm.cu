@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "ecc_act.cuh"
 #include "ecc_gemm.h"
 #include "ecc_tensor.cuh"
 
@@ -49,19 +50,13 @@ struct GemmBars {
 };
 
 // ---------------------------------------------------------------- epilogue
-__device__ __forceinline__ float act_of(uint32_t act, float a)
+template <uint32_t ACT, int W> __device__ __forceinline__ void activate(float (&a)[W])
 {
-    switch (act) {
-    case ECC_ACT_RELU:
-        return a < 0.f ? 0.f : a; // NaN stays
-    case ECC_ACT_GELU:
-        return 0.5f * a * (1.f + erff(a * 0.70710678f));
-    case ECC_ACT_GELU_TANH: // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
-        return __fdividef(a, 1.f + __expf(-1.59576912f * (a + 0.044715f * a * a * a)));
-    case ECC_ACT_SILU:
-        return __fdividef(a, 1.f + __expf(-a));
-    default:
-        return a;
+#pragma unroll
+    for (int j = 0; j < W; j += 2) {
+        const float2 v = act_value2<ACT>(make_float2(a[j], a[j + 1]));
+        a[j] = v.x;
+        a[j + 1] = v.y;
     }
 }
 
@@ -105,23 +100,14 @@ __device__ __forceinline__ void finish(const Epilogue &e, float (&a)[W], uint64_
         else
             store_rows<__half>(e.pre, e.ldpre, at, n, a, 1.f);
     }
-    if (e.act == ECC_ACT_RELU) {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            a[j] = act_of(ECC_ACT_RELU, a[j]);
-    } else if (e.act == ECC_ACT_GELU) {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            a[j] = act_of(ECC_ACT_GELU, a[j]);
-    } else if (e.act == ECC_ACT_GELU_TANH) {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            a[j] = act_of(ECC_ACT_GELU_TANH, a[j]);
-    } else if (e.act == ECC_ACT_SILU) {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            a[j] = act_of(ECC_ACT_SILU, a[j]);
-    }
+    if (e.act == ECC_ACT_RELU)
+        activate<ECC_ACT_RELU>(a);
+    else if (e.act == ECC_ACT_GELU)
+        activate<ECC_ACT_GELU>(a);
+    else if (e.act == ECC_ACT_GELU_TANH)
+        activate<ECC_ACT_GELU_TANH>(a);
+    else if (e.act == ECC_ACT_SILU)
+        activate<ECC_ACT_SILU>(a);
     if (e.residual) {
         const uint64_t at = r0 * e.ldres + c;
         if (e.res_type == ECC_F32)

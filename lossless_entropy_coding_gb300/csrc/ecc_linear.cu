@@ -9,33 +9,13 @@
 #include <algorithm>
 #include <cmath>
 
+#include "ecc_act.cuh"
 #include "ecc_gemm.h"
-#include "ecc_lm.cuh"
 
 namespace ecc {
 
 constexpr int kRowThreads = 256;
 constexpr uint32_t kSlopeParts = 64; // partial column sums of t at most
-
-__device__ __forceinline__ float act_slope(uint32_t act, float a)
-{
-    switch (act) {
-    case ECC_ACT_RELU:
-        return a > 0.f ? 1.f : (a != a ? a : 0.f);
-    case ECC_ACT_GELU: // Phi(a) + a phi(a)
-        return 0.5f * (1.f + erff(a * 0.70710678f)) + a * 0.39894228f * __expf(-0.5f * a * a);
-    case ECC_ACT_GELU_TANH: { // with h = (1 + tanh u) / 2 = 1 / (1 + e^-2u): h + 2 a h (1 - h) u'
-        const float u2 = 1.59576912f * (a + 0.044715f * a * a * a), h = __fdividef(1.f, 1.f + __expf(-u2));
-        return h + a * h * (1.f - h) * 1.59576912f * (1.f + 0.134145f * a * a);
-    }
-    case ECC_ACT_SILU: {
-        const float h = __fdividef(1.f, 1.f + __expf(-a));
-        return h * (1.f + a * (1.f - h));
-    }
-    default:
-        return 1.f;
-    }
-}
 
 // t = dy * act'(pre), rounded to the operand type (the tensor cores' input);
 // the column sums of t before that rounding
@@ -44,62 +24,71 @@ struct SlopeParams {
     void *t;     // [M, ldt]; NULL: only the sums
     float *part; // [parts][N]; NULL: no sums
     uint64_t M, N, lddy, ldpre, ldt;
-    uint32_t pre_type, act, parts;
+    uint32_t act, parts;
     uint32_t *status;
 };
 
-// a block: 32 * V columns, one share of the rows, eight rows at a time
-template <typename T, int V> __global__ void __launch_bounds__(kRowThreads) slope_kernel(SlopeParams p)
+// V values from element i of an array, in pairs (V = 1: the second is 0)
+template <typename T, int V> __device__ __forceinline__ void load_values(const void *p, uint64_t i, float2 (&f)[(V + 1) / 2])
 {
+    const T *q = static_cast<const T *>(p) + i;
+    if constexpr (V == 1) {
+        f[0] = make_float2(to_f32(*q), 0.f);
+    } else {
+        constexpr int E = 16 / sizeof(T);
+#pragma unroll
+        for (int k = 0; k < V; k += E)
+            unpack2<T>(*reinterpret_cast<const uint4 *>(q + k), f + k / 2);
+    }
+}
+
+// a block: 32 * V columns, one share of the rows, eight warps a row each
+template <typename T, typename PT, int V, uint32_t ACT>
+__global__ void __launch_bounds__(kRowThreads) slope_kernel(SlopeParams p)
+{
+    constexpr int H = (V + 1) / 2, W = V == 1 ? 1 : 2; // pairs; values used of a pair
     __shared__ float sums[8][32 * V + 1];
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
         *p.status = ECC_OK;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const uint64_t c = ((uint64_t)blockIdx.x * 32 + tx) * V;
     const uint64_t per = (p.M + p.parts - 1) / p.parts, r0 = blockIdx.y * per, r1 = min(p.M, r0 + per);
-    struct alignas(V * sizeof(T)) Vec {
-        T v[V];
-    };
-    float s[V] = {};
+    float2 s[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        s[i] = both(0.f);
     if (c < p.N)
+#pragma unroll 2
         for (uint64_t r = r0 + ty; r < r1; r += 8) {
-            const Vec d = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.dy) + r * p.lddy + c);
-            float v[V];
+            float2 v[H];
+            load_values<T, V>(p.dy, r * p.lddy + c, v);
+            if constexpr (ACT != ECC_ACT_NONE) {
+                float2 a[H];
+                load_values<PT, V>(p.pre, r * p.ldpre + c, a);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[i] = to_f32(d.v[i]);
-            if (p.act != ECC_ACT_NONE) {
-                float a[V];
-                if (p.pre_type == TypeCode<T>::value) {
-                    const Vec q = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.pre) + r * p.ldpre + c);
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        a[i] = to_f32(q.v[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        a[i] = load_any(p.pre, r * p.ldpre + c + i, p.pre_type);
+                for (int i = 0; i < H; ++i) { // (the sum fused, so that it is the same with and without t)
+                    a[i] = act_slope2<ACT>(a[i]);
+                    s[i] = fma2(v[i], a[i], s[i]);
+                    v[i] = mul2(v[i], a[i]);
                 }
+            } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    v[i] *= act_slope(p.act, a[i]);
+                for (int i = 0; i < H; ++i)
+                    s[i] = add2(s[i], v[i]);
             }
             if (p.t) {
-                Vec o;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    o.v[i] = from_f32<T>(v[i]);
-                *reinterpret_cast<Vec *>(static_cast<T *>(p.t) + r * p.ldt + c) = o;
+                T *o = static_cast<T *>(p.t) + r * p.ldt + c;
+                if constexpr (V == 1)
+                    *o = from_f32<T>(v[0].x);
+                else
+                    *reinterpret_cast<uint4 *>(o) = pack2<T>(v);
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                s[i] += v[i];
         }
     if (!p.part)
         return;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        sums[ty][tx + 32 * i] = s[i];
+        sums[ty][tx + 32 * i] = i % W ? s[i / 2].y : s[i / W].x;
     __syncthreads();
     for (uint64_t k = threadIdx.x; k < 32 * V; k += kRowThreads) {
         const uint64_t at = (uint64_t)blockIdx.x * 32 * V + (k & 31) * V + (k >> 5);
@@ -124,24 +113,31 @@ __global__ void __launch_bounds__(kRowThreads) sum_parts_kernel(const float *par
     out[c] = s;
 }
 
-// rows of `cols` elements to rows of ldd elements on 16-byte boundaries
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) pad_rows_kernel(const T *src, uint64_t ld, uint64_t rows, uint64_t cols,
-                                                               T *dst, uint64_t ldd)
+// Rows of `cols` elements to rows of ldd elements on 16-byte boundaries, for
+// up to two operands in one launch (blockIdx.y).
+struct PadJob {
+    const void *src;
+    void *dst;
+    uint64_t ld, rows, cols, ldd;
+};
+template <typename T> __global__ void __launch_bounds__(kRowThreads) pad_rows_kernel(PadJob a, PadJob b)
 {
     constexpr int V = 16 / sizeof(T);
     struct alignas(16) Vec {
         T v[V];
     };
-    const uint64_t vecs = ldd / V, n = rows * vecs;
+    const PadJob &j = blockIdx.y ? b : a;
+    const uint32_t vecs = (uint32_t)(j.ldd / V);
+    const uint64_t n = j.rows * vecs;
     for (uint64_t i = (uint64_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += (uint64_t)gridDim.x * kRowThreads) {
-        const uint64_t r = i / vecs, c = (i - r * vecs) * V;
-        const T *s = src + r * ld + c;
+        const uint64_t r = n >> 32 ? i / vecs : (uint32_t)i / vecs;
+        const uint32_t c = (uint32_t)(i - r * vecs) * V;
+        const T *s = static_cast<const T *>(j.src) + r * j.ld + c;
         Vec o;
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            o.v[k] = c + k < cols ? s[k] : T(0);
-        *reinterpret_cast<Vec *>(dst + r * ldd + c) = o;
+            o.v[k] = c + k < j.cols ? s[k] : T(0);
+        *reinterpret_cast<Vec *>(static_cast<T *>(j.dst) + r * j.ldd + c) = o;
     }
 }
 
@@ -160,21 +156,36 @@ size_t copy_bytes(const void *p, uint64_t ld, uint64_t rows, uint64_t cols, uint
     return rows && cols && !tma_rows(p, ld, type, rows) ? pad256(rows * padded(cols, type) * type_bytes(type)) : 0;
 }
 
-// the operand itself, or its copy at ws (advanced past it)
-Operand readable(const void *p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t type, uint8_t *&ws, cudaStream_t st)
+// The operands (arrays a and b of `type`), each itself or its copy at ws
+// (advanced past it); rows = 0: not wanted.
+struct Array {
+    const void *p;
+    uint64_t ld, rows, cols;
+};
+void readable(const Array &a, const Array &b, uint32_t type, uint8_t *&ws, cudaStream_t st, Operand &oa, Operand &ob)
 {
-    const size_t bytes = copy_bytes(p, ld, rows, cols, type);
-    if (!bytes)
-        return {p, ld, false};
-    const uint64_t ldd = padded(cols, type), vecs = rows * ldd * type_bytes(type) / 16;
-    const unsigned grid = (unsigned)std::min<uint64_t>((vecs + kRowThreads - 1) / kRowThreads, 1u << 16);
+    PadJob jobs[2];
+    int n = 0;
+    uint64_t most = 0;
+    auto one = [&](const Array &x, Operand &o) {
+        o = {x.p, x.ld, false};
+        const size_t bytes = copy_bytes(x.p, x.ld, x.rows, x.cols, type);
+        if (bytes) {
+            o = {ws, padded(x.cols, type), false};
+            jobs[n++] = {x.p, ws, x.ld, x.rows, x.cols, o.ld};
+            most = std::max<uint64_t>(most, bytes / 16);
+            ws += bytes;
+        }
+    };
+    one(a, oa);
+    one(b, ob);
+    if (!n)
+        return;
+    const dim3 grid((unsigned)std::min<uint64_t>((most + kRowThreads - 1) / kRowThreads, 1u << 15), n);
     if (type == ECC_E4M3)
-        pad_rows_kernel<uint8_t><<<grid, kRowThreads, 0, st>>>((const uint8_t *)p, ld, rows, cols, ws, ldd);
+        pad_rows_kernel<uint8_t><<<grid, kRowThreads, 0, st>>>(jobs[0], jobs[n - 1]);
     else
-        pad_rows_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>((const uint16_t *)p, ld, rows, cols, (uint16_t *)ws, ldd);
-    const Operand o{ws, ldd, false};
-    ws += bytes;
-    return o;
+        pad_rows_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>(jobs[0], jobs[n - 1]);
 }
 
 bool linear_ok(const ecc_linear_job &j)
@@ -241,19 +252,31 @@ GradPlan grad_plan(const ecc_linear_grad_job &j)
     return g;
 }
 
-template <typename T> ecc_status slope_launch(SlopeParams p, cudaStream_t st)
+template <typename T, typename PT, int V> auto slope_of(uint32_t act)
 {
-    const auto whole = [](const void *q, uint64_t ld) { return ((uintptr_t)q & 15) == 0 && ld % 8 == 0; };
-    // eight values a load where the rows allow it (1: 16-bit rows anywhere)
-    const bool v8 = p.N % 8 == 0 && whole(p.dy, p.lddy) && (!p.t || whole(p.t, p.ldt)) &&
-                    (p.act == ECC_ACT_NONE || p.pre_type != TypeCode<T>::value || whole(p.pre, p.ldpre));
+    return act == ECC_ACT_NONE    ? slope_kernel<T, PT, V, ECC_ACT_NONE>
+           : act == ECC_ACT_RELU  ? slope_kernel<T, PT, V, ECC_ACT_RELU>
+           : act == ECC_ACT_GELU  ? slope_kernel<T, PT, V, ECC_ACT_GELU>
+           : act == ECC_ACT_SILU  ? slope_kernel<T, PT, V, ECC_ACT_SILU>
+                                  : slope_kernel<T, PT, V, ECC_ACT_GELU_TANH>;
+}
+template <typename T, typename PT> ecc_status slope_launch(const SlopeParams &p, cudaStream_t st)
+{
+    const auto whole = [](const void *q, uint64_t ld, size_t size) { return ((uintptr_t)q & 15) == 0 && ld * size % 16 == 0; };
+    // eight values a load where the rows allow it
+    const bool v8 = p.N % 8 == 0 && whole(p.dy, p.lddy, sizeof(T)) && (!p.t || whole(p.t, p.ldt, sizeof(T))) &&
+                    (p.act == ECC_ACT_NONE || whole(p.pre, p.ldpre, sizeof(PT)));
     const uint64_t per = v8 ? 256 : 32;
     const dim3 grid((unsigned)((p.N + per - 1) / per), p.parts);
-    if (v8)
-        slope_kernel<T, 8><<<grid, kRowThreads, 0, st>>>(p);
-    else
-        slope_kernel<T, 1><<<grid, kRowThreads, 0, st>>>(p);
+    const auto f = v8 ? slope_of<T, PT, 8>(p.act) : slope_of<T, PT, 1>(p.act);
+    f<<<grid, kRowThreads, 0, st>>>(p);
     return launch_status(cudaGetLastError());
+}
+template <typename T> ecc_status slope_launch(const SlopeParams &p, uint32_t pre_type, cudaStream_t st)
+{
+    return pre_type == ECC_F32    ? slope_launch<T, float>(p, st)
+           : pre_type == ECC_BF16 ? slope_launch<T, bf16>(p, st)
+                                  : slope_launch<T, __half>(p, st);
 }
 
 } // namespace
@@ -283,8 +306,8 @@ ecc_status ecc_linear(const ecc_linear_job *job, void *ws, size_t ws_bytes, uint
     if (need && (!ws || !aligned16(ws) || ws_bytes < need))
         return ECC_ERR_ARG;
     uint8_t *w = (uint8_t *)ws;
-    const Operand x = readable(j.x, j.ldx, j.M, j.K, j.in_type, w, st);
-    const Operand wt = readable(j.w, j.ldw, j.N, j.K, j.in_type, w, st);
+    Operand x, wt;
+    readable({j.x, j.ldx, j.M, j.K}, {j.w, j.ldw, j.N, j.K}, j.in_type, w, st, x, wt);
     const Epilogue e{j.bias,  j.residual,  j.out,       j.pre,      j.ldres,    j.ldout,    j.ldpre,
                      j.scale, j.out_scale, j.bias_type, j.res_type, j.out_type, j.pre_type, j.act};
     return gemm(wt, x, j.M, j.N, j.K, j.in_type, e, status, true, st);
@@ -312,9 +335,10 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
     ecc_status rc = ECC_OK;
     const bool slope = j.N && (j.M || j.dbias) && (g.make_t || j.dbias);
     if (slope) {
-        const SlopeParams p{j.dy,  j.pre,  g.make_t ? t : nullptr, part, j.M, j.N, j.lddy, j.ldpre, g.ldt,
-                            j.pre_type, j.act, g.parts, status};
-        rc = j.in_type == ECC_BF16 ? slope_launch<bf16>(p, st) : slope_launch<__half>(p, st);
+        const SlopeParams p{j.dy,  j.pre, g.make_t ? t : nullptr, part, j.M, j.N, j.lddy, j.ldpre, g.ldt, j.act,
+                            g.parts, status};
+        const uint32_t pre_type = j.act == ECC_ACT_NONE ? j.in_type : j.pre_type;
+        rc = j.in_type == ECC_BF16 ? slope_launch<bf16>(p, pre_type, st) : slope_launch<__half>(p, pre_type, st);
         if (rc == ECC_OK && j.dbias) {
             sum_parts_kernel<<<(unsigned)((j.N + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st>>>(part, g.parts, j.N,
                                                                                                     j.dbias);
@@ -323,20 +347,20 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
     } else if (cudaMemsetAsync(status, 0, sizeof(uint32_t), st) != cudaSuccess) {
         rc = launch_status(cudaErrorUnknown);
     }
+    Operand x, wt; // read down their columns
+    if (rc == ECC_OK)
+        readable({j.x, j.ldx, j.dw ? j.M : 0, j.K}, {j.w, j.ldw, j.dx ? j.N : 0, j.K}, j.in_type, w, st, x, wt);
+    x.mn = wt.mn = true;
     Epilogue e{};
     e.scale = j.scale;
     e.out_scale = 1.f;
-    if (rc == ECC_OK && j.dx && j.M && j.K) { // rows M, columns K, reduction N: w is read down its columns
-        Operand wt = readable(j.w, j.ldw, j.N, j.K, j.in_type, w, st);
-        wt.mn = true;
+    if (rc == ECC_OK && j.dx && j.M && j.K) { // rows M, columns K, reduction N
         e.out = j.dx;
         e.ldout = j.lddx;
         e.out_type = j.in_type;
         rc = gemm(wt, {t, g.ldt, false}, j.M, j.K, j.N, j.in_type, e, status, false, st);
     }
-    if (rc == ECC_OK && j.dw && j.N && j.K) { // rows N, columns K, reduction M: t and x are read down their columns
-        Operand x = readable(j.x, j.ldx, j.M, j.K, j.in_type, w, st);
-        x.mn = true;
+    if (rc == ECC_OK && j.dw && j.N && j.K) { // rows N, columns K, reduction M
         e.out = j.dw;
         e.ldout = j.lddw;
         e.out_type = j.dw_type;

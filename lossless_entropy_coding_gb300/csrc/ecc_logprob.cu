@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
         struct {
             int64_t tok;
             T logit, single;
-        } next;
+        } next{-1, T(0.f), T(0.f)};
         auto token_of = [&](uint64_t r) { return r < p.rows && p.tokens && tid == 0 && rank == 0 ? p.tokens[r] : (int64_t)-1; };
         auto ask = [&](uint64_t r) {
             if (r >= p.rows)
@@ -723,7 +723,6 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
                 next.single = a.row.x[a.row.single(tid - 8)];
         };
         next.tok = token_of(r0);
-        next.logit = next.single = T(0.f);
         ask(r0);
         uint32_t b = 0;
         for (uint64_t r = r0; r < p.rows; r += step, b ^= 1) {
