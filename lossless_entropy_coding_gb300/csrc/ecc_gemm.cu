@@ -11,7 +11,7 @@
 //
 // gemm_pair_kernel: pairs of CTAs (tcgen05 cta_group::2) on 256 x `bn` tiles;
 // per CTA a TMA warp, a product warp (of the pair's first CTA) and four
-// epilogue warps.  The pairs are persistent, and the epilogue works on one
+// or eight epilogue warps.  The pairs are persistent, and the epilogue works on one
 // accumulator while the products fill the other.  For many tiles.
 // gemm_split_kernel: one 128 x `bn` tile a cluster of up to 8 CTAs that share
 // its reduction, for few tiles: the parts are joined through distributed
@@ -27,7 +27,8 @@
 
 namespace ecc {
 
-constexpr int kGemmThreads = 192; // TMA warp, product warp, 4 epilogue warps
+constexpr int kSplitThreads = 192; // TMA warp, product warp, 4 epilogue warps
+constexpr int kPairThreads = 320;  // 8 of them: half a tile's rows each (reductions of 1024 are shorter than an epilogue)
 constexpr uint32_t kPTile = 128;  // P rows of a CTA
 constexpr uint32_t kMaxStages = 12;
 constexpr uint32_t kPBytes = kPTile * kTileBytes;
@@ -215,7 +216,7 @@ __device__ __forceinline__ TilePos tile_pos(uint32_t t, uint32_t ptiles, uint32_
 }
 
 template <bool PMN, bool QMN, bool F8>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ GemmArgs g)
 {
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], 8); // four epilogue warps of each CTA
+            mbar_init(&s.tempty[i], 16); // eight epilogue warps of each CTA
         }
         fence_mbar_init();
     }
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
     } else {
         const uint32_t quad = warp & 3; // a warp reads the lanes of its number modulo 4
+        const uint32_t j0 = warp < 6 ? 0 : g.bn / 2, j1 = j0 + g.bn / 2;
         uint32_t acc = 0, aph = 0;
         for (uint32_t t = pair; t < tiles; t += pairs) {
             const TilePos pos = tile_pos(t, g.ptiles, g.qtiles);
@@ -330,10 +332,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint64_t left = g.rows - r0;
             uint32_t res[2][32]; // of this chunk of 32 rows and the next
             auto ask = [&](uint32_t j, uint32_t (&v)[32]) {
-                if (col_ok && j < g.bn && j < left)
+                if (col_ok && j < j1 && j < left)
                     ask_residual(g.e, v, r0 + j, (uint32_t)min((uint64_t)32, left - j), c);
             };
-            ask(0, res[0]);
+            ask(j0, res[0]);
             if (!__all_sync(~0u, mbar_wait(&s.tfull[acc], aph, g.limit_ns))) {
                 if (lane == 0)
                     set_status(g.status, ECC_ERR_TIMEOUT);
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             auto chunk = [&](uint32_t j, const uint32_t (&v)[32]) {
                 float a[32];
                 tmem_load32(tmem + (quad * 32 << 16) + acc * g.bn + j, a);
-                if (j + 32 == g.bn) { // the accumulator is read: products may fill it again
+                if (j + 32 == j1) { // the accumulator is read: products may fill it again
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0)
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (col_ok && j < left)
                     finish(g.e, a, v, r0 + j, (uint32_t)min((uint64_t)32, left - j), c, bias);
             };
-            for (uint32_t j = 0; j < g.bn; j += 64) { // (bn is 128 or 256)
+            for (uint32_t j = j0; j < j1; j += 64) { // (bn is 128 or 256)
                 ask(j + 32, res[1]);
                 chunk(j, res[0]);
                 ask(j + 64, res[0]);
@@ -407,7 +409,7 @@ __device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, 
 }
 
 template <bool PMN, bool QMN, bool F8>
-__global__ void __launch_bounds__(kGemmThreads, 2)
+__global__ void __launch_bounds__(kSplitThreads, 2)
     gemm_split_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ GemmArgs g)
 {
@@ -643,10 +645,11 @@ ecc_status gemm_launch(const Operand &P, const Operand &Q, uint64_t K, uint32_t 
     g.stages = std::min(kMaxStages, budget / stage_bytes);
     const size_t smem = kSmemHead + (size_t)g.stages * stage_bytes;
     const void *f = pair ? (const void *)gemm_pair_kernel<PMN, QMN, F8> : (const void *)gemm_split_kernel<PMN, QMN, F8>;
-    if (occupancy(f, kGemmThreads, smem) <= 0)
+    const int threads = pair ? kPairThreads : kSplitThreads;
+    if (occupancy(f, threads, smem) <= 0)
         return ECC_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kGemmThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.gridDim = dim3(pair ? 2 * std::min<uint32_t>(tiles, sms / 2) : tiles * g.split);
