@@ -553,16 +553,17 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 MAX_TOP = 32
 
 _types = {}  # torch element type -> C code, filled by _bind
-_empty = _raw_stream = _current_device = _f32 = _i32 = _i64 = _u8t = None
+_empty = _empty_strided = _empty_like = _raw_stream = _current_device = _f32 = _i32 = _i64 = _u8t = None
 
 
 def _bind():
     """Look up once what every call below needs."""
-    global _empty, _raw_stream, _current_device, _f32, _i32, _i64, _u8t
+    global _empty, _empty_strided, _empty_like, _raw_stream, _current_device, _f32, _i32, _i64, _u8t
     torch = _torch()
     _types.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3,
                    torch.uint8: E4M3})
     _empty, _f32, _i32, _i64, _u8t = torch.empty, torch.float32, torch.int32, torch.int64, torch.uint8
+    _empty_strided, _empty_like = torch.empty_strided, torch.empty_like
     torch.cuda.init()
     _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _load()
@@ -570,6 +571,16 @@ def _bind():
 
 def _refuse(what: str):
     raise EccError(ERR_ARG, what)
+
+
+def _new(shape, dtype, device):
+    """A contiguous tensor (torch.empty takes twice as long over a shape that is a tuple)."""
+    n = len(shape)
+    if n == 1:
+        return _empty(shape[0], dtype=dtype, device=device)
+    if n == 2:
+        return _empty_strided(shape, (shape[1] or 1, 1), dtype=dtype, device=device)
+    return _empty(shape, dtype=dtype, device=device)
 
 
 def _type(t, what: str) -> int:
@@ -620,7 +631,8 @@ def _on_stream(f):
         if dev < 0:
             _refuse(f.__name__ + ": needs CUDA tensors")
         if stream is None and dev == _current_device():
-            return f(x, *args, stream=_raw_stream(dev), **kw)
+            kw["stream"] = _raw_stream(dev)
+            return f(x, *args, **kw)
         torch = _torch()
         with torch.cuda.device(dev):
             s = torch.cuda.current_stream() if stream is None else stream
@@ -635,24 +647,33 @@ def ecc_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, out_d
     """Layer norm over the last dimension of device tensor x; returns (out,
     mean, rstd).  out_dtype: x's type (default), or uint8 / float8_e4m3fn for
     e4m3 values of out * out_scale.  weight, bias: of x's type or float32."""
-    dev = x.get_device()
+    dev, device, shape, dtype = x.get_device(), x.device, x.shape, x.dtype
     rows, cols, ldx = _matrix(x, "ecc_layer_norm: x")
     if out is None:
-        out = _empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    elif out.shape != x.shape or out.get_device() != dev:
+        out = _new(shape, out_dtype or dtype, device)
+        ldy = cols
+    elif out.shape != shape or out.get_device() != dev:
         _refuse("ecc_layer_norm: out")
-    _, _, ldy = _matrix(out, "ecc_layer_norm: out")
+    else:
+        ldy = _matrix(out, "ecc_layer_norm: out")[2]
+    lead = (rows,) if len(shape) == 2 else shape[:-1]
     if mean is None:
-        mean = _empty(x.shape[:-1], dtype=_f32, device=x.device)
+        mean = _new(lead, _f32, device)
+        pmean = mean.data_ptr()
+    else:
+        pmean = _vector(mean, rows, dev, "ecc_layer_norm: mean", _f32)
     if rstd is None:
-        rstd = _empty(x.shape[:-1], dtype=_f32, device=x.device)
-    p_dtype = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
-    _check(_lib.ecc_layer_norm(
-        x.data_ptr(), ldx, _type(x.dtype, "ecc_layer_norm"),
-        _vector(weight, cols, dev, "ecc_layer_norm: weight"), _vector(bias, cols, dev, "ecc_layer_norm: bias", p_dtype),
-        _type(p_dtype, "ecc_layer_norm"), rows, cols, eps, out.data_ptr(), ldy, _type(out.dtype, "ecc_layer_norm"),
-        out_scale, _vector(mean, rows, dev, "ecc_layer_norm: mean", _f32),
-        _vector(rstd, rows, dev, "ecc_layer_norm: rstd", _f32), stream), "ecc_layer_norm")
+        rstd = _new(lead, _f32, device)
+        prstd = rstd.data_ptr()
+    else:
+        prstd = _vector(rstd, rows, dev, "ecc_layer_norm: rstd", _f32)
+    p_dtype = weight.dtype if weight is not None else bias.dtype if bias is not None else dtype
+    code = _lib.ecc_layer_norm(
+        x.data_ptr(), ldx, _type(dtype, "ecc_layer_norm"), _vector(weight, cols, dev, "ecc_layer_norm: weight"),
+        _vector(bias, cols, dev, "ecc_layer_norm: bias", p_dtype), _type(p_dtype, "ecc_layer_norm"), rows, cols, eps,
+        out.data_ptr(), ldy, _type(out.dtype, "ecc_layer_norm"), out_scale, pmean, prstd, stream)
+    if code:
+        _check(code, "ecc_layer_norm")
     return out, mean, rstd
 
 
@@ -670,7 +691,7 @@ def ecc_layer_norm_grad(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=
         _refuse("ecc_layer_norm_grad: x")
     _, _, lddy = _matrix(dy, "ecc_layer_norm_grad: dy")
     if dx is None:
-        dx = _empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = _new(x.shape, x.dtype, x.device)
     elif dx.shape != x.shape or dx.dtype != x.dtype or dx.get_device() != dev:
         _refuse("ecc_layer_norm_grad: dx")
     _, _, lddx = _matrix(dx, "ecc_layer_norm_grad: dx")
@@ -732,8 +753,8 @@ def ecc_linear(x, w, bias=None, residual=None, act: str = "none", scale: float =
     if w_type != in_type:
         _refuse("ecc_linear: x and w of different types")
     if out is None:
-        out = _empty((*x.shape[:-1], N), device=x.device,
-                          dtype=out_dtype or (_torch().bfloat16 if in_type == E4M3 else x.dtype))
+        shape = (M, N) if x.dim() == 2 else (*x.shape[:-1], N)
+        out = _new(shape, out_dtype or (_torch().bfloat16 if in_type == E4M3 else x.dtype), x.device)
     if status is None:
         status = _empty(1, dtype=_i32, device=x.device)
     pout, ldout, out_type = _operand(out, M, N, dev, "ecc_linear: out")
@@ -769,9 +790,9 @@ def ecc_linear_grad(dy, x, w, pre=None, act: str = "none", scale: float = 1.0, d
         _refuse("ecc_linear_grad: dy, x and w of different types")
     ppre, ldpre, pre_type = _operand(pre, M, N, dev, "ecc_linear_grad: pre")
     if dx is None and "dx" in want:
-        dx = _empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = _new(x.shape, x.dtype, x.device)
     if dw is None and "dw" in want:
-        dw = _empty((N, K), dtype=dw_dtype or x.dtype, device=x.device)
+        dw = _new((N, K), dw_dtype or x.dtype, x.device)
     if dbias is None and "dbias" in want:
         dbias = _empty(N, dtype=_f32, device=x.device)
     if status is None:
@@ -811,17 +832,18 @@ def ecc_token_logprob(logits, tokens=None, top: int = 0, scale: float = 1.0, str
     `top` most probable tokens (at most 32)."""
     dev = logits.get_device()
     rows, vocab, ld = _matrix(logits, "ecc_token_logprob: logits")
-    lead = logits.shape[:-1]
+    lead = (rows,) if logits.dim() == 2 else logits.shape[:-1]
     if not 0 <= top <= MAX_TOP:
         _refuse("ecc_token_logprob: top")
     ptok = _vector(tokens, rows, dev, "ecc_token_logprob: tokens", _i64)
-    logprob = _empty(lead, dtype=_f32, device=logits.device) if tokens is not None else None
-    entropy = _empty(lead, dtype=_f32, device=logits.device)
-    lse = _empty(lead, dtype=_f32, device=logits.device)
+    device = logits.device
+    logprob = _new(lead, _f32, device) if tokens is not None else None
+    entropy = _new(lead, _f32, device)
+    lse = _new(lead, _f32, device)
     top_logprob = top_index = None
     if top:
-        top_logprob = _empty((*lead, top), dtype=_f32, device=logits.device)
-        top_index = _empty((*lead, top), dtype=_i32, device=logits.device)
+        top_logprob = _new((*lead, top), _f32, device)
+        top_index = _new((*lead, top), _i32, device)
     _check(_lib.ecc_token_logprob(
         logits.data_ptr(), ld, _type(logits.dtype, "ecc_token_logprob"), ptok, rows, vocab, scale, top,
         0 if logprob is None else logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logprob.data_ptr() if top else 0,
@@ -838,7 +860,7 @@ def ecc_token_logprob_grad(logits, tokens, lse, entropy=None, dlogprob=None, den
     dev = logits.get_device()
     rows, vocab, ld = _matrix(logits, "ecc_token_logprob_grad: logits")
     if dlogits is None:
-        dlogits = _empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        dlogits = _new(logits.shape, logits.dtype, logits.device)
     elif dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or dlogits.get_device() != dev:
         _refuse("ecc_token_logprob_grad: dlogits")
     _, _, ldd = _matrix(dlogits, "ecc_token_logprob_grad: dlogits")

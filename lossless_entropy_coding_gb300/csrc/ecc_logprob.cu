@@ -175,10 +175,9 @@ template <int N, int C> struct Team {
 
     static __device__ __forceinline__ void sync()
     {
-        if constexpr (N == 32)
-            __syncwarp();
-        else
-            asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+        __syncwarp();
+        if constexpr (N > 32) // (the form that allows a warp to arrive in parts)
+            asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory");
     }
     static __device__ __forceinline__ uint32_t thread() { return threadIdx.x % N; }
 };
@@ -555,14 +554,18 @@ struct StreamShared {
     BlockTeam team;
     uint64_t full[kStages], empty[kStages];
 };
-// hand a buffer over between the eight and the four warps (barriers 2 to 5)
+// Hand a buffer over between the eight and the four warps (barriers 2 to 5).
+// A warp arrives as a whole: had it split at the branch before (a lane that
+// writes for its warp), the aligned form would count it twice.
 __device__ __forceinline__ void buffer_arrive(uint32_t id)
 {
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kLpThreads + kSelThreads) : "memory");
+    __syncwarp();
+    asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "n"(kLpThreads + kSelThreads) : "memory");
 }
 __device__ __forceinline__ void buffer_sync(uint32_t id)
 {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kLpThreads + kSelThreads) : "memory");
+    __syncwarp();
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(kLpThreads + kSelThreads) : "memory");
 }
 
 template <typename T>
@@ -672,8 +675,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
                             }
                     }
                     if (count) {
+                        // The values have to be in registers before the copy warp may fill the stage again: an
+                        // arrival alone does not wait for this warp's loads (float32 values, which nothing
+                        // converts, were still on their way).
+                        fence_proxy_async();
                         __syncwarp();
-                        if ((tid & 31) == 0) // the stage is in registers
+                        if ((tid & 31) == 0)
                             asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&ss.empty[st])) : "memory");
                         if (++st == kStages) {
                             st = 0;

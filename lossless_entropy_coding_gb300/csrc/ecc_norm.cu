@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(ROWS > 1 ? 128 : 1024, ROWS > 1 ? 5 : 1) norm_
 // ---------------------------------------------------------------- backward, rows in registers
 __device__ __forceinline__ void group_barrier(uint32_t id, uint32_t threads) // id below 15
 {
-    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+    __syncwarp(); // (a lane wrote for its warp: the warp arrives as a whole)
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
 }
 // The sums over a group's threads of 2 ROWS values each, known to all of them
 // on return: within a warp the values are halved over the lanes (each lane

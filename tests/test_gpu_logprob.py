@@ -101,6 +101,20 @@ def test_logprob_shapes(rows, vocab, dtype):
     check(x, None, 1)
 
 
+@pytest.mark.parametrize("dtype,rows,vocab,top", [(F32, 1300, 50021, 20), (F32, 2000, 9001, 32), (BF16, 1300, 40003, 32),
+                                                  (BF16, 3000, 4099, 5), (F16, 1000, 131072, 8)])
+def test_logprob_many_long_rows(dtype, rows, vocab, top):
+    """Several rows a block, the selection of a row slower than the next one's sums."""
+    gen = torch.Generator("cuda").manual_seed(rows + vocab)
+    x = logits_of(gen, rows, vocab, dtype)
+    tok = torch.randint(0, vocab, (rows,), generator=gen, device="cuda")
+    first = check(x, tok, top, 0.7)
+    for _ in range(3):
+        again = ecc.ecc_token_logprob(x, tok, top=top, scale=0.7)
+        assert torch.equal(again.lse, first.lse) and torch.equal(again.top_index, first.top_index)
+        assert torch.equal(again.logprob, first.logprob) and torch.equal(again.entropy, first.entropy)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 def test_logprob_masks(dtype):
     gen = torch.Generator("cuda").manual_seed(3)
