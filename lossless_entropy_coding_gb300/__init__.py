@@ -14,10 +14,12 @@ from __future__ import annotations
 
 import ctypes as ct
 import functools
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import numpy as np
 
@@ -544,137 +546,67 @@ def bf16_escape_decode(enc: Encoded, top7, out=None, status=None, stream=None):
 # ---------------------------------------------------------------- language-model operators
 # Matrices are torch tensors [..., columns] whose last dimension is contiguous
 # and whose leading dimensions collapse to rows of one stride.  e4m3 tensors
-# are uint8 (the coders' bytes) or torch.float8_e4m3fn.  A call on another
-# stream than the current one allocates its outputs and scratch for that
-# stream; the caller orders the streams, as for the coding calls.
+# are uint8 (the coders' bytes) or torch.float8_e4m3fn.  The tensors are
+# checked and unpacked by the module built from csrc/torch/ecc_torch.cpp; what
+# it refuses raises EccError with ERR_ARG.  A call on another stream than the
+# current one allocates its outputs and scratch for that stream; the caller
+# orders the streams, as for the coding calls.
 
 F32, BF16, F16, E4M3 = range(4)
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 MAX_TOP = 32
+TORCH_LIB_PATH = os.path.join(_HERE, "_build", "ecc_torch.so")
 
-_types = {}  # torch element type -> C code, filled by _bind
-_empty = _empty_strided = _empty_like = _raw_stream = _current_device = _f32 = _i32 = _i64 = _u8t = None
-
-
-def _bind():
-    """Look up once what every call below needs."""
-    global _empty, _empty_strided, _empty_like, _raw_stream, _current_device, _f32, _i32, _i64, _u8t
-    torch = _torch()
-    _types.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3,
-                   torch.uint8: E4M3})
-    _empty, _f32, _i32, _i64, _u8t = torch.empty, torch.float32, torch.int32, torch.int64, torch.uint8
-    _empty_strided, _empty_like = torch.empty_strided, torch.empty_like
-    torch.cuda.init()
-    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _load()
+_torch_lib = None
 
 
-def _refuse(what: str):
-    raise EccError(ERR_ARG, what)
-
-
-def _new(shape, dtype, device):
-    """A contiguous tensor (torch.empty takes twice as long over a shape that is a tuple)."""
-    n = len(shape)
-    if n == 1:
-        return _empty(shape[0], dtype=dtype, device=device)
-    if n == 2:
-        return _empty_strided(shape, (shape[1] or 1, 1), dtype=dtype, device=device)
-    return _empty(shape, dtype=dtype, device=device)
-
-
-def _type(t, what: str) -> int:
-    code = _types.get(t)
-    return _refuse(what + ": element type") if code is None else code
-
-
-def _matrix(t, what: str):
-    """(rows, columns, leading dimension) of a tensor of rows."""
-    shape, stride = t.shape, t.stride()
-    n = len(shape)
-    if n == 0 or (stride[-1] != 1 and shape[-1] > 1):
-        _refuse(what + ": rows are not contiguous")
-    cols = shape[-1]
-    if n == 2:
-        rows = shape[0]
-        return rows, cols, stride[0] if rows > 1 else cols
-    rows, ld = 1, cols
-    for i in range(n - 2, -1, -1):
-        if shape[i] == 1:
-            continue
-        if rows == 1:
-            ld = stride[i]
-        elif shape[i] and stride[i] != rows * ld:
-            _refuse(what + ": leading dimensions do not collapse")
-        rows *= shape[i]
-    return rows, cols, ld
-
-
-def _vector(t, n: int, dev: int, what: str, dtype=None):
-    """Pointer of a contiguous tensor of n elements (0 for None)."""
-    if t is None:
-        return 0
-    if t.numel() != n or not t.is_contiguous() or t.get_device() != dev or (dtype is not None and t.dtype != dtype):
-        _refuse(what)
-    return t.data_ptr()
+def _marshal():
+    """The module that reads tensors (raises if it has not been built)."""
+    global _torch_lib
+    if _torch_lib is None:
+        torch = _torch()
+        _load()
+        if not os.path.exists(TORCH_LIB_PATH):
+            raise RuntimeError(f"ecc_torch is not built ({TORCH_LIB_PATH} missing): run "
+                               "`python -m lossless_entropy_coding_gb300.build`")
+        if torch.cuda.is_available():
+            torch.cuda.init()
+        loader = importlib.machinery.ExtensionFileLoader("ecc_torch", TORCH_LIB_PATH)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("ecc_torch", loader))
+        loader.exec_module(mod)
+        mod.set_error(EccError)
+        _torch_lib = mod
+    return _torch_lib
 
 
 def _on_stream(f):
-    """Run f with the device of its first tensor current and, where a stream is
-    given, with that stream current (so that what f allocates belongs to it);
-    f gets the stream's handle."""
+    """f on the given stream (made current, so that what f allocates belongs to
+    it); without one, on the current stream."""
     @functools.wraps(f)
     def call(x, *args, stream=None, **kw):
-        if _empty is None:
-            _bind()
-        dev = x.get_device()
-        if dev < 0:
-            _refuse(f.__name__ + ": needs CUDA tensors")
-        if stream is None and dev == _current_device():
-            kw["stream"] = _raw_stream(dev)
+        if stream is None:
             return f(x, *args, **kw)
-        torch = _torch()
-        with torch.cuda.device(dev):
-            s = torch.cuda.current_stream() if stream is None else stream
-            with torch.cuda.stream(s):
-                return f(x, *args, stream=s.cuda_stream, **kw)
+        if x.device != stream.device:
+            raise EccError(ERR_ARG, f.__name__ + ": stream of another device")
+        with _torch().cuda.stream(stream):
+            return f(x, *args, **kw)
     return call
+
+
+def _activation(act: str, what: str) -> int:
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise EccError(ERR_ARG, what + ": activation")
+    return code
 
 
 @_on_stream
 def ecc_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, out_dtype=None, out_scale: float = 1.0,
-                   mean=None, rstd=None, stream=None):
+                   mean=None, rstd=None):
     """Layer norm over the last dimension of device tensor x; returns (out,
     mean, rstd).  out_dtype: x's type (default), or uint8 / float8_e4m3fn for
     e4m3 values of out * out_scale.  weight, bias: of x's type or float32."""
-    dev, device, shape, dtype = x.get_device(), x.device, x.shape, x.dtype
-    rows, cols, ldx = _matrix(x, "ecc_layer_norm: x")
-    if out is None:
-        out = _new(shape, out_dtype or dtype, device)
-        ldy = cols
-    elif out.shape != shape or out.get_device() != dev:
-        _refuse("ecc_layer_norm: out")
-    else:
-        ldy = _matrix(out, "ecc_layer_norm: out")[2]
-    lead = (rows,) if len(shape) == 2 else shape[:-1]
-    if mean is None:
-        mean = _new(lead, _f32, device)
-        pmean = mean.data_ptr()
-    else:
-        pmean = _vector(mean, rows, dev, "ecc_layer_norm: mean", _f32)
-    if rstd is None:
-        rstd = _new(lead, _f32, device)
-        prstd = rstd.data_ptr()
-    else:
-        prstd = _vector(rstd, rows, dev, "ecc_layer_norm: rstd", _f32)
-    p_dtype = weight.dtype if weight is not None else bias.dtype if bias is not None else dtype
-    code = _lib.ecc_layer_norm(
-        x.data_ptr(), ldx, _type(dtype, "ecc_layer_norm"), _vector(weight, cols, dev, "ecc_layer_norm: weight"),
-        _vector(bias, cols, dev, "ecc_layer_norm: bias", p_dtype), _type(p_dtype, "ecc_layer_norm"), rows, cols, eps,
-        out.data_ptr(), ldy, _type(out.dtype, "ecc_layer_norm"), out_scale, pmean, prstd, stream)
-    if code:
-        _check(code, "ecc_layer_norm")
-    return out, mean, rstd
+    return (_torch_lib or _marshal()).layer_norm(x, weight, bias, eps, out, out_dtype, out_scale, mean, rstd)
 
 
 def layer_norm_grad_workspace_bytes(rows: int, cols: int) -> int:
@@ -682,141 +614,37 @@ def layer_norm_grad_workspace_bytes(rows: int, cols: int) -> int:
 
 
 @_on_stream
-def ecc_layer_norm_grad(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, ws=None, stream=None):
+def ecc_layer_norm_grad(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, ws=None):
     """Backward pass of ecc_layer_norm; returns (dx, dweight, dbias), the last
     two float32.  weight None: ones (dweight and dbias are still summed)."""
-    dev = dy.get_device()
-    rows, cols, ldx = _matrix(x, "ecc_layer_norm_grad: x")
-    if x.shape != dy.shape or x.dtype != dy.dtype or x.get_device() != dev:
-        _refuse("ecc_layer_norm_grad: x")
-    _, _, lddy = _matrix(dy, "ecc_layer_norm_grad: dy")
-    if dx is None:
-        dx = _new(x.shape, x.dtype, x.device)
-    elif dx.shape != x.shape or dx.dtype != x.dtype or dx.get_device() != dev:
-        _refuse("ecc_layer_norm_grad: dx")
-    _, _, lddx = _matrix(dx, "ecc_layer_norm_grad: dx")
-    if dweight is None:
-        dweight = _empty(cols, dtype=_f32, device=x.device)
-    if dbias is None:
-        dbias = _empty(cols, dtype=_f32, device=x.device)
-    lib = _lib
-    if ws is None:
-        ws = _empty(lib.ecc_layer_norm_grad_workspace_bytes(rows, cols), dtype=_u8t, device=x.device)
-    if mean is None or rstd is None:
-        _refuse("ecc_layer_norm_grad: mean and rstd")
-    _check(lib.ecc_layer_norm_grad(
-        dy.data_ptr(), lddy, x.data_ptr(), ldx, _type(x.dtype, "ecc_layer_norm_grad"),
-        _vector(weight, cols, dev, "ecc_layer_norm_grad: weight"),
-        _type(x.dtype if weight is None else weight.dtype, "ecc_layer_norm_grad"),
-        _vector(mean, rows, dev, "ecc_layer_norm_grad: mean", _f32),
-        _vector(rstd, rows, dev, "ecc_layer_norm_grad: rstd", _f32), rows, cols, dx.data_ptr(), lddx,
-        _vector(dweight, cols, dev, "ecc_layer_norm_grad: dweight", _f32),
-        _vector(dbias, cols, dev, "ecc_layer_norm_grad: dbias", _f32), ws.data_ptr(), ws.numel(), stream),
-        "ecc_layer_norm_grad")
-    return dx, dweight, dbias
-
-
-_LINEAR_JOB = struct.Struct("@6P8Q2f6I")        # ecc_linear_job
-_LINEAR_GRAD_JOB = struct.Struct("@7P9Qf5I")    # ecc_linear_grad_job
-
-
-def _activation(act: str, what: str) -> int:
-    code = ACTIVATIONS.get(act)
-    return _refuse(what + ": activation") if code is None else code
-
-
-def _operand(t, rows: int, cols: int, dev: int, what: str):
-    """(pointer, leading dimension, type) of a [rows, cols] tensor (zeros for None)."""
-    if t is None:
-        return 0, 0, 0
-    r, c, ld = _matrix(t, what)
-    if r != rows or c != cols or t.get_device() != dev:
-        _refuse(what + ": shape or device")
-    return t.data_ptr(), ld, _type(t.dtype, what)
+    return (_torch_lib or _marshal()).layer_norm_grad(dy, x, weight, mean, rstd, dx, dweight, dbias, ws)
 
 
 @_on_stream
 def ecc_linear(x, w, bias=None, residual=None, act: str = "none", scale: float = 1.0, out=None, out_dtype=None,
-               out_scale: float = 1.0, pre=None, ws=None, status=None, stream=None):
+               out_scale: float = 1.0, pre=None, ws=None, status=None):
     """act(scale * x w^T + bias) + residual of device tensors x [..., K] and
     w [N, K] (bfloat16, float16 or e4m3); returns (out [..., N], status).
     out_dtype: x's type by default, bfloat16 for e4m3 operands; uint8 or
     float8_e4m3fn: e4m3 values of out * out_scale.  pre: a tensor [..., N]
     that receives the activation's argument, for ecc_linear_grad."""
-    dev = x.get_device()
-    M, K, ldx = _matrix(x, "ecc_linear: x")
-    in_type = _type(x.dtype, "ecc_linear: x")
-    if w.dim() != 2:
-        _refuse("ecc_linear: w")
-    N = w.shape[0]
-    pw, ldw, w_type = _operand(w, N, K, dev, "ecc_linear: w")
-    if w_type != in_type:
-        _refuse("ecc_linear: x and w of different types")
-    if out is None:
-        shape = (M, N) if x.dim() == 2 else (*x.shape[:-1], N)
-        out = _new(shape, out_dtype or (_torch().bfloat16 if in_type == E4M3 else x.dtype), x.device)
-    if status is None:
-        status = _empty(1, dtype=_i32, device=x.device)
-    pout, ldout, out_type = _operand(out, M, N, dev, "ecc_linear: out")
-    pres, ldres, res_type = _operand(residual, M, N, dev, "ecc_linear: residual")
-    ppre, ldpre, pre_type = _operand(pre, M, N, dev, "ecc_linear: pre")
-    job = _LINEAR_JOB.pack(x.data_ptr(), pw, _vector(bias, N, dev, "ecc_linear: bias"), pres, pout, ppre, M, N, K, ldx,
-                           ldw, ldres, ldout, ldpre, scale, out_scale, in_type,
-                           0 if bias is None else _type(bias.dtype, "ecc_linear: bias"), res_type, out_type, pre_type,
-                           _activation(act, "ecc_linear"))
-    lib = _lib
-    if ws is None:
-        need = lib.ecc_linear_workspace_bytes(job)
-        ws = _empty(need, dtype=_u8t, device=x.device) if need else None
-    _check(lib.ecc_linear(job, 0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                          _vector(status, 1, dev, "ecc_linear: status", _i32), stream), "ecc_linear")
-    return out, status
+    return (_torch_lib or _marshal()).linear(x, w, bias, residual, _activation(act, "ecc_linear"), scale, out, out_dtype,
+                                             out_scale, pre, ws, status)
 
 
 @_on_stream
 def ecc_linear_grad(dy, x, w, pre=None, act: str = "none", scale: float = 1.0, dx=None, dw=None, dbias=None,
-                    dw_dtype=None, want=("dx", "dw", "dbias"), ws=None, status=None, stream=None):
+                    dw_dtype=None, want=("dx", "dw", "dbias"), ws=None, status=None):
     """Backward pass of ecc_linear's product; returns (dx, dw, dbias, status),
     None for what `want` leaves out.  pre: the activation's argument (needed
     unless act is "none").  dw_dtype: x's type (default) or float32; dbias is
     float32."""
-    dev = dy.get_device()
-    M, N, lddy = _matrix(dy, "ecc_linear_grad: dy")
-    in_type = _type(dy.dtype, "ecc_linear_grad: dy")
-    K = x.shape[-1]
-    px, ldx, x_type = _operand(x, M, K, dev, "ecc_linear_grad: x")
-    pw, ldw, w_type = _operand(w, N, K, dev, "ecc_linear_grad: w")
-    if x_type != in_type or w_type != in_type:
-        _refuse("ecc_linear_grad: dy, x and w of different types")
-    ppre, ldpre, pre_type = _operand(pre, M, N, dev, "ecc_linear_grad: pre")
-    if dx is None and "dx" in want:
-        dx = _new(x.shape, x.dtype, x.device)
-    if dw is None and "dw" in want:
-        dw = _new((N, K), dw_dtype or x.dtype, x.device)
-    if dbias is None and "dbias" in want:
-        dbias = _empty(N, dtype=_f32, device=x.device)
-    if status is None:
-        status = _empty(1, dtype=_i32, device=x.device)
-    pdx, lddx, dx_type = _operand(dx, M, K, dev, "ecc_linear_grad: dx")
-    if dx is not None and dx_type != in_type:
-        _refuse("ecc_linear_grad: dx")
-    pdw, lddw, dw_type = _operand(dw, N, K, dev, "ecc_linear_grad: dw")
-    job = _LINEAR_GRAD_JOB.pack(dy.data_ptr(), px, pw, ppre, pdx, pdw,
-                                _vector(dbias, N, dev, "ecc_linear_grad: dbias", _f32), M, N, K, lddy, ldx,
-                                ldw, ldpre, lddx, lddw, scale, in_type, pre_type, dw_type,
-                                _activation(act, "ecc_linear_grad"), 0)
-    lib = _lib
-    if ws is None:
-        need = lib.ecc_linear_grad_workspace_bytes(job)
-        ws = _empty(need, dtype=_u8t, device=x.device) if need else None
-    _check(lib.ecc_linear_grad(job, 0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                               _vector(status, 1, dev, "ecc_linear_grad: status", _i32), stream),
-           "ecc_linear_grad")
-    return dx, dw, dbias, status
+    bits = ("dx" in want) + 2 * ("dw" in want) + 4 * ("dbias" in want)
+    return (_torch_lib or _marshal()).linear_grad(dy, x, w, pre, _activation(act, "ecc_linear_grad"), scale, dx, dw, dbias,
+                                                  dw_dtype, bits, ws, status)
 
 
-@dataclass
-class TokenLogprob:
+class TokenLogprob(NamedTuple):
     """Device tensors of ecc_token_logprob (None where not asked for), in nats."""
     logprob: object
     entropy: object
@@ -826,51 +654,17 @@ class TokenLogprob:
 
 
 @_on_stream
-def ecc_token_logprob(logits, tokens=None, top: int = 0, scale: float = 1.0, stream=None) -> TokenLogprob:
+def ecc_token_logprob(logits, tokens=None, top: int = 0, scale: float = 1.0) -> TokenLogprob:
     """Log probabilities of tokens (int64 [...], negative: none) under softmax
     of scale * logits [..., vocab], with each row's entropy, log partition and
     `top` most probable tokens (at most 32)."""
-    dev = logits.get_device()
-    rows, vocab, ld = _matrix(logits, "ecc_token_logprob: logits")
-    lead = (rows,) if logits.dim() == 2 else logits.shape[:-1]
-    if not 0 <= top <= MAX_TOP:
-        _refuse("ecc_token_logprob: top")
-    ptok = _vector(tokens, rows, dev, "ecc_token_logprob: tokens", _i64)
-    device = logits.device
-    logprob = _new(lead, _f32, device) if tokens is not None else None
-    entropy = _new(lead, _f32, device)
-    lse = _new(lead, _f32, device)
-    top_logprob = top_index = None
-    if top:
-        top_logprob = _new((*lead, top), _f32, device)
-        top_index = _new((*lead, top), _i32, device)
-    _check(_lib.ecc_token_logprob(
-        logits.data_ptr(), ld, _type(logits.dtype, "ecc_token_logprob"), ptok, rows, vocab, scale, top,
-        0 if logprob is None else logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logprob.data_ptr() if top else 0,
-        top_index.data_ptr() if top else 0, stream), "ecc_token_logprob")
-    return TokenLogprob(logprob, entropy, lse, top_logprob, top_index)
+    return TokenLogprob._make((_torch_lib or _marshal()).token_logprob(logits, tokens, top, scale))
 
 
 @_on_stream
 def ecc_token_logprob_grad(logits, tokens, lse, entropy=None, dlogprob=None, dentropy=None, scale: float = 1.0,
-                           dlogits=None, stream=None):
+                           dlogits=None):
     """Gradient with respect to the logits of sum(dlogprob * logprob +
     dentropy * entropy); returns dlogits (which may be given as logits
     itself)."""
-    dev = logits.get_device()
-    rows, vocab, ld = _matrix(logits, "ecc_token_logprob_grad: logits")
-    if dlogits is None:
-        dlogits = _new(logits.shape, logits.dtype, logits.device)
-    elif dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or dlogits.get_device() != dev:
-        _refuse("ecc_token_logprob_grad: dlogits")
-    _, _, ldd = _matrix(dlogits, "ecc_token_logprob_grad: dlogits")
-    f = _f32
-    _check(_lib.ecc_token_logprob_grad(
-        logits.data_ptr(), ld, _type(logits.dtype, "ecc_token_logprob_grad"),
-        _vector(tokens, rows, dev, "ecc_token_logprob_grad: tokens", _i64), rows, vocab, scale,
-        _vector(lse, rows, dev, "ecc_token_logprob_grad: lse", f),
-        _vector(entropy, rows, dev, "ecc_token_logprob_grad: entropy", f),
-        _vector(dlogprob, rows, dev, "ecc_token_logprob_grad: dlogprob", f),
-        _vector(dentropy, rows, dev, "ecc_token_logprob_grad: dentropy", f), dlogits.data_ptr(), ldd, stream),
-        "ecc_token_logprob_grad")
-    return dlogits
+    return (_torch_lib or _marshal()).token_logprob_grad(logits, tokens, lse, entropy, dlogprob, dentropy, scale, dlogits)

@@ -3,6 +3,8 @@ process, linked into lossless_entropy_coding_gb300/_build/libecc_gb300.so.
 build(checked=True) builds the index-checked variant (-DECC_CHECKED: the
 kernels test their shared- and global-memory indices, skip an access out of
 range and report ECC_ERR_CHECK) into _build_checked/libecc_gb300_checked.so.
+build_torch() builds the Python module that unpacks torch tensors for the
+language-model operators (g++, torch's headers) into _build/ecc_torch.so.
 
     python -m lossless_entropy_coding_gb300.build [--force] [--checked]
 """
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -65,5 +68,30 @@ def build(force: bool = False, extra=(), checked: bool = False) -> str:
     return lib
 
 
+TORCH_LIB = os.path.join(OUT_DIR, "ecc_torch.so")
+
+
+def build_torch(force: bool = False) -> str:
+    """After build(): the module links against the library."""
+    import torch
+
+    src = os.path.join(CSRC, "torch", "ecc_torch.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "ecc_lm.h"), os.path.join(INCLUDE, "ecc.h")))
+    if not force and os.path.exists(TORCH_LIB) and os.path.getmtime(TORCH_LIB) >= newest:
+        return TORCH_LIB
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        "g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-I", INCLUDE, "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+        "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], src, "-o", tmp,
+        "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+        f"-Wl,-rpath,{os.path.join(home, 'lib')}", "-L", OUT_DIR, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, checked="--checked" in sys.argv))
+    print(build_torch(force="--force" in sys.argv))

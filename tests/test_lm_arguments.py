@@ -3,9 +3,12 @@ before any CUDA call (so they run without a GPU): every refusal is ECC_ERR_ARG
 and calls over no rows are accepted."""
 import ctypes as ct
 import math
+import struct
 
 import lossless_entropy_coding_gb300 as ecc
 
+LINEAR_JOB = struct.Struct("@6P8Q2f6I")        # ecc_linear_job
+LINEAR_GRAD_JOB = struct.Struct("@7P9Qf5I")    # ecc_linear_grad_job
 P = 1 << 20   # an aligned address that is never read: the calls return before any launch
 
 
@@ -42,14 +45,14 @@ def linear(status=P, ws=0, ws_bytes=0, **kw):
              scale=1.0, out_scale=1.0, in_type=ecc.BF16, bias_type=ecc.F32, res_type=ecc.F32, out_type=ecc.BF16,
              pre_type=ecc.BF16, act=0)
     a.update(kw)
-    return ecc.lib().ecc_linear(ecc._LINEAR_JOB.pack(*a.values()), ws, ws_bytes, status, 0)
+    return ecc.lib().ecc_linear(LINEAR_JOB.pack(*a.values()), ws, ws_bytes, status, 0)
 
 
 def linear_grad(status=P, ws=0, ws_bytes=0, **kw):
     a = dict(dy=P, x=P, w=P, pre=0, dx=2 * P, dw=2 * P, dbias=0, M=4, N=8, K=16, lddy=8, ldx=16, ldw=16, ldpre=8,
              lddx=16, lddw=16, scale=1.0, in_type=ecc.BF16, pre_type=ecc.BF16, dw_type=ecc.BF16, act=0, reserved=0)
     a.update(kw)
-    return ecc.lib().ecc_linear_grad(ecc._LINEAR_GRAD_JOB.pack(*a.values()), ws, ws_bytes, status, 0)
+    return ecc.lib().ecc_linear_grad(LINEAR_GRAD_JOB.pack(*a.values()), ws, ws_bytes, status, 0)
 
 
 def refused(call, cases):
@@ -97,7 +100,7 @@ def test_linear_arguments():
 
 
 def struct_sizes():
-    return ecc._LINEAR_JOB.size, ecc._LINEAR_GRAD_JOB.size
+    return LINEAR_JOB.size, LINEAR_GRAD_JOB.size
 
 
 def test_workspace_sizes_need_no_gpu():
