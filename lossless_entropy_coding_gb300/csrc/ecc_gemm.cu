@@ -203,6 +203,15 @@ __device__ __forceinline__ void multiply_block(uint32_t d, uint32_t pa, uint32_t
         tensor_product<CG, F8>(d, a + k * operand_step<PMN>(), b + k * operand_step<QMN>(), idesc, !first || k > 0);
 }
 
+// behind the launch's own preparation: wait for what it reads
+__device__ __forceinline__ void begin(const GemmArgs &g)
+{
+    wait_for_previous();
+    let_next_start();
+    if (g.clear_status && blockIdx.x == 0 && threadIdx.x == 0) // waits that give up do so a second from now at the earliest
+        *(volatile uint32_t *)g.status = ECC_OK;
+}
+
 // ---------------------------------------------------------------- pairs of CTAs, many tiles
 // Tiles in groups of 8 column tiles, a group row tile by row tile: the tiles
 // in work at a time form a block that shares its operands through L2.
@@ -228,8 +237,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t qn = g.bn / 2, stage_bytes = kPBytes + qn * kTileBytes;
     const uint32_t tiles = g.ptiles * g.qtiles, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     if (threadIdx.x == 0) {
-        if (g.clear_status && blockIdx.x == 0) // waits that give up do so a second from now at the earliest
-            *(volatile uint32_t *)g.status = ECC_OK;
         for (uint32_t i = 0; i < g.stages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
@@ -254,6 +261,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)&s.tmem;
+    begin(g);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -425,8 +433,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const uint32_t kb1 = (uint32_t)((uint64_t)g.kblocks * (rank + 1) / g.split);
     const uint32_t tcols = g.bn < 32 ? 32 : g.bn;
     if (threadIdx.x == 0) {
-        if (g.clear_status && blockIdx.x == 0)
-            *(volatile uint32_t *)g.status = ECC_OK;
         for (uint32_t i = 0; i < g.stages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
@@ -447,6 +453,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)&s.tmem;
+    begin(g);
 
     const uint32_t quad = warp & 3;
     const uint64_t c = p0 + quad * 32 + lane;
@@ -631,7 +638,7 @@ Shape choose_shape(uint64_t rows, uint64_t cols, uint64_t K, uint32_t kblocks, b
 
 template <bool PMN, bool QMN, bool F8>
 ecc_status gemm_launch(const Operand &P, const Operand &Q, uint64_t K, uint32_t type, GemmArgs g, bool pair, int sms,
-                       cudaStream_t st)
+                       bool behind, cudaStream_t st)
 {
     CUtensorMap pm{}, qm{};
     const uint32_t qn = pair ? g.bn / 2 : g.bn;
@@ -653,12 +660,14 @@ ecc_status gemm_launch(const Operand &P, const Operand &Q, uint64_t K, uint32_t 
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.gridDim = dim3(pair ? 2 * std::min<uint32_t>(tiles, sms / 2) : tiles * g.split);
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = pair ? 2 : g.split;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = behind ? 2 : 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     void *args[] = {&pm, &qm, &g};
     return launch_status(cudaLaunchKernelExC(&cfg, f, args));
 }
@@ -672,7 +681,7 @@ bool tma_rows(const void *p, uint64_t ld, uint32_t type, uint64_t rows)
 }
 
 ecc_status gemm(const Operand &P, const Operand &Q, uint64_t rows, uint64_t cols, uint64_t K, uint32_t type,
-                const Epilogue &e, uint32_t *status, bool clear_status, cudaStream_t st)
+                const Epilogue &e, uint32_t *status, bool clear_status, bool behind, cudaStream_t st)
 {
     const int sms = sm_count();
     if (sms <= 0)
@@ -698,12 +707,12 @@ ecc_status gemm(const Operand &P, const Operand &Q, uint64_t rows, uint64_t cols
     const bool pair = shape.pair;
     g.idesc = product_desc(type, P.mn, Q.mn, pair ? 256 : 128, g.bn);
     if (f8)
-        return gemm_launch<false, false, true>(P, Q, K, type, g, pair, sms, st);
+        return gemm_launch<false, false, true>(P, Q, K, type, g, pair, sms, behind, st);
     if (P.mn && Q.mn)
-        return gemm_launch<true, true, false>(P, Q, K, type, g, pair, sms, st);
+        return gemm_launch<true, true, false>(P, Q, K, type, g, pair, sms, behind, st);
     if (P.mn)
-        return gemm_launch<true, false, false>(P, Q, K, type, g, pair, sms, st);
-    return gemm_launch<false, false, false>(P, Q, K, type, g, pair, sms, st);
+        return gemm_launch<true, false, false>(P, Q, K, type, g, pair, sms, behind, st);
+    return gemm_launch<false, false, false>(P, Q, K, type, g, pair, sms, behind, st);
 }
 
 } // namespace ecc

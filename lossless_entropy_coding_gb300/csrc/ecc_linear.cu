@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kRowThreads) slope_kernel(SlopeParams p)
 {
     constexpr int H = (V + 1) / 2, W = V == 1 ? 1 : 2; // pairs; values used of a pair
     __shared__ float sums[8][32 * V + 1];
+    let_next_start();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
         *p.status = ECC_OK;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -104,10 +105,12 @@ __global__ void __launch_bounds__(kRowThreads) slope_kernel(SlopeParams p)
 
 __global__ void __launch_bounds__(kRowThreads) sum_parts_kernel(const float *part, uint32_t parts, uint64_t n, float *out)
 {
+    wait_for_previous();
     const uint64_t c = (uint64_t)blockIdx.x * kRowThreads + threadIdx.x;
     if (c >= n)
         return;
     float s = 0.f;
+#pragma unroll 8
     for (uint32_t k = 0; k < parts; ++k)
         s += part[k * n + c];
     out[c] = s;
@@ -123,9 +126,7 @@ struct PadJob {
 template <typename T> __global__ void __launch_bounds__(kRowThreads) pad_rows_kernel(PadJob a, PadJob b)
 {
     constexpr int V = 16 / sizeof(T);
-    struct alignas(16) Vec {
-        T v[V];
-    };
+    let_next_start();
     const PadJob &j = blockIdx.y ? b : a;
     const uint32_t vecs = (uint32_t)(j.ldd / V);
     const uint64_t n = j.rows * vecs;
@@ -133,11 +134,31 @@ template <typename T> __global__ void __launch_bounds__(kRowThreads) pad_rows_ke
         const uint64_t r = n >> 32 ? i / vecs : (uint32_t)i / vecs;
         const uint32_t c = (uint32_t)(i - r * vecs) * V;
         const T *s = static_cast<const T *>(j.src) + r * j.ld + c;
-        Vec o;
+        uint32_t o[4];
+        const uint32_t off = (uint32_t)(uintptr_t)s & 3;
+        if (c + V + 4 / sizeof(T) <= j.cols && c) { // five words around the 16 bytes, all inside the row
+            const uint32_t *w = reinterpret_cast<const uint32_t *>((uintptr_t)s & ~(uintptr_t)3);
+            uint32_t q[5];
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            o.v[k] = c + k < j.cols ? s[k] : T(0);
-        *reinterpret_cast<Vec *>(static_cast<T *>(j.dst) + r * j.ldd + c) = o;
+            for (int k = 0; k < 5; ++k)
+                q[k] = w[k];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[k] = __funnelshift_r(q[k], q[k + 1], off * 8);
+        } else { // a row's first and last ones
+            struct alignas(16) {
+                T v[V];
+            } t;
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                t.v[k] = c + k < j.cols ? s[k] : T(0);
+            const uint4 q = *reinterpret_cast<const uint4 *>(&t);
+            o[0] = q.x;
+            o[1] = q.y;
+            o[2] = q.z;
+            o[3] = q.w;
+        }
+        *reinterpret_cast<uint4 *>(static_cast<T *>(j.dst) + r * j.ldd + c) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -157,12 +178,12 @@ size_t copy_bytes(const void *p, uint64_t ld, uint64_t rows, uint64_t cols, uint
 }
 
 // The operands (arrays a and b of `type`), each itself or its copy at ws
-// (advanced past it); rows = 0: not wanted.
+// (advanced past it); rows = 0: not wanted.  Whether something was launched.
 struct Array {
     const void *p;
     uint64_t ld, rows, cols;
 };
-void readable(const Array &a, const Array &b, uint32_t type, uint8_t *&ws, cudaStream_t st, Operand &oa, Operand &ob)
+bool readable(const Array &a, const Array &b, uint32_t type, uint8_t *&ws, cudaStream_t st, Operand &oa, Operand &ob)
 {
     PadJob jobs[2];
     int n = 0;
@@ -180,12 +201,13 @@ void readable(const Array &a, const Array &b, uint32_t type, uint8_t *&ws, cudaS
     one(a, oa);
     one(b, ob);
     if (!n)
-        return;
+        return false;
     const dim3 grid((unsigned)std::min<uint64_t>((most + kRowThreads - 1) / kRowThreads, 1u << 15), n);
     if (type == ECC_E4M3)
         pad_rows_kernel<uint8_t><<<grid, kRowThreads, 0, st>>>(jobs[0], jobs[n - 1]);
     else
         pad_rows_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>(jobs[0], jobs[n - 1]);
+    return true;
 }
 
 bool linear_ok(const ecc_linear_job &j)
@@ -307,10 +329,10 @@ ecc_status ecc_linear(const ecc_linear_job *job, void *ws, size_t ws_bytes, uint
         return ECC_ERR_ARG;
     uint8_t *w = (uint8_t *)ws;
     Operand x, wt;
-    readable({j.x, j.ldx, j.M, j.K}, {j.w, j.ldw, j.N, j.K}, j.in_type, w, st, x, wt);
+    const bool copied = readable({j.x, j.ldx, j.M, j.K}, {j.w, j.ldw, j.N, j.K}, j.in_type, w, st, x, wt);
     const Epilogue e{j.bias,  j.residual,  j.out,       j.pre,      j.ldres,    j.ldout,    j.ldpre,
                      j.scale, j.out_scale, j.bias_type, j.res_type, j.out_type, j.pre_type, j.act};
-    return gemm(wt, x, j.M, j.N, j.K, j.in_type, e, status, true, st);
+    return gemm(wt, x, j.M, j.N, j.K, j.in_type, e, status, true, copied, st);
 }
 
 size_t ecc_linear_grad_workspace_bytes(const ecc_linear_grad_job *job)
@@ -333,24 +355,19 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
     float *part = j.dbias ? (float *)w : nullptr;
     w += g.part_bytes;
     ecc_status rc = ECC_OK;
+    Operand x, wt; // read down their columns
+    bool own = readable({j.x, j.ldx, j.dw ? j.M : 0, j.K}, {j.w, j.ldw, j.dx ? j.N : 0, j.K}, j.in_type, w, st, x, wt);
+    x.mn = wt.mn = true;
     const bool slope = j.N && (j.M || j.dbias) && (g.make_t || j.dbias);
     if (slope) {
         const SlopeParams p{j.dy,  j.pre, g.make_t ? t : nullptr, part, j.M, j.N, j.lddy, j.ldpre, g.ldt, j.act,
                             g.parts, status};
         const uint32_t pre_type = j.act == ECC_ACT_NONE ? j.in_type : j.pre_type;
         rc = j.in_type == ECC_BF16 ? slope_launch<bf16>(p, pre_type, st) : slope_launch<__half>(p, pre_type, st);
-        if (rc == ECC_OK && j.dbias) {
-            sum_parts_kernel<<<(unsigned)((j.N + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st>>>(part, g.parts, j.N,
-                                                                                                    j.dbias);
-            rc = launch_status(cudaGetLastError());
-        }
-    } else if (cudaMemsetAsync(status, 0, sizeof(uint32_t), st) != cudaSuccess) {
-        rc = launch_status(cudaErrorUnknown);
+        own = true;
     }
-    Operand x, wt; // read down their columns
-    if (rc == ECC_OK)
-        readable({j.x, j.ldx, j.dw ? j.M : 0, j.K}, {j.w, j.ldw, j.dx ? j.N : 0, j.K}, j.in_type, w, st, x, wt);
-    x.mn = wt.mn = true;
+    // status: cleared by t's kernel, or by the first product, or by itself
+    bool clear = !slope;
     Epilogue e{};
     e.scale = j.scale;
     e.out_scale = 1.f;
@@ -358,14 +375,23 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
         e.out = j.dx;
         e.ldout = j.lddx;
         e.out_type = j.in_type;
-        rc = gemm(wt, {t, g.ldt, false}, j.M, j.K, j.N, j.in_type, e, status, false, st);
+        rc = gemm(wt, {t, g.ldt, false}, j.M, j.K, j.N, j.in_type, e, status, clear, own, st);
+        own = true;
+        clear = false;
     }
     if (rc == ECC_OK && j.dw && j.N && j.K) { // rows N, columns K, reduction M
         e.out = j.dw;
         e.ldout = j.lddw;
         e.out_type = j.dw_type;
-        rc = gemm(x, {t, g.ldt, true}, j.N, j.K, j.M, j.in_type, e, status, false, st);
+        rc = gemm(x, {t, g.ldt, true}, j.N, j.K, j.M, j.in_type, e, status, clear, own, st);
+        own = true;
+        clear = false;
     }
+    if (rc == ECC_OK && slope && j.dbias)
+        rc = launch_status(launch_behind(sum_parts_kernel, dim3((unsigned)((j.N + kRowThreads - 1) / kRowThreads)), kRowThreads, 0,
+                                         st, (const float *)part, g.parts, j.N, j.dbias));
+    if (rc == ECC_OK && clear)
+        rc = launch_status(cudaMemsetAsync(status, 0, sizeof(uint32_t), st));
     return rc;
 }
 

@@ -589,6 +589,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
         ss.row[0].failed = ss.row[1].failed = 0;
     }
     __syncthreads();
+    int64_t row_tok = -1; // of the cluster's one row
+    float row_xtok = 0.f;
     auto share_of = [&](uint64_t r) {
         const RowView<T> row(static_cast<const T *>(p.logits) + r * p.ld, p.vocab);
         // (split is a power of two)
@@ -772,8 +774,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
             BlockTeam::sync();
             if (r + 2 * step < p.rows)
                 buffer_arrive(4 + b);
-            if (split > 1)
-                break; // one row a cluster; its parts are joined below
+            if (split > 1) { // one row a cluster; its parts are joined below
+                row_tok = tok;
+                row_xtok = xtok;
+                break;
+            }
             ask(r + step);
             write_row(p, sh, r, tok, xtok);
             BlockTeam::sync(); // the next row writes what write_row reads
@@ -785,9 +790,6 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
     cluster_sync(); // every part is there
     if (rank == 0 && threadIdx.x >= kLpThreads && threadIdx.x < kLpThreads + kSelThreads) {
         const uint32_t tid = BlockTeam::thread();
-        const int64_t tok = p.tokens && tid == 0 ? p.tokens[r0] : -1;
-        const T *x = static_cast<const T *>(p.logits) + r0 * p.ld;
-        const float xtok = tok >= 0 && tok < (int64_t)p.vocab ? to_f32(x[tok]) : 0.f;
         if (tid < 32) {
             Softmax sm;
             if (tid < split) {
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
         if (p.top)
             rank_keys(sh, sh.n_key, p.top);
         BlockTeam::sync();
-        write_row(p, sh, r0, tok, xtok);
+        write_row(p, sh, r0, row_tok, row_xtok);
     }
     __syncwarp();
     cluster_sync(); // the first block has read the others' parts

@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_parts_kernel(const float *p
                                                                   float *dweight, float *dbias)
 {
     __shared__ float sums[8][33];
+    wait_for_previous();
     const uint32_t tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const uint64_t c = (uint64_t)blockIdx.x * 32 + tx;
     float *out = blockIdx.y ? dbias : dweight;
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_parts_kernel(const float *p
     part += (uint64_t)blockIdx.y * parts * cols;
     float s = 0.f;
     if (c < cols)
+#pragma unroll 4
         for (uint32_t k = ty; k < parts; k += 8)
             s += part[k * cols + c];
     sums[ty][tx] = s;
@@ -453,6 +455,7 @@ __global__ void __launch_bounds__(NT, 1) norm_grad_kernel(NormGradParams p, uint
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ float part[2][NT / 32][2 * ROWS];
     constexpr int PER = E / V;
+    let_next_start();
     const uint32_t tid = threadIdx.x, group = tid / width, t = tid - group * width;
     const uint32_t groups = NT / width, warp0 = group * (width / 32);
     const uint32_t n = (uint32_t)(p.cols / V);
@@ -710,9 +713,14 @@ template <typename T> ecc_status norm_grad_launch(NormGradParams p, cudaStream_t
         if (p.dx)
             norm_dx_rows_kernel<T><<<row_grid(p.rows), kNormThreads, 0, st>>>(p);
     }
-    if (sums)
-        norm_parts_kernel<<<dim3((unsigned)((p.cols + 31) / 32), 2), kNormThreads, 0, st>>>(p.part, p.parts, p.cols, p.dweight,
-                                                                                           p.dbias);
+    const ecc_status rc = launch_status(cudaGetLastError());
+    if (rc != ECC_OK || !sums)
+        return rc;
+    const dim3 grid((unsigned)((p.cols + 31) / 32), 2);
+    if (p.rows && done) // lets it start early
+        return launch_status(launch_behind(norm_parts_kernel, grid, kNormThreads, 0, st, (const float *)p.part, p.parts, p.cols,
+                                           p.dweight, p.dbias));
+    norm_parts_kernel<<<grid, kNormThreads, 0, st>>>(p.part, p.parts, p.cols, p.dweight, p.dbias);
     return launch_status(cudaGetLastError());
 }
 
