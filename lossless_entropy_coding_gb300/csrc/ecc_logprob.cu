@@ -293,6 +293,7 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
         Tm::sync();
     } else {
         float own = -INFINITY;
+#pragma unroll 2
         for (uint32_t k = 0; k < slots; ++k)
 #pragma unroll
             for (uint32_t t = 0; t < C; t += N)
@@ -300,6 +301,7 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
         // warps whose lanes all have a vector; with none, every value above -infinity is a candidate
         const uint32_t full = min(N / 32, (a.v1 - a.v0) / 32), take = full ? (top + full - 1) / full : 0;
         uint32_t mine = order_bits(own), low = 0;
+#pragma unroll 1
         for (uint32_t i = 0; i < take; ++i) {
             low = __reduce_max_sync(~0u, mine);
             if (lane == __ffs(__ballot_sync(~0u, mine == low)) - 1)
@@ -315,8 +317,9 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
             bound = max(bound, b);
         }
     }
+#pragma unroll 1
     for (uint32_t k = 0; k < slots; ++k)
-#pragma unroll
+#pragma unroll 1
         for (uint32_t t = 0; t < C; t += N) {
             const uint32_t bits = order_bits(gmax[k][t + tid]);
             if (bits >= bound) {
@@ -803,20 +806,34 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
                 sh.sum[0] = sm.m;
                 sh.sum[1] = sm.s;
                 sh.sum[2] = sm.t;
-                sh.n_key = 0;
             }
         }
-        BlockTeam::sync();
-        const uint32_t n = split * p.top; // at most 256 keys; a short share's missing ones are 0
+        // the blocks' lists are in order (a short one ends in zeros): a key's rank is its place and the
+        // number of larger keys in each other list
+        const uint32_t n = split * p.top; // at most 256
         for (uint32_t i = tid; i < n; i += kSelThreads) {
             const uint32_t at = cluster_addr(smem_u32(sh.best + i % p.top), i / p.top);
             const uint32_t lo = __float_as_uint(cluster_load(at)), hi = __float_as_uint(cluster_load(at + 4));
-            if (hi)
-                sh.key[atomicAdd(&sh.n_key, 1u)] = (unsigned long long)hi << 32 | lo;
+            sh.key[i] = (unsigned long long)hi << 32 | lo;
         }
         BlockTeam::sync();
-        if (p.top)
-            rank_keys(sh, sh.n_key, p.top);
+#pragma unroll 1
+        for (uint32_t i = tid; i < n; i += kSelThreads) {
+            const unsigned long long key = sh.key[i];
+            const uint32_t own = i / p.top;
+            uint32_t rank_of = i - own * p.top;
+            for (uint32_t q = 0; q < split; ++q) {
+                uint32_t count = 0; // keys of list q above this one
+#pragma unroll
+                for (uint32_t step = 16; step; step >>= 1)
+                    if (count + step <= p.top && sh.key[q * p.top + count + step - 1] > key)
+                        count += step;
+                if (q != own)
+                    rank_of += count < p.top && sh.key[q * p.top + count] > key ? count + 1 : count;
+            }
+            if (key && rank_of < p.top)
+                sh.best[rank_of] = key;
+        }
         BlockTeam::sync();
         write_row(p, sh, r0, row_tok, row_xtok);
     }
