@@ -416,18 +416,16 @@ __device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, 
     }
 }
 
+// block: this CTA's number among the product's
 template <bool PMN, bool QMN, bool F8>
-__global__ void __launch_bounds__(kSplitThreads, 2)
-    gemm_split_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
-                      const __grid_constant__ GemmArgs g)
+__device__ __forceinline__ void split_tile(const CUtensorMap &pmap, const CUtensorMap &qmap, const GemmArgs &g, uint32_t block,
+                                           uint8_t *smem_raw, GemmBars &s)
 {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ GemmBars s;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = g.split > 1 ? cluster_rank() : 0;
     const uint32_t off = (kSmemHead - (smem_u32(smem_raw) & (kSmemHead - 1))) & (kSmemHead - 1);
     const uint32_t stage0 = smem_u32(smem_raw) + off;
     const uint32_t stage_bytes = kPBytes + g.bn * kTileBytes;
-    const uint32_t tile = blockIdx.x / g.split;
+    const uint32_t tile = block / g.split;
     const uint64_t p0 = (uint64_t)(tile % g.ptiles) * kPTile, q0 = (uint64_t)(tile / g.ptiles) * g.bn;
     const uint32_t kb0 = (uint32_t)((uint64_t)g.kblocks * rank / g.split);
     const uint32_t kb1 = (uint32_t)((uint64_t)g.kblocks * (rank + 1) / g.split);
@@ -542,6 +540,34 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         tmem_free<1>(tmem, tcols);
 }
 
+template <bool PMN, bool QMN, bool F8>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+    gemm_split_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ GemmArgs g)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ GemmBars s;
+    split_tile<PMN, QMN, F8>(pmap, qmap, g, blockIdx.x, smem_raw, s);
+}
+
+// A layer's two backward products in one launch: the first `n1` CTAs work on
+// dx (w down its columns, t along its rows), the others on dw (both down
+// their columns).  For layers whose products leave SMs idle: one after the
+// other they took 22 us for 100 x 1000 x 1000, of which the kernels' starts and
+// ends are most.
+__global__ void __launch_bounds__(kSplitThreads, 2)
+    gemm_both_kernel(const __grid_constant__ CUtensorMap p1, const __grid_constant__ CUtensorMap q1,
+                     const __grid_constant__ GemmArgs g1, const __grid_constant__ CUtensorMap p2,
+                     const __grid_constant__ CUtensorMap q2, const __grid_constant__ GemmArgs g2, uint32_t n1)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ GemmBars s;
+    if (blockIdx.x < n1)
+        split_tile<true, false, false>(p1, q1, g1, blockIdx.x, smem_raw, s);
+    else
+        split_tile<true, true, false>(p2, q2, g2, blockIdx.x - n1, smem_raw, s);
+}
+
 // ---------------------------------------------------------------- host side
 namespace {
 
@@ -636,40 +662,81 @@ Shape choose_shape(uint64_t rows, uint64_t cols, uint64_t K, uint32_t kblocks, b
     return best;
 }
 
-template <bool PMN, bool QMN, bool F8>
-ecc_status gemm_launch(const Operand &P, const Operand &Q, uint64_t K, uint32_t type, GemmArgs g, bool pair, int sms,
-                       bool behind, cudaStream_t st)
-{
+// A product made ready: its maps, its arguments.
+struct Plan {
     CUtensorMap pm{}, qm{};
-    const uint32_t qn = pair ? g.bn / 2 : g.bn;
-    if (K && (!encode_tiled() || !make_map(&pm, P, g.cols, K, type, PMN ? 64 : kPTile) ||
-              !make_map(&qm, Q, g.rows, K, type, QMN ? 64 : qn)))
+    GemmArgs g{};
+    bool pair = false;
+    uint32_t stage_bytes = 0;
+    uint32_t tiles() const { return g.ptiles * g.qtiles; }
+};
+
+Shape shape_of(const Product &x, uint32_t type, int sms)
+{
+    const uint32_t per = type == ECC_E4M3 ? 128 : 64;
+    return choose_shape(x.rows, x.cols, x.K, (uint32_t)up(x.K, per), x.Q.mn, type == ECC_E4M3, sms);
+}
+
+ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t type, uint32_t *status, bool clear_status)
+{
+    const uint64_t ptiles = up(x.cols, shape.pair ? 2 * kPTile : kPTile), qtiles = up(x.rows, shape.bn);
+    if (ptiles * qtiles >= (1u << 27))
+        return ECC_ERR_ARG;
+    GemmArgs &g = plan.g;
+    g.e = x.e;
+    g.rows = x.rows;
+    g.cols = x.cols;
+    g.kblocks = (uint32_t)up(x.K, type == ECC_E4M3 ? 128 : 64);
+    g.status = status;
+    g.clear_status = clear_status;
+    g.limit_ns = kWaitLimitNs + 1000ull * g.kblocks; // an epilogue waits for a whole reduction
+    g.bn = shape.bn;
+    g.split = shape.split;
+    g.ptiles = (uint32_t)ptiles;
+    g.qtiles = (uint32_t)qtiles;
+    g.idesc = product_desc(type, x.P.mn, x.Q.mn, shape.pair ? 256 : 128, g.bn);
+    plan.pair = shape.pair;
+    const uint32_t qn = shape.pair ? g.bn / 2 : g.bn;
+    plan.stage_bytes = kPBytes + qn * kTileBytes;
+    if (x.K && (!encode_tiled() || !make_map(&plan.pm, x.P, g.cols, x.K, type, x.P.mn ? 64 : kPTile) ||
+                !make_map(&plan.qm, x.Q, g.rows, x.K, type, x.Q.mn ? 64 : qn)))
         return ECC_ERR_CUDA;
-    const uint32_t stage_bytes = kPBytes + qn * kTileBytes;
-    const uint32_t tiles = g.ptiles * g.qtiles;
-    const bool alone = pair || tiles * g.split <= (uint32_t)sms; // one CTA an SM
+    return ECC_OK;
+}
+
+// stages and shared memory of a launch of `ctas` CTAs
+size_t stage_memory(Plan &plan, uint32_t ctas, int sms)
+{
+    const bool alone = plan.pair || ctas <= (uint32_t)sms; // one CTA an SM
     const uint32_t budget = (alone ? kAloneSmem : kSharedSmem) - kSmemHead - (uint32_t)sizeof(GemmBars);
-    g.stages = std::min(kMaxStages, budget / stage_bytes);
-    const size_t smem = kSmemHead + (size_t)g.stages * stage_bytes;
-    const void *f = pair ? (const void *)gemm_pair_kernel<PMN, QMN, F8> : (const void *)gemm_split_kernel<PMN, QMN, F8>;
-    const int threads = pair ? kPairThreads : kSplitThreads;
+    plan.g.stages = std::min(kMaxStages, budget / plan.stage_bytes);
+    return kSmemHead + (size_t)plan.g.stages * plan.stage_bytes;
+}
+
+ecc_status launch_plan(const void *f, int threads, uint32_t ctas, uint32_t cluster, size_t smem, void **args, bool behind,
+                       cudaStream_t st)
+{
     if (occupancy(f, threads, smem) <= 0)
         return ECC_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cfg.gridDim = dim3(pair ? 2 * std::min<uint32_t>(tiles, sms / 2) : tiles * g.split);
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = pair ? 2 : g.split;
+    at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = behind ? 2 : 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
-    void *args[] = {&pm, &qm, &g};
+    cfg.attrs = at;
+    cfg.numAttrs = behind ? 2 : 1;
     return launch_status(cudaLaunchKernelExC(&cfg, f, args));
+}
+
+template <bool PMN, bool QMN, bool F8> const void *kernel_of(bool pair)
+{
+    return pair ? (const void *)gemm_pair_kernel<PMN, QMN, F8> : (const void *)gemm_split_kernel<PMN, QMN, F8>;
 }
 
 } // namespace
@@ -680,39 +747,54 @@ bool tma_rows(const void *p, uint64_t ld, uint32_t type, uint64_t rows)
     return ((uintptr_t)p & 15) == 0 && (rows <= 1 || ((bytes & 15) == 0 && bytes < (1ull << 40)));
 }
 
-ecc_status gemm(const Operand &P, const Operand &Q, uint64_t rows, uint64_t cols, uint64_t K, uint32_t type,
-                const Epilogue &e, uint32_t *status, bool clear_status, bool behind, cudaStream_t st)
+ecc_status gemm(const Product &x, uint32_t type, uint32_t *status, bool clear_status, bool behind, cudaStream_t st)
 {
     const int sms = sm_count();
     if (sms <= 0)
         return ECC_ERR_CUDA;
-    const bool f8 = type == ECC_E4M3;
-    const uint32_t per = f8 ? 128 : 64;
-    GemmArgs g{};
-    g.e = e;
-    g.rows = rows;
-    g.cols = cols;
-    g.kblocks = (uint32_t)((K + per - 1) / per);
-    g.status = status;
-    g.clear_status = clear_status;
-    g.limit_ns = kWaitLimitNs + 1000ull * g.kblocks; // an epilogue waits for a whole reduction
-    const Shape shape = choose_shape(rows, cols, K, g.kblocks, Q.mn, f8, sms);
-    const uint64_t ptiles = up(cols, shape.pair ? 2 * kPTile : kPTile), qtiles = up(rows, shape.bn);
-    if (ptiles * qtiles >= (1u << 27))
-        return ECC_ERR_ARG;
-    g.bn = shape.bn;
-    g.split = shape.split;
-    g.ptiles = (uint32_t)ptiles;
-    g.qtiles = (uint32_t)qtiles;
-    const bool pair = shape.pair;
-    g.idesc = product_desc(type, P.mn, Q.mn, pair ? 256 : 128, g.bn);
-    if (f8)
-        return gemm_launch<false, false, true>(P, Q, K, type, g, pair, sms, behind, st);
-    if (P.mn && Q.mn)
-        return gemm_launch<true, true, false>(P, Q, K, type, g, pair, sms, behind, st);
-    if (P.mn)
-        return gemm_launch<true, false, false>(P, Q, K, type, g, pair, sms, behind, st);
-    return gemm_launch<false, false, false>(P, Q, K, type, g, pair, sms, behind, st);
+    Plan plan;
+    const ecc_status rc = make_plan(plan, x, shape_of(x, type, sms), type, status, clear_status);
+    if (rc != ECC_OK)
+        return rc;
+    const bool pair = plan.pair;
+    const uint32_t ctas = pair ? 2 * std::min<uint32_t>(plan.tiles(), sms / 2) : plan.tiles() * plan.g.split;
+    const size_t smem = stage_memory(plan, ctas, sms);
+    const void *f = type == ECC_E4M3           ? kernel_of<false, false, true>(pair)
+                    : x.P.mn && x.Q.mn         ? kernel_of<true, true, false>(pair)
+                    : x.P.mn                   ? kernel_of<true, false, false>(pair)
+                                               : kernel_of<false, false, false>(pair);
+    void *args[] = {&plan.pm, &plan.qm, &plan.g};
+    return launch_plan(f, pair ? kPairThreads : kSplitThreads, ctas, pair ? 2 : plan.g.split, smem, args, behind, st);
+}
+
+ecc_status gemm_backward(const Product &dx, const Product &dw, uint32_t type, uint32_t *status, bool clear_status, bool behind,
+                         cudaStream_t st)
+{
+    const int sms = sm_count();
+    if (sms <= 0)
+        return ECC_ERR_CUDA;
+    Shape s1 = shape_of(dx, type, sms), s2 = shape_of(dw, type, sms);
+    // in one launch where neither fills the GPU by itself and both fit it, two CTAs an SM
+    const uint64_t t1 = up(dx.cols, kPTile) * up(dx.rows, s1.bn), t2 = up(dw.cols, kPTile) * up(dw.rows, s2.bn);
+    uint32_t split = std::min(s1.split, s2.split);
+    while (split > 1 && (t1 + t2) * split > 2ull * sms)
+        split /= 2;
+    if (s1.pair || s2.pair || !dx.K || !dw.K || (t1 + t2) * split > 2ull * sms) {
+        const ecc_status rc = gemm(dx, type, status, clear_status, behind, st);
+        return rc == ECC_OK ? gemm(dw, type, status, false, true, st) : rc;
+    }
+    s1.split = s2.split = split;
+    Plan a, b;
+    ecc_status rc = make_plan(a, dx, s1, type, status, clear_status);
+    if (rc == ECC_OK)
+        rc = make_plan(b, dw, s2, type, status, false);
+    if (rc != ECC_OK)
+        return rc;
+    uint32_t n1 = a.tiles() * split;
+    const uint32_t ctas = n1 + b.tiles() * split;
+    const size_t m1 = stage_memory(a, ctas, sms), m2 = stage_memory(b, ctas, sms);
+    void *args[] = {&a.pm, &a.qm, &a.g, &b.pm, &b.qm, &b.g, &n1};
+    return launch_plan((const void *)gemm_both_kernel, kSplitThreads, ctas, split, std::max(m1, m2), args, behind, st);
 }
 
 } // namespace ecc

@@ -28,10 +28,18 @@ struct Operand {
 
 // whether an array of `rows` rows can be read by tiled TMA as it is
 bool tma_rows(const void *p, uint64_t ld, uint32_t type, uint64_t rows);
-// P holds the output's columns, Q its rows; clear_status: the launch sets
-// *status to ECC_OK; behind: the stream's last launch is one of the same
-// call's that lets this one start early
-ecc_status gemm(const Operand &P, const Operand &Q, uint64_t rows, uint64_t cols, uint64_t K, uint32_t type,
-                const Epilogue &e, uint32_t *status, bool clear_status, bool behind, cudaStream_t st);
+// rows x cols values from a reduction of K; P holds the output's columns, Q its rows
+struct Product {
+    Operand P, Q;
+    uint64_t rows, cols, K;
+    Epilogue e;
+};
+// clear_status: the launch sets *status to ECC_OK; behind: the stream's last
+// launch is one of the same call's that lets this one start early
+ecc_status gemm(const Product &x, uint32_t type, uint32_t *status, bool clear_status, bool behind, cudaStream_t st);
+// a layer's two backward products: dx with Q along its rows, dw with both
+// operands down their columns (16-bit types)
+ecc_status gemm_backward(const Product &dx, const Product &dw, uint32_t type, uint32_t *status, bool clear_status, bool behind,
+                         cudaStream_t st);
 
 } // namespace ecc

@@ -332,7 +332,7 @@ ecc_status ecc_linear(const ecc_linear_job *job, void *ws, size_t ws_bytes, uint
     const bool copied = readable({j.x, j.ldx, j.M, j.K}, {j.w, j.ldw, j.N, j.K}, j.in_type, w, st, x, wt);
     const Epilogue e{j.bias,  j.residual,  j.out,       j.pre,      j.ldres,    j.ldout,    j.ldpre,
                      j.scale, j.out_scale, j.bias_type, j.res_type, j.out_type, j.pre_type, j.act};
-    return gemm(wt, x, j.M, j.N, j.K, j.in_type, e, status, true, copied, st);
+    return gemm({wt, x, j.M, j.N, j.K, e}, j.in_type, status, true, copied, st);
 }
 
 size_t ecc_linear_grad_workspace_bytes(const ecc_linear_grad_job *job)
@@ -368,25 +368,22 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
     }
     // status: cleared by t's kernel, or by the first product, or by itself
     bool clear = !slope;
-    Epilogue e{};
-    e.scale = j.scale;
-    e.out_scale = 1.f;
-    if (rc == ECC_OK && j.dx && j.M && j.K) { // rows M, columns K, reduction N
-        e.out = j.dx;
-        e.ldout = j.lddx;
-        e.out_type = j.in_type;
-        rc = gemm(wt, {t, g.ldt, false}, j.M, j.K, j.N, j.in_type, e, status, clear, own, st);
-        own = true;
+    Product dx{wt, {t, g.ldt, false}, j.M, j.K, j.N, {}}, dw{x, {t, g.ldt, true}, j.N, j.K, j.M, {}};
+    dx.e.scale = dw.e.scale = j.scale;
+    dx.e.out_scale = dw.e.out_scale = 1.f;
+    dx.e.out = j.dx;
+    dx.e.ldout = j.lddx;
+    dx.e.out_type = j.in_type;
+    dw.e.out = j.dw;
+    dw.e.ldout = j.lddw;
+    dw.e.out_type = j.dw_type;
+    const bool want_dx = j.dx && j.M && j.K, want_dw = j.dw && j.N && j.K;
+    if (rc == ECC_OK && want_dx && want_dw)
+        rc = gemm_backward(dx, dw, j.in_type, status, clear, own, st);
+    else if (rc == ECC_OK && (want_dx || want_dw))
+        rc = gemm(want_dx ? dx : dw, j.in_type, status, clear, own, st);
+    if (want_dx || want_dw)
         clear = false;
-    }
-    if (rc == ECC_OK && j.dw && j.N && j.K) { // rows N, columns K, reduction M
-        e.out = j.dw;
-        e.ldout = j.lddw;
-        e.out_type = j.dw_type;
-        rc = gemm(x, {t, g.ldt, true}, j.N, j.K, j.M, j.in_type, e, status, clear, own, st);
-        own = true;
-        clear = false;
-    }
     if (rc == ECC_OK && slope && j.dbias)
         rc = launch_status(launch_behind(sum_parts_kernel, dim3((unsigned)((j.N + kRowThreads - 1) / kRowThreads)), kRowThreads, 0,
                                          st, (const float *)part, g.parts, j.N, j.dbias));
