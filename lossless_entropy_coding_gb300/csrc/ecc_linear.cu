@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(kRowThreads) slope_kernel(SlopeParams p)
                     *reinterpret_cast<uint4 *>(o) = pack2<T>(v);
             }
         }
+    // (launched behind the padding, which it does not read: whatever waits for this kernel waits for both)
+    wait_for_previous();
     if (!p.part)
         return;
 #pragma unroll
@@ -282,7 +284,7 @@ template <typename T, typename PT, int V> auto slope_of(uint32_t act)
            : act == ECC_ACT_SILU  ? slope_kernel<T, PT, V, ECC_ACT_SILU>
                                   : slope_kernel<T, PT, V, ECC_ACT_GELU_TANH>;
 }
-template <typename T, typename PT> ecc_status slope_launch(const SlopeParams &p, cudaStream_t st)
+template <typename T, typename PT> ecc_status slope_launch(const SlopeParams &p, bool behind, cudaStream_t st)
 {
     const auto whole = [](const void *q, uint64_t ld, size_t size) { return ((uintptr_t)q & 15) == 0 && ld * size % 16 == 0; };
     // eight values a load where the rows allow it
@@ -291,14 +293,16 @@ template <typename T, typename PT> ecc_status slope_launch(const SlopeParams &p,
     const uint64_t per = v8 ? 256 : 32;
     const dim3 grid((unsigned)((p.N + per - 1) / per), p.parts);
     const auto f = v8 ? slope_of<T, PT, 8>(p.act) : slope_of<T, PT, 1>(p.act);
+    if (behind)
+        return launch_status(launch_behind(f, grid, kRowThreads, 0, st, p));
     f<<<grid, kRowThreads, 0, st>>>(p);
     return launch_status(cudaGetLastError());
 }
-template <typename T> ecc_status slope_launch(const SlopeParams &p, uint32_t pre_type, cudaStream_t st)
+template <typename T> ecc_status slope_launch(const SlopeParams &p, uint32_t pre_type, bool behind, cudaStream_t st)
 {
-    return pre_type == ECC_F32    ? slope_launch<T, float>(p, st)
-           : pre_type == ECC_BF16 ? slope_launch<T, bf16>(p, st)
-                                  : slope_launch<T, __half>(p, st);
+    return pre_type == ECC_F32    ? slope_launch<T, float>(p, behind, st)
+           : pre_type == ECC_BF16 ? slope_launch<T, bf16>(p, behind, st)
+                                  : slope_launch<T, __half>(p, behind, st);
 }
 
 } // namespace
@@ -363,7 +367,7 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
         const SlopeParams p{j.dy,  j.pre, g.make_t ? t : nullptr, part, j.M, j.N, j.lddy, j.ldpre, g.ldt, j.act,
                             g.parts, status};
         const uint32_t pre_type = j.act == ECC_ACT_NONE ? j.in_type : j.pre_type;
-        rc = j.in_type == ECC_BF16 ? slope_launch<bf16>(p, pre_type, st) : slope_launch<__half>(p, pre_type, st);
+        rc = j.in_type == ECC_BF16 ? slope_launch<bf16>(p, pre_type, own, st) : slope_launch<__half>(p, pre_type, own, st);
         own = true;
     }
     // status: cleared by t's kernel, or by the first product, or by itself

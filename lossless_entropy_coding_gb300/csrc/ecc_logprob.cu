@@ -1002,12 +1002,12 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads) logprob_grad
 
 namespace {
 
-// CTAs a row, in powers of two: enough for `ctas` in all while a CTA keeps at
+// CTAs a row, in powers of two: at most `ctas` in all while a CTA keeps at
 // least `least` values
 uint32_t row_split(uint64_t rows, uint64_t vocab, uint64_t ctas, uint64_t least)
 {
     uint32_t s = 1;
-    while (s < 8 && rows * s < ctas && vocab / (2 * s) >= least)
+    while (s < 8 && rows * s * 2 <= ctas && vocab / (2 * s) >= least)
         s *= 2;
     return s;
 }
@@ -1055,7 +1055,7 @@ template <typename T> ecc_status logprob_grad_launch(const LogprobGradParams &p,
     const int sms = sm_count();
     if (sms <= 0)
         return ECC_ERR_CUDA;
-    const uint32_t split = row_split(p.rows, p.vocab, 8ull * sms, 4096);
+    const uint32_t split = row_split(p.rows, p.vocab, 16ull * sms, 4096);
     if (p.rows >= (1ull << 31) / split)
         return ECC_ERR_ARG;
     cudaLaunchAttribute at;
