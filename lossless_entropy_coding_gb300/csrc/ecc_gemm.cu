@@ -61,36 +61,51 @@ template <uint32_t ACT, int W> __device__ __forceinline__ void activate(float (&
     }
 }
 
+// W rows of a column, the first n of them in range.  The rows' addresses are
+// the same for the whole warp (uniform registers); a lane adds its column.
 template <typename T, int W>
-__device__ __forceinline__ void store_rows(void *base, uint64_t ld, uint64_t at, uint32_t n, const float (&a)[W], float s)
+__device__ __forceinline__ void store_rows(void *base, uint64_t ld, uint64_t r0, uint32_t n, uint32_t c, const float (&a)[W],
+                                           float s)
 {
-    T *p = static_cast<T *>(base) + at;
+    T *row = static_cast<T *>(base) + r0 * ld;
+    if (n == W) {
 #pragma unroll
-    for (int j = 0; j < W; ++j, p += ld)
-        if (j < n)
-            *p = from_f32<T>(a[j] * s);
+        for (int j = 0; j < W; ++j, row += ld)
+            row[c] = from_f32<T>(sizeof(T) == 1 ? a[j] * s : a[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j, row += ld)
+            if (j < n)
+                row[c] = from_f32<T>(sizeof(T) == 1 ? a[j] * s : a[j]);
+    }
 }
 // The residual of W rows of a column, as it is stored: asked for before the
 // products are waited for (with the loads after them a 8192 x 16384 x 4096
 // product took 906 us instead of 560).
 template <typename T, int W>
-__device__ __forceinline__ void load_rows(const void *base, uint64_t ld, uint64_t at, uint32_t n, uint32_t (&v)[W])
+__device__ __forceinline__ void load_rows(const void *base, uint64_t ld, uint64_t r0, uint32_t n, uint32_t c, uint32_t (&v)[W])
 {
-    const T *p = static_cast<const T *>(base) + at;
+    const T *row = static_cast<const T *>(base) + r0 * ld;
+    if (n == W) {
 #pragma unroll
-    for (int j = 0; j < W; ++j, p += ld)
-        if (j < n)
-            v[j] = *p;
+        for (int j = 0; j < W; ++j, row += ld)
+            v[j] = row[c];
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j, row += ld)
+            if (j < n)
+                v[j] = row[c];
+    }
 }
 template <int W>
-__device__ __forceinline__ void ask_residual(const Epilogue &e, uint32_t (&v)[W], uint64_t r0, uint32_t n, uint64_t c)
+__device__ __forceinline__ void ask_residual(const Epilogue &e, uint32_t (&v)[W], uint64_t r0, uint32_t n, uint32_t c)
 {
     if (!e.residual)
         return;
     if (e.res_type == ECC_F32)
-        load_rows<uint32_t>(e.residual, e.ldres, r0 * e.ldres + c, n, v);
+        load_rows<uint32_t>(e.residual, e.ldres, r0, n, c, v);
     else
-        load_rows<uint16_t>(e.residual, e.ldres, r0 * e.ldres + c, n, v);
+        load_rows<uint16_t>(e.residual, e.ldres, r0, n, c, v);
 }
 template <int W> __device__ __forceinline__ void add_residual(uint32_t type, const uint32_t (&v)[W], float (&a)[W])
 {
@@ -112,19 +127,18 @@ template <int W> __device__ __forceinline__ void add_residual(uint32_t type, con
 // W rows from row `r0` (the first n of them in range) of this thread's column c
 template <int W>
 __device__ __forceinline__ void finish(const Epilogue &e, float (&a)[W], const uint32_t (&res)[W], uint64_t r0, uint32_t n,
-                                       uint64_t c, float bias)
+                                       uint32_t c, float bias)
 {
 #pragma unroll
     for (int j = 0; j < W; ++j)
         a[j] = a[j] * e.scale + bias;
     if (e.pre) {
-        const uint64_t at = r0 * e.ldpre + c;
         if (e.pre_type == ECC_F32)
-            store_rows<float>(e.pre, e.ldpre, at, n, a, 1.f);
+            store_rows<float>(e.pre, e.ldpre, r0, n, c, a, 1.f);
         else if (e.pre_type == ECC_BF16)
-            store_rows<bf16>(e.pre, e.ldpre, at, n, a, 1.f);
+            store_rows<bf16>(e.pre, e.ldpre, r0, n, c, a, 1.f);
         else
-            store_rows<__half>(e.pre, e.ldpre, at, n, a, 1.f);
+            store_rows<__half>(e.pre, e.ldpre, r0, n, c, a, 1.f);
     }
     if (e.act == ECC_ACT_RELU)
         activate<ECC_ACT_RELU>(a);
@@ -136,15 +150,14 @@ __device__ __forceinline__ void finish(const Epilogue &e, float (&a)[W], const u
         activate<ECC_ACT_SILU>(a);
     if (e.residual)
         add_residual(e.res_type, res, a);
-    const uint64_t at = r0 * e.ldout + c;
     if (e.out_type == ECC_F32)
-        store_rows<float>(e.out, e.ldout, at, n, a, 1.f);
+        store_rows<float>(e.out, e.ldout, r0, n, c, a, 1.f);
     else if (e.out_type == ECC_BF16)
-        store_rows<bf16>(e.out, e.ldout, at, n, a, 1.f);
+        store_rows<bf16>(e.out, e.ldout, r0, n, c, a, 1.f);
     else if (e.out_type == ECC_F16)
-        store_rows<__half>(e.out, e.ldout, at, n, a, 1.f);
+        store_rows<__half>(e.out, e.ldout, r0, n, c, a, 1.f);
     else
-        store_rows<e4m3>(e.out, e.ldout, at, n, a, e.out_scale);
+        store_rows<e4m3>(e.out, e.ldout, r0, n, c, a, e.out_scale);
 }
 
 // This CTA's part of a tile, [column of tensor memory][lane], for the join.
@@ -157,7 +170,7 @@ template <int W> __device__ __forceinline__ void keep_part(float *parts, const f
 // Share `share` of a tile's rows [r0, ...): the sum of the g.split CTAs'
 // parts, eight rows at a time so that their loads are in flight together,
 // then the epilogue.  `at`: this lane's first value in its CTA's part.
-__device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint32_t share, uint64_t r0, uint64_t c)
+__device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint32_t share, uint64_t r0, uint32_t c)
 {
     const uint32_t n = (uint32_t)min((uint64_t)g.bn, g.rows - r0), per = (n + g.split - 1) / g.split;
     const uint32_t j0 = share * per, j1 = min(n, j0 + per);
@@ -334,7 +347,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint32_t acc = 0, aph = 0;
         for (uint32_t t = pair; t < tiles; t += pairs) {
             const TilePos pos = tile_pos(t, g.ptiles, g.qtiles);
-            const uint64_t c = (uint64_t)pos.p * 2 * kPTile + rank * kPTile + quad * 32 + lane, r0 = (uint64_t)pos.q * g.bn;
+            const uint32_t c = pos.p * 2 * kPTile + rank * kPTile + quad * 32 + lane;
+            const uint64_t r0 = (uint64_t)pos.q * g.bn;
             const bool col_ok = c < g.cols;
             const float bias = g.e.bias && col_ok ? load_any(g.e.bias, c, g.e.bias_type) : 0.f;
             const uint64_t left = g.rows - r0;
@@ -385,7 +399,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------- clusters that share a tile's reduction
 // `wait` waits for the products (the first residual is asked for before)
 template <int W, typename Wait>
-__device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, uint32_t quad, uint32_t lane, uint64_t c,
+__device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, uint32_t quad, uint32_t lane, uint32_t c,
                                               uint64_t r0, bool col_ok, float bias, bool direct, float *part, Wait wait)
 {
     const uint64_t left = g.rows - r0;
@@ -454,7 +468,7 @@ __device__ __forceinline__ void split_tile(const CUtensorMap &pmap, const CUtens
     begin(g);
 
     const uint32_t quad = warp & 3;
-    const uint64_t c = p0 + quad * 32 + lane;
+    const uint32_t c = (uint32_t)p0 + quad * 32 + lane;
     const bool col_ok = c < g.cols;
     float bias = 0.f;
     bool ok = true;
