@@ -169,8 +169,9 @@ template <int W> __device__ __forceinline__ void keep_part(float *parts, const f
 }
 // Share `share` of a tile's rows [r0, ...): the sum of the g.split CTAs'
 // parts, eight rows at a time so that their loads are in flight together,
-// then the epilogue.  `at`: this lane's first value in its CTA's part.
-__device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint32_t share, uint64_t r0, uint32_t c)
+// then the epilogue.  `at`: this lane's first value in its CTA's part;
+// `base`: the cluster's rank of the first of those CTAs.
+__device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint32_t base, uint32_t share, uint64_t r0, uint32_t c)
 {
     const uint32_t n = (uint32_t)min((uint64_t)g.bn, g.rows - r0), per = (n + g.split - 1) / g.split;
     const uint32_t j0 = share * per, j1 = min(n, j0 + per);
@@ -182,7 +183,7 @@ __device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint3
         uint32_t res[8];
         ask_residual(g.e, res, r0 + j, min(8u, j1 - j), c);
         for (uint32_t k = 0; k < g.split; ++k) {
-            const uint32_t from = cluster_addr(at + j * kPTile * 4, k);
+            const uint32_t from = cluster_addr(at + j * kPTile * 4, base + k);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (j + i < j1)
@@ -435,11 +436,20 @@ template <bool PMN, bool QMN, bool F8>
 __device__ __forceinline__ void split_tile(const CUtensorMap &pmap, const CUtensorMap &qmap, const GemmArgs &g, uint32_t block,
                                            uint8_t *smem_raw, GemmBars &s)
 {
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = g.split > 1 ? cluster_rank() : 0;
+    // the CTAs that share a tile are g.split neighbours of the cluster, `base` the first of them
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, crank = cluster_rank();
+    const uint32_t rank = crank & (g.split - 1), base = crank - rank;
     const uint32_t off = (kSmemHead - (smem_u32(smem_raw) & (kSmemHead - 1))) & (kSmemHead - 1);
     const uint32_t stage0 = smem_u32(smem_raw) + off;
     const uint32_t stage_bytes = kPBytes + g.bn * kTileBytes;
     const uint32_t tile = block / g.split;
+    if (tile >= g.ptiles * g.qtiles) { // fills up the last cluster
+        if (g.split > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
     const uint64_t p0 = (uint64_t)(tile % g.ptiles) * kPTile, q0 = (uint64_t)(tile / g.ptiles) * g.bn;
     const uint32_t kb0 = (uint32_t)((uint64_t)g.kblocks * rank / g.split);
     const uint32_t kb1 = (uint32_t)((uint64_t)g.kblocks * (rank + 1) / g.split);
@@ -542,7 +552,7 @@ __device__ __forceinline__ void split_tile(const CUtensorMap &pmap, const CUtens
     if (g.split > 1) {
         cluster_sync(); // all parts are written
         if (warp >= 2)
-            join_parts(g, stage0 + (quad * 32 + lane) * 4, rank, q0, c);
+            join_parts(g, stage0 + (quad * 32 + lane) * 4, base, rank, q0, c);
         __syncwarp();
         cluster_sync(); // nobody reads this CTA's part any more
     } else {
@@ -790,25 +800,26 @@ ecc_status gemm_backward(const Product &dx, const Product &dw, uint32_t type, ui
     Shape s1 = shape_of(dx, type, sms), s2 = shape_of(dw, type, sms);
     // in one launch where neither fills the GPU by itself and both fit it, two CTAs an SM
     const uint64_t t1 = up(dx.cols, kPTile) * up(dx.rows, s1.bn), t2 = up(dw.cols, kPTile) * up(dw.rows, s2.bn);
-    uint32_t split = std::min(s1.split, s2.split);
-    while (split > 1 && (t1 + t2) * split > 2ull * sms)
-        split /= 2;
-    if (s1.pair || s2.pair || !dx.K || !dw.K || (t1 + t2) * split > 2ull * sms) {
-        const ecc_status rc = gemm(dx, type, status, clear_status, behind, st);
+    while (t1 * s1.split + t2 * s2.split > 2ull * sms && (s1.split > 1 || s2.split > 1)) {
+        uint32_t &s = t1 * s1.split > t2 * s2.split ? (s1.split > 1 ? s1.split : s2.split) : (s2.split > 1 ? s2.split : s1.split);
+        s /= 2;
+    }
+    if (s1.pair || s2.pair || !dx.K || !dw.K || t1 * s1.split + t2 * s2.split > 2ull * sms) {
+        const ecc_status rc = gemm(dx, type, status, clear_status, behind, st); // (each in its own shape)
         return rc == ECC_OK ? gemm(dw, type, status, false, true, st) : rc;
     }
-    s1.split = s2.split = split;
     Plan a, b;
     ecc_status rc = make_plan(a, dx, s1, type, status, clear_status);
     if (rc == ECC_OK)
         rc = make_plan(b, dw, s2, type, status, false);
     if (rc != ECC_OK)
         return rc;
-    uint32_t n1 = a.tiles() * split;
-    const uint32_t ctas = n1 + b.tiles() * split;
+    const uint32_t cluster = std::max(s1.split, s2.split);
+    uint32_t n1 = (uint32_t)up(a.tiles() * s1.split, cluster) * cluster;
+    const uint32_t ctas = n1 + (uint32_t)up(b.tiles() * s2.split, cluster) * cluster;
     const size_t m1 = stage_memory(a, ctas, sms), m2 = stage_memory(b, ctas, sms);
     void *args[] = {&a.pm, &a.qm, &a.g, &b.pm, &b.qm, &b.g, &n1};
-    return launch_plan((const void *)gemm_both_kernel, kSplitThreads, ctas, split, std::max(m1, m2), args, behind, st);
+    return launch_plan((const void *)gemm_both_kernel, kSplitThreads, ctas, cluster, std::max(m1, m2), args, behind, st);
 }
 
 } // namespace ecc
