@@ -142,6 +142,42 @@ template <> __device__ __forceinline__ uint4 pack2<__half>(const float2 *f)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 16 bytes at p, on any boundary of an element: the two aligned vectors around
+// them, shifted together.  Only vectors that lie inside [begin, end), the
+// bytes of the whole array, are read; where one does not, single elements.
+template <typename T>
+__device__ __forceinline__ uint4 load_anywhere(const T *p, const void *begin, const void *end)
+{
+    const uintptr_t at = (uintptr_t)p, low = at & ~(uintptr_t)15;
+    const uint32_t off = (uint32_t)(at - low);
+    if (off == 0)
+        return *reinterpret_cast<const uint4 *>(p);
+    if (low < (uintptr_t)begin || low + 32 > (uintptr_t)end) {
+        struct alignas(16) {
+            T v[16 / sizeof(T)];
+        } t;
+#pragma unroll
+        for (int k = 0; k < (int)(16 / sizeof(T)); ++k)
+            t.v[k] = p[k];
+        return *reinterpret_cast<const uint4 *>(&t);
+    }
+    const uint4 a = *reinterpret_cast<const uint4 *>(low), b = *reinterpret_cast<const uint4 *>(low + 16);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (off & 8) {
+#pragma unroll
+        for (int k = 0; k < 6; ++k)
+            w[k] = w[k + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k)
+            w[k] = w[k + 1];
+    }
+    const uint32_t s = (off & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll

@@ -980,23 +980,48 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads) logprob_grad
                 const float f = to_f32(x[i]);
                 d[i] = from_f32<T>((uint64_t)row.tok == i ? row.token_value(f) : row.value(f));
             }
-    } else { // a value a thread
-        const uint64_t e0 = p.vocab * part / split, e1 = p.vocab * (part + 1) / split;
-        for (uint64_t i0 = e0 + tid; i0 < e1; i0 += 8 * kLpThreads) {
-            T q[8];
+    } else { // the gradient's vectors begin elsewhere: the logits are read across boundaries
+        const RowView<T> out_view(d, p.vocab);
+        const uint32_t v0 = (uint64_t)out_view.vecs * part / split, v1 = (uint64_t)out_view.vecs * (part + 1) / split;
+        uint4 *out = reinterpret_cast<uint4 *>(d + out_view.head);
+        const T *from = x + out_view.head;
+        const void *begin = p.logits, *end = static_cast<const T *>(p.logits) + (p.rows - 1) * p.ld + p.vocab;
+        const uint64_t tv = row.tok >= (int64_t)out_view.head ? (uint64_t)(row.tok - out_view.head) / V : ~0ull;
+        for (uint32_t i0 = v0 + tid; i0 < v1; i0 += 2 * kLpThreads) {
+            uint4 q[2];
 #pragma unroll
-            for (uint32_t u = 0; u < 8; ++u)
-                if (i0 + u * kLpThreads < e1)
-                    q[u] = x[i0 + u * kLpThreads];
+            for (uint32_t u = 0; u < 2; ++u)
+                if (i0 + u * kLpThreads < v1)
+                    q[u] = load_anywhere(from + (uint64_t)(i0 + u * kLpThreads) * V, begin, end);
 #pragma unroll
-            for (uint32_t u = 0; u < 8; ++u) {
-                const uint64_t i = i0 + u * kLpThreads;
-                if (i < e1) {
-                    const float f = to_f32(q[u]);
-                    d[i] = from_f32<T>((uint64_t)row.tok == i ? row.token_value(f) : row.value(f));
+            for (uint32_t u = 0; u < 2; ++u) {
+                const uint32_t i = i0 + u * kLpThreads;
+                if (i < v1) {
+                    float2 f[V / 2], o[V / 2];
+                    unpack2<T>(q[u], f);
+#pragma unroll
+                    for (uint32_t k = 0; k < V / 2; ++k)
+                        o[k] = row.value2(f[k]);
+                    if (i == tv) {
+                        const uint32_t at = (uint32_t)(row.tok - out_view.head) % V;
+#pragma unroll
+                        for (uint32_t k = 0; k < V / 2; ++k) {
+                            if (at == 2 * k)
+                                o[k].x = row.token_value(f[k].x);
+                            if (at == 2 * k + 1)
+                                o[k].y = row.token_value(f[k].y);
+                        }
+                    }
+                    st_stream16(out + i, pack2<T>(o));
                 }
             }
         }
+        if (part == 0)
+            for (uint32_t k = tid; k < out_view.head + out_view.tail; k += kLpThreads) {
+                const uint32_t i = out_view.single(k);
+                const float f = to_f32(x[i]);
+                d[i] = from_f32<T>((uint64_t)row.tok == i ? row.token_value(f) : row.value(f));
+            }
     }
 }
 

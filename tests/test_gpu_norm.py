@@ -70,6 +70,28 @@ def test_norm_shapes(rows, cols, dtype):
     check_norm(x, None, None, 1e-5, dtype)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,cols", [(2101, 513), (700, 1537), (300, 5003), (270, 4099), (150, 8190), (2500, 1024),
+                                       (2501, 256), (2600, 97), (2437, 4096), (2433, 2040)])
+def test_norm_many_rows(rows, cols, dtype):
+    """Enough rows for the kernels that several rows, or rows on any boundary, go through."""
+    gen = torch.Generator("cuda").manual_seed(rows + cols)
+    w, b = rows_of(gen, 1, cols + 3, dtype)[0], rows_of(gen, 1, cols + 1, dtype)[0]
+    for pad, off in ((0, 0), (5, 3), (8, 1), (3, 0)):
+        x = rows_of(gen, rows, cols, dtype, pad, off)
+        check_norm(x, w[:cols], b[1:], 1e-5, dtype)          # parameters on any boundary too
+        check_norm(x, w[3:].float(), None, 1e-5, E4M3, 16.0)
+        out = torch.empty_strided((rows, cols), (cols + 7, 1), dtype=dtype, device="cuda")
+        check_norm(x, None, b[:cols], 1e-5, dtype, out=out)
+        # in place: the bits of a call that writes rows of the same layout elsewhere
+        base = torch.empty(rows * (cols + pad) + 8, dtype=dtype, device="cuda")
+        y = base[:rows * (cols + pad)].view(rows, cols + pad)[:, :cols].copy_(x)
+        other = torch.empty_like(base)[:rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+        ecc.ecc_layer_norm(y, out=other)
+        ecc.ecc_layer_norm(y, out=y)
+        assert torch.equal(y, other)
+
+
 def test_norm_large_mean_constant_rows_and_eps():
     gen = torch.Generator("cuda").manual_seed(5)
     x = rows_of(gen, 64, 1536, F32, mean=1000.0)   # a one-pass variance would lose all digits here
