@@ -135,11 +135,14 @@ template <typename T> __global__ void __launch_bounds__(kNormThreads) norm_dw_ro
     p.part[(p.parts + blockIdx.y) * p.cols + c] = b;
 }
 
-// a block: 32 columns, the parts in eight shares
-__global__ void __launch_bounds__(kNormThreads) norm_parts_kernel(const float *part, uint32_t parts, uint64_t cols,
-                                                                  float *dweight, float *dbias)
+// A block: 32 columns, the parts in 16 shares, a thread's loads all under way
+// at once (in eight shares, four at a time, and with a single group's sums
+// through shared memory, 16384 x 4096 took 4 us more).
+__global__ void __launch_bounds__(512) norm_parts_kernel(const float *part, uint32_t parts, uint64_t cols, float *dweight,
+                                                         float *dbias)
 {
-    __shared__ float sums[8][33];
+    constexpr uint32_t AHEAD = 10; // (of 16 shares of 152 parts)
+    __shared__ float sums[16][33];
     wait_for_previous();
     const uint32_t tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const uint64_t c = (uint64_t)blockIdx.x * 32 + tx;
@@ -149,14 +152,20 @@ __global__ void __launch_bounds__(kNormThreads) norm_parts_kernel(const float *p
     part += (uint64_t)blockIdx.y * parts * cols;
     float s = 0.f;
     if (c < cols)
-#pragma unroll 4
-        for (uint32_t k = ty; k < parts; k += 8)
-            s += part[k * cols + c];
+        for (uint32_t k0 = ty; k0 < parts; k0 += 16 * AHEAD) {
+            float v[AHEAD];
+#pragma unroll
+            for (uint32_t k = 0; k < AHEAD; ++k)
+                v[k] = k0 + 16 * k < parts ? part[(uint64_t)(k0 + 16 * k) * cols + c] : 0.f;
+#pragma unroll
+            for (uint32_t k = 0; k < AHEAD; ++k)
+                s += v[k];
+        }
     sums[ty][tx] = s;
     __syncthreads();
     if (ty || c >= cols)
         return;
-    for (int k = 1; k < 8; ++k)
+    for (int k = 1; k < 16; ++k)
         s += sums[k][tx];
     out[c] = s;
 }
@@ -251,6 +260,26 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t at)
     uint4 q;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
     return q;
+}
+__device__ __forceinline__ void store_shared16(uint32_t at, const uint4 &v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+template <typename T> __device__ __forceinline__ void store_shared(uint32_t at, T v) // of 2 or 4 bytes
+{
+    if constexpr (sizeof(T) == 2)
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<uint16_t *>(&v)) : "memory");
+    else
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<uint32_t *>(&v)) : "memory");
+}
+template <typename T> __device__ __forceinline__ T load_shared(uint32_t at)
+{
+    T v;
+    if constexpr (sizeof(T) == 2)
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(*reinterpret_cast<uint16_t *>(&v)) : "r"(at) : "memory");
+    else
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(*reinterpret_cast<uint32_t *>(&v)) : "r"(at) : "memory");
+    return v;
 }
 
 // ROWS rows by `warps` warps: they are read once and both passes over them
@@ -547,24 +576,102 @@ __device__ __forceinline__ void group_sums(float (&v)[2 * ROWS], float (*part)[2
         v[i] = __shfl_sync(~0u, s, i * SPAN);
 }
 
+// The compiler takes v as new: what it computed from v before is not kept, but computed again.
+__device__ __forceinline__ void forget(uint4 &v)
+{
+    asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
+}
+// A row at any boundary of an element into a slot of 16-byte pieces: piece v
+// holds the v-th aligned 16 bytes from the one with the row's first value on.
+// A thread copies the pieces t + k width for k < PER, the first thread one
+// more.  (Those of a row at the array's ends may stick out of it: they are
+// copied by element.)
+template <typename T, int PER>
+__device__ __forceinline__ void fetch_row(uint32_t slot, uint32_t t, uint32_t width, const T *row, uint32_t cols,
+                                          const T *begin, const T *end)
+{
+    const uintptr_t low = (uintptr_t)row & ~(uintptr_t)15;
+    const uint32_t bytes = ((uint32_t)(uintptr_t)row & 15) + cols * (uint32_t)sizeof(T);
+    const bool inside = low >= (uintptr_t)begin && low + ((bytes + 15) & ~15u) <= (uintptr_t)end;
+#pragma unroll
+    for (int k = 0; k <= PER; ++k) {
+        const uint32_t v = t + k * width;
+        if (v * 16 >= bytes || (k == PER && t))
+            return;
+        if (inside) {
+            copy_async16(slot + v * 16, reinterpret_cast<const void *>(low + v * 16));
+            continue;
+        }
+        const T *q = reinterpret_cast<const T *>(low + v * 16);
+        for (uint32_t i = 0; i < 16 / sizeof(T); ++i)
+            if (q + i >= begin && q + i < end)
+                store_shared(slot + v * 16 + i * (uint32_t)sizeof(T), q[i]);
+    }
+}
+// the row's v-th vector, 0 past its end
+template <typename T>
+__device__ __forceinline__ uint4 read_piece(uint32_t slot, uint32_t v, uint32_t off, uint32_t cols)
+{
+    constexpr uint32_t V = 16 / sizeof(T);
+    uint4 a = load_shared16(slot + v * 16);
+    if (off)
+        a = shift16<false>(a, load_shared16(slot + v * 16 + 16), off);
+    if (v * V + V > cols) {
+        const uint32_t left = cols > v * V ? (cols - v * V) * (uint32_t)sizeof(T) : 0; // bytes
+        uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            w[i] &= left >= 4 * i + 4 ? ~0u : left > 4 * i ? 0xffffu : 0u; // (two bytes of a word, or all)
+        a = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return a;
+}
+// A warp's 32 V values (vectors v, v + 1, ...) to their place at any boundary:
+// through its pieces of the slot, then vectors on the boundaries of the place
+// and, for the at most 2 (V - 1) values around them, a lane each.
+template <typename T, int V>
+__device__ __forceinline__ void write_pieces(uint32_t slot, uint32_t v, T *row, uint32_t cols, const float2 *f)
+{
+    const uint32_t lane = threadIdx.x & 31, first = (v - lane) * V, from = slot + (v - lane) * 16;
+    const uint32_t count = cols > first ? min(cols - first, 32u * V) : 0;
+    store_shared16(slot + v * 16, pack2<T>(f));
+    __syncwarp();
+    T *o = row + first;
+    const uint32_t head = min(((16 - ((uint32_t)(uintptr_t)o & 15)) & 15) / (uint32_t)sizeof(T), count);
+    const uint32_t full = (count - head) / V, tail = head + full * V;
+    if (lane < full) {
+        uint4 a = load_shared16(from + lane * 16);
+        if (head)
+            a = shift16<false>(a, load_shared16(from + lane * 16 + 16), head * (uint32_t)sizeof(T));
+        *reinterpret_cast<uint4 *>(o + head + lane * V) = a;
+    }
+    const uint32_t i = lane < head ? lane : tail + (lane - head);
+    if (i < count)
+        o[i] = load_shared<T>(from + i * (uint32_t)sizeof(T));
+}
+
 // Persistent, a block an SM: groups of `width` of its NT threads walk their
 // rows ROWS at a time; each thread keeps its columns' sums of dy * xh and dy
-// in registers, so x and dy are read once for all three gradients.  With
-// RING > 0 a thread copies its 16-byte pieces of the next RING - 1 steps
-// ahead into its own part of shared memory (nobody else reads it: no
-// barrier); otherwise (V = 1) it loads as it goes.  One barrier a step joins
-// the warps' sums.  The groups' column sums are added in shared memory and
+// in registers, so x and dy are read once for all three gradients.  A ring in
+// shared memory holds the next steps' rows.  On 16-byte boundaries a thread
+// copies what it will read itself, RING - 1 steps ahead, without a barrier.
+// SHIFT, rows on any boundary: the rows' aligned pieces, which neighbours read
+// too, are copied RING - 2 steps ahead, and the barrier that joins a step's
+// sums also publishes the next step's pieces; dx leaves through the pieces of
+// x just read.  (A value an access, 16384 x 4097 bf16 took 312 us, now 194:
+// the shifts' instructions; the aligned 16384 x 4096 71 us, 16384 x 8192 132,
+// 5.6 and 6.1 TB/s.)  The groups' column sums are added in shared memory and
 // the blocks' in norm_parts_kernel, both in a fixed order.  Bound by HBM.
-template <typename T, int NT, int V, int E, int RING, int ROWS>
+template <typename T, int NT, int E, int RING, int ROWS, bool SHIFT>
 __global__ void __launch_bounds__(NT, 1) norm_grad_kernel(NormGradParams p, uint32_t width)
 {
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ float part[2][NT / 32][2 * ROWS];
-    constexpr int PER = E / V;
+    constexpr int V = 16 / sizeof(T), PER = E / V;
     let_next_start();
     const uint32_t tid = threadIdx.x, group = tid / width, t = tid - group * width;
-    const uint32_t groups = NT / width, warp0 = group * (width / 32);
-    const uint32_t n = (uint32_t)(p.cols / V);
+    const uint32_t groups = NT / width, warp0 = group * (width / 32), cols = (uint32_t)p.cols;
+    const uint32_t n = (cols + V - 1) / V;
     const uint64_t step = (uint64_t)gridDim.x * groups * ROWS;
     const float inv = 1.f / (float)p.cols;
     float2 w[E / 2], aw[E / 2], ab[E / 2];
@@ -578,48 +685,66 @@ __global__ void __launch_bounds__(NT, 1) norm_grad_kernel(NormGradParams p, uint
     T *dx = static_cast<T *>(p.dx);
     if (works) {
         if (p.weight) {
-            if constexpr (V == 1) {
-                float q[E];
-                load_singles<T, E>(p.weight, p.p_type, t, width, n, 1.f, q);
 #pragma unroll
-                for (int k = 0; k < E / 2; ++k)
-                    w[k] = make_float2(q[2 * k], q[2 * k + 1]);
-            } else {
+            for (int k = 0; k < PER; ++k)
+                if (t + k * width < n) {
+                    float2 *q = w + k * V / 2;
+                    const uint32_t c = (t + k * width) * V;
+                    if constexpr (SHIFT) {
 #pragma unroll
-                for (int k = 0; k < PER; ++k)
-                    if (t + k * width < n) {
-                        float2 q[V / 2];
-                        load_params<T, V>(p.weight, t + k * width, p.p_type, q);
+                        for (int i = 0; i < V / 2; ++i) {
+                            q[i].x = c + 2 * i < cols ? load_any(p.weight, c + 2 * i, p.p_type) : 0.f;
+                            q[i].y = c + 2 * i + 1 < cols ? load_any(p.weight, c + 2 * i + 1, p.p_type) : 0.f;
+                        }
+                    } else {
+                        float2 u[V / 2];
+                        load_params<T, V>(p.weight, t + k * width, p.p_type, u);
 #pragma unroll
                         for (int i = 0; i < V / 2; ++i)
-                            w[k * V / 2 + i] = q[i];
+                            q[i] = u[i];
                     }
-            }
+                }
         }
         const uint64_t r0 = ((uint64_t)blockIdx.x * groups + group) * ROWS;
-        // piece i of a step (row, access, x or dy) at i * NT * 16
-        const uint32_t slots = smem_u32(raw) + tid * 16;
-        constexpr uint32_t pieces = ROWS * PER * 2;
+        // SHIFT: a row's slot holds one piece more than the group's threads read
+        const uint32_t row_bytes = SHIFT ? (PER * width + 1) * 16 : PER * width * 16;
+        const uint32_t ring0 = smem_u32(raw) + group * (2 * ROWS * RING) * row_bytes;
+        auto slot = [&](uint32_t at, int j) { return ring0 + (at * ROWS + j) * 2 * row_bytes; }; // x's row, then dy's
+        const T *x_end = x + (p.rows - 1) * p.ldx + p.cols, *dy_end = dy + (p.rows - 1) * p.lddy + p.cols;
         auto fetch = [&](uint64_t r, uint32_t at) {
-            if constexpr (RING > 0) {
 #pragma unroll
-                for (int j = 0; j < ROWS; ++j)
-                    if (r + j < p.rows) {
+            for (int j = 0; j < ROWS; ++j)
+                if (r + j < p.rows) {
+                    const uint32_t to = slot(at, j);
+                    const T *xr = x + (r + j) * p.ldx, *dyr = dy + (r + j) * p.lddy;
+                    if constexpr (SHIFT) {
+                        fetch_row<T, PER>(to, t, width, xr, cols, x, x_end);
+                        fetch_row<T, PER>(to + row_bytes, t, width, dyr, cols, dy, dy_end);
+                    } else {
 #pragma unroll
                         for (int k = 0; k < PER; ++k)
                             if (t + k * width < n) {
-                                const uint64_t c = (uint64_t)(t + k * width) * V;
-                                const uint32_t to = slots + (at * pieces + (j * PER + k) * 2) * NT * 16;
-                                copy_async16(to, x + (r + j) * p.ldx + c);
-                                copy_async16(to + NT * 16, dy + (r + j) * p.lddy + c);
+                                const uint32_t v = t + k * width;
+                                copy_async16(to + v * 16, xr + (uint64_t)v * V);
+                                copy_async16(to + row_bytes + v * 16, dyr + (uint64_t)v * V);
                             }
                     }
-                copy_async_commit();
-            }
+                }
+            copy_async_commit();
+        };
+        auto publish = [&] { // the pieces copied so far to the group
+            if (width == 32)
+                __syncwarp();
+            else
+                group_barrier(group, width);
         };
 #pragma unroll
         for (int k = 0; k + 1 < RING; ++k)
             fetch(r0 + k * step, k);
+        if constexpr (SHIFT) {
+            copy_async_wait<RING - 2>();
+            publish();
+        }
         uint32_t at = 0, flip = 0;
         float mean[ROWS], rstd[ROWS];
         auto stats = [&](uint64_t r) {
@@ -631,92 +756,126 @@ __global__ void __launch_bounds__(NT, 1) norm_grad_kernel(NormGradParams p, uint
         };
         stats(r0);
         for (uint64_t r = r0; r < p.rows; r += step) {
-            if constexpr (RING > 0) {
-                fetch(r + (RING - 1) * step, at ? at - 1 : RING - 1);
+            fetch(r + (RING - 1) * step, at ? at - 1 : RING - 1);
+            if constexpr (!SHIFT)
                 copy_async_wait<RING - 1>();
-            }
-            float2 g[ROWS][E / 2], xh[ROWS][E / 2];
-            float v[2 * ROWS], rs[ROWS];
+            // the pieces stay as read: as float32 values they would take twice
+            // the registers, and half the rows in flight
+            uint4 rx[ROWS][PER], rd[ROWS][PER];
+            float2 minus[ROWS], r2[ROWS];
+            float v[2 * ROWS];
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
-                if constexpr (RING > 0) {
-#pragma unroll
-                    for (int k = 0; k < PER; ++k) {
-                        const uint32_t s0 = slots + (at * pieces + (j * PER + k) * 2) * NT * 16;
-                        const bool in = r + j < p.rows && t + k * width < n;
-                        const uint4 zero = make_uint4(0, 0, 0, 0);
-                        unpack2<T>(in ? load_shared16(s0) : zero, xh[j] + k * V / 2);
-                        unpack2<T>(in ? load_shared16(s0 + NT * 16) : zero, g[j] + k * V / 2);
-                    }
-                } else {
-                    const uint32_t m = r + j < p.rows ? n : 0;
-                    load_row<T, V, E>(x + (r + j) * p.ldx, t, width, m, xh[j]);
-                    load_row<T, V, E>(dy + (r + j) * p.lddy, t, width, m, g[j]);
-                }
-                const float2 minus = both(-mean[j]), r2 = both(rstd[j]);
+                minus[j] = both(-mean[j]);
+                r2[j] = both(rstd[j]);
                 float2 s = both(0.f), q = both(0.f);
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i) {
-                    const float2 d = g[j][i];
-                    xh[j][i] = mul2(add2(xh[j][i], minus), r2);
-                    g[j][i] = mul2(d, w[i]);
-                    s = add2(s, g[j][i]);
-                    q = fma2(g[j][i], xh[j][i], q);
-                    aw[i] = fma2(d, xh[j][i], aw[i]);
-                    ab[i] = add2(ab[i], d);
+                for (int k = 0; k < PER; ++k) {
+                    const uint32_t s0 = slot(at, j), u = t + k * width;
+                    if constexpr (SHIFT) {
+                        const uint32_t m = r + j < p.rows ? cols : 0;
+                        rx[j][k] = read_piece<T>(s0, u, (uint32_t)(uintptr_t)(x + (r + j) * p.ldx) & 15, m);
+                        rd[j][k] = read_piece<T>(s0 + row_bytes, u, (uint32_t)(uintptr_t)(dy + (r + j) * p.lddy) & 15, m);
+                    } else {
+                        const bool in = r + j < p.rows && u < n;
+                        const uint4 zero = make_uint4(0, 0, 0, 0);
+                        rx[j][k] = in ? load_shared16(s0 + u * 16) : zero;
+                        rd[j][k] = in ? load_shared16(s0 + row_bytes + u * 16) : zero;
+                    }
+                    float2 xh[V / 2], d[V / 2];
+                    unpack2<T>(rx[j][k], xh);
+                    unpack2<T>(rd[j][k], d);
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        const int c = k * V / 2 + i;
+                        xh[i] = mul2(add2(xh[i], minus[j]), r2[j]);
+                        const float2 g = mul2(d[i], w[c]);
+                        s = add2(s, g);
+                        q = fma2(g, xh[i], q);
+                        aw[c] = fma2(d[i], xh[i], aw[c]);
+                        ab[c] = add2(ab[c], d[i]);
+                    }
                 }
                 v[2 * j] = s.x + s.y;
                 v[2 * j + 1] = q.x + q.y;
-                rs[j] = rstd[j];
             }
             stats(r + step); // a step ahead: they would be waited for
+            if constexpr (SHIFT) {
+                copy_async_wait<RING - 2>();
+                if (!p.dx || width == 32)
+                    publish(); // (else the sums' barrier does it)
+            }
             if (p.dx) {
                 group_sums<ROWS>(v, part[flip], group, width, warp0);
                 flip ^= 1;
 #pragma unroll
                 for (int j = 0; j < ROWS; ++j)
                     if (r + j < p.rows) {
-                        const float2 s = both(-v[2 * j] * inv), q = both(-v[2 * j + 1] * inv), r2 = both(rs[j]);
+                        const float2 s = both(-v[2 * j] * inv), q = both(-v[2 * j + 1] * inv);
                         T *o = dx + (r + j) * p.lddx;
 #pragma unroll
-                        for (int i = 0; i < E / 2; ++i)
-                            g[j][i] = mul2(fma2(xh[j][i], q, add2(g[j][i], s)), r2);
+                        for (int k = 0; k < PER; ++k) {
+                            const uint32_t u = t + k * width;
+                            float2 xh[V / 2], g[V / 2];
+                            forget(rx[j][k]);
+                            forget(rd[j][k]);
+                            unpack2<T>(rx[j][k], xh);
+                            unpack2<T>(rd[j][k], g);
 #pragma unroll
-                        for (int k = 0; k < PER; ++k)
-                            if (t + k * width < n) {
-                                if constexpr (V == 1)
-                                    o[t + k * width] = from_f32<T>(k & 1 ? g[j][k / 2].y : g[j][k / 2].x);
-                                else
-                                    store_values<T, V>(o + (uint64_t)(t + k * width) * V, g[j] + k * V / 2);
+                            for (int i = 0; i < V / 2; ++i) {
+                                xh[i] = mul2(add2(xh[i], minus[j]), r2[j]);
+                                g[i] = mul2(fma2(xh[i], q, add2(mul2(g[i], w[k * V / 2 + i]), s)), r2[j]);
                             }
+                            if (SHIFT && (cols % V || ((uintptr_t)o & 15)))
+                                write_pieces<T, V>(slot(at, j), u, o, cols, g);
+                            else if (u < n)
+                                store_values<T, V>(o + (uint64_t)u * V, g);
+                        }
                     }
+                if constexpr (SHIFT)
+                    __syncwarp(); // before the pieces are filled again
             }
             at = at + 1 == RING ? 0 : at + 1;
         }
-        if constexpr (RING > 0)
-            copy_async_wait<0>();
+        copy_async_wait<0>();
     }
     if (!p.part)
         return;
-    // the groups' sums, then their sum in the groups' order
+    // the groups' sums, then their sum in the groups' order; a single group's go straight out
     float *sums = reinterpret_cast<float *>(raw); // [groups][2][cols]
+    float *out_w = p.part + (uint64_t)blockIdx.x * p.cols, *out_b = p.part + (uint64_t)(p.parts + blockIdx.x) * p.cols;
     __syncthreads();
     if (works) {
-        float *mine = sums + (uint64_t)group * 2 * p.cols;
+        float *to_w = groups == 1 ? out_w : sums + (uint64_t)group * 2 * p.cols, *to_b = groups == 1 ? out_b : to_w + p.cols;
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (t + (i / V) * width < n) {
-                const uint32_t c = (t + (i / V) * width) * V + i % V;
-                mine[c] = i & 1 ? aw[i / 2].y : aw[i / 2].x;
-                mine[p.cols + c] = i & 1 ? ab[i / 2].y : ab[i / 2].x;
+        for (int k = 0; k < PER; ++k)
+            if (t + k * width < n) {
+                const uint32_t c = (t + k * width) * V;
+                const float2 *pw = aw + k * V / 2, *pb = ab + k * V / 2;
+                if constexpr (SHIFT) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (c + i < cols) {
+                            to_w[c + i] = i & 1 ? pw[i / 2].y : pw[i / 2].x;
+                            to_b[c + i] = i & 1 ? pb[i / 2].y : pb[i / 2].x;
+                        }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V / 2; i += 2) {
+                        *reinterpret_cast<float4 *>(to_w + c + 2 * i) = make_float4(pw[i].x, pw[i].y, pw[i + 1].x, pw[i + 1].y);
+                        *reinterpret_cast<float4 *>(to_b + c + 2 * i) = make_float4(pb[i].x, pb[i].y, pb[i + 1].x, pb[i + 1].y);
+                    }
+                }
             }
     }
+    if (groups == 1)
+        return;
     __syncthreads();
     for (uint32_t c = tid; c < 2 * p.cols; c += NT) {
         float s = 0.f;
         for (uint32_t k = 0; k < groups; ++k)
             s += sums[k * 2 * p.cols + c];
-        p.part[c < p.cols ? (uint64_t)blockIdx.x * p.cols + c : (uint64_t)(p.parts + blockIdx.x) * p.cols + (c - p.cols)] = s;
+        (c < p.cols ? out_w + c : out_b + (c - p.cols))[0] = s;
     }
 }
 
@@ -786,20 +945,41 @@ template <typename T> ecc_status norm_launch(const NormParams &p, uint32_t y_typ
     return y_type == ECC_E4M3 ? norm_launch_to<T, e4m3>(p, st) : norm_launch_to<T, T>(p, st);
 }
 
-template <typename T, int NT, int V, int E, int RING, int ROWS>
+template <typename T, int NT, int E, int RING, int ROWS, bool SHIFT>
 bool norm_grad_registers(NormGradParams &p, cudaStream_t st)
 {
-    const uint64_t n = p.cols / V, width = (n * V + E * 32 - 1) / (E * 32) * 32;
+    constexpr uint64_t V = 16 / sizeof(T);
+    const uint64_t width = (p.cols + E * 32 - 1) / (E * 32) * 32;
     if (width > NT)
         return false;
-    const size_t smem = std::max<size_t>((size_t)RING * ROWS * 2 * (E / V) * NT * 16, p.part ? NT / width * p.cols * 8 : 0);
-    const void *f = (const void *)norm_grad_kernel<T, NT, V, E, RING, ROWS>;
+    const uint64_t steps = (p.rows + ROWS - 1) / ROWS, groups = NT / width;
+    const size_t row = (width * (E / V) + SHIFT) * 16;
+    const size_t smem = std::max<size_t>(groups * RING * ROWS * 2 * row, p.part && groups > 1 ? groups * p.cols * 8 : 0);
+    const void *f = (const void *)norm_grad_kernel<T, NT, E, RING, ROWS, SHIFT>;
     if (smem > kMaxDynSmem - 2048 || occupancy(f, NT, smem) <= 0)
         return false;
-    const uint64_t steps = (p.rows + ROWS - 1) / ROWS, groups = NT / width;
     p.parts = (uint32_t)std::min<uint64_t>((steps + groups - 1) / groups, p.parts);
-    norm_grad_kernel<T, NT, V, E, RING, ROWS><<<p.parts, NT, smem, st>>>(p, (uint32_t)width);
+    norm_grad_kernel<T, NT, E, RING, ROWS, SHIFT><<<p.parts, NT, smem, st>>>(p, (uint32_t)width);
     return true;
+}
+
+// Values a thread.  float32: the fewest that let a block of 512 threads hold a
+// row (its threads' sums take 128 registers).  16-bit types, rows of up to
+// 4096: 8 values and 4 rows a step or 16 and 2, whichever leaves fewer threads
+// without columns (16384 x 2049: 113 us with 8, 82 with 16; 20000 x 514: 39
+// and 45); else 8 for few rows (2400 x 4096: 20.5 and 22.5 us; 16384 x 4096:
+// 73.6 and 71.4).  Longer ones: at last 1024 threads.
+template <typename T, bool SHIFT> bool norm_grad_any(NormGradParams &p, int sms, cudaStream_t st)
+{
+    if constexpr (sizeof(T) == 4)
+        return norm_grad_registers<T, 512, 8, 3, 2, SHIFT>(p, st) || norm_grad_registers<T, 512, 16, 3, 1, SHIFT>(p, st);
+    else {
+        auto groups = [&](uint64_t e) { return 512 / ((p.cols + e * 32 - 1) / (e * 32) * 32); };
+        const uint64_t g8 = 2 * groups(8), g16 = groups(16); // (in halves: a group of 16 values a thread covers twice the columns)
+        if ((g8 > g16 || (g8 == g16 && p.rows < 64ull * sms)) && norm_grad_registers<T, 512, 8, 3, 4, SHIFT>(p, st))
+            return true;
+        return norm_grad_registers<T, 512, 16, 3, 2, SHIFT>(p, st) || norm_grad_registers<T, 1024, 16, 3, 1, SHIFT>(p, st);
+    }
 }
 
 template <typename T> ecc_status norm_grad_launch(NormGradParams p, cudaStream_t st)
@@ -818,15 +998,7 @@ template <typename T> ecc_status norm_grad_launch(NormGradParams p, cudaStream_t
         const bool vec = p.cols % V == 0 && whole(p.x, p.ldx, sizeof(T)) && whole(p.dy, p.lddy, sizeof(T)) &&
                          (!p.dx || whole(p.dx, p.lddx, sizeof(T))) &&
                          (p.p_type != TypeCode<T>::value || whole(p.weight, 0, 1));
-        // the fewest values a thread that let a block of 512 threads hold a
-        // row (its threads' sums take 128 registers), at last 1024 threads
-        constexpr int ring = sizeof(T) == 4 ? 3 : 4;
-        if (vec)
-            done = norm_grad_registers<T, 512, V, 8, ring, 2>(p, st) || norm_grad_registers<T, 512, V, 16, ring, 1>(p, st) ||
-                   (sizeof(T) == 2 && norm_grad_registers<T, 1024, V, 16, 3, 1>(p, st));
-        else
-            done = norm_grad_registers<T, 512, 1, 8, 0, 2>(p, st) || norm_grad_registers<T, 512, 1, 16, 0, 1>(p, st) ||
-                   norm_grad_registers<T, 1024, 1, 16, 0, 1>(p, st);
+        done = vec ? norm_grad_any<T, false>(p, sms, st) : norm_grad_any<T, true>(p, sms, st);
     }
     if (!done) { // longer rows
         if (sums) // before dx, which may overwrite dy or x
@@ -839,9 +1011,9 @@ template <typename T> ecc_status norm_grad_launch(NormGradParams p, cudaStream_t
         return rc;
     const dim3 grid((unsigned)((p.cols + 31) / 32), 2);
     if (p.rows && done) // lets it start early
-        return launch_status(launch_behind(norm_parts_kernel, grid, kNormThreads, 0, st, (const float *)p.part, p.parts, p.cols,
+        return launch_status(launch_behind(norm_parts_kernel, grid, 512, 0, st, (const float *)p.part, p.parts, p.cols,
                                            p.dweight, p.dbias));
-    norm_parts_kernel<<<grid, kNormThreads, 0, st>>>(p.part, p.parts, p.cols, p.dweight, p.dbias);
+    norm_parts_kernel<<<grid, 512, 0, st>>>(p.part, p.parts, p.cols, p.dweight, p.dbias);
     return launch_status(cudaGetLastError());
 }
 

@@ -184,6 +184,33 @@ def test_norm_grad_shapes(rows, cols, dtype):
     check_grad(dy, x, w.float(), m, r)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,cols", [(2501, 513), (3001, 7), (2900, 256), (1301, 1537), (1503, 4099), (1100, 4096), (801, 8190),
+                                       (700, 9001), (650, 16000)])
+def test_norm_grad_many_rows(rows, cols, dtype):
+    """Several steps of every ring, rows on and off 16-byte boundaries, each
+    of the arrays on its own; dx in place, next to other rows' bytes."""
+    gen = torch.Generator("cuda").manual_seed(rows * 9 + cols)
+    for pad, off, dpad, doff in ((0, 0, 0, 0), (0, 0, 8, 0), (3, 1, 0, 0), (1, 3, 6, 5)):
+        x, dy = rows_of(gen, rows, cols, dtype, pad, off), rows_of(gen, rows, cols, dtype, dpad, doff)
+        w = rows_of(gen, 1, cols, dtype, 0, off)[0]
+        m, r = stats(x)
+        dx, dw, db = check_grad(dy, x, w, m, r)
+        rest = ecc.ecc_layer_norm_grad(dy, x, w, m, r)
+        assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), rest))
+        # in place: the padding stays, the rest are the bits of a call on the same layout
+        for into, ld in ((x, cols + pad), (dy, cols + dpad)):
+            base = torch.full((rows * ld + 8,), 7.0, dtype=dtype, device="cuda")
+            y = base[off if into is x else doff:][:rows * ld].view(rows, ld)[:, :cols].copy_(into)
+            args = (dy, y, w, m, r) if into is x else (y, x, w, m, r)
+            kept = ecc.ecc_layer_norm_grad(*args, dx=torch.empty_like(base)[off if into is x else doff:][:rows * ld]
+                                           .view(rows, ld)[:, :cols])
+            got = ecc.ecc_layer_norm_grad(*args, dx=y)
+            assert all(torch.equal(p, q) for p, q in zip(kept, got))
+            whole = base[off if into is x else doff:][:rows * ld].view(rows, ld)
+            assert bool((whole[:, cols:] == 7).all()) and bool((base[:off if into is x else doff] == 7).all())
+
+
 def test_norm_grad_in_place_and_empty():
     gen = torch.Generator("cuda").manual_seed(9)
     for cols in (1024, 40003):
