@@ -21,6 +21,8 @@
  *  - outputs never depend on the order in which blocks run: the same call on
  *    the same inputs gives the same bits;
  *  - an output may not overlap an input unless the entry says so;
+ *  - the elements between a row's end and the next row's start may be read
+ *    (their values change nothing); they are never written;
  *  - a count of zero rows is valid: nothing is read, sums over rows are zero.
  */
 #ifndef ECC_LM_H
