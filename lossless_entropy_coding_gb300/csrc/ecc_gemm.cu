@@ -653,7 +653,7 @@ struct Shape {
 // - a wave is one CTA an SM (two of the single ones share an SM's time), and
 //   the operands cannot arrive faster than HBM gives them;
 // - an epilogue, and joining a shared reduction.
-// So 1 x 16384 x 4096 takes 26.7 us in 16-row tiles (28 in 64-row ones), 128
+// So 8 x 16384 x 4096 takes 26.8 us in 16-row tiles (28 in 64-row ones), 128
 // x 4096 x 4096 15.5 us as 64-row tiles of four CTAs each (25 as pairs, 18 as
 // 64-row tiles of two), 1024 x 4096 x 4096 28.5 us as pairs (32 as 128-row
 // tiles).

@@ -4,7 +4,7 @@
 //
 // The products read their operands by TMA, which wants rows on 16-byte
 // boundaries: an operand with other rows is first copied to the workspace
-// with padded rows.
+// with padded rows.  Products of a few rows read theirs as they lie.
 
 #include <algorithm>
 #include <cmath>
@@ -164,6 +164,122 @@ template <typename T> __global__ void __launch_bounds__(kRowThreads) pad_rows_ke
     }
 }
 
+// ---------------------------------------------------------------- few rows
+constexpr int kFewColumns = 4;
+struct FewRows {
+    const void *x, *w;
+    uint64_t ldx, ldw, N, K;
+    uint32_t warps; // that share kFewColumns columns of the output
+    Epilogue e;
+    uint32_t *status;
+};
+template <typename T> __device__ __forceinline__ void unpack_all(const uint4 &q, float2 (&f)[8 / sizeof(T)])
+{
+    if constexpr (sizeof(T) == 2) {
+        unpack2<T>(q, f);
+    } else {
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[i / 2] >> (i & 1) * 16), __NV_E4M3);
+            f[i] = __half22float2(__half2(h));
+        }
+    }
+}
+// M rows of x by the rows of w, on any boundaries: the weights are read once,
+// as vectors shifted from the aligned ones around them, and multiplied as they
+// come.  A warp (or p.warps of them) takes four columns of the output, so that
+// they share the conversion of x; its lanes' sums are joined in a fixed order.
+// Bound by HBM for one token, 1 x 16384 x 4096 bf16 25.3 us, 5.3 TB/s (two
+// columns a warp 29.5, two vectors of four columns at a time 30.1); off
+// 16-byte boundaries by the shifts, 1 x 12616 x 14088 131 us, 2.7 TB/s; with
+// more rows by the multiplications, M of them a weight.
+template <typename T, int M>
+__global__ void __launch_bounds__(kRowThreads) few_rows_kernel(const __grid_constant__ FewRows p)
+{
+    constexpr int R = kFewColumns, V = 16 / sizeof(T), H = V / 2, OUT = R * M;
+    __shared__ float sums[8][OUT];
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *p.status = ECC_OK;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / p.warps, part = warp % p.warps;
+    const uint64_t n0 = ((uint64_t)blockIdx.x * (8 / p.warps) + group) * R;
+    const T *x = static_cast<const T *>(p.x), *w = static_cast<const T *>(p.w);
+    const T *x_end = x + (M - 1) * p.ldx + p.K, *w_end = w + (p.N - 1) * p.ldw + p.K;
+    const T *wr[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        wr[r] = w + min(n0 + r, p.N - 1) * p.ldw;
+    float2 acc[R][M];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            acc[r][m] = both(0.f);
+    const uint64_t vecs = p.K / V, step = (uint64_t)p.warps * 32;
+    for (uint64_t v = part * 32 + lane; v < vecs; v += step) {
+        float2 f[R][H];
+        uint4 q[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            q[r] = load_anywhere(wr[r] + v * V, w, w_end);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            unpack_all<T>(q[r], f[r]);
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            float2 g[H];
+            unpack_all<T>(load_anywhere(x + m * p.ldx + v * V, x, x_end), g);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    acc[r][m] = fma2(f[r][i], g[i], acc[r][m]);
+        }
+    }
+    if (part == 0)
+        for (uint64_t k = vecs * V + lane; k < p.K; k += 32)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    acc[r][m].x = fmaf(to_f32(wr[r][k]), to_f32(x[m * p.ldx + k]), acc[r][m].x);
+    float a = 0.f; // lane r M + m keeps column r's sum of row m
+#pragma unroll
+    for (int i = 0; i < OUT; ++i) {
+        const float t = warp_sum(acc[i / M][i % M].x + acc[i / M][i % M].y);
+        if (lane == i)
+            a = t;
+    }
+    if (p.warps > 1) {
+        if (lane < OUT)
+            sums[warp][lane] = a;
+        __syncthreads();
+        if (part)
+            return;
+        if (lane < OUT)
+            for (uint32_t i = 1; i < p.warps; ++i)
+                a += sums[warp + i][lane];
+    }
+    const uint64_t c = n0 + lane / M, r = lane % M;
+    if (lane >= OUT || c >= p.N)
+        return;
+    const Epilogue &e = p.e;
+    a = a * e.scale + (e.bias ? load_any(e.bias, c, e.bias_type) : 0.f);
+    if (e.pre)
+        store_any(e.pre, r * e.ldpre + c, e.pre_type, a);
+    if (e.act == ECC_ACT_RELU)
+        a = act_value2<ECC_ACT_RELU>(both(a)).x;
+    else if (e.act == ECC_ACT_GELU)
+        a = act_value2<ECC_ACT_GELU>(both(a)).x;
+    else if (e.act == ECC_ACT_GELU_TANH)
+        a = act_value2<ECC_ACT_GELU_TANH>(both(a)).x;
+    else if (e.act == ECC_ACT_SILU)
+        a = act_value2<ECC_ACT_SILU>(both(a)).x;
+    if (e.residual)
+        a += load_any(e.residual, r * e.ldres + c, e.res_type);
+    store_any(e.out, r * e.ldout + c, e.out_type, e.out_type == ECC_E4M3 ? a * e.out_scale : a);
+}
+
 namespace {
 
 constexpr uint64_t kMostDim = 1ull << 31;
@@ -210,6 +326,34 @@ bool readable(const Array &a, const Array &b, uint32_t type, uint8_t *&ws, cudaS
     else
         pad_rows_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>(jobs[0], jobs[n - 1]);
     return true;
+}
+
+// Which products few_rows_kernel takes, in place of the tensor cores' kernels
+// (with the padding copy they need off 16-byte boundaries), us on both sides:
+// one token's with 16-bit weights, 1 x 16384 x 4096 25.3 and 27.0, 1 x 4096 x
+// 4096 9.5 and 12.3, 1 x 4096 x 4097 14.3 and 20.5; two rows off boundaries,
+// 2 x 4096 x 4097 22.8 and 28.7 (on them 2 x 4096 x 4096 14.4 and 12.3); up to
+// four of a small layer, 4 x 2048 x 2048 8.2 and 12.3 (4 x 4096 x 4096 18.5
+// and 12.3).  (8-bit weights convert slower: 1 x 16384 x 4096 22 and 16.5.)
+bool few_rows(const ecc_linear_job &j)
+{
+    if (j.M > 4 || !j.K)
+        return false;
+    if (j.N * j.K <= 1ull << 22)
+        return true;
+    return j.in_type != ECC_E4M3 && (j.M == 1 || (j.M == 2 && !tma_rows(j.w, j.ldw, j.in_type, j.N)));
+}
+template <typename T> void few_rows_launch(const ecc_linear_job &j, FewRows p, int sms, cudaStream_t st)
+{
+    // as many warps to four columns as the GPU has room for, each with two vectors a lane at least
+    const uint64_t teams = (j.N + kFewColumns - 1) / kFewColumns;
+    p.warps = 1;
+    while (p.warps < 8 && teams * p.warps < 32ull * sms && j.K * sizeof(T) >= 2048ull * p.warps)
+        p.warps *= 2;
+    const unsigned blocks = (unsigned)((teams * p.warps + 7) / 8);
+    const auto f = j.M == 1 ? few_rows_kernel<T, 1> : j.M == 2 ? few_rows_kernel<T, 2> : j.M == 3 ? few_rows_kernel<T, 3>
+                                                                                                : few_rows_kernel<T, 4>;
+    f<<<blocks, kRowThreads, 0, st>>>(p);
 }
 
 bool linear_ok(const ecc_linear_job &j)
@@ -314,7 +458,7 @@ extern "C" {
 
 size_t ecc_linear_workspace_bytes(const ecc_linear_job *job)
 {
-    if (!job || !job->M || !job->N || !job->K)
+    if (!job || !job->M || !job->N || !job->K || few_rows(*job))
         return 0;
     return copy_bytes(job->x, job->ldx, job->M, job->K, job->in_type) +
            copy_bytes(job->w, job->ldw, job->N, job->K, job->in_type);
@@ -331,11 +475,24 @@ ecc_status ecc_linear(const ecc_linear_job *job, void *ws, size_t ws_bytes, uint
     const size_t need = ecc_linear_workspace_bytes(job);
     if (need && (!ws || !aligned16(ws) || ws_bytes < need))
         return ECC_ERR_ARG;
+    const Epilogue e{j.bias,  j.residual,  j.out,       j.pre,      j.ldres,    j.ldout,    j.ldpre,
+                     j.scale, j.out_scale, j.bias_type, j.res_type, j.out_type, j.pre_type, j.act};
+    if (few_rows(j)) {
+        const int sms = sm_count();
+        if (sms <= 0)
+            return ECC_ERR_CUDA;
+        const FewRows p{j.x, j.w, j.ldx, j.ldw, j.N, j.K, 1, e, status};
+        if (j.in_type == ECC_BF16)
+            few_rows_launch<bf16>(j, p, sms, st);
+        else if (j.in_type == ECC_F16)
+            few_rows_launch<__half>(j, p, sms, st);
+        else
+            few_rows_launch<e4m3>(j, p, sms, st);
+        return launch_status(cudaGetLastError());
+    }
     uint8_t *w = (uint8_t *)ws;
     Operand x, wt;
     const bool copied = readable({j.x, j.ldx, j.M, j.K}, {j.w, j.ldw, j.N, j.K}, j.in_type, w, st, x, wt);
-    const Epilogue e{j.bias,  j.residual,  j.out,       j.pre,      j.ldres,    j.ldout,    j.ldpre,
-                     j.scale, j.out_scale, j.bias_type, j.res_type, j.out_type, j.pre_type, j.act};
     return gemm({wt, x, j.M, j.N, j.K, e}, j.in_type, status, true, copied, st);
 }
 

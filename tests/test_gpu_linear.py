@@ -94,6 +94,26 @@ def test_linear_epilogues(M, act, out_dtype):
     check(x, w, None, None, act, -0.5, out_dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, E4M3])
+@pytest.mark.parametrize("M", [1, 2, 3, 4])
+@pytest.mark.parametrize("N,K", [(1, 1), (3, 15), (6, 131), (130, 2049), (8197, 513), (2048, 2048), (70001, 33), (1025, 4095),
+                                 (4097, 4103), (130, 40001)])
+def test_linear_few_rows(M, N, K, dtype):
+    """Single tokens and the next few, on and off 16-byte boundaries, odd ends, every epilogue."""
+    gen = torch.Generator("cuda").manual_seed(M * 31 + N + K)
+    acts, outs = list(ACTS), [BF16, F16, F32, E4M3]
+    for i, (pad, off) in enumerate(((0, 0), (8, 0), (5, 3), (1, 1))):
+        x, w = rows_of(gen, M, K, dtype, pad, off), rows_of(gen, N, K, dtype, 2 * pad, off, std=K**-0.5)
+        bias = torch.randn(N, generator=gen, device="cuda")
+        res = torch.randn(M, N + pad, generator=gen, device="cuda").to(BF16)[:, :N]
+        out = outs[(M + i) % 4]
+        first = check(x, w, bias if i else None, res if i % 2 else None, act=acts[(M + i) % len(acts)], scale=0.75, out_dtype=out,
+                      out_scale=2.0 if out == E4M3 else 1.0, pre_dtype=F16 if i > 1 else None)
+        again = check(x, w, bias if i else None, res if i % 2 else None, act=acts[(M + i) % len(acts)], scale=0.75, out_dtype=out,
+                      out_scale=2.0 if out == E4M3 else 1.0, pre_dtype=F16 if i > 1 else None)
+        assert torch.equal(first.view(torch.uint8), again.view(torch.uint8))
+
+
 def test_linear_long_sums_and_large_offsets():
     gen = torch.Generator("cuda").manual_seed(3)
     check(rows_of(gen, 130, 60000, BF16), rows_of(gen, 140, 60000, BF16), scale=0.01, out_dtype=F32)
