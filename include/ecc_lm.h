@@ -90,7 +90,8 @@ ecc_status ecc_layer_norm_grad(const void *dy, uint64_t lddy, const void *x, uin
  *         NULL.
  *   M, N, K  any, K = 0 giving a = bias.  M and N below 2^31, K below 2^31.
  *   ws    16-byte aligned scratch of ecc_linear_workspace_bytes(job) bytes
- *         (0 when the rows of x and w start on 16-byte boundaries).
+ *         (0 when the rows of x and w start on 16-byte boundaries, and for
+ *         single tokens and small products of up to four rows).
  *   status  device uint32[1]: ECC_OK, or ECC_ERR_TIMEOUT if a bounded wait of
  *         the kernel ran out (the output is then incomplete).
  * Errors: ECC_ERR_ARG, ECC_ERR_CUDA.

@@ -190,10 +190,11 @@ template <typename T> __device__ __forceinline__ void unpack_all(const uint4 &q,
 // as vectors shifted from the aligned ones around them, and multiplied as they
 // come.  A warp (or p.warps of them) takes four columns of the output, so that
 // they share the conversion of x; its lanes' sums are joined in a fixed order.
-// Bound by HBM for one token, 1 x 16384 x 4096 bf16 25.3 us, 5.3 TB/s (two
-// columns a warp 29.5, two vectors of four columns at a time 30.1); off
-// 16-byte boundaries by the shifts, 1 x 12616 x 14088 131 us, 2.7 TB/s; with
-// more rows by the multiplications, M of them a weight.
+// Bound by HBM for one token, 1 x 16384 x 4096 bf16 25.5 us, 5.3 TB/s, 1 x
+// 12616 x 14088 63 us, 5.6 TB/s (at 1 x 16384 x 4096, two columns a warp 29.5,
+// two vectors of four columns at a time 30.1, the next vectors loaded ahead
+// 30.7); off 16-byte boundaries by the shifts, the second 129 us; with more
+// rows by the multiplications, M of them a weight.
 template <typename T, int M>
 __global__ void __launch_bounds__(kRowThreads) few_rows_kernel(const __grid_constant__ FewRows p)
 {
@@ -330,9 +331,9 @@ bool readable(const Array &a, const Array &b, uint32_t type, uint8_t *&ws, cudaS
 
 // Which products few_rows_kernel takes, in place of the tensor cores' kernels
 // (with the padding copy they need off 16-byte boundaries), us on both sides:
-// one token's with 16-bit weights, 1 x 16384 x 4096 25.3 and 27.0, 1 x 4096 x
-// 4096 9.5 and 12.3, 1 x 4096 x 4097 14.3 and 20.5; two rows off boundaries,
-// 2 x 4096 x 4097 22.8 and 28.7 (on them 2 x 4096 x 4096 14.4 and 12.3); up to
+// one token's with 16-bit weights, 1 x 16384 x 4096 25.5 and 27.0, 1 x 4096 x
+// 4096 8.2 and 12.3, 1 x 4096 x 4097 14.3 and 20.5; two rows off boundaries,
+// 2 x 4096 x 4097 22.5 and 28.7 (on them 2 x 4096 x 4096 14.4 and 12.3); up to
 // four of a small layer, 4 x 2048 x 2048 8.2 and 12.3 (4 x 4096 x 4096 18.5
 // and 12.3).  (8-bit weights convert slower: 1 x 16384 x 4096 22 and 16.5.)
 bool few_rows(const ecc_linear_job &j)
@@ -345,10 +346,11 @@ bool few_rows(const ecc_linear_job &j)
 }
 template <typename T> void few_rows_launch(const ecc_linear_job &j, FewRows p, int sms, cudaStream_t st)
 {
-    // as many warps to four columns as the GPU has room for, each with two vectors a lane at least
+    // more warps to four columns while 16 an SM are not reached, each with two vectors a lane at least (32 an SM: 1 x
+    // 4096 x 4096 9.3 us instead of 8.2, 1 x 12616 x 14088 66 instead of 63)
     const uint64_t teams = (j.N + kFewColumns - 1) / kFewColumns;
     p.warps = 1;
-    while (p.warps < 8 && teams * p.warps < 32ull * sms && j.K * sizeof(T) >= 2048ull * p.warps)
+    while (p.warps < 8 && teams * p.warps < 16ull * sms && j.K * sizeof(T) >= 2048ull * p.warps)
         p.warps *= 2;
     const unsigned blocks = (unsigned)((teams * p.warps + 7) / 8);
     const auto f = j.M == 1 ? few_rows_kernel<T, 1> : j.M == 2 ? few_rows_kernel<T, 2> : j.M == 3 ? few_rows_kernel<T, 3>
