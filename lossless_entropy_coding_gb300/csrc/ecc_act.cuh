@@ -79,9 +79,11 @@ template <uint32_t ACT> __device__ __forceinline__ float2 act_slope2(float2 a)
         gauss2(a, Phi, e);
         return fma2(mul2(a, both(0.39894228f)), e, Phi);
     } else if constexpr (ACT == ECC_ACT_GELU_TANH) { // h + a h (1 - h) u'
+        // (a h (1 - h) first, and a finite u': for large a it is 0 times what overflows)
         const float2 h = logistic2(tanh_argument2(a));
         const float2 du = fma2(mul2(a, a), both(3.f * 1.59576912f * 0.044715f), both(1.59576912f));
-        return fma2(mul2(a, du), fma2(mul2(h, both(-1.f)), h, h), h);
+        const float2 t = mul2(a, fma2(mul2(h, both(-1.f)), h, h));
+        return fma2(t, make_float2(fminf(du.x, 3e38f), fminf(du.y, 3e38f)), h);
     } else if constexpr (ACT == ECC_ACT_SILU) { // h (1 + a (1 - h))
         const float2 h = logistic2(a);
         return fma2(a, fma2(mul2(h, both(-1.f)), h, h), h);
