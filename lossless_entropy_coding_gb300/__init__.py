@@ -581,15 +581,18 @@ def _marshal():
 
 def _on_stream(f):
     """f on the given stream (made current, so that what f allocates belongs to
-    it); without one, on the current stream."""
+    it); without one, on the current stream.  f's first argument is a tensor."""
+    first = f.__code__.co_varnames[0]
+
     @functools.wraps(f)
-    def call(x, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         if stream is None:
-            return f(x, *args, **kw)
-        if x.device != stream.device:
+            return f(*args, **kw)
+        x = args[0] if args else kw.get(first)
+        if getattr(x, "device", None) != stream.device:
             raise EccError(ERR_ARG, f.__name__ + ": stream of another device")
         with _torch().cuda.stream(stream):
-            return f(x, *args, **kw)
+            return f(*args, **kw)
     return call
 
 

@@ -33,3 +33,29 @@ def test_slopes_at_large_arguments(act, pre_dtype):
         pre = far.expand(M, N).contiguous().to(pre_dtype)
         dx, dw, db = check_linear_grad(dy, x, w, pre, act)
         assert bool(dx.isfinite().all()) and bool(dw.isfinite().all()) and bool(db.isfinite().all())
+
+
+def test_arguments_by_name():
+    gen = torch.Generator("cuda").manual_seed(2)
+    x, dy, w = rows_of(gen, 8, 64, BF16), rows_of(gen, 8, 32, BF16), rows_of(gen, 32, 64, BF16)
+    tok = torch.arange(8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+
+    def same(a, b):
+        torch.cuda.synchronize()
+        return all(p is q or torch.equal(p, q) for p, q in zip(a, b))
+
+    y, mean, rstd = ref = ecc.ecc_layer_norm(x)
+    r = ecc.ecc_token_logprob(x, tok)
+    for kw in ({}, {"stream": s}):
+        assert same(ecc.ecc_layer_norm(x=x, **kw), ref)
+        assert same(ecc.ecc_layer_norm_grad(dy=y, x=x, weight=None, mean=mean, rstd=rstd, **kw),
+                    ecc.ecc_layer_norm_grad(y, x, None, mean, rstd))
+        assert same(ecc.ecc_layer_norm_grad(y, x=x, weight=None, mean=mean, rstd=rstd, **kw),
+                    ecc.ecc_layer_norm_grad(y, x, None, mean, rstd))
+        assert same(ecc.ecc_linear(x=x, w=w, **kw), ecc.ecc_linear(x, w))
+        assert same(ecc.ecc_linear_grad(dy=dy, x=x, w=w, **kw), ecc.ecc_linear_grad(dy, x, w))
+        assert same(ecc.ecc_token_logprob(logits=x, tokens=tok, **kw), r)
+        assert same([ecc.ecc_token_logprob_grad(logits=x, tokens=tok, lse=r.lse, dlogprob=mean, **kw)],
+                    [ecc.ecc_token_logprob_grad(x, tok, r.lse, None, mean)])
