@@ -936,8 +936,9 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads) logprob_grad
     if (lse == -INFINITY) { // no token has a probability
         row.A = row.B = row.m = row.l = 0.f;
         row.tok = -1;
-    } else if (!(lse < INFINITY)) {
+    } else if (!(lse < INFINITY)) { // every value is NaN, the token's too
         row.A = NAN;
+        row.tok = -1;
     }
     const RowView<T> view(x, p.vocab);
     if ((((uintptr_t)x ^ (uintptr_t)d) & 15) == 0) { // both rows' vectors start at the same value

@@ -35,6 +35,30 @@ def test_slopes_at_large_arguments(act, pre_dtype):
         assert bool(dx.isfinite().all()) and bool(dw.isfinite().all()) and bool(db.isfinite().all())
 
 
+# ---------------------------------------------------------------- log probabilities
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("V", [50, 9001, 40003])
+def test_gradient_of_rows_without_a_number_is_nan(V, dtype):
+    """Rows with a NaN or +infinity, the token at the row's start, middle and end, on the logits' boundary and another."""
+    rows = 9
+    x = torch.randn(rows, V + 5, generator=torch.Generator("cuda").manual_seed(V), device="cuda").to(dtype)[:, :V]
+    tok = torch.tensor([0, 1, V // 2, V - 1, V // 2 + 1, 3, -1, V - 1, 5], device="cuda")
+    clean = [1, 7]
+    x[0, 5], x[2, V // 2], x[3, 0], x[4, V - 1], x[5, 3] = math.nan, math.nan, math.nan, INF, INF
+    x[6, 7], x[8, 0], x[8, 1] = math.nan, INF, math.nan
+    r = ecc.ecc_token_logprob(x, tok)
+    one, half = torch.ones(rows, device="cuda"), torch.full((rows,), 0.5, device="cuda")
+    for off in (0, 1, 3):
+        out = torch.empty(rows * (V + 5) + 8, dtype=dtype, device="cuda")[off:off + rows * (V + 5)].view(rows, V + 5)[:, :V]
+        for dlp, dent in ((one, None), (one, half), (None, half)):
+            d = ecc.ecc_token_logprob_grad(x, tok, r.lse, r.entropy, dlp, dent, dlogits=out)
+            bad = [i for i in range(rows) if i not in clean]
+            assert bool(d[bad].isnan().all())
+            c = ecc.ecc_token_logprob_grad(x[clean], tok[clean], r.lse[clean], r.entropy[clean],
+                                           None if dlp is None else dlp[clean], None if dent is None else dent[clean])
+            assert bool(d[clean].isfinite().all()) and torch.allclose(d[clean].float(), c.float(), rtol=1e-2, atol=1e-5)
+
+
 def test_arguments_by_name():
     gen = torch.Generator("cuda").manual_seed(2)
     x, dy, w = rows_of(gen, 8, 64, BF16), rows_of(gen, 8, 32, BF16), rows_of(gen, 32, 64, BF16)
