@@ -410,7 +410,7 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
             unsigned long long big = 0;
             auto look = [&](uint32_t i) {
                 const unsigned long long key = order_key(to_f32(x[i]), i);
-                if (key < before && key > big)
+                if ((k == 0 || key < before) && key > big) // (a NaN at index 0 is the largest key of all, ~0)
                     big = key;
             };
             for (uint32_t i = a.row.head + a.v0 * V + tid; i < last; i += N)

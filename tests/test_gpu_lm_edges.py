@@ -59,6 +59,41 @@ def test_gradient_of_rows_without_a_number_is_nan(V, dtype):
             assert bool(d[clean].isfinite().all()) and torch.allclose(d[clean].float(), c.float(), rtol=1e-2, atol=1e-5)
 
 
+def order_of(x, top):
+    """NaN first, then larger logits, equal ones by the lower index."""
+    key = torch.where(x.isnan(), 2.0, 1.0).double()
+    v = torch.where(x.isnan(), 0.0, x.double() + 0.0)
+    by_value = torch.sort(v, dim=-1, descending=True, stable=True).indices
+    by_nan = torch.sort(key.gather(1, by_value), dim=-1, descending=True, stable=True).indices
+    return by_value.gather(1, by_nan)[:, :top]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,V", [(7, 40), (5, 2000), (1300, 3001), (3, 60000), (400, 20011), (2, 131072)])
+def test_alternatives_among_many_candidates(rows, V, dtype):
+    """More values at the bound than are ranked at a time: NaN, constants, few levels, ascending runs, plateaus."""
+    gen = torch.Generator("cuda").manual_seed(rows + V)
+    top = 32
+    at = torch.arange(V, device="cuda")
+    kinds = [torch.full((V,), math.nan, device="cuda"), torch.zeros(V, device="cuda"),
+             torch.randint(0, 3, (V,), generator=gen, device="cuda").float(),
+             torch.where(at % 2 == 0, math.nan, 1.0), torch.where(at == 0, math.nan, 4.0),
+             torch.where(at < 20, -INF, 2.5), (at // 700).float(), torch.where((at >= 17) & (at < 1500), at * 2.0 ** -12 + 1, 0.0),
+             torch.where(at % 3 == 1, -INF, -0.0), torch.where(at == V - 1, 7.0, -3.0)]
+    z = torch.stack([kinds[r % len(kinds)].roll((r // len(kinds)) * 37) for r in range(rows)]).to(dtype)
+    pad = torch.full((rows, V + 3), 9.0, device="cuda", dtype=dtype)
+    pad[:, :V] = z
+    want = order_of(z.float(), top)
+    for x in (z, pad[:, :V]):
+        r = ecc.ecc_token_logprob(x, None, top=top)
+        assert torch.equal(r.top_index.long(), want)
+        has = ~z.float().isnan().any(-1)
+        assert bool(r.top_logprob[~has].isnan().all()) and bool(r.lse[has].isfinite().all())
+        if bool(has.any()):
+            logp = reference(z[has])[2].gather(1, want[has])
+            assert torch.allclose(r.top_logprob[has].double(), logp, rtol=1e-5, atol=float(error_of(V)) + 1e-5)
+
+
 def test_arguments_by_name():
     gen = torch.Generator("cuda").manual_seed(2)
     x, dy, w = rows_of(gen, 8, 64, BF16), rows_of(gen, 8, 32, BF16), rows_of(gen, 32, 64, BF16)
