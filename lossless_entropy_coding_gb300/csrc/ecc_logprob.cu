@@ -166,12 +166,11 @@ template <int N, int C> struct Team {
     static constexpr uint32_t threads = N, columns = C, keys = N == 32 ? 256 : 512; // keys: candidates that are ranked
     unsigned long long key[keys];
     unsigned long long best[ECC_MAX_TOP]; // the alternatives, in order
-    unsigned long long largest;
     uint16_t pair[C * (N == 32 ? kWarpSlots : kSlots)]; // slot << 8 | column
     uint32_t low[N / 32];
     float sum[3];
     uint16_t kept[N == 32 ? 1 : keys];
-    uint32_t n_key, n_pair, n_kept;
+    uint32_t n_key, n_pair, n_kept, hit[2];
 
     static __device__ __forceinline__ void sync()
     {
@@ -351,6 +350,8 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
     // the slots' values, eight loads a thread at a time
     const uint32_t log_v = sizeof(T) == 4 ? 2 : 3, log_slot = shift + log_v, items = pairs << log_slot;
     for (uint32_t i0 = tid; i0 < items; i0 += 8 * N) {
+        if (*(volatile uint32_t *)&sh.n_key > Tm::keys)
+            break; // too many (all threads will see it)
         T q[8];
         uint32_t at[8];
 #pragma unroll
@@ -401,29 +402,69 @@ __device__ __forceinline__ void select_top(Tm &sh, const float (*gmax)[Tm::colum
                     break;
             }
         }
-    } else { // many equal values: one alternative a pass, the largest key below the last one
-        unsigned long long before = ~0ull;
-        for (uint32_t k = 0; k < top; ++k) {
-            if (tid == 0)
-                sh.largest = 0;
+    } else {
+        // More candidates than are ranked at a time, as among many equal values: the share is read again with the best
+        // so far in hand.  Where the next candidates might not fit, the best `top` stay, and the last of them is
+        // what the rest have to exceed: equal values that follow do not, so a constant row costs little more than
+        // reading it again (top 32, a pass for each alternative and now: 4096 x 50021 float32 zeros 10.6 and 0.92 ms,
+        // 4096 x 131072 bf16 27.2 and 1.47, 5184 x 1375 f16 0.27 and 0.12).
+        constexpr uint32_t U = 4;
+        unsigned long long least = (unsigned long long)bound << 32; // keys from here on
+        Tm::sync(); // (n is read)
+        if (tid == 0)
+            sh.n_key = sh.hit[0] = sh.hit[1] = 0;
+        Tm::sync();
+        uint32_t have = 0;
+        auto take = [&](bool in, uint32_t i) { // a value of each thread
+            const unsigned long long key = in ? order_key(to_f32(x[i]), i) : 0;
+            if (in && key >= least)
+                sh.key[atomicAdd(&sh.n_key, 1u)] = key;
             Tm::sync();
-            unsigned long long big = 0;
-            auto look = [&](uint32_t i) {
-                const unsigned long long key = order_key(to_f32(x[i]), i);
-                if ((k == 0 || key < before) && key > big) // (a NaN at index 0 is the largest key of all, ~0)
-                    big = key;
-            };
-            for (uint32_t i = a.row.head + a.v0 * V + tid; i < last; i += N)
-                look(i);
-            for (uint32_t i = tid; i < a.singles; i += N)
-                look(a.row.single(i));
-            atomicMax(&sh.largest, big);
+            have = sh.n_key;
+            if (have > Tm::keys - N) {
+                rank_keys(sh, have, top);
+                Tm::sync();
+                if (tid < top)
+                    sh.key[tid] = sh.best[tid];
+                if (tid == 0)
+                    sh.n_key = top;
+                least = sh.best[top - 1];
+                have = top;
+            }
             Tm::sync();
-            before = sh.largest;
-            if (tid == 0)
-                sh.best[k] = before;
+        };
+        take(tid < a.singles, tid < a.singles ? a.row.single(tid) : 0);
+        uint32_t chunk = 0; // U vectors a thread; `hit` in turn for the odd and the even ones, set by any thread
+#pragma unroll 1
+        for (uint32_t v0 = a.v0 + tid; v0 - tid < a.v1; v0 += U * N, ++chunk) {
+            uint4 q[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u)
+                if (v0 + u * N < a.v1)
+                    q[u] = *a.row.vec(v0 + u * N);
+            bool hit = false;
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u)
+                if (v0 + u * N < a.v1) {
+                    float2 f[V / 2];
+                    unpack2<T>(q[u], f);
+                    const uint32_t i = a.row.head + (v0 + u * N) * V;
+#pragma unroll
+                    for (uint32_t k = 0; k < V; ++k)
+                        hit |= order_key(k & 1 ? f[k / 2].y : f[k / 2].x, i + k) >= least;
+                }
+            if (hit)
+                sh.hit[chunk & 1] = chunk + 1;
             Tm::sync();
+            if (*(volatile uint32_t *)&sh.hit[chunk & 1] != chunk + 1)
+                continue;
+#pragma unroll 1
+            for (uint32_t k = 0; k < U * V; ++k) {
+                const uint32_t v = v0 + k / V * N;
+                take(v < a.v1, a.row.head + v * V + k % V);
+            }
         }
+        rank_keys(sh, have, top);
     }
     Tm::sync();
 }
@@ -612,10 +653,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2) logprob_stream_kernel(Logpr
         if (threadIdx.x == kLpThreads + kSelThreads) {
             uint32_t st = 0, ph = 0, issued = 0;
             bool ok = true;
+            // the ring may be full while an earlier row's alternatives are looked for: at worst (every value a new
+            // best one, ranked 352 at a time) that takes some 50 ns a value
+            const uint64_t limit = kWaitLimitNs + 200 * p.vocab;
             for (uint64_t r = r0; r < p.rows && ok; r += step) {
                 const Share<T> a = share_of(r);
                 for (uint32_t v = a.v0; v < a.v1; v += kStageVecs) {
-                    if (!(ok = mbar_wait(&ss.empty[st], ph ^ 1, kWaitLimitNs)))
+                    if (!(ok = mbar_wait(&ss.empty[st], ph ^ 1, limit)))
                         break;
                     const uint32_t bytes = min(kStageVecs, a.v1 - v) * 16;
                     mbar_expect_tx(&ss.full[st], bytes);

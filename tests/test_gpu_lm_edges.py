@@ -94,6 +94,26 @@ def test_alternatives_among_many_candidates(rows, V, dtype):
             assert torch.allclose(r.top_logprob[has].double(), logp, rtol=1e-5, atol=float(error_of(V)) + 1e-5)
 
 
+def test_rows_of_equal_logits_keep_up():
+    """The alternatives of a constant row (a head that starts at zero) cost a pass over it, not one for each of them."""
+    x = torch.randn(1000, 50021, device="cuda")
+    flat = torch.zeros_like(x)
+
+    def ms(z):
+        best = INF
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            ecc.ecc_token_logprob(z, None, top=32)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    usual, equal = ms(x), ms(flat)
+    assert equal < 20 * usual, (usual, equal)
+
+
 def test_arguments_by_name():
     gen = torch.Generator("cuda").manual_seed(2)
     x, dy, w = rows_of(gen, 8, 64, BF16), rows_of(gen, 8, 32, BF16), rows_of(gen, 32, 64, BF16)
