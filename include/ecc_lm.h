@@ -153,7 +153,9 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
  * A logit of -infinity is a token without probability.  A row of nothing
  * else has lse and every log probability -infinity and entropy 0.  A row
  * with a NaN has NaN results; a row with +infinity has lse = +infinity and
- * entropy NaN.
+ * entropy NaN.  Where scale * logits leaves float32's range lse does too
+ * (+-infinity); the log probabilities and the entropy are those of the values
+ * all the same.
  * Errors: ECC_ERR_ARG (no columns, vocab >= 2^31, ...), ECC_ERR_CUDA.
  */
 #define ECC_MAX_TOP 32

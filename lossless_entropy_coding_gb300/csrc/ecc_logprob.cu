@@ -57,26 +57,27 @@ struct RowResult {
     __device__ __forceinline__ RowResult(float m_, float s, float t, float scale_)
         : m(m_), scale(scale_), logs(logf(s))
     {
-        if (m == -INFINITY && s == 0.f) { // no token has a probability
+        if (m == -INFINITY) { // no token has a probability
             lse = -INFINITY;
             entropy = 0.f;
-        } else if (m == INFINITY && s == s) {
+        } else if (m == INFINITY) {
             lse = INFINITY;
             entropy = NAN;
         } else {
-            lse = m * scale + logs;
+            lse = m * scale + logs; // (infinite where m * scale leaves float32; the rest does without it)
             entropy = logs - t / s;
         }
     }
     __device__ __forceinline__ float logprob(float x) const
     {
-        return lse == -INFINITY ? -INFINITY : lse == INFINITY ? x - m : (x - m) * scale - logs;
+        return m == -INFINITY ? -INFINITY : m == INFINITY ? x - m : (x - m) * scale - logs;
     }
 };
 
 // log p in the gradient: from lse, unless lse is so large that rounding it
 // to float32 (2^-24 |lse|) would show; the row's maximum and log sum are then
-// found again.
+// found again.  So they are where lse is infinite and a scale above 1 may
+// have made it so (a row of the type's lowest value).
 constexpr float kLseMost = 256.f;
 
 // ---------------------------------------------------------------- rows in vectors
@@ -962,11 +963,14 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads) logprob_grad
     row.c = p.scale * 1.44269504f;
     row.m = 0.f;
     row.l = lse * 1.44269504f;
-    if (fabsf(lse) > kLseMost && fabsf(lse) < INFINITY) {
+    bool none = lse == -INFINITY, nan = !(lse < INFINITY);
+    if (fabsf(lse) > kLseMost && (fabsf(lse) < INFINITY || p.scale > 1.f)) {
         float m = -INFINITY, s = 0.f;
         for (uint64_t i = tid; i < p.vocab; i += kLpThreads)
             m = fmaxf(m, to_f32(x[i]));
         row.m = block_reduce(m, [](float a, float b) { return fmaxf(a, b); });
+        none = row.m == -INFINITY;
+        nan = row.m == INFINITY;
         for (uint64_t i = tid; i < p.vocab; i += kLpThreads)
             s += exp2_fast(fmaxf((to_f32(x[i]) - row.m) * row.c, -200.f));
         row.l = log2f(block_reduce(s, [](float a, float b) { return a + b; }));
@@ -977,10 +981,10 @@ template <typename T> __global__ void __launch_bounds__(kLpThreads) logprob_grad
     }
     row.A = -p.scale * fmaf(row.dent, row.ent, row.dlp);
     row.B = -p.scale * row.dent * 0.69314718f;
-    if (lse == -INFINITY) { // no token has a probability
+    if (none) { // no token has a probability
         row.A = row.B = row.m = row.l = 0.f;
         row.tok = -1;
-    } else if (!(lse < INFINITY)) { // every value is NaN, the token's too
+    } else if (nan) { // every value is NaN, the token's too
         row.A = NAN;
         row.tok = -1;
     }

@@ -114,6 +114,45 @@ def test_rows_of_equal_logits_keep_up():
     assert equal < 20 * usual, (usual, equal)
 
 
+@pytest.mark.parametrize("dtype,scale", [(F32, 1.4), (BF16, 1.4), (BF16, 3.0), (F16, 1e34)])
+@pytest.mark.parametrize("V", [40, 5000, 131073])
+def test_logits_whose_scaled_values_leave_float32(V, dtype, scale):
+    """scale * logits past float32's range: lse is infinite there, the probabilities are what they are."""
+    low, high = torch.finfo(dtype).min, torch.finfo(dtype).max
+    x = torch.randn(6, V, generator=torch.Generator("cuda").manual_seed(V), device="cuda").to(dtype)
+    x[0] = low                               # a mask that left nothing, by the type's lowest value
+    x[1] = low
+    x[1, ::3] = -INF
+    x[2] = high
+    x[3, 3], x[3, 9] = high, high
+    x[4] = -INF
+    tok = torch.tensor([1, 2, V - 1, 9, 0, 5], device="cuda")
+    top = 5
+    r = ecc.ecc_token_logprob(x, tok, top=top, scale=scale)
+    s = as_passed(scale)
+    lse, ent, logp, p = reference(x.double() * s)
+    e = error_of(V) * (math.log(V + 1) + 40)
+    assert r.lse[:5].tolist() == [-INF, -INF, INF, INF, -INF]
+    want = order_of(x.float(), top)
+    assert torch.equal(r.top_index.long(), want)
+    for got, ref in ((r.entropy[:4], ent[:4]), (r.logprob[:4], logp.gather(1, tok[:, None])[:4, 0]),
+                     (r.top_logprob[:4], logp.gather(1, want)[:4])):
+        ref = ref.float().double()           # (a logarithm below float32's range is -infinity there)
+        assert bool(((got.double() == ref) | ((got.double() - ref).abs() <= e)).all())
+    assert float(r.entropy[4]) == 0 and float(r.logprob[4]) == -INF
+    if dtype == F16:                         # (its gradient is as large as the scale)
+        return
+    one, half = torch.ones(6, device="cuda"), torch.full((6,), 0.5, device="cuda")
+    hot = torch.zeros_like(p).scatter_(1, tok[:, None], 1.0)
+    mid = torch.where(p > 0, p * (logp + ent[:, None]), 0.0)
+    for dent in (None, half):
+        for out in (None, x.clone()):        # also in place
+            d = ecc.ecc_token_logprob_grad(x if out is None else out, tok, r.lse, r.entropy, one, dent, scale=scale, dlogits=out)
+            ref = s * (hot - p - (0.0 if dent is None else 0.5) * mid)
+            assert not d[4].any()
+            assert bool(((d.double() - ref).abs()[:4] <= 1.01 * U[dtype] * ref.abs()[:4] + 4 * s * error_of(V)).all())
+
+
 def test_arguments_by_name():
     gen = torch.Generator("cuda").manual_seed(2)
     x, dy, w = rows_of(gen, 8, 64, BF16), rows_of(gen, 8, 32, BF16), rows_of(gen, 32, 64, BF16)
