@@ -111,19 +111,28 @@ Matrix matrix(const at::Tensor &t, c10::Device dev, const char *what)
 {
     const auto size = t.sizes(), stride = t.strides();
     const int64_t n = (int64_t)size.size();
-    if (n == 0 || t.device() != dev || (size[n - 1] > 1 && stride[n - 1] != 1))
+    if (n == 0 || t.device() != dev)
         refuse(what);
     Matrix m;
     m.cols = (uint64_t)size[n - 1];
     int64_t rows = 1, ld = size[n - 1];
-    for (int64_t i = n - 2; i >= 0; --i) {
-        if (size[i] == 1)
-            continue;
-        if (rows == 1)
-            ld = stride[i];
-        else if (size[i] && stride[i] != rows * ld)
+    bool empty = false; // no rows: whatever the strides
+    for (int64_t i = 0; i < n - 1; ++i)
+        empty |= size[i] == 0;
+    if (empty) {
+        rows = 0;
+    } else {
+        if (size[n - 1] > 1 && stride[n - 1] != 1)
             refuse(what);
-        rows *= size[i];
+        for (int64_t i = n - 2; i >= 0; --i) {
+            if (size[i] == 1)
+                continue;
+            if (rows == 1)
+                ld = stride[i];
+            else if (stride[i] != rows * ld)
+                refuse(what);
+            rows *= size[i];
+        }
     }
     m.rows = (uint64_t)rows;
     m.ld = rows > 1 ? (uint64_t)ld : m.cols;

@@ -153,6 +153,28 @@ def test_logits_whose_scaled_values_leave_float32(V, dtype, scale):
             assert bool(((d.double() - ref).abs()[:4] <= 1.01 * U[dtype] * ref.abs()[:4] + 4 * s * error_of(V)).all())
 
 
+# ---------------------------------------------------------------- the calls
+def test_batches_without_rows():
+    def e(*s, dtype=BF16):
+        return torch.empty(*s, dtype=dtype, device="cuda")
+
+    w, stat = torch.randn(24, 16, device="cuda").to(BF16), e(2, 0, 3, dtype=F32)
+    for lead in ((2, 0, 3), (2, 0), (0, 2), (3, 1, 0)):
+        stat = e(*lead, dtype=F32)
+        y, mean, rstd = ecc.ecc_layer_norm(e(*lead, 16))
+        assert y.shape == (*lead, 16) and mean.shape == lead and rstd.shape == lead
+        dx, dweight, dbias = ecc.ecc_layer_norm_grad(e(*lead, 16), e(*lead, 16), None, stat, stat)
+        assert dx.shape == (*lead, 16) and not dweight.any() and not dbias.any()
+        y, st = ecc.ecc_linear(e(*lead, 16), w, residual=e(*lead, 24), pre=e(*lead, 24))
+        assert y.shape == (*lead, 24) and int(st.item()) == 0
+        dx, dw, db, st = ecc.ecc_linear_grad(e(*lead, 24), e(*lead, 16), w, e(*lead, 24), act="gelu")
+        assert dx.shape == (*lead, 16) and not dw.any() and not db.any() and int(st.item()) == 0
+        r = ecc.ecc_token_logprob(e(*lead, 50), e(*lead, dtype=torch.int64), top=4)
+        assert r.lse.shape == lead and r.top_index.shape == (*lead, 4)
+        d = ecc.ecc_token_logprob_grad(e(*lead, 50), e(*lead, dtype=torch.int64), stat, None, stat)
+        assert d.shape == (*lead, 50)
+
+
 def test_arguments_by_name():
     gen = torch.Generator("cuda").manual_seed(2)
     x, dy, w = rows_of(gen, 8, 64, BF16), rows_of(gen, 8, 32, BF16), rows_of(gen, 32, 64, BF16)
