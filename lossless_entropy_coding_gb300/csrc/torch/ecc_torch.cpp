@@ -168,8 +168,11 @@ at::Tensor output(Opt given, at::IntArrayRef size, at::ScalarType type, c10::Dev
 {
     return given ? *given : fresh(size, type, dev);
 }
-at::Tensor scratch(Opt given, size_t bytes, c10::Device dev)
+// (a given one is written from its first byte on, as far as it is long)
+at::Tensor scratch(Opt given, size_t bytes, c10::Device dev, const char *what)
 {
+    if (given && (given->device() != dev || !given->is_contiguous()))
+        refuse(what);
     return given ? *given : bytes ? fresh({(int64_t)bytes}, at::kByte, dev) : at::Tensor();
 }
 void *where(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -265,7 +268,7 @@ FUNCTION(layer_norm_grad, 9)
     at::Tensor dw = output(tensor(a[6], "ecc_layer_norm_grad: dweight"), {cols}, at::kFloat, on.dev);
     at::Tensor db = output(tensor(a[7], "ecc_layer_norm_grad: dbias"), {cols}, at::kFloat, on.dev);
     at::Tensor ws = scratch(tensor(a[8], "ecc_layer_norm_grad: ws"), ecc_layer_norm_grad_workspace_bytes(mx.rows, mx.cols),
-                            on.dev);
+                            on.dev, "ecc_layer_norm_grad: ws");
     check(ecc_layer_norm_grad(
               md.p, md.ld, mx.p, mx.ld, mx.type, vector(weight, mx.cols, on.dev, "ecc_layer_norm_grad: weight"),
               weight ? type_of(weight->scalar_type(), "ecc_layer_norm_grad: weight") : mx.type,
@@ -329,7 +332,7 @@ FUNCTION(linear, 12)
     j.out_type = mo.type;
     j.pre_type = mp.type;
     j.act = (uint32_t)integer(a[4]);
-    at::Tensor ws = scratch(tensor(a[10], "ecc_linear: ws"), ecc_linear_workspace_bytes(&j), on.dev);
+    at::Tensor ws = scratch(tensor(a[10], "ecc_linear: ws"), ecc_linear_workspace_bytes(&j), on.dev, "ecc_linear: ws");
     check(ecc_linear(&j, where(ws), bytes_of(ws), status_word(status, on.dev, "ecc_linear: status"), on.stream), "ecc_linear");
     return results(out, status);
 }
@@ -385,7 +388,8 @@ FUNCTION(linear_grad, 13)
     j.pre_type = mp.type;
     j.dw_type = mdw.type;
     j.act = (uint32_t)integer(a[4]);
-    at::Tensor ws = scratch(tensor(a[11], "ecc_linear_grad: ws"), ecc_linear_grad_workspace_bytes(&j), on.dev);
+    at::Tensor ws = scratch(tensor(a[11], "ecc_linear_grad: ws"), ecc_linear_grad_workspace_bytes(&j), on.dev,
+                            "ecc_linear_grad: ws");
     check(ecc_linear_grad(&j, where(ws), bytes_of(ws), status_word(status, on.dev, "ecc_linear_grad: status"), on.stream),
           "ecc_linear_grad");
     return results(dx, dw, db, status);

@@ -199,3 +199,26 @@ def test_arguments_by_name():
         assert same(ecc.ecc_token_logprob(logits=x, tokens=tok, **kw), r)
         assert same([ecc.ecc_token_logprob_grad(logits=x, tokens=tok, lse=r.lse, dlogprob=mean, **kw)],
                     [ecc.ecc_token_logprob_grad(x, tok, r.lse, None, mean)])
+
+
+def test_scratch_of_the_caller():
+    """A given workspace is the device's, in one piece and long enough, or the call is refused."""
+    gen = torch.Generator("cuda").manual_seed(3)
+    x, dy, w = rows_of(gen, 30, 64, BF16, 5), rows_of(gen, 30, 40, BF16, 5), rows_of(gen, 40, 64, BF16, 5)   # copied to ws
+    y, mean, rstd = ecc.ecc_layer_norm(x)
+    calls = [lambda ws: ecc.ecc_layer_norm_grad(x, x, None, mean, rstd, ws=ws), lambda ws: ecc.ecc_linear(x, w, ws=ws),
+             lambda ws: ecc.ecc_linear_grad(dy, x, w, dy, act="gelu", ws=ws)]
+    for call in calls:
+        ref = call(None)
+        for ws in (torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), torch.empty(64, 4096, device="cuda")):
+            got = call(ws)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, dtype=torch.uint8).pin_memory(),
+                   torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20),
+                   torch.empty(1 << 21, dtype=torch.uint8, device="cuda")[::2],
+                   torch.empty(1024, 1024, device="cuda").t(), torch.empty(16, dtype=torch.uint8, device="cuda"),
+                   torch.empty((1 << 20) + 8, dtype=torch.uint8, device="cuda")[8:]):
+            with pytest.raises(ecc.EccError) as e:
+                call(ws)
+            assert e.value.code == ecc.ERR_ARG
