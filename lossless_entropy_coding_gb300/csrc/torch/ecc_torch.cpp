@@ -203,6 +203,17 @@ struct On {
     }
 };
 
+// torch.OutOfMemoryError, as for torch's own allocations
+void out_of_memory(const char *what)
+{
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *cls = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (cls)
+        PyErr_SetString(cls, what);
+    Py_XDECREF(cls);
+    Py_XDECREF(torch);
+}
+
 #define FUNCTION(name, count)                                                                                          \
     PyObject *name##_body(PyObject *const *a);                                                                         \
     PyObject *name(PyObject *, PyObject *const *a, Py_ssize_t n)                                                       \
@@ -214,6 +225,8 @@ struct On {
         try {                                                                                                          \
             return name##_body(a);                                                                                     \
         } catch (const Refused &) {                                                                                    \
+        } catch (const c10::OutOfMemoryError &e) {                                                                     \
+            out_of_memory(e.what_without_backtrace());                                                                 \
         } catch (const std::exception &e) {                                                                            \
             PyErr_SetString(PyExc_RuntimeError, e.what());                                                             \
         }                                                                                                              \

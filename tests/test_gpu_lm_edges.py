@@ -222,3 +222,12 @@ def test_scratch_of_the_caller():
             with pytest.raises(ecc.EccError) as e:
                 call(ws)
             assert e.value.code == ecc.ERR_ARG
+
+
+def test_memory_that_is_not_there():
+    """An output that does not fit raises what torch raises for its own."""
+    x = torch.zeros(1 << 20, 8, device="cuda", dtype=BF16)
+    with pytest.raises(torch.OutOfMemoryError):
+        ecc.ecc_linear(x, x)
+    y, st = ecc.ecc_linear(x[:16], x[:24])
+    assert int(st.item()) == 0 and not y.any()
