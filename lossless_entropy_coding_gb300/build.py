@@ -92,6 +92,17 @@ def build_torch(force: bool = False) -> str:
     return TORCH_LIB
 
 
+def main(argv) -> None:
+    force, checked = "--force" in argv, "--checked" in argv
+    print(build(force=force, checked=checked))
+    if checked:
+        return
+    try:
+        print(build_torch(force=force))
+    except ImportError:
+        print("PyTorch is not installed: the library is built, ecc_torch (the Python entry points of the "
+              "language-model operators) is not", file=sys.stderr)
+
+
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, checked="--checked" in sys.argv))
-    print(build_torch(force="--force" in sys.argv))
+    main(sys.argv[1:])
