@@ -37,7 +37,9 @@ extern "C" {
 enum { ECC_F32 = 0, ECC_BF16 = 1, ECC_F16 = 2, ECC_E4M3 = 3 };
 
 /* Activations: identity, max(a, 0), a Phi(a) (the exact erf form),
- * a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2, a / (1 + e^-a). */
+ * a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2, a / (1 + e^-a).  Phi is
+ * computed to an absolute 1.5e-7 (which is a relative 2e-3 of it at a = -5 and
+ * 1e-2 at -8), the exponentials to a relative 2^-22 (1 + |argument|). */
 enum { ECC_ACT_NONE = 0, ECC_ACT_RELU = 1, ECC_ACT_GELU = 2, ECC_ACT_GELU_TANH = 3, ECC_ACT_SILU = 4 };
 
 /*
@@ -90,8 +92,8 @@ ecc_status ecc_layer_norm_grad(const void *dy, uint64_t lddy, const void *x, uin
  *         NULL.
  *   M, N, K  any, K = 0 giving a = bias.  M and N below 2^31, K below 2^31.
  *   ws    16-byte aligned scratch of ecc_linear_workspace_bytes(job) bytes
- *         (0 when the rows of x and w start on 16-byte boundaries, and for
- *         single tokens and small products of up to four rows).
+ *         (0 when the rows of x and w start on 16-byte boundaries, for single
+ *         tokens of 16-bit types and for small products of up to four rows).
  *   status  device uint32[1]: ECC_OK, or ECC_ERR_TIMEOUT if a bounded wait of
  *         the kernel ran out (the output is then incomplete).
  * Errors: ECC_ERR_ARG, ECC_ERR_CUDA.
@@ -169,7 +171,10 @@ ecc_status ecc_token_logprob(const void *logits, uint64_t ld, uint32_t type, con
  *   dlogits = scale * (dlogprob (1[v = token] - p) - dentropy p (log p + H)),
  * p = e^(z - lse), the second term 0 where p = 0.
  *   lse, entropy  as written by ecc_token_logprob for the same logits and
- *           scale; entropy may be NULL if dentropy is.
+ *           scale (not joined from several calls: where |lse| is above 256,
+ *           too large for its float32 rounding not to show, the row's maximum
+ *           and log sum are found again, at two more reads of the row);
+ *           entropy may be NULL if dentropy is.
  *   dlogprob, dentropy  float32[rows]; NULL = zeros.  Rows whose token is
  *           negative or >= vocab take no part in dlogprob; a row of -infinity
  *           only has gradient 0, one with a NaN or +infinity has gradient NaN.

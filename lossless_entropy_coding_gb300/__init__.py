@@ -548,7 +548,9 @@ def bf16_escape_decode(enc: Encoded, top7, out=None, status=None, stream=None):
 # and whose leading dimensions collapse to rows of one stride.  e4m3 tensors
 # are uint8 (the coders' bytes) or torch.float8_e4m3fn.  The tensors are
 # checked and unpacked by the module built from csrc/torch/ecc_torch.cpp; what
-# it refuses raises EccError with ERR_ARG.  A call on another stream than the
+# it refuses raises EccError with ERR_ARG.  The calls record nothing for
+# autograd: results have no graph, whatever their arguments require; the
+# gradients are the *_grad calls.  A call on another stream than the
 # current one allocates its outputs and scratch for that stream; the caller
 # orders the streams, as for the coding calls.
 
