@@ -187,6 +187,60 @@ ecc_status ecc_token_logprob_grad(const void *logits, uint64_t ld, uint32_t type
                                   const float *entropy, const float *dlogprob, const float *dentropy, void *dlogits,
                                   uint64_t ldd, void *stream);
 
+/*
+ * ecc_adamw -- one step of AdamW over many tensors at once.  With g =
+ * grad_scale * grad, t = step:
+ *   m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in float32, with m and v as they are before they are stored.
+ *   param   [n] of param_type, grad [n] of grad_type (F32, BF16 or F16).
+ *   master  float32[n] or NULL: with it, p is read from and written to it,
+ *           and param receives its rounding.
+ *   m, v    by state_type: ECC_F32, float32[n] of the moments, or ECC_E4M3,
+ *           bytes[n] with a scale for each ECC_ADAMW_GROUP values (the last
+ *           group may be shorter): m = m_scale * byte, sqrt(v) = v_scale *
+ *           byte, scale = largest magnitude of the group / 448.  A value is
+ *           stored as one of its two e4m3 neighbours, the upper one with the
+ *           probability that its distance from the lower one is of theirs (so
+ *           that the mean of many steps is kept, where rounding to nearest
+ *           would never take a step smaller than half their distance), but a
+ *           positive v is at least the smallest positive code.  The random bits of
+ *           value i are mix((i mod 2^32) ^ mix(mix(mix(seed) + step) + i /
+ *           2^32)), the upper 16 for m, the lower for v: the same call gives the
+ *           same bytes.  (mix: see the kernel.)  A root is off by 4% a step on
+ *           average, and the errors of 1 / (1 - beta2) steps add up: at beta2 =
+ *           0.95 to a sixth, at 0.999 to more than the root, which wants float32
+ *           states.  A group with a NaN or an infinity gets scales of NaN, and
+ *           one of magnitudes below 1e-36 zeros.
+ *   step    1 for the first.  step_at, lr_at, grad_scale_at: device int64 and
+ *           float32 read by the kernel in place of step, lr and grad_scale (for
+ *           a captured step that is replayed), or NULL.
+ * All arrays contiguous, aligned to an element; none that is written may
+ * overlap another one of the job.  Tensors with n = 0 are passed over.
+ * Errors: ECC_ERR_ARG (a NULL or misaligned pointer, overlapping arrays, a
+ * type not listed, n >= 2^40, beta outside [0, 1), eps below 0, a value that is
+ * not finite, step = 0), ECC_ERR_CUDA.
+ */
+#define ECC_ADAMW_GROUP 256
+typedef struct ecc_adamw_tensor {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale, *master;
+    uint64_t n;
+    uint32_t param_type, grad_type, state_type, reserved;
+} ecc_adamw_tensor;
+typedef struct ecc_adamw_job {
+    const ecc_adamw_tensor *tensors;
+    uint64_t count;
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    uint64_t step;
+    const int64_t *step_at;
+    const float *lr_at, *grad_scale_at;
+    uint32_t seed, reserved;
+} ecc_adamw_job;
+ecc_status ecc_adamw(const ecc_adamw_job *job, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -111,6 +111,7 @@ def _load():
             "ecc_linear": (I32, [P, P, Z, P, P]),
             "ecc_linear_grad_workspace_bytes": (Z, [P]),
             "ecc_linear_grad": (I32, [P, P, Z, P, P]),
+            "ecc_adamw": (I32, [P, P]),
             "ecc_token_logprob": (I32, [P, U64, U32, P, U64, U64, F, U32, P, P, P, P, P, P]),
             "ecc_token_logprob_grad": (I32, [P, U64, U32, P, U64, U64, F, P, P, P, P, P, U64, P]),
         }
@@ -673,3 +674,53 @@ def ecc_token_logprob_grad(logits, tokens, lse, entropy=None, dlogprob=None, den
     dentropy * entropy); returns dlogits (which may be given as logits
     itself)."""
     return (_torch_lib or _marshal()).token_logprob_grad(logits, tokens, lse, entropy, dlogprob, dentropy, scale, dlogits)
+
+
+ADAMW_GROUP = 256
+
+
+class AdamWState(NamedTuple):
+    """State of ecc_adamw: lists of device tensors, one for each parameter.
+    m, v: float32 moments, or (with m_scale and v_scale, float32 for each
+    ADAMW_GROUP values) uint8 or float8_e4m3fn: m = m_scale * e4m3, sqrt(v) =
+    v_scale * e4m3.  master: float32 values of the parameters of 16-bit types
+    (entries of None: none), or None."""
+    m: list
+    v: list
+    m_scale: object = None
+    v_scale: object = None
+    master: object = None
+
+
+def adamw_state(params, bits: int = 32, master: bool = False) -> AdamWState:
+    """A state of zeros for device tensors params, in float32 (bits=32) or in
+    e4m3 bytes that the coders take (bits=8)."""
+    torch = _torch()
+    if bits not in (8, 32):
+        raise EccError(ERR_ARG, "adamw_state: bits")
+    kind = torch.float32 if bits == 32 else torch.uint8
+
+    def zeros():
+        return [torch.zeros(p.shape, dtype=kind, device=p.device) for p in params]
+
+    def scales():
+        return [torch.zeros(-(-p.numel() // ADAMW_GROUP), device=p.device) for p in params] if bits == 8 else None
+
+    return AdamWState(zeros(), zeros(), scales(), scales(),
+                      [p.float() if p.dtype != torch.float32 else None for p in params] if master else None)
+
+
+def ecc_adamw(params, grads, state: AdamWState, step, lr=1e-3, beta1: float = 0.9, beta2: float = 0.95,
+              eps: float = 1e-8, weight_decay: float = 0.01, grad_scale=1.0, seed: int = 0, stream=None):
+    """One step of AdamW, in place: params, grads lists of contiguous device
+    tensors (a gradient of None leaves its parameter and state alone).  step
+    counts from 1; step, lr and grad_scale may be device tensors of one value
+    (int64, float32, float32), which a captured and replayed call reads anew."""
+    m = _torch_lib or _marshal()
+    rest = (step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed)
+    if stream is None:
+        return m.adamw(params, grads, *state, *rest)
+    if any(p.device != stream.device for p in params[:1]):
+        raise EccError(ERR_ARG, "ecc_adamw: stream of another device")
+    with _torch().cuda.stream(stream):
+        return m.adamw(params, grads, *state, *rest)

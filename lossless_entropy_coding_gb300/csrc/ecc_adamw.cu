@@ -1,0 +1,514 @@
+// ecc_adamw.cu -- AdamW over many tensors in one launch, states in float32 or
+// in e4m3 bytes with a scale for each kAdamGroup values.
+//
+// Each value is read, updated and written once.  A warp takes a group of 256
+// values, so that the largest magnitude of an 8-bit state's group is one warp
+// reduction; the tensors' pointers travel as kernel parameters, so nothing is
+// copied to the device first and a captured call keeps them.
+
+#include <algorithm>
+#include <cmath>
+#include <limits>
+#include <utility>
+#include <vector>
+
+#include "ecc_act.cuh"
+
+namespace ecc {
+
+constexpr int kAdamThreads = 256;
+constexpr uint32_t kAdamGroup = ECC_ADAMW_GROUP;
+constexpr uint32_t kAdamVectors = 16; // of a tensor's kind: 16-byte accesses
+constexpr uint32_t kAdamTile = kAdamThreads / 32 * kAdamGroup; // values of a block's step
+
+struct AdamTensor {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale, *master;
+    uint64_t n;
+};
+struct AdamHyper {
+    float beta1, beta2, gain1, gain2; // gain = 1 - beta
+    float log_beta1, log_beta2, eps, weight_decay, lr, grad_scale;
+    float rate, root; // 1 / (1 - beta1^step), sqrt(1 / (1 - beta2^step))
+    uint32_t seed, step;
+    const float *lr_at, *grad_scale_at;
+    const int64_t *step_at;
+};
+// Up to CAP tensors: their first tiles, and kinds (types of parameter and
+// gradient, 2 bits each, and the bit above).
+template <int CAP> struct AdamArgs {
+    AdamHyper h;
+    uint32_t count;
+    uint32_t first[CAP + 1];
+    AdamTensor t[CAP];
+    uint8_t kind[CAP];
+};
+
+// A mixing of 32-bit numbers: two multiplications between three shifts.
+__host__ __device__ inline uint32_t mix32(uint32_t x)
+{
+    x = (x ^ x >> 16) * 0x7FEB352Du;
+    x = (x ^ x >> 15) * 0x846CA68Bu;
+    return x ^ x >> 16;
+}
+
+// what a step's values have in common
+struct AdamStep {
+    float beta1, beta2, gain1, gain2, eps, keep, rate, root, grad_scale;
+    uint32_t key;
+};
+__device__ __forceinline__ AdamStep step_of(const AdamHyper &h)
+{
+    AdamStep s;
+    const float lr = h.lr_at ? *h.lr_at : h.lr;
+    s.beta1 = h.beta1;
+    s.beta2 = h.beta2;
+    s.gain1 = h.gain1;
+    s.gain2 = h.gain2;
+    s.eps = h.eps;
+    s.keep = 1.f - lr * h.weight_decay;
+    s.grad_scale = h.grad_scale_at ? *h.grad_scale_at : h.grad_scale;
+    uint32_t step = h.step;
+    s.rate = h.rate;
+    s.root = h.root;
+    if (h.step_at) {
+        const int64_t t = *h.step_at;
+        step = (uint32_t)t;
+        s.rate = -1.f / expm1f((float)t * h.log_beta1);
+        s.root = sqrtf(-1.f / expm1f((float)t * h.log_beta2));
+    }
+    s.rate *= lr;
+    s.key = mix32(mix32(h.seed) + step);
+    return s;
+}
+
+__device__ __forceinline__ float rsqrt_approx(float x)
+{
+    float y;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// sqrt(x), x >= 0: a Newton step on the approximate reciprocal root (the
+// result is the nearest float32 but for about one in a million)
+__device__ __forceinline__ float2 root2(float2 x)
+{
+    const float2 y = make_float2(rsqrt_approx(x.x), rsqrt_approx(x.y)), r = mul2(x, y);
+    const float2 e = fma2(mul2(r, both(-1.f)), r, x), f = fma2(e, mul2(y, both(0.5f)), r);
+    return make_float2(x.x > 0.f ? f.x : x.x, x.y > 0.f ? f.y : x.y);
+}
+
+// p, m, v of two values.  The roundings of the moments are those of separate
+// multiplications and sums, so that a step can be followed to the bit; the
+// parameter takes this step's moments as they are before they are stored.
+// Returns sqrt(v).
+__device__ __forceinline__ float2 update2(const AdamStep &s, float2 g, float2 &p, float2 &m, float2 &v)
+{
+    g = mul2(g, both(s.grad_scale));
+    m = add2(mul2(m, both(s.beta1)), mul2(g, both(s.gain1)));
+    v = add2(mul2(v, both(s.beta2)), mul2(mul2(g, g), both(s.gain2)));
+    const float2 r = root2(v);
+    p = fma2(p, both(s.keep), mul2(mul2(m, both(-s.rate)), rcp_both(fma2(r, both(s.root), both(s.eps)))));
+    return r;
+}
+
+// The e4m3 code of a magnitude of at most 448, in the top byte: one of its two
+// neighbours, the upper one with the probability that the remainder is of
+// their distance (16 random bits, at bit 8 of d, added below the kept 3 bits of
+// the mantissa; d's top byte takes the difference of the exponents' biases).  Below 2^-6, where the neighbours are 2^-9
+// apart, that is done behind a shift into the binade that has this distance;
+// the larger of the two results is the right one everywhere: above 2^-6 the
+// shifted value's neighbours are further apart, below 2^-6 the value's own
+// code, taken as a normal one, is the smaller.
+__device__ __forceinline__ uint32_t dithered(float a, uint32_t d)
+{
+    const uint32_t n = (__float_as_uint(fmaxf(a, 0.0078125f)) << 4) + d;
+    return max(n, (__float_as_uint(a + 0.015625f) << 4) + d - (8u << 24));
+}
+// for m (signed) and sqrt(v), from 448 / the group's largest
+__device__ __forceinline__ uint32_t m_dithered(float y, uint32_t d)
+{
+    return dithered(fminf(fabsf(y), 448.f), __byte_perm(d, 0x40000000u, 0x7324));
+}
+__device__ __forceinline__ uint32_t v_dithered(float y, uint32_t d)
+{
+    return dithered(y > 0.f ? fminf(fmaxf(y, 0.001953125f), 448.f) : 0.f, __byte_perm(d, 0x40000000u, 0x7104));
+}
+// the top bytes of four words
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+// A group's scales from the bits of its largest magnitudes (a NaN or infinity
+// lies above all others); returns 448 / largest
+__device__ __forceinline__ float group_scale(float *scale, uint32_t bits, bool root, bool finite, bool write)
+{
+    float top = __uint_as_float(bits);
+    if (root)
+        top = root2(both(top)).x;
+    if (write)
+        *scale = finite ? __fmul_rn(top, 1.f / 448.f) : __int_as_float(0x7FC00000);
+    return finite && top > 1e-36f ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
+}
+
+// 8 values from element i, as read: 4-byte types fill both vectors
+__device__ __forceinline__ void read8(const void *p, uint64_t i, bool wide, uint4 (&q)[2])
+{
+    if (wide) {
+        q[0] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i));
+        q[1] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i) + 1);
+    } else {
+        q[0] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i));
+    }
+}
+__device__ __forceinline__ void unpack8(const uint4 (&q)[2], uint32_t type, float2 (&f)[4])
+{
+    if (type == ECC_F32) {
+        unpack2<float>(q[0], f);
+        unpack2<float>(q[1], f + 2);
+    } else if (type == ECC_BF16) {
+        unpack2<bf16>(q[0], f);
+    } else {
+        unpack2<__half>(q[0], f);
+    }
+}
+__device__ __forceinline__ void write8(void *p, uint64_t i, uint32_t type, const float2 (&f)[4])
+{
+    if (type == ECC_F32) {
+        __stcs(reinterpret_cast<uint4 *>(static_cast<float *>(p) + i), pack2<float>(f));
+        __stcs(reinterpret_cast<uint4 *>(static_cast<float *>(p) + i) + 1, pack2<float>(f + 2));
+    } else {
+        __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i), type == ECC_BF16 ? pack2<bf16>(f) : pack2<__half>(f));
+    }
+}
+__device__ __forceinline__ void unpack_e4m3(uint2 q, float scale, float2 (&f)[4])
+{
+    const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[k], __NV_E4M3);
+        f[k] = mul2(__half22float2(__half2(h)), both(scale));
+    }
+}
+
+// A warp's group of a tensor whose arrays start on 16-byte boundaries (8 for
+// byte states) and that has all 256 values: 8 neighbours a lane.  Everything is
+// asked for before anything is used.
+template <bool BYTES>
+__device__ __forceinline__ void group_by_vectors(const AdamTensor &t, uint32_t kind, uint64_t e0, uint32_t lane, const AdamStep &s)
+{
+    const uint32_t ptype = kind & 3, gtype = kind >> 2 & 3;
+    const uint64_t i = e0 + lane * 8;
+    const void *from = t.master ? t.master : t.param;
+    const uint32_t from_type = t.master ? ECC_F32 : ptype;
+    uint4 pq[2], gq[2];
+    float2 p[4], g[4];
+    if constexpr (BYTES) {
+        uint8_t *mp = static_cast<uint8_t *>(t.m) + i, *vp = static_cast<uint8_t *>(t.v) + i;
+        float *msp = t.m_scale + e0 / kAdamGroup, *vsp = t.v_scale + e0 / kAdamGroup;
+        const uint2 mq = __ldcs(reinterpret_cast<const uint2 *>(mp)), vq = __ldcs(reinterpret_cast<const uint2 *>(vp));
+        const float ms = *msp, vs = *vsp;
+        read8(from, i, from_type == ECC_F32, pq);
+        read8(t.grad, i, gtype == ECC_F32, gq);
+        unpack8(pq, from_type, p);
+        unpack8(gq, gtype, g);
+        float2 m[4], r[4];
+        unpack_e4m3(mq, ms, m);
+        unpack_e4m3(vq, vs, r);
+        uint32_t mm = 0, vm = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float2 v = mul2(r[k], r[k]);
+            r[k] = update2(s, g[k], p[k], m[k], v);
+            mm = max(mm, max(__float_as_uint(m[k].x) & 0x7FFFFFFFu, __float_as_uint(m[k].y) & 0x7FFFFFFFu));
+            vm = max(vm, max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu));
+        }
+        if (t.master)
+            write8(t.master, i, ECC_F32, p);
+        write8(t.param, i, ptype, p);
+        mm = __reduce_max_sync(~0u, mm);
+        vm = __reduce_max_sync(~0u, vm);
+        const bool finite = mm < 0x7F800000u && vm < 0x7F800000u;
+        const float mi = group_scale(msp, mm, false, finite, lane == 0);
+        const float vi = group_scale(vsp, vm, true, finite, lane == 0);
+        const uint32_t key = mix32(s.key + (uint32_t)(e0 >> 32));
+        uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
+        if (finite) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t mc[4], vc[4], sign[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t d = mix32((uint32_t)(i + h * 4 + k) ^ key);
+                    const float2 y2 = mul2(m[h * 2 + k / 2], both(mi)), z2 = mul2(r[h * 2 + k / 2], both(vi));
+                    const float y = k & 1 ? y2.y : y2.x;
+                    sign[k] = __float_as_uint(y);
+                    mc[k] = m_dithered(y, d);
+                    vc[k] = v_dithered(k & 1 ? z2.y : z2.x, d);
+                }
+                mw[h] = top_bytes(mc[0], mc[1], mc[2], mc[3]) | (top_bytes(sign[0], sign[1], sign[2], sign[3]) & 0x80808080u);
+                vw[h] = top_bytes(vc[0], vc[1], vc[2], vc[3]);
+            }
+        }
+        __stcs(reinterpret_cast<uint2 *>(mp), make_uint2(mw[0], mw[1]));
+        __stcs(reinterpret_cast<uint2 *>(vp), make_uint2(vw[0], vw[1]));
+    } else {
+        uint4 mq[2], vq[2];
+        read8(t.m, i, true, mq);
+        read8(t.v, i, true, vq);
+        read8(from, i, from_type == ECC_F32, pq);
+        read8(t.grad, i, gtype == ECC_F32, gq);
+        unpack8(pq, from_type, p);
+        unpack8(gq, gtype, g);
+        float2 m[4], v[4];
+        unpack8(mq, ECC_F32, m);
+        unpack8(vq, ECC_F32, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            update2(s, g[k], p[k], m[k], v[k]);
+        write8(t.m, i, ECC_F32, m);
+        write8(t.v, i, ECC_F32, v);
+        if (t.master)
+            write8(t.master, i, ECC_F32, p);
+        write8(t.param, i, ptype, p);
+    }
+}
+
+// Any other group, a value at a time: the lanes on neighbours.
+template <bool BYTES>
+__device__ __noinline__ void group_by_values(const AdamTensor &t, uint32_t kind, uint64_t e0, uint32_t lane, const AdamStep &s)
+{
+    const uint32_t ptype = kind & 3, gtype = kind >> 2 & 3;
+    const uint64_t group = e0 / kAdamGroup;
+    const float ms = BYTES ? t.m_scale[group] : 1.f, vs = BYTES ? t.v_scale[group] : 1.f;
+    float m[8], r[8];
+    uint32_t mm = 0, vm = 0;
+#pragma unroll 2
+    for (int k = 0; k < 8; ++k) {
+        const uint64_t i = e0 + k * 32 + lane;
+        m[k] = r[k] = 0.f;
+        if (i >= t.n)
+            continue;
+        float2 p2 = both(t.master ? t.master[i] : load_any(t.param, i, ptype)), m2, v2;
+        if constexpr (BYTES) {
+            m2 = both(__fmul_rn(to_f32(static_cast<const e4m3 *>(t.m)[i]), ms));
+            v2 = both(__fmul_rn(to_f32(static_cast<const e4m3 *>(t.v)[i]), vs));
+            v2 = mul2(v2, v2);
+        } else {
+            m2 = both(static_cast<const float *>(t.m)[i]);
+            v2 = both(static_cast<const float *>(t.v)[i]);
+        }
+        r[k] = update2(s, both(load_any(t.grad, i, gtype)), p2, m2, v2).x;
+        m[k] = m2.x;
+        mm = max(mm, __float_as_uint(m2.x) & 0x7FFFFFFFu);
+        vm = max(vm, __float_as_uint(v2.x) & 0x7FFFFFFFu);
+        if (t.master)
+            t.master[i] = p2.x;
+        store_any(t.param, i, ptype, p2.x);
+        if constexpr (!BYTES) {
+            static_cast<float *>(t.m)[i] = m2.x;
+            static_cast<float *>(t.v)[i] = v2.x;
+        }
+    }
+    if constexpr (!BYTES)
+        return;
+    mm = __reduce_max_sync(~0u, mm);
+    vm = __reduce_max_sync(~0u, vm);
+    const bool finite = mm < 0x7F800000u && vm < 0x7F800000u;
+    const float mi = group_scale(t.m_scale + group, mm, false, finite, lane == 0);
+    const float vi = group_scale(t.v_scale + group, vm, true, finite, lane == 0);
+    const uint32_t key = mix32(s.key + (uint32_t)(e0 >> 32));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint64_t i = e0 + k * 32 + lane;
+        if (i >= t.n)
+            continue;
+        const uint32_t d = mix32((uint32_t)i ^ key);
+        const float y = __fmul_rn(m[k], mi);
+        const uint32_t mc = m_dithered(y, d) >> 24 | (__float_as_uint(y) >> 24 & 0x80u);
+        const uint32_t vc = v_dithered(__fmul_rn(r[k], vi), d) >> 24;
+        static_cast<uint8_t *>(t.m)[i] = finite ? (uint8_t)mc : 0;
+        static_cast<uint8_t *>(t.v)[i] = finite ? (uint8_t)vc : 0;
+    }
+}
+
+// Blocks an SM: 3 for 8-bit states, whose instructions are the bound (82 a
+// value; 265 M values, bf16: 778 us, 3.4 TB/s; 2 blocks 889, 4 blocks 799), 2
+// for float32 states, which are bound by HBM (184 M values with masters: 794 us,
+// 6.4 TB/s; 3 blocks 859, 4 blocks 861).
+constexpr int kAdamBlocks = 2, kAdamBlocksBytes = 3;
+template <int CAP, bool BYTES>
+__global__ void __launch_bounds__(kAdamThreads, BYTES ? kAdamBlocksBytes : kAdamBlocks) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a)
+{
+    const AdamStep s = step_of(a.h);
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t at = 0;
+    for (uint32_t tile = blockIdx.x; tile < a.first[a.count]; tile += gridDim.x) {
+        if (tile >= a.first[at + 1]) { // the last tensor that starts at or before this tile
+            uint32_t lo = at + 1, hi = a.count - 1;
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi + 1) / 2;
+                if (a.first[mid] <= tile)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            at = lo;
+        }
+        const AdamTensor &t = a.t[at];
+        const uint32_t kind = a.kind[at];
+        const uint64_t e0 = (uint64_t)(tile - a.first[at]) * kAdamTile + warp * kAdamGroup;
+        if (e0 >= t.n)
+            continue;
+        if ((kind & kAdamVectors) && e0 + kAdamGroup <= t.n)
+            group_by_vectors<BYTES>(t, kind, e0, lane, s);
+        else
+            group_by_values<BYTES>(t, kind, e0, lane, s);
+    }
+}
+
+namespace {
+
+// Types and pointers of a tensor; nothing of an empty one is looked at.
+bool tensor_ok(const ecc_adamw_tensor &t)
+{
+    if (!wide_type(t.param_type) || !wide_type(t.grad_type) || (t.state_type != ECC_F32 && t.state_type != ECC_E4M3) || t.reserved)
+        return false;
+    if (!t.n)
+        return true;
+    if (t.n >= 1ull << 40 || !t.param || !t.grad || !t.m || !t.v || !aligned_to(t.param, t.param_type) ||
+        !aligned_to(t.grad, t.grad_type) || !aligned_to(t.m, t.state_type) || !aligned_to(t.v, t.state_type) ||
+        !aligned_to(t.master, ECC_F32))
+        return false;
+    return t.state_type == ECC_F32 ||
+           (t.m_scale && t.v_scale && aligned_to(t.m_scale, ECC_F32) && aligned_to(t.v_scale, ECC_F32));
+}
+
+bool by_vectors(const ecc_adamw_tensor &t)
+{
+    const uintptr_t states = (uintptr_t)t.m | (uintptr_t)t.v;
+    return (((uintptr_t)t.param | (uintptr_t)t.grad | (uintptr_t)t.master) & 15) == 0 &&
+           (states & (t.state_type == ECC_E4M3 ? 7 : 15)) == 0;
+}
+
+// Whether two of the written arrays overlap (a tensor given twice would be
+// updated by two warps at once).
+bool apart(const ecc_adamw_job &j)
+{
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+    spans.reserve(j.count * 6);
+    auto add = [&](const void *p, uint64_t bytes) {
+        if (p)
+            spans.emplace_back((uintptr_t)p, (uintptr_t)p + bytes);
+    };
+    for (uint64_t i = 0; i < j.count; ++i) {
+        const ecc_adamw_tensor &t = j.tensors[i];
+        if (!t.n)
+            continue;
+        const uint64_t state = t.n * type_bytes(t.state_type), scales = (t.n + kAdamGroup - 1) / kAdamGroup * sizeof(float);
+        add(t.param, t.n * type_bytes(t.param_type));
+        add(t.m, state);
+        add(t.v, state);
+        add(t.master, t.n * sizeof(float));
+        if (t.state_type == ECC_E4M3) {
+            add(t.m_scale, scales);
+            add(t.v_scale, scales);
+        }
+    }
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i)
+        if (spans[i].first < spans[i - 1].second)
+            return false;
+    return true;
+}
+
+// the next tensors with states of the one kind
+template <int CAP, bool BYTES> ecc_status launch_tensors(const ecc_adamw_job &j, const AdamHyper &h, uint64_t &next, cudaStream_t st)
+{
+    AdamArgs<CAP> a;
+    a.h = h;
+    a.count = 0;
+    uint64_t tiles = 0;
+    for (; next < j.count && a.count < CAP; ++next) {
+        const ecc_adamw_tensor &t = j.tensors[next];
+        if ((t.state_type == ECC_E4M3) != BYTES)
+            continue;
+        const uint64_t own = (t.n + kAdamTile - 1) / kAdamTile;
+        if (!own)
+            continue;
+        if (tiles + own >= 1ull << 31)
+            break; // (one tensor has fewer than 2^29 tiles)
+        a.first[a.count] = (uint32_t)tiles;
+        a.t[a.count] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.master, t.n};
+        a.kind[a.count] = (uint8_t)(t.param_type | t.grad_type << 2 | (by_vectors(t) ? kAdamVectors : 0));
+        ++a.count;
+        tiles += own;
+    }
+    if (!a.count)
+        return ECC_OK;
+    a.first[a.count] = (uint32_t)tiles;
+    const int sms = sm_count();
+    if (sms <= 0)
+        return ECC_ERR_CUDA;
+    const uint64_t most = (uint64_t)sms * (BYTES ? kAdamBlocksBytes : kAdamBlocks);
+    adamw_kernel<CAP, BYTES><<<(unsigned)std::min(tiles, most), kAdamThreads, 0, st>>>(a);
+    return launch_status(cudaGetLastError());
+}
+
+bool job_ok(const ecc_adamw_job &j)
+{
+    if ((j.count && !j.tensors) || j.reserved || !std::isfinite(j.lr) || !(j.beta1 >= 0 && j.beta1 < 1) ||
+        !(j.beta2 >= 0 && j.beta2 < 1) || !(j.eps >= 0) || !std::isfinite(j.eps) || !std::isfinite(j.weight_decay) ||
+        !std::isfinite(j.grad_scale) || (!j.step_at && j.step < 1) || ((uintptr_t)j.step_at & 7) || !aligned_to(j.lr_at, ECC_F32) ||
+        !aligned_to(j.grad_scale_at, ECC_F32))
+        return false;
+    for (uint64_t i = 0; i < j.count; ++i)
+        if (!tensor_ok(j.tensors[i]))
+            return false;
+    return true;
+}
+
+} // namespace
+} // namespace ecc
+
+using namespace ecc;
+
+extern "C" ecc_status ecc_adamw(const ecc_adamw_job *job, void *stream)
+try {
+    if (!job || !job_ok(*job) || !apart(*job))
+        return ECC_ERR_ARG;
+    const ecc_adamw_job &j = *job;
+    AdamHyper h{};
+    h.beta1 = (float)j.beta1;
+    h.beta2 = (float)j.beta2;
+    h.gain1 = (float)(1 - j.beta1);
+    h.gain2 = (float)(1 - j.beta2);
+    // (beta = 0: 1 - beta^step is 1 for every step)
+    h.log_beta1 = j.beta1 > 0 ? (float)std::log(j.beta1) : -200.f;
+    h.log_beta2 = j.beta2 > 0 ? (float)std::log(j.beta2) : -200.f;
+    h.eps = (float)j.eps;
+    h.weight_decay = (float)j.weight_decay;
+    h.lr = (float)j.lr;
+    h.grad_scale = (float)j.grad_scale;
+    h.seed = j.seed;
+    if (!j.step_at) {
+        h.step = (uint32_t)j.step;
+        h.rate = (float)(1 / (1 - std::pow(j.beta1, (double)j.step)));
+        h.root = (float)std::sqrt(1 / (1 - std::pow(j.beta2, (double)j.step)));
+    }
+    h.lr_at = j.lr_at;
+    h.grad_scale_at = j.grad_scale_at;
+    h.step_at = j.step_at;
+    ecc_status rc = ECC_OK;
+    // (parameters of 2 KiB or of 31 KiB: the launch copies them)
+    cudaStream_t st = (cudaStream_t)stream;
+    for (uint64_t next = 0; rc == ECC_OK && next < j.count;)
+        rc = j.count - next <= 24 ? launch_tensors<24, false>(j, h, next, st) : launch_tensors<448, false>(j, h, next, st);
+    for (uint64_t next = 0; rc == ECC_OK && next < j.count;)
+        rc = j.count - next <= 24 ? launch_tensors<24, true>(j, h, next, st) : launch_tensors<448, true>(j, h, next, st);
+    return rc;
+} catch (...) { // no memory for the list of spans
+    return ECC_ERR_ARG;
+}

@@ -18,6 +18,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
+#include <vector>
 
 #include "ecc_lm.h"
 
@@ -456,6 +457,107 @@ FUNCTION(token_logprob_grad, 8)
     return wrap(d);
 }
 
+// A list argument: its tensors by number (None: none at all)
+struct List {
+    PyObject *seq = nullptr;
+    List(PyObject *o, Py_ssize_t n, const char *what) // n < 0: as many as there are
+    {
+        if (o == Py_None)
+            return;
+        if (!PyList_Check(o) && !PyTuple_Check(o))
+            refuse(what);
+        if (n >= 0 && PySequence_Fast_GET_SIZE(o) != n)
+            refuse(what);
+        seq = o;
+    }
+    Opt operator()(Py_ssize_t i, const char *what) const
+    {
+        return seq ? tensor(PySequence_Fast_GET_ITEM(seq, i), what) : nullptr;
+    }
+};
+// a number, or a tensor of one value that the kernel reads
+template <typename T> const T *value_at(PyObject *o, c10::Device dev, const char *what)
+{
+    if (!THPVariable_Check(o))
+        return nullptr;
+    return (const T *)vector(tensor(o, what), 1, dev, what, sizeof(T) == 8 ? at::kLong : at::kFloat);
+}
+
+// params, grads, m, v, m_scale, v_scale, master, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed
+FUNCTION(adamw, 15)
+{
+    const char *what = "ecc_adamw: params and grads";
+    if (!PyList_Check(a[0]) && !PyTuple_Check(a[0]))
+        refuse(what);
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(a[0]);
+    const List params(a[0], n, what), grads(a[1], n, what), ms(a[2], n, "ecc_adamw: m"), vs(a[3], n, "ecc_adamw: v");
+    const List mss(a[4], n, "ecc_adamw: m_scale"), vss(a[5], n, "ecc_adamw: v_scale"), masters(a[6], n, "ecc_adamw: master");
+    if (!grads.seq || !ms.seq || !vs.seq)
+        refuse(what);
+    std::optional<On> on;
+    std::vector<ecc_adamw_tensor> list;
+    list.reserve((size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        Opt p = params(i, what), g = grads(i, what);
+        if (!g) // nothing to learn from
+            continue;
+        if (!p || !p->is_cuda() || p->sizes() != g->sizes())
+            refuse(what);
+        if (!on)
+            on.emplace(*p);
+        const c10::Device dev = on->dev;
+        const uint64_t len = (uint64_t)p->numel();
+        ecc_adamw_tensor t{};
+        t.n = len;
+        t.param = vector(p, len, dev, what);
+        t.param_type = type_of(p->scalar_type(), what);
+        t.grad = vector(g, len, dev, what);
+        t.grad_type = type_of(g->scalar_type(), what);
+        Opt m = ms(i, "ecc_adamw: m"), v = vs(i, "ecc_adamw: v");
+        if (!m || !v)
+            refuse("ecc_adamw: m and v");
+        t.m = vector(m, len, dev, "ecc_adamw: m");
+        t.state_type = type_of(m->scalar_type(), "ecc_adamw: m");
+        t.v = vector(v, len, dev, "ecc_adamw: v", m->scalar_type());
+        if (t.state_type == ECC_E4M3) {
+            const uint64_t groups = (len + ECC_ADAMW_GROUP - 1) / ECC_ADAMW_GROUP;
+            Opt s = mss(i, "ecc_adamw: m_scale"), r = vss(i, "ecc_adamw: v_scale");
+            if (!s || !r)
+                refuse("ecc_adamw: m_scale and v_scale");
+            t.m_scale = (float *)vector(s, groups, dev, "ecc_adamw: m_scale", at::kFloat);
+            t.v_scale = (float *)vector(r, groups, dev, "ecc_adamw: v_scale", at::kFloat);
+        }
+        t.master = (float *)vector(masters(i, "ecc_adamw: master"), len, dev, "ecc_adamw: master", at::kFloat);
+        list.push_back(t);
+    }
+    ecc_adamw_job j{};
+    j.tensors = list.data();
+    j.count = list.size();
+    if (!on)
+        Py_RETURN_NONE;
+    j.step_at = value_at<int64_t>(a[7], on->dev, "ecc_adamw: step");
+    j.lr_at = value_at<float>(a[8], on->dev, "ecc_adamw: lr");
+    j.grad_scale_at = value_at<float>(a[13], on->dev, "ecc_adamw: grad_scale");
+    if (!j.step_at) {
+        const long step = integer(a[7]);
+        if (step < 1)
+            refuse("ecc_adamw: step");
+        j.step = (uint64_t)step;
+    }
+    j.lr = j.lr_at ? 0.0 : number(a[8]);
+    j.beta1 = number(a[9]);
+    j.beta2 = number(a[10]);
+    j.eps = number(a[11]);
+    j.weight_decay = number(a[12]);
+    j.grad_scale = j.grad_scale_at ? 1.0 : number(a[13]);
+    const long seed = integer(a[14]);
+    if (seed < 0 || seed > 0xFFFFFFFFL)
+        refuse("ecc_adamw: seed");
+    j.seed = (uint32_t)seed;
+    check(ecc_adamw(&j, on->stream), "ecc_adamw");
+    Py_RETURN_NONE;
+}
+
 PyObject *set_error(PyObject *, PyObject *cls)
 {
     Py_INCREF(cls);
@@ -465,7 +567,7 @@ PyObject *set_error(PyObject *, PyObject *cls)
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {METHOD(layer_norm),    METHOD(layer_norm_grad), METHOD(linear), METHOD(linear_grad),
-                           METHOD(token_logprob), METHOD(token_logprob_grad), {"set_error", set_error, METH_O, nullptr},
+                           METHOD(token_logprob), METHOD(token_logprob_grad), METHOD(adamw), {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "ecc_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
