@@ -139,6 +139,60 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
                            void *stream);
 
 /*
+ * ecc_gated_linear -- out = act(g) * u with g = scale * x w_gate^T + bias_gate
+ * and u = up_scale * x w_up^T + bias_up: a gated feed-forward block's
+ * projections, its activation and their product.
+ *   x     [M, K], w_gate, w_up [N, K] of in_type: BF16, F16 or E4M3.
+ *   bias_gate, bias_up  [N] of bias_type (F32, BF16, F16), each NULL if there
+ *         is none.
+ *   out   [M, N] of out_type (F32, BF16, F16, or E4M3 = out * out_scale;
+ *         out_scale must be 1 for the other types).
+ *   pre_gate, pre_up  [M, N] of pre_type (F32, BF16, F16): g and u, for the
+ *         backward pass; or both NULL.
+ * M, N, K, ws, status and errors as for ecc_linear (`reserved` is 0).
+ */
+typedef struct ecc_gated_linear_job {
+    const void *x, *w_gate, *w_up, *bias_gate, *bias_up;
+    void *out, *pre_gate, *pre_up;
+    uint64_t M, N, K;
+    uint64_t ldx, ldgate, ldup, ldout, ldpre_gate, ldpre_up;
+    float scale, up_scale, out_scale;
+    uint32_t in_type, bias_type, out_type, pre_type, act, reserved;
+} ecc_gated_linear_job;
+
+size_t ecc_gated_linear_workspace_bytes(const ecc_gated_linear_job *job);
+ecc_status ecc_gated_linear(const ecc_gated_linear_job *job, void *ws, size_t ws_bytes, uint32_t *status, void *stream);
+
+/*
+ * ecc_gated_linear_grad -- the backward pass: with tg = dy u act'(g) and tu =
+ * dy act(g), g and u as kept in pre_gate and pre_up,
+ *   dx = scale * tg w_gate + up_scale * tu w_up,
+ *   dw_gate = scale * tg^T x, dw_up = up_scale * tu^T x,
+ *   dbias_gate, dbias_up = sums over rows of tg, tu.
+ *   dy    [M, N], x [M, K], w_gate, w_up [N, K], dx [M, K] of in_type (BF16 or
+ *         F16); pre_gate, pre_up [M, N] of pre_type (F32, BF16, F16).
+ *   dw_gate, dw_up  [N, K] of dw_type (in_type or F32), both or neither.
+ *   dbias_gate, dbias_up  float32[N], both or neither.
+ *   dx, dw_*, dbias_*: NULL if not wanted.
+ *   tg and tu, each times its scale's share of the larger scale, are rounded to
+ *   in_type before the products; the dbias sums are taken before that.
+ * ws, status and errors as for ecc_linear.
+ */
+typedef struct ecc_gated_linear_grad_job {
+    const void *dy, *x, *w_gate, *w_up, *pre_gate, *pre_up;
+    void *dx, *dw_gate, *dw_up;
+    float *dbias_gate, *dbias_up;
+    uint64_t M, N, K;
+    uint64_t lddy, ldx, ldgate, ldup, ldpre_gate, ldpre_up, lddx, lddw_gate, lddw_up;
+    float scale, up_scale;
+    uint32_t in_type, pre_type, dw_type, act;
+} ecc_gated_linear_grad_job;
+
+size_t ecc_gated_linear_grad_workspace_bytes(const ecc_gated_linear_grad_job *job);
+ecc_status ecc_gated_linear_grad(const ecc_gated_linear_grad_job *job, void *ws, size_t ws_bytes, uint32_t *status,
+                                 void *stream);
+
+/*
  * ecc_token_logprob -- for each row z = scale * logits: the log partition
  * lse = log sum e^z, the given token's log probability z[token] - lse, the
  * entropy H = -sum p log p (p log p = 0 where p = 0) and the `top` most

@@ -111,6 +111,10 @@ def _load():
             "ecc_linear": (I32, [P, P, Z, P, P]),
             "ecc_linear_grad_workspace_bytes": (Z, [P]),
             "ecc_linear_grad": (I32, [P, P, Z, P, P]),
+            "ecc_gated_linear_workspace_bytes": (Z, [P]),
+            "ecc_gated_linear": (I32, [P, P, Z, P, P]),
+            "ecc_gated_linear_grad_workspace_bytes": (Z, [P]),
+            "ecc_gated_linear_grad": (I32, [P, P, Z, P, P]),
             "ecc_adamw": (I32, [P, P]),
             "ecc_token_logprob": (I32, [P, U64, U32, P, U64, U64, F, U32, P, P, P, P, P, P]),
             "ecc_token_logprob_grad": (I32, [P, U64, U32, P, U64, U64, F, P, P, P, P, P, U64, P]),
@@ -648,6 +652,32 @@ def ecc_linear_grad(dy, x, w, pre=None, act: str = "none", scale: float = 1.0, d
     bits = ("dx" in want) + 2 * ("dw" in want) + 4 * ("dbias" in want)
     return (_torch_lib or _marshal()).linear_grad(dy, x, w, pre, _activation(act, "ecc_linear_grad"), scale, dx, dw, dbias,
                                                   dw_dtype, bits, ws, status)
+
+
+@_on_stream
+def ecc_gated_linear(x, w_gate, w_up, bias_gate=None, bias_up=None, act: str = "silu", scale: float = 1.0, up_scale=None,
+                     out=None, out_dtype=None, out_scale: float = 1.0, pre_gate=None, pre_up=None, ws=None, status=None):
+    """act(g) * u with g = scale * x w_gate^T + bias_gate and u = up_scale *
+    x w_up^T + bias_up (up_scale: scale by default) of device tensors x [..., K],
+    w_gate and w_up [N, K] (bfloat16, float16 or e4m3); returns (out [..., N],
+    status).  out_dtype and out_scale as for ecc_linear.  pre_gate, pre_up:
+    tensors [..., N] of one type that receive g and u, for
+    ecc_gated_linear_grad."""
+    return (_torch_lib or _marshal()).gated_linear(x, w_gate, w_up, bias_gate, bias_up, _activation(act, "ecc_gated_linear"),
+                                                   scale, up_scale, out, out_dtype, out_scale, pre_gate, pre_up, ws, status)
+
+
+@_on_stream
+def ecc_gated_linear_grad(dy, x, w_gate, w_up, pre_gate, pre_up, act: str = "silu", scale: float = 1.0, up_scale=None,
+                          dx=None, dw_gate=None, dw_up=None, dbias_gate=None, dbias_up=None, dw_dtype=None,
+                          want=("dx", "dw", "dbias"), ws=None, status=None):
+    """Backward pass of ecc_gated_linear; returns (dx, dw_gate, dw_up,
+    dbias_gate, dbias_up, status), None for what `want` leaves out.  dw_dtype:
+    x's type (default) or float32; the dbias are float32."""
+    bits = ("dx" in want) + 2 * ("dw" in want) + 4 * ("dbias" in want)
+    return (_torch_lib or _marshal()).gated_linear_grad(
+        dy, x, w_gate, w_up, pre_gate, pre_up, _activation(act, "ecc_gated_linear_grad"), scale, up_scale, dx, dw_gate, dw_up,
+        dbias_gate, dbias_up, dw_dtype, bits, ws, status)
 
 
 class TokenLogprob(NamedTuple):

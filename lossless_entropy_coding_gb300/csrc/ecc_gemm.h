@@ -8,6 +8,9 @@
 
 namespace ecc {
 
+// What a kernel makes of its products (ecc_gemm.cuh)
+enum GemmMode { kPlain, kGated, kDual, kStats, kSlopes };
+
 // out[r, c] = act(scale * sum over k of Q[r, k] P[c, k] + bias[c]) + residual[r, c]
 struct Epilogue {
     const void *bias, *residual;
@@ -15,6 +18,16 @@ struct Epilogue {
     uint64_t ldres, ldout, ldpre;
     float scale, out_scale;
     uint32_t bias_type, res_type, out_type, pre_type, act;
+    // gated products: act(scale * sum + bias) * (scale2 * sum2 + bias2); pre2 beside pre
+    const void *bias2;
+    void *pre2;
+    uint64_t ldpre2;
+    float scale2;
+    // a second output: rows from rswitch on (a multiple of 64) go to out2, and
+    // both have rows2 rows
+    void *out2;
+    uint64_t ldout2, rswitch, rows2;
+    const float *factor; // multiplies scale (read on the device); NULL: 1
 };
 
 // An operand: `rows` x K values, either stored a matrix row after the other
@@ -29,10 +42,16 @@ struct Operand {
 // whether an array of `rows` rows can be read by tiled TMA as it is
 bool tma_rows(const void *p, uint64_t ld, uint32_t type, uint64_t rows);
 // rows x cols values from a reduction of K; P holds the output's columns, Q its rows
+// (kGated: P and P2 hold the columns' gates and ups;
+// kDual: the reduction's indices from kswitch on, a multiple of 64, are
+// P2's; both have kfirst of them)
 struct Product {
     Operand P, Q;
     uint64_t rows, cols, K;
     Epilogue e;
+    GemmMode mode = kPlain;
+    Operand P2{};
+    uint64_t kswitch = 0, kfirst = 0;
 };
 // clear_status: the launch sets *status to ECC_OK; behind: the stream's last
 // launch is one of the same call's that lets this one start early
@@ -41,5 +60,10 @@ ecc_status gemm(const Product &x, uint32_t type, uint32_t *status, bool clear_st
 // operands down their columns (16-bit types)
 ecc_status gemm_backward(const Product &dx, const Product &dw, uint32_t type, uint32_t *status, bool clear_status, bool behind,
                          cudaStream_t st);
+
+// kernels that are built apart
+const void *gated_kernel(bool f8, bool pair);
+const void *dual_kernel(bool pair);
+const void *dual_both_kernel();
 
 } // namespace ecc

@@ -409,6 +409,145 @@ FUNCTION(linear_grad, 13)
     return results(dx, dw, db, status);
 }
 
+// x, w_gate, w_up, bias_gate, bias_up, act, scale, up_scale, out, out_dtype, out_scale, pre_gate, pre_up, ws, status
+FUNCTION(gated_linear, 15)
+{
+    const at::Tensor &x = first(a[0], "ecc_gated_linear: needs CUDA tensors");
+    const On on(x);
+    const Matrix mx = matrix(x, on.dev, "ecc_gated_linear: x");
+    Opt wg = tensor(a[1], "ecc_gated_linear: w_gate"), wu = tensor(a[2], "ecc_gated_linear: w_up");
+    if (!wg || !wu || wg->dim() != 2 || wu->dim() != 2)
+        refuse("ecc_gated_linear: w_gate and w_up");
+    const uint64_t N = (uint64_t)wg->size(0);
+    const Matrix mg = operand(wg, N, mx.cols, on.dev, "ecc_gated_linear: w_gate"), mu = operand(wu, N, mx.cols, on.dev, "ecc_gated_linear: w_up");
+    if (mg.type != mx.type || mu.type != mx.type)
+        refuse("ecc_gated_linear: x, w_gate and w_up of different types");
+    Opt bg = tensor(a[3], "ecc_gated_linear: bias_gate"), bu = tensor(a[4], "ecc_gated_linear: bias_up");
+    const at::ScalarType b_type = bg ? bg->scalar_type() : bu ? bu->scalar_type() : at::kFloat;
+    at::DimVector size(x.sizes().begin(), x.sizes().end());
+    size.back() = (int64_t)N;
+    at::Tensor out = output(tensor(a[8], "ecc_gated_linear: out"), size,
+                            dtype(a[9], "ecc_gated_linear: out_dtype").value_or(mx.type == ECC_E4M3 ? at::kBFloat16 : x.scalar_type()),
+                            on.dev);
+    at::Tensor status = output(tensor(a[14], "ecc_gated_linear: status"), {1}, at::kInt, on.dev);
+    const Matrix mo = operand(&out, mx.rows, N, on.dev, "ecc_gated_linear: out");
+    const Matrix pg = operand(tensor(a[11], "ecc_gated_linear: pre_gate"), mx.rows, N, on.dev, "ecc_gated_linear: pre_gate");
+    const Matrix pu = operand(tensor(a[12], "ecc_gated_linear: pre_up"), mx.rows, N, on.dev, "ecc_gated_linear: pre_up");
+    if ((a[11] == Py_None) != (a[12] == Py_None) || (pg.p && pg.type != pu.type))
+        refuse("ecc_gated_linear: pre_gate and pre_up");
+    ecc_gated_linear_job j{};
+    j.x = mx.p;
+    j.w_gate = mg.p;
+    j.w_up = mu.p;
+    j.bias_gate = vector(bg, N, on.dev, "ecc_gated_linear: bias_gate", b_type);
+    j.bias_up = vector(bu, N, on.dev, "ecc_gated_linear: bias_up", b_type);
+    j.out = mo.p;
+    j.pre_gate = pg.p;
+    j.pre_up = pu.p;
+    j.M = mx.rows;
+    j.N = N;
+    j.K = mx.cols;
+    j.ldx = mx.ld;
+    j.ldgate = mg.ld;
+    j.ldup = mu.ld;
+    j.ldout = mo.ld;
+    j.ldpre_gate = pg.ld;
+    j.ldpre_up = pu.ld;
+    j.scale = (float)number(a[6]);
+    j.up_scale = a[7] == Py_None ? j.scale : (float)number(a[7]);
+    j.out_scale = (float)number(a[10]);
+    j.in_type = mx.type;
+    j.bias_type = type_of(b_type, "ecc_gated_linear: bias");
+    j.out_type = mo.type;
+    j.pre_type = pg.type;
+    j.act = (uint32_t)integer(a[5]);
+    at::Tensor ws = scratch(tensor(a[13], "ecc_gated_linear: ws"), ecc_gated_linear_workspace_bytes(&j), on.dev, "ecc_gated_linear: ws");
+    check(ecc_gated_linear(&j, where(ws), bytes_of(ws), status_word(status, on.dev, "ecc_gated_linear: status"), on.stream),
+          "ecc_gated_linear");
+    return results(out, status);
+}
+
+// dy, x, w_gate, w_up, pre_gate, pre_up, act, scale, up_scale, dx, dw_gate, dw_up, dbias_gate, dbias_up, dw_dtype,
+// want (bits: 1 dx, 2 dw, 4 dbias), ws, status
+FUNCTION(gated_linear_grad, 18)
+{
+    const at::Tensor &dy = first(a[0], "ecc_gated_linear_grad: needs CUDA tensors");
+    const On on(dy);
+    const Matrix md = matrix(dy, on.dev, "ecc_gated_linear_grad: dy");
+    const at::Tensor &x = first(a[1], "ecc_gated_linear_grad: x");
+    const at::Tensor &wg = first(a[2], "ecc_gated_linear_grad: w_gate"), &wu = first(a[3], "ecc_gated_linear_grad: w_up");
+    if (!x.dim())
+        refuse("ecc_gated_linear_grad: x");
+    const uint64_t M = md.rows, N = md.cols, K = (uint64_t)x.size(-1);
+    const Matrix mx = operand(&x, M, K, on.dev, "ecc_gated_linear_grad: x"), mg = operand(&wg, N, K, on.dev, "ecc_gated_linear_grad: w_gate"),
+                 mu = operand(&wu, N, K, on.dev, "ecc_gated_linear_grad: w_up");
+    if (mx.type != md.type || mg.type != md.type || mu.type != md.type)
+        refuse("ecc_gated_linear_grad: dy, x, w_gate and w_up of different types");
+    Opt og = tensor(a[4], "ecc_gated_linear_grad: pre_gate"), ou = tensor(a[5], "ecc_gated_linear_grad: pre_up");
+    if (!og || !ou || og->scalar_type() != ou->scalar_type())
+        refuse("ecc_gated_linear_grad: pre_gate and pre_up");
+    const Matrix pg = operand(og, M, N, on.dev, "ecc_gated_linear_grad: pre_gate"), pu = operand(ou, M, N, on.dev, "ecc_gated_linear_grad: pre_up");
+    const long want = integer(a[15]);
+    Opt gx = tensor(a[9], "ecc_gated_linear_grad: dx"), gg = tensor(a[10], "ecc_gated_linear_grad: dw_gate");
+    Opt gu = tensor(a[11], "ecc_gated_linear_grad: dw_up"), hg = tensor(a[12], "ecc_gated_linear_grad: dbias_gate");
+    Opt hu = tensor(a[13], "ecc_gated_linear_grad: dbias_up");
+    at::Tensor dx, dg, du, bg, bu;
+    if (gx || (want & 1))
+        dx = output(gx, x.sizes(), x.scalar_type(), on.dev);
+    if (gg || gu || (want & 2)) {
+        const at::ScalarType type = gg   ? gg->scalar_type()
+                                    : gu ? gu->scalar_type()
+                                         : dtype(a[14], "ecc_gated_linear_grad: dw_dtype").value_or(x.scalar_type());
+        dg = output(gg, {(int64_t)N, (int64_t)K}, type, on.dev);
+        du = output(gu, {(int64_t)N, (int64_t)K}, type, on.dev);
+    }
+    if (hg || hu || (want & 4)) {
+        bg = output(hg, {(int64_t)N}, at::kFloat, on.dev);
+        bu = output(hu, {(int64_t)N}, at::kFloat, on.dev);
+    }
+    at::Tensor status = output(tensor(a[17], "ecc_gated_linear_grad: status"), {1}, at::kInt, on.dev);
+    const Matrix mdx = operand(dx.defined() ? &dx : nullptr, M, K, on.dev, "ecc_gated_linear_grad: dx");
+    const Matrix mdg = operand(dg.defined() ? &dg : nullptr, N, K, on.dev, "ecc_gated_linear_grad: dw_gate");
+    const Matrix mdu = operand(du.defined() ? &du : nullptr, N, K, on.dev, "ecc_gated_linear_grad: dw_up");
+    if ((dx.defined() && mdx.type != md.type) || mdg.type != mdu.type)
+        refuse("ecc_gated_linear_grad: dx, dw_gate or dw_up of another type");
+    ecc_gated_linear_grad_job j{};
+    j.dy = md.p;
+    j.x = mx.p;
+    j.w_gate = mg.p;
+    j.w_up = mu.p;
+    j.pre_gate = pg.p;
+    j.pre_up = pu.p;
+    j.dx = mdx.p;
+    j.dw_gate = mdg.p;
+    j.dw_up = mdu.p;
+    j.dbias_gate = (float *)vector(bg.defined() ? &bg : nullptr, N, on.dev, "ecc_gated_linear_grad: dbias_gate", at::kFloat);
+    j.dbias_up = (float *)vector(bu.defined() ? &bu : nullptr, N, on.dev, "ecc_gated_linear_grad: dbias_up", at::kFloat);
+    j.M = M;
+    j.N = N;
+    j.K = K;
+    j.lddy = md.ld;
+    j.ldx = mx.ld;
+    j.ldgate = mg.ld;
+    j.ldup = mu.ld;
+    j.ldpre_gate = pg.ld;
+    j.ldpre_up = pu.ld;
+    j.lddx = mdx.ld;
+    j.lddw_gate = mdg.ld;
+    j.lddw_up = mdu.ld;
+    j.scale = (float)number(a[7]);
+    j.up_scale = a[8] == Py_None ? j.scale : (float)number(a[8]);
+    j.in_type = md.type;
+    j.pre_type = pg.type;
+    j.dw_type = mdg.type;
+    j.act = (uint32_t)integer(a[6]);
+    at::Tensor ws = scratch(tensor(a[16], "ecc_gated_linear_grad: ws"), ecc_gated_linear_grad_workspace_bytes(&j), on.dev,
+                            "ecc_gated_linear_grad: ws");
+    check(ecc_gated_linear_grad(&j, where(ws), bytes_of(ws), status_word(status, on.dev, "ecc_gated_linear_grad: status"), on.stream),
+          "ecc_gated_linear_grad");
+    return results(dx, dg, du, bg, bu, status);
+}
+
 // logits, tokens, top, scale
 FUNCTION(token_logprob, 4)
 {
@@ -567,7 +706,8 @@ PyObject *set_error(PyObject *, PyObject *cls)
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {METHOD(layer_norm),    METHOD(layer_norm_grad), METHOD(linear), METHOD(linear_grad),
-                           METHOD(token_logprob), METHOD(token_logprob_grad), METHOD(adamw), {"set_error", set_error, METH_O, nullptr},
+                           METHOD(token_logprob), METHOD(token_logprob_grad), METHOD(adamw),
+                           METHOD(gated_linear), METHOD(gated_linear_grad), {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "ecc_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
