@@ -242,6 +242,70 @@ ecc_status ecc_token_logprob_grad(const void *logits, uint64_t ld, uint32_t type
                                   uint64_t ldd, void *stream);
 
 /*
+ * ecc_linear_logprob -- what ecc_token_logprob gives of z = scale * x w^T (a
+ * head's logits), which are never stored: the log partition lse, the entropy
+ * and the given token's log probability of each row, from float32 logits.
+ *   x     [rows, K], w [vocab, K] of in_type: BF16, F16 or E4M3.
+ *   tokens  int64[rows], or NULL.  A negative token means none: its log
+ *         probability is 0.  A token >= vocab gets NaN.
+ *   logprob, entropy, lse  float32[rows]; logprob is not written without
+ *         tokens; each may be NULL.
+ *   A row with a logit that is not finite has NaN results.
+ *   ws    16-byte aligned scratch of ecc_linear_logprob_workspace_bytes(job)
+ *         bytes (16 bytes a row for each 64 to 128 tokens of the vocabulary, and
+ *         a copy of x and w whose rows are not on 16-byte boundaries).
+ * vocab from 1 to 2^31 - 1, rows and K below 2^31; K = 0 gives logits of 0.
+ * status and errors as for ecc_linear (`reserved` is 0).
+ */
+typedef struct ecc_linear_logprob_job {
+    const void *x, *w;
+    const int64_t *tokens;
+    float *logprob, *entropy, *lse;
+    uint64_t rows, vocab, K, ldx, ldw;
+    float scale;
+    uint32_t in_type, reserved;
+} ecc_linear_logprob_job;
+
+size_t ecc_linear_logprob_workspace_bytes(const ecc_linear_logprob_job *job);
+ecc_status ecc_linear_logprob(const ecc_linear_logprob_job *job, void *ws, size_t ws_bytes, uint32_t *status, void *stream);
+
+/*
+ * ecc_linear_logprob_grad -- the gradient of sum over rows of dlogprob * logprob
+ * + dentropy * entropy: with
+ *   t = dlogprob (1[v = token] - p) - dentropy p (log p + H), p = e^(z - lse),
+ *   dx = scale * t w, dw = scale * t^T x.
+ * The logits are computed again, a piece of the vocabulary at a time.
+ *   x [rows, K], w [vocab, K], dx [rows, K] of in_type (BF16 or F16).
+ *   lse, entropy  as written by ecc_linear_logprob for the same x and w (lse's
+ *         rounding is p's relative error: 2^-24 |lse|); entropy may be NULL
+ *         if dentropy is.
+ *   dlogprob, dentropy  float32[rows]; NULL = zeros.  Rows whose token is
+ *         negative or >= vocab take no part in dlogprob.
+ *   dw    [vocab, K] of dw_type (in_type or F32).
+ *   dx, dw: NULL if not wanted.
+ *   t is rounded to in_type before the products; with F16 the rows' largest
+ *   dlogprob and dentropy give a power of two that keeps small probabilities
+ *   in its range.
+ *   ws    16-byte aligned scratch of ecc_linear_logprob_grad_workspace_bytes(job)
+ *         bytes (t of a piece, at most 256 MiB or 512 bytes a row, dx's sum
+ *         over the pieces, copies as above).
+ * status and errors as for ecc_linear (`reserved` is 0).
+ */
+typedef struct ecc_linear_logprob_grad_job {
+    const void *x, *w;
+    const int64_t *tokens;
+    const float *lse, *entropy, *dlogprob, *dentropy;
+    void *dx, *dw;
+    uint64_t rows, vocab, K, ldx, ldw, lddx, lddw;
+    float scale;
+    uint32_t in_type, dw_type, reserved;
+} ecc_linear_logprob_grad_job;
+
+size_t ecc_linear_logprob_grad_workspace_bytes(const ecc_linear_logprob_grad_job *job);
+ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void *ws, size_t ws_bytes, uint32_t *status,
+                                   void *stream);
+
+/*
  * ecc_adamw -- one step of AdamW over many tensors at once.  With g =
  * grad_scale * grad, t = step:
  *   m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2,

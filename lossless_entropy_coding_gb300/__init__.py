@@ -115,6 +115,10 @@ def _load():
             "ecc_gated_linear": (I32, [P, P, Z, P, P]),
             "ecc_gated_linear_grad_workspace_bytes": (Z, [P]),
             "ecc_gated_linear_grad": (I32, [P, P, Z, P, P]),
+            "ecc_linear_logprob_workspace_bytes": (Z, [P]),
+            "ecc_linear_logprob": (I32, [P, P, Z, P, P]),
+            "ecc_linear_logprob_grad_workspace_bytes": (Z, [P]),
+            "ecc_linear_logprob_grad": (I32, [P, P, Z, P, P]),
             "ecc_adamw": (I32, [P, P]),
             "ecc_token_logprob": (I32, [P, U64, U32, P, U64, U64, F, U32, P, P, P, P, P, P]),
             "ecc_token_logprob_grad": (I32, [P, U64, U32, P, U64, U64, F, P, P, P, P, P, U64, P]),
@@ -704,6 +708,36 @@ def ecc_token_logprob_grad(logits, tokens, lse, entropy=None, dlogprob=None, den
     dentropy * entropy); returns dlogits (which may be given as logits
     itself)."""
     return (_torch_lib or _marshal()).token_logprob_grad(logits, tokens, lse, entropy, dlogprob, dentropy, scale, dlogits)
+
+
+class LinearLogprob(NamedTuple):
+    """Device tensors of ecc_linear_logprob (logprob None without tokens), in
+    nats, and its status."""
+    logprob: object
+    entropy: object
+    lse: object
+    status: object
+
+
+@_on_stream
+def ecc_linear_logprob(x, w, tokens=None, scale: float = 1.0, ws=None, status=None) -> LinearLogprob:
+    """Log probabilities of tokens (int64 [...], negative: none) under softmax
+    of scale * x w^T, with each row's entropy and log partition, of device
+    tensors x [..., K] and w [vocab, K] (bfloat16, float16 or e4m3); the logits
+    are never stored."""
+    return LinearLogprob._make((_torch_lib or _marshal()).linear_logprob(x, w, tokens, scale, ws, status))
+
+
+@_on_stream
+def ecc_linear_logprob_grad(x, w, tokens, lse, entropy=None, dlogprob=None, dentropy=None, scale: float = 1.0, dx=None, dw=None,
+                            dw_dtype=None, want=("dx", "dw"), ws=None, status=None):
+    """Gradient with respect to x and w of sum(dlogprob * logprob + dentropy *
+    entropy) of ecc_linear_logprob (bfloat16 or float16); returns (dx, dw,
+    status), None for what `want` leaves out.  dw_dtype: x's type (default) or
+    float32."""
+    bits = ("dx" in want) + 2 * ("dw" in want)
+    return (_torch_lib or _marshal()).linear_logprob_grad(x, w, tokens, lse, entropy, dlogprob, dentropy, scale, dx, dw, dw_dtype,
+                                                          bits, ws, status)
 
 
 ADAMW_GROUP = 256

@@ -190,6 +190,10 @@ const void *kernel_of(const Product &x, bool f8, bool pair)
         return gated_kernel(f8, pair);
     if (x.mode == kDual)
         return dual_kernel(pair);
+    if (x.mode == kStats)
+        return stats_kernel(f8, pair);
+    if (x.mode == kSlopes)
+        return slopes_kernel(pair);
     return f8                     ? gemm_kernel<false, false, true, kPlain>(pair)
            : x.P.mn && x.Q.mn     ? gemm_kernel<true, true, false, kPlain>(pair)
            : x.P.mn               ? gemm_kernel<true, false, false, kPlain>(pair)
@@ -202,6 +206,15 @@ bool tma_rows(const void *p, uint64_t ld, uint32_t type, uint64_t rows)
 {
     const uint64_t bytes = ld * type_bytes(type);
     return ((uintptr_t)p & 15) == 0 && (rows <= 1 || ((bytes & 15) == 0 && bytes < (1ull << 40)));
+}
+
+uint32_t stats_parts(const Product &x, uint32_t type)
+{
+    const int sms = sm_count();
+    if (sms <= 0)
+        return 0;
+    const Shape s = shape_of(x, type, sms);
+    return (uint32_t)up(x.rows, s.bn) * (s.pair ? 2 : s.split);
 }
 
 ecc_status gemm(const Product &x, uint32_t type, uint32_t *status, bool clear_status, bool behind, cudaStream_t st)

@@ -194,7 +194,13 @@ __device__ __forceinline__ void finish(const Epilogue &e, float (&a)[W], const u
     else
         store_rows<e4m3>(out, ld, r0, n, c, a, e.out_scale);
 }
-__device__ __forceinline__ float scale_of(const Epilogue &e) { return e.factor ? e.scale * *e.factor : e.scale; }
+template <int MODE> __device__ __forceinline__ float scale_of(const Epilogue &e)
+{
+    if constexpr (MODE == kStats || MODE == kSlopes)
+        return e.scale * 1.44269504f;
+    else
+        return e.factor ? e.scale * *e.factor : e.scale;
+}
 
 // ---------------------------------------------------------------- gated epilogue
 // Lanes 0 to 15: W rows of column c's gate; lanes 16 to 31: of its up.  They
@@ -244,6 +250,109 @@ __device__ __forceinline__ void finish_gated(const Epilogue &e, float (&a)[W], u
         store_rows<e4m3>(e.out, e.ldout, r0, n, c, gate, e.out_scale);
 }
 
+// ---------------------------------------------------------------- logits' epilogues
+// A share of the vocabulary of one token: y = log2 e * logit, m the largest, s
+// the sum of 2^(y - m), t the sum of 2^(y - m) (y - m).  A logit that is not
+// finite makes t NaN, and with it the row's results.
+struct LogitsPart {
+    float m = -INFINITY, s = 0.f, t = 0.f;
+};
+// the next W logits, the first n of them in range; rel: the token's place among them
+template <int W>
+__device__ __forceinline__ void add_logits(const Epilogue &e, float (&a)[W], uint32_t n, float scale, int64_t rel, uint32_t c,
+                                           LogitsPart &p)
+{
+    float2 y[W / 2];
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j)
+        y[j] = mul2(make_float2(a[2 * j], a[2 * j + 1]), both(scale));
+    float top = -INFINITY;
+    if (n == W) {
+#pragma unroll
+        for (int j = 0; j < W / 2; ++j)
+            top = fmaxf(top, fmaxf(y[j].x, y[j].y));
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (j < n)
+                top = fmaxf(top, j & 1 ? y[j / 2].y : y[j / 2].x);
+    }
+    const float m = fmaxf(p.m, top), back = p.s > 0.f ? p.m - m : 0.f, r = exp2_approx(back);
+    float2 s = make_float2(p.s * r, 0.f), t = make_float2(r * fmaf(back, p.s, p.t), 0.f);
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) {
+        float2 d = add2(y[j], both(-m)), x = exp2_both(d);
+        if (n < W) { // outside the vocabulary
+            if (2 * j >= n)
+                d.x = x.x = 0.f;
+            if (2 * j + 1 >= n)
+                d.y = x.y = 0.f;
+        }
+        s = add2(s, x);
+        t = fma2(x, d, t);
+    }
+    p.m = m;
+    p.s = s.x + s.y;
+    p.t = t.x + t.y;
+    if (rel >= 0 && rel < (int64_t)n) {
+        float v = 0.f; // (a sum, so that y stays in registers)
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            v += j == (int)rel ? (j & 1 ? y[j / 2].y : y[j / 2].x) : 0.f;
+        e.token_logit[c] = v;
+    }
+}
+
+// What a token's gradient with respect to its logits is made of:
+// t = dlogprob 1[token] - p (dlogprob + dentropy (log p + H))
+struct LogitsSlope {
+    float lse = 0.f, one = 0.f, all = 0.f, each = 0.f; // log2 e lse; dlogprob; dlogprob + dentropy H; dentropy log 2
+    int64_t token = -1;
+};
+__device__ __forceinline__ LogitsSlope slope_of_token(const Epilogue &e, uint32_t c, bool col_ok)
+{
+    LogitsSlope s;
+    if (!col_ok)
+        return s;
+    const float factor = e.factor ? *e.factor : 1.f;
+    s.lse = e.lse[c] * 1.44269504f;
+    s.token = e.tokens ? e.tokens[c] : -1;
+    if (e.dlogprob && s.token >= 0 && s.token < (int64_t)e.vocab)
+        s.one = e.dlogprob[c] * factor;
+    else
+        s.token = -1;
+    s.all = s.one;
+    if (e.dentropy) {
+        const float dh = e.dentropy[c] * factor;
+        s.all = fmaf(dh, e.entropy[c], s.one);
+        s.each = dh * 0.69314718f;
+    }
+    return s;
+}
+// W logits from vocabulary index v of this launch's part (a multiple of 8) on; rel: the token's place among them
+template <int W>
+__device__ __forceinline__ void store_slopes(const Epilogue &e, const float (&a)[W], uint64_t v, uint32_t c, float scale, int64_t rel,
+                                             const LogitsSlope &s)
+{
+    float2 t[W / 2];
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) {
+        const float2 d = fma2(make_float2(a[2 * j], a[2 * j + 1]), both(scale), both(-s.lse));
+        t[j] = mul2(mul2(exp2_both(d), both(-1.f)), fma2(d, both(s.each), both(s.all)));
+    }
+    if (rel >= 0 && rel < W) {
+#pragma unroll
+        for (int j = 0; j < W / 2; ++j) {
+            t[j].x += 2 * j == (int)rel ? s.one : 0.f;
+            t[j].y += 2 * j + 1 == (int)rel ? s.one : 0.f;
+        }
+    }
+    uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(e.out) + c * e.ldout + v);
+#pragma unroll
+    for (int j = 0; j < W / 8; ++j)
+        out[j] = e.out_type == ECC_BF16 ? pack2<bf16>(t + 4 * j) : pack2<__half>(t + 4 * j);
+}
+
 template <int MODE> __device__ __forceinline__ float bias_of(const Epilogue &e, uint32_t c, bool col_ok, uint32_t lane)
 {
     const void *bias = MODE == kGated && (lane & 16) ? e.bias2 : e.bias;
@@ -270,16 +379,20 @@ template <int MODE>
 __device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint32_t base, uint32_t share, uint64_t r0, uint32_t c,
                                            uint32_t lane)
 {
-    const uint32_t n = (uint32_t)min((uint64_t)g.bn, g.rows - r0), per = (n + g.split - 1) / g.split;
+    const uint32_t n = (uint32_t)min((uint64_t)g.bn, g.rows - r0), even = (n + g.split - 1) / g.split;
+    const uint32_t per = MODE == kSlopes ? (even + 7) & ~7u : even; // (slopes are stored by eights)
     const uint32_t j0 = share * per, j1 = min(n, j0 + per);
     const bool col_ok = c < g.cols;
     if (MODE != kGated && !col_ok)
         return;
-    const float bias = bias_of<MODE>(g.e, c, col_ok, lane), scale = scale_of(g.e);
+    const float bias = bias_of<MODE>(g.e, c, col_ok, lane), scale = scale_of<MODE>(g.e);
+    LogitsPart p;
+    const LogitsSlope slope = MODE == kSlopes ? slope_of_token(g.e, c, col_ok) : LogitsSlope();
+    const int64_t token = MODE == kStats && g.e.tokens ? g.e.tokens[c] : -1;
     for (uint32_t j = j0; j < j1; j += 8) {
         float a[8] = {};
         uint32_t res[8];
-        if constexpr (MODE != kGated)
+        if constexpr (MODE == kPlain || MODE == kDual)
             ask_residual(g.e, res, r0 + j, min(8u, j1 - j), c);
         for (uint32_t k = 0; k < g.split; ++k) {
             const uint32_t from = cluster_addr(at + j * kPTile * 4, base + k);
@@ -290,9 +403,15 @@ __device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint3
         }
         if constexpr (MODE == kGated)
             finish_gated(g.e, a, r0 + j, min(8u, j1 - j), c, col_ok, bias, lane);
+        else if constexpr (MODE == kStats)
+            add_logits(g.e, a, min(8u, j1 - j), scale, token - (int64_t)(r0 + j), c, p);
+        else if constexpr (MODE == kSlopes)
+            store_slopes(g.e, a, r0 + j, c, scale, slope.token - (int64_t)(g.e.first + r0 + j), slope);
         else
             finish(g.e, a, res, r0 + j, min(8u, j1 - j), c, bias, scale);
     }
+    if constexpr (MODE == kStats)
+        g.e.part[(r0 / g.bn * g.split + share) * g.cols + c] = make_float4(p.m, p.s, p.t, 0.f);
 }
 
 // ---------------------------------------------------------------- loads and products of a reduction block
@@ -469,7 +588,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t quad = warp & 3; // a warp reads the lanes of its number modulo 4
         const uint32_t j0 = warp < 6 ? 0 : g.bn / 2, j1 = j0 + g.bn / 2;
         uint32_t acc = 0, aph = 0;
-        const float scale = scale_of(g.e);
+        const float scale = scale_of<MODE>(g.e);
         for (uint32_t t = pair; t < tiles; t += pairs) {
             const TilePos pos = tile_pos(t, g.ptiles, g.qtiles);
             const uint32_t c = column_of<MODE>((pos.p * 2 + rank) * kPCols<MODE>, quad, lane);
@@ -477,6 +596,39 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const bool col_ok = c < g.cols;
             const float bias = bias_of<MODE>(g.e, c, col_ok, lane);
             const uint64_t left = g.rows - r0;
+            if constexpr (MODE == kStats || MODE == kSlopes) {
+                LogitsPart p;
+                const int64_t token = MODE == kStats && g.e.tokens && col_ok ? g.e.tokens[c] : -1;
+                const LogitsSlope slope = MODE == kSlopes ? slope_of_token(g.e, c, col_ok) : LogitsSlope();
+                if (!__all_sync(~0u, mbar_wait(&s.tfull[acc], aph, g.limit_ns))) {
+                    if (lane == 0)
+                        set_status(g.status, ECC_ERR_TIMEOUT);
+                    break;
+                }
+                tmem_fence_after();
+                for (uint32_t j = j0; j < j1; j += 32) {
+                    float a[32];
+                    tmem_load32(tmem + (quad * 32 << 16) + acc * g.bn + j, a);
+                    if (j + 32 == j1) { // the accumulator is read: products may fill it again
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            cluster_arrive(cluster_addr(smem_u32(&s.tempty[acc]), 0));
+                    }
+                    if (!col_ok || j >= left)
+                        continue;
+                    if constexpr (MODE == kStats)
+                        add_logits(g.e, a, (uint32_t)min((uint64_t)32, left - j), scale, token - (int64_t)(r0 + j), c, p);
+                    else
+                        store_slopes(g.e, a, r0 + j, c, scale, slope.token - (int64_t)(g.e.first + r0 + j), slope);
+                }
+                if (MODE == kStats && col_ok)
+                    g.e.part[(pos.q * 2 + (j0 ? 1 : 0)) * g.cols + c] = make_float4(p.m, p.s, p.t, 0.f);
+                if (acc)
+                    aph ^= 1;
+                acc ^= 1;
+                continue;
+            }
             uint32_t res[2][32]; // of this chunk of 32 rows and the next
             auto ask = [&](uint32_t j, uint32_t (&v)[32]) {
                 if (MODE != kGated && col_ok && j < j1 && j < left)
@@ -533,12 +685,15 @@ __device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, 
                                               uint64_t r0, bool col_ok, float bias, bool direct, float *part, Wait wait)
 {
     const uint64_t left = g.rows - r0;
-    const float scale = scale_of(g.e);
+    const float scale = scale_of<MODE>(g.e);
+    LogitsPart p;
+    const int64_t token = MODE == kStats && direct && g.e.tokens && col_ok ? g.e.tokens[c] : -1;
+    const LogitsSlope slope = MODE == kSlopes && direct ? slope_of_token(g.e, c, col_ok) : LogitsSlope();
     for (uint32_t j = 0; j < g.bn && j < left; j += W) {
         float a[W];
         uint32_t res[W];
         const uint32_t n = (uint32_t)min((uint64_t)W, left - j);
-        if (MODE != kGated && direct && col_ok)
+        if ((MODE == kPlain || MODE == kDual) && direct && col_ok)
             ask_residual(g.e, res, r0 + j, n, c);
         if (j == 0 && g.kblocks && !wait())
             return;
@@ -555,12 +710,20 @@ __device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, 
         if (direct) {
             if constexpr (MODE == kGated)
                 finish_gated(g.e, a, r0 + j, n, c, col_ok, bias, lane);
-            else if (col_ok)
+            else if constexpr (MODE == kStats) {
+                if (col_ok)
+                    add_logits(g.e, a, n, scale, token - (int64_t)(r0 + j), c, p);
+            } else if constexpr (MODE == kSlopes) {
+                if (col_ok)
+                    store_slopes(g.e, a, r0 + j, c, scale, slope.token - (int64_t)(g.e.first + r0 + j), slope);
+            } else if (col_ok)
                 finish(g.e, a, res, r0 + j, n, c, bias, scale);
         } else {
             keep_part(part, a, j, quad * 32 + lane);
         }
     }
+    if (MODE == kStats && direct && col_ok)
+        g.e.part[r0 / g.bn * g.cols + c] = make_float4(p.m, p.s, p.t, 0.f);
 }
 
 // block: this CTA's number among the product's

@@ -28,6 +28,14 @@ struct Epilogue {
     void *out2;
     uint64_t ldout2, rswitch, rows2;
     const float *factor; // multiplies scale (read on the device); NULL: 1
+    // logits, never stored: columns are tokens, rows the vocabulary from `first` on
+    const int64_t *tokens;
+    uint64_t first;
+    float4 *part;       // kStats: [share of the vocabulary][token]: maximum, sum, entropy sum (base 2)
+    float *token_logit; // kStats: [token], scaled by log2 e
+    // kSlopes, of each token; dlogprob and dentropy may be NULL; out: [token][vocabulary] of out_type
+    const float *lse, *entropy, *dlogprob, *dentropy;
+    uint64_t vocab;
 };
 
 // An operand: `rows` x K values, either stored a matrix row after the other
@@ -65,5 +73,9 @@ ecc_status gemm_backward(const Product &dx, const Product &dw, uint32_t type, ui
 const void *gated_kernel(bool f8, bool pair);
 const void *dual_kernel(bool pair);
 const void *dual_both_kernel();
+const void *stats_kernel(bool f8, bool pair);
+const void *slopes_kernel(bool pair);
+// shares of the vocabulary that a kStats product writes parts for
+uint32_t stats_parts(const Product &x, uint32_t type);
 
 } // namespace ecc

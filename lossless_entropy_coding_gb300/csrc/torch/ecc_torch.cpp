@@ -596,6 +596,99 @@ FUNCTION(token_logprob_grad, 8)
     return wrap(d);
 }
 
+// x, w, tokens, scale, ws, status
+FUNCTION(linear_logprob, 6)
+{
+    const at::Tensor &x = first(a[0], "ecc_linear_logprob: needs CUDA tensors");
+    const On on(x);
+    const Matrix mx = matrix(x, on.dev, "ecc_linear_logprob: x");
+    Opt w = tensor(a[1], "ecc_linear_logprob: w"), tokens = tensor(a[2], "ecc_linear_logprob: tokens");
+    if (!w || w->dim() != 2)
+        refuse("ecc_linear_logprob: w");
+    const Matrix mw = operand(w, (uint64_t)w->size(0), mx.cols, on.dev, "ecc_linear_logprob: w");
+    if (mw.type != mx.type)
+        refuse("ecc_linear_logprob: x and w of different types");
+    const auto lead = x.sizes().slice(0, x.dim() - 1);
+    ecc_linear_logprob_job j{};
+    j.x = mx.p;
+    j.w = mw.p;
+    j.tokens = (const int64_t *)vector(tokens, mx.rows, on.dev, "ecc_linear_logprob: tokens", at::kLong);
+    j.rows = mx.rows;
+    j.vocab = (uint64_t)w->size(0);
+    j.K = mx.cols;
+    j.ldx = mx.ld;
+    j.ldw = mw.ld;
+    j.scale = (float)number(a[3]);
+    j.in_type = mx.type;
+    at::Tensor logprob, entropy = fresh(lead, at::kFloat, on.dev), lse = fresh(lead, at::kFloat, on.dev);
+    if (tokens)
+        logprob = fresh(lead, at::kFloat, on.dev);
+    j.logprob = (float *)where(logprob);
+    j.entropy = (float *)where(entropy);
+    j.lse = (float *)where(lse);
+    at::Tensor status = output(tensor(a[5], "ecc_linear_logprob: status"), {1}, at::kInt, on.dev);
+    at::Tensor ws = scratch(tensor(a[4], "ecc_linear_logprob: ws"), ecc_linear_logprob_workspace_bytes(&j), on.dev,
+                            "ecc_linear_logprob: ws");
+    check(ecc_linear_logprob(&j, where(ws), bytes_of(ws), status_word(status, on.dev, "ecc_linear_logprob: status"), on.stream),
+          "ecc_linear_logprob");
+    return results(logprob, entropy, lse, status);
+}
+
+// x, w, tokens, lse, entropy, dlogprob, dentropy, scale, dx, dw, dw_dtype, want (bits: 1 dx, 2 dw), ws, status
+FUNCTION(linear_logprob_grad, 14)
+{
+    const at::Tensor &x = first(a[0], "ecc_linear_logprob_grad: needs CUDA tensors");
+    const On on(x);
+    const Matrix mx = matrix(x, on.dev, "ecc_linear_logprob_grad: x");
+    Opt w = tensor(a[1], "ecc_linear_logprob_grad: w");
+    if (!w || w->dim() != 2)
+        refuse("ecc_linear_logprob_grad: w");
+    const uint64_t V = (uint64_t)w->size(0);
+    const Matrix mw = operand(w, V, mx.cols, on.dev, "ecc_linear_logprob_grad: w");
+    if (mw.type != mx.type)
+        refuse("ecc_linear_logprob_grad: x and w of different types");
+    auto f32 = [&](int i, const char *what) { return (const float *)vector(tensor(a[i], what), mx.rows, on.dev, what, at::kFloat); };
+    const char *tw = "ecc_linear_logprob_grad: tokens";
+    const long want = integer(a[11]);
+    Opt gx = tensor(a[8], "ecc_linear_logprob_grad: dx"), gw = tensor(a[9], "ecc_linear_logprob_grad: dw");
+    at::Tensor dx, dw;
+    if (gx || (want & 1))
+        dx = output(gx, x.sizes(), x.scalar_type(), on.dev);
+    if (gw || (want & 2))
+        dw = output(gw, {(int64_t)V, (int64_t)mx.cols}, dtype(a[10], "ecc_linear_logprob_grad: dw_dtype").value_or(x.scalar_type()), on.dev);
+    at::Tensor status = output(tensor(a[13], "ecc_linear_logprob_grad: status"), {1}, at::kInt, on.dev);
+    const Matrix mdx = operand(dx.defined() ? &dx : nullptr, mx.rows, mx.cols, on.dev, "ecc_linear_logprob_grad: dx");
+    const Matrix mdw = operand(dw.defined() ? &dw : nullptr, V, mx.cols, on.dev, "ecc_linear_logprob_grad: dw");
+    if (dx.defined() && mdx.type != mx.type)
+        refuse("ecc_linear_logprob_grad: dx");
+    ecc_linear_logprob_grad_job j{};
+    j.x = mx.p;
+    j.w = mw.p;
+    j.tokens = (const int64_t *)vector(tensor(a[2], tw), mx.rows, on.dev, tw, at::kLong);
+    j.lse = f32(3, "ecc_linear_logprob_grad: lse");
+    j.entropy = f32(4, "ecc_linear_logprob_grad: entropy");
+    j.dlogprob = f32(5, "ecc_linear_logprob_grad: dlogprob");
+    j.dentropy = f32(6, "ecc_linear_logprob_grad: dentropy");
+    j.dx = mdx.p;
+    j.dw = mdw.p;
+    j.rows = mx.rows;
+    j.vocab = V;
+    j.K = mx.cols;
+    j.ldx = mx.ld;
+    j.ldw = mw.ld;
+    j.lddx = mdx.ld;
+    j.lddw = mdw.ld;
+    j.scale = (float)number(a[7]);
+    j.in_type = mx.type;
+    j.dw_type = mdw.type;
+    at::Tensor ws = scratch(tensor(a[12], "ecc_linear_logprob_grad: ws"), ecc_linear_logprob_grad_workspace_bytes(&j), on.dev,
+                            "ecc_linear_logprob_grad: ws");
+    check(ecc_linear_logprob_grad(&j, where(ws), bytes_of(ws), status_word(status, on.dev, "ecc_linear_logprob_grad: status"),
+                                  on.stream),
+          "ecc_linear_logprob_grad");
+    return results(dx, dw, status);
+}
+
 // A list argument: its tensors by number (None: none at all)
 struct List {
     PyObject *seq = nullptr;
@@ -707,7 +800,8 @@ PyObject *set_error(PyObject *, PyObject *cls)
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {METHOD(layer_norm),    METHOD(layer_norm_grad), METHOD(linear), METHOD(linear_grad),
                            METHOD(token_logprob), METHOD(token_logprob_grad), METHOD(adamw),
-                           METHOD(gated_linear), METHOD(gated_linear_grad), {"set_error", set_error, METH_O, nullptr},
+                           METHOD(gated_linear), METHOD(gated_linear_grad),
+                           METHOD(linear_logprob), METHOD(linear_logprob_grad), {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "ecc_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
