@@ -106,8 +106,11 @@ __device__ __forceinline__ float2 root2(float2 x)
 __device__ __forceinline__ float2 update2(const AdamStep &s, float2 g, float2 &p, float2 &m, float2 &v)
 {
     g = mul2(g, both(s.grad_scale));
-    m = add2(mul2(m, both(s.beta1)), mul2(g, both(s.gain1)));
-    v = add2(mul2(v, both(s.beta2)), mul2(mul2(g, g), both(s.gain2)));
+    // (packed sums of packed products would be fused)
+    const float2 a = mul2(m, both(s.beta1)), b = mul2(g, both(s.gain1));
+    m = make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+    const float2 c = mul2(v, both(s.beta2)), d = mul2(mul2(g, g), both(s.gain2));
+    v = make_float2(__fadd_rn(c.x, d.x), __fadd_rn(c.y, d.y));
     const float2 r = root2(v);
     p = fma2(p, both(s.keep), mul2(mul2(m, both(-s.rate)), rcp_both(fma2(r, both(s.root), both(s.eps)))));
     return r;
@@ -126,14 +129,26 @@ __device__ __forceinline__ uint32_t dithered(float a, uint32_t d)
     const uint32_t n = (__float_as_uint(fmaxf(a, 0.0078125f)) << 4) + d;
     return max(n, (__float_as_uint(a + 0.015625f) << 4) + d - (8u << 24));
 }
+// The same for a value of at least 2^-6, of any sign, that may exceed 448 by a
+// few last places (which the addition does not carry over).
+__device__ __forceinline__ uint32_t dithered_normal(float y, uint32_t d) { return (__float_as_uint(y) << 4) + d; }
+__device__ __forceinline__ uint32_t m_bits(uint32_t d) { return __byte_perm(d, 0x40000000u, 0x7324); }
+__device__ __forceinline__ uint32_t v_bits(uint32_t d) { return __byte_perm(d, 0x40000000u, 0x7104); }
+// the larger one, or NaN if there is one
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 // for m (signed) and sqrt(v), from 448 / the group's largest
 __device__ __forceinline__ uint32_t m_dithered(float y, uint32_t d)
 {
-    return dithered(fminf(fabsf(y), 448.f), __byte_perm(d, 0x40000000u, 0x7324));
+    return dithered(fminf(fabsf(y), 448.f), m_bits(d));
 }
 __device__ __forceinline__ uint32_t v_dithered(float y, uint32_t d)
 {
-    return dithered(y > 0.f ? fminf(fmaxf(y, 0.001953125f), 448.f) : 0.f, __byte_perm(d, 0x40000000u, 0x7104));
+    return dithered(y > 0.f ? fminf(fmaxf(y, 0.001953125f), 448.f) : 0.f, v_bits(d));
 }
 // the top bytes of four words
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
@@ -217,24 +232,27 @@ __device__ __forceinline__ void group_by_vectors(const AdamTensor &t, uint32_t k
         float2 m[4], r[4];
         unpack_e4m3(mq, ms, m);
         unpack_e4m3(vq, vs, r);
-        uint32_t mm = 0, vm = 0;
+        float m_most = 0.f, v_most = 0.f, m_least = INFINITY, r_least = INFINITY;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float2 v = mul2(r[k], r[k]);
             r[k] = update2(s, g[k], p[k], m[k], v);
-            mm = max(mm, max(__float_as_uint(m[k].x) & 0x7FFFFFFFu, __float_as_uint(m[k].y) & 0x7FFFFFFFu));
-            vm = max(vm, max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu));
+            m_most = max_nan(max_nan(m_most, fabsf(m[k].x)), fabsf(m[k].y));
+            v_most = max_nan(max_nan(v_most, v.x), v.y);
+            m_least = fminf(fminf(m_least, fabsf(m[k].x)), fabsf(m[k].y));
+            r_least = fminf(fminf(r_least, r[k].x), r[k].y);
         }
         if (t.master)
             write8(t.master, i, ECC_F32, p);
         write8(t.param, i, ptype, p);
-        mm = __reduce_max_sync(~0u, mm);
-        vm = __reduce_max_sync(~0u, vm);
+        const uint32_t mm = __reduce_max_sync(~0u, __float_as_uint(m_most)), vm = __reduce_max_sync(~0u, __float_as_uint(v_most));
         const bool finite = mm < 0x7F800000u && vm < 0x7F800000u;
         const float mi = group_scale(msp, mm, false, finite, lane == 0);
         const float vi = group_scale(vsp, vm, true, finite, lane == 0);
         const uint32_t key = mix32(s.key + (uint32_t)(e0 >> 32));
         uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
+        // (no value so small that its neighbours are 2^-9 apart, which few groups have: a third fewer instructions)
+        const bool normal = __all_sync(~0u, finite && __fmul_rn(m_least, mi) >= 0.015625f && __fmul_rn(r_least, vi) >= 0.015625f);
         if (finite) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -243,10 +261,15 @@ __device__ __forceinline__ void group_by_vectors(const AdamTensor &t, uint32_t k
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t d = mix32((uint32_t)(i + h * 4 + k) ^ key);
                     const float2 y2 = mul2(m[h * 2 + k / 2], both(mi)), z2 = mul2(r[h * 2 + k / 2], both(vi));
-                    const float y = k & 1 ? y2.y : y2.x;
+                    const float y = k & 1 ? y2.y : y2.x, z = k & 1 ? z2.y : z2.x;
                     sign[k] = __float_as_uint(y);
-                    mc[k] = m_dithered(y, d);
-                    vc[k] = v_dithered(k & 1 ? z2.y : z2.x, d);
+                    if (normal) {
+                        mc[k] = dithered_normal(y, m_bits(d));
+                        vc[k] = dithered_normal(z, v_bits(d));
+                    } else {
+                        mc[k] = m_dithered(y, d);
+                        vc[k] = v_dithered(z, d);
+                    }
                 }
                 mw[h] = top_bytes(mc[0], mc[1], mc[2], mc[3]) | (top_bytes(sign[0], sign[1], sign[2], sign[3]) & 0x80808080u);
                 vw[h] = top_bytes(vc[0], vc[1], vc[2], vc[3]);
@@ -334,10 +357,10 @@ __device__ __noinline__ void group_by_values(const AdamTensor &t, uint32_t kind,
     }
 }
 
-// Blocks an SM: 3 for 8-bit states, whose instructions are the bound (82 a
-// value; 265 M values, bf16: 778 us, 3.4 TB/s; 2 blocks 889, 4 blocks 799), 2
-// for float32 states, which are bound by HBM (184 M values with masters: 794 us,
-// 6.4 TB/s; 3 blocks 859, 4 blocks 861).
+// Blocks an SM: 3 for 8-bit states, whose instructions are the bound (265 M
+// values, bf16: 708 us, 3.8 TB/s; 4 blocks 710, 5 blocks 754), 2 for float32
+// states, which are bound by HBM (184 M values with masters: 797 us, 6.4 TB/s; 3
+// blocks 859, 4 blocks 861).
 constexpr int kAdamBlocks = 2, kAdamBlocksBytes = 3;
 template <int CAP, bool BYTES>
 __global__ void __launch_bounds__(kAdamThreads, BYTES ? kAdamBlocksBytes : kAdamBlocks) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a)

@@ -28,6 +28,13 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
+CUtensorMapDataType map_type(uint32_t type)
+{
+    return type == ECC_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+           : type == ECC_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                             : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+}
+
 // map of an operand: boxes of 128 bytes x `box_rows`
 bool make_map(CUtensorMap *map, const Operand &o, uint64_t rows, uint64_t K, uint32_t type, uint32_t box_rows)
 {
@@ -37,10 +44,22 @@ bool make_map(CUtensorMap *map, const Operand &o, uint64_t rows, uint64_t K, uin
     // the stride of a single row is never used, but has to be a multiple of 16 bytes
     const cuuint64_t stride[1] = {outer > 1 ? o.ld * size : (inner * size + 15) / 16 * 16};
     const cuuint32_t box[2] = {kTileBytes / size, box_rows}, one[2] = {1, 1};
-    const CUtensorMapDataType dt = type == ECC_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                   : type == ECC_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                     : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    return encode_tiled()(map, dt, 2, const_cast<void *>(o.p), dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return encode_tiled()(map, map_type(type), 2, const_cast<void *>(o.p), dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One map over two matrices of `rows` rows of one stride, 16 rows of each in
+// turns: the second one's distance is a stride.  Whether there can be one.
+bool make_turns_map(CUtensorMap *map, const Operand &lower, const Operand &upper, uint64_t rows, uint64_t K, uint32_t type)
+{
+    const uint32_t size = type_bytes(type);
+    const uint64_t apart = (const uint8_t *)upper.p - (const uint8_t *)lower.p;
+    if (rows % 16 || lower.ld != upper.ld || apart % 16 || apart >= 1ull << 40 || lower.ld * size >= 1ull << 36)
+        return false;
+    const cuuint64_t dims[4] = {K, 16, 2, rows / 16}, stride[3] = {lower.ld * size, apart, 16 * lower.ld * size};
+    const cuuint32_t box[4] = {kTileBytes / size, 16, 2, kPTile / 32}, one[4] = {1, 1, 1, 1};
+    return encode_tiled()(map, map_type(type), 4, const_cast<void *>(lower.p), dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -114,8 +133,12 @@ struct Plan {
 Shape shape_of(const Product &x, uint32_t type, int sms)
 {
     const uint32_t per = type == ECC_E4M3 ? 128 : 64;
-    return choose_shape(x.rows, x.mode == kGated ? 2 * x.cols : x.cols, x.K, (uint32_t)up(x.K, per), x.Q.mn, type == ECC_E4M3,
-                        sms);
+    Shape s = choose_shape(x.rows, x.mode == kGated ? 2 * x.cols : x.cols, x.K, (uint32_t)up(x.K, per), x.Q.mn, type == ECC_E4M3,
+                           sms);
+    // Logits: pairs on 256 x 256 tiles as soon as every pair has one.
+    if ((x.mode == kStats || x.mode == kSlopes) && x.K && (s.pair || 2 * up(x.cols, 256) * up(x.rows, 256) >= (uint64_t)sms))
+        s = {true, 256, 1};
+    return s;
 }
 
 ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t type, uint32_t *status, bool clear_status)
@@ -147,9 +170,16 @@ ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t 
     // (kDual: the first matrix's reduction ends somewhere in its last block, whose rest reads as zeros)
     const uint32_t box = gated ? 16 : x.P.mn ? 64 : kPTile;
     const uint64_t k1 = x.mode == kDual ? x.kfirst : x.K;
-    if (!encode_tiled() || !make_map(&plan.pm, x.P, g.cols, k1, type, box) ||
-        ((gated || x.mode == kDual) && !make_map(&plan.pm2, x.P2, g.cols, k1, type, box)) ||
-        !make_map(&plan.qm, x.Q, g.rows, x.K, type, x.Q.mn ? 64 : qn))
+    if (!encode_tiled() || !make_map(&plan.qm, x.Q, g.rows, x.K, type, x.Q.mn ? 64 : qn))
+        return ECC_ERR_CUDA;
+    if (gated) {
+        g.e.swapped = x.P2.p < x.P.p;
+        if ((g.one_box = make_turns_map(&plan.pm, g.e.swapped ? x.P2 : x.P, g.e.swapped ? x.P : x.P2, g.cols, x.K, type)))
+            return ECC_OK;
+        g.e.swapped = false;
+    }
+    if (!make_map(&plan.pm, x.P, g.cols, k1, type, box) ||
+        ((gated || x.mode == kDual) && !make_map(&plan.pm2, x.P2, g.cols, k1, type, box)))
         return ECC_ERR_CUDA;
     return ECC_OK;
 }
@@ -184,6 +214,43 @@ ecc_status launch_plan(const void *f, int threads, uint32_t ctas, uint32_t clust
     return launch_status(cudaLaunchKernelExC(&cfg, f, args));
 }
 
+// Whether a few tokens' statistics stream the head (P: tokens, Q: the head)
+// through a persistent CTA an SM: with tiles for most of them.
+bool streams(const Product &x, int sms) { return x.mode == kStats && x.K && x.cols <= 64 && 2 * up(x.rows, kPTile) >= (uint64_t)sms; }
+
+uint32_t stream_ctas(const Product &x, int sms) { return (uint32_t)std::min<uint64_t>(up(x.rows, kPTile), sms); }
+
+ecc_status stream_stats(const Product &x, uint32_t type, uint32_t *status, bool behind, int sms, cudaStream_t st)
+{
+    CUtensorMap wm, xm;
+    StreamArgs g{};
+    g.e = x.e;
+    g.vocab = x.rows;
+    g.tokens = x.cols;
+    g.kblocks = (uint32_t)up(x.K, type == ECC_E4M3 ? 128 : 64);
+    g.tiles = (uint32_t)up(x.rows, kPTile);
+    g.bn = x.cols <= 16 ? 16 : x.cols <= 32 ? 32 : 64;
+    g.segs = std::min(256 / g.bn, (g.kblocks + kSegment - 1) / kSegment);
+    const uint32_t stage_bytes = kPBytes + g.bn * kTileBytes;
+    g.stages = std::min(kMaxStages, (kAloneSmem - kSmemHead - (uint32_t)sizeof(StreamBars)) / stage_bytes);
+    g.idesc = product_desc(type, false, false, 128, g.bn);
+    g.status = status;
+    g.limit_ns = kWaitLimitNs + 1000ull * g.kblocks;
+    if (!encode_tiled() || !make_map(&wm, x.Q, x.rows, x.K, type, kPTile) || !make_map(&xm, x.P, x.cols, x.K, type, g.bn))
+        return ECC_ERR_CUDA;
+    void *args[] = {&wm, &xm, &g};
+    return launch_plan(stats_stream(type == ECC_E4M3), kStreamThreads, stream_ctas(x, sms), 1,
+                       kSmemHead + (size_t)g.stages * stage_bytes, args, behind, st);
+}
+
+// Whether a kernel is launched with `n` registers a thread: one whose warps
+// share them out differently would wait forever if there were fewer.
+bool registers_of(const void *f, int n)
+{
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, f) == cudaSuccess && a.numRegs == n;
+}
+
 const void *kernel_of(const Product &x, bool f8, bool pair)
 {
     if (x.mode == kGated)
@@ -213,6 +280,8 @@ uint32_t stats_parts(const Product &x, uint32_t type)
     const int sms = sm_count();
     if (sms <= 0)
         return 0;
+    if (streams(x, sms))
+        return 4 * stream_ctas(x, sms);
     const Shape s = shape_of(x, type, sms);
     return (uint32_t)up(x.rows, s.bn) * (s.pair ? 2 : s.split);
 }
@@ -222,6 +291,8 @@ ecc_status gemm(const Product &x, uint32_t type, uint32_t *status, bool clear_st
     const int sms = sm_count();
     if (sms <= 0)
         return ECC_ERR_CUDA;
+    if (streams(x, sms))
+        return stream_stats(x, type, status, behind, sms, st);
     Plan plan;
     const ecc_status rc = make_plan(plan, x, shape_of(x, type, sms), type, status, clear_status);
     if (rc != ECC_OK)
@@ -231,7 +302,9 @@ ecc_status gemm(const Product &x, uint32_t type, uint32_t *status, bool clear_st
     const size_t smem = stage_memory(plan, ctas, sms);
     const void *f = kernel_of(x, type == ECC_E4M3, pair);
     void *args[] = {&plan.pm, &plan.pm2, &plan.qm, &plan.g};
-    return launch_plan(f, pair ? kPairThreads : kSplitThreads, ctas, pair ? 2 : plan.g.split, smem, args, behind, st);
+    if (pair && x.mode == kStats && !registers_of(f, kStatsRegisters))
+        return ECC_ERR_CUDA;
+    return launch_plan(f, pair ? (x.mode == kStats ? kStatsThreads : kPairThreads) : kSplitThreads, ctas, pair ? 2 : plan.g.split, smem, args, behind, st);
 }
 
 ecc_status gemm_backward(const Product &dx, const Product &dw, uint32_t type, uint32_t *status, bool clear_status, bool behind,

@@ -49,6 +49,7 @@ constexpr uint32_t kSmemHead = 1024; // room to align the stages to 1024 bytes
 struct GemmArgs {
     Epilogue e;
     uint32_t kswitch; // kDual: the reduction block where the second matrix starts
+    bool one_box;     // kGated: P's map has both matrices, in turns of 16 rows
     uint64_t rows, cols;
     uint32_t kblocks; // reduction blocks of 128 bytes (64 reduction indices for MN-major operands)
     uint32_t ptiles, qtiles, bn, stages, idesc, split;
@@ -61,8 +62,29 @@ struct GemmBars {
     uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
     uint32_t tmem;
 };
+// kStats: reduction blocks (512 indices of 16 bits, 1024 of 8) after which an
+// accumulator is read and the sum goes on in registers: the tensor cores'
+// additions truncate, and 4096 products in one accumulator leave logits a
+// relative 1e-5 short (lse off by 3e-6 of itself; by segments: 4e-7).  The
+// other accumulator is filled meanwhile, so the products do not wait.
+constexpr uint32_t kSegment = 8;
 // P's rows of a CTA that are columns of the output
 template <int MODE> constexpr uint32_t kPCols = MODE == kGated ? kPTile / 2 : kPTile;
+
+// the head streamed past a few tokens (ecc_head_gemm.cu)
+constexpr int kStreamThreads = 192; // TMA warp, product warp, 4 epilogue warps
+struct StreamArgs {
+    Epilogue e;
+    uint64_t vocab, tokens;
+    uint32_t kblocks, tiles, bn, segs, stages, idesc;
+    uint32_t *status;
+    uint64_t limit_ns;
+};
+struct StreamBars {
+    uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+    uint32_t tmem;
+    int32_t token[64];
+};
 
 // ---------------------------------------------------------------- epilogue
 template <uint32_t ACT, int W> __device__ __forceinline__ void activate(float (&a)[W])
@@ -203,13 +225,14 @@ template <int MODE> __device__ __forceinline__ float scale_of(const Epilogue &e)
 }
 
 // ---------------------------------------------------------------- gated epilogue
-// Lanes 0 to 15: W rows of column c's gate; lanes 16 to 31: of its up.  They
-// exchange halves, and each makes W / 2 rows of the column.
+// Lanes 0 to 15: W rows of column c's gate; lanes 16 to 31: of its up (or the
+// other way round).  They exchange halves, and each makes W / 2 rows of the
+// column.
 template <int W>
 __device__ __forceinline__ void finish_gated(const Epilogue &e, float (&a)[W], uint64_t r0, uint32_t n, uint32_t c, bool col_ok,
                                              float bias, uint32_t lane)
 {
-    const bool up = lane & 16;
+    const bool up = e.swapped != (bool)(lane & 16);
     const float scale = up ? e.scale2 : e.scale;
 #pragma unroll
     for (int j = 0; j < W; ++j)
@@ -224,18 +247,19 @@ __device__ __forceinline__ void finish_gated(const Epilogue &e, float (&a)[W], u
         else
             store_rows<__half>(pre, ld, r0, n, c, a, 1.f);
     }
+    const bool second = lane & 16; // of the halves of the rows
     float gate[W / 2], other[W / 2];
 #pragma unroll
     for (int j = 0; j < W / 2; ++j) {
-        const float got = __shfl_xor_sync(~0u, up ? a[j] : a[j + W / 2], 16);
-        gate[j] = up ? got : a[j];
-        other[j] = up ? a[j + W / 2] : got;
+        const float got = __shfl_xor_sync(~0u, second ? a[j] : a[j + W / 2], 16), own = second ? a[j + W / 2] : a[j];
+        gate[j] = up ? got : own;
+        other[j] = up ? own : got;
     }
     activate_by(e.act, gate);
 #pragma unroll
     for (int j = 0; j < W / 2; ++j)
         gate[j] *= other[j];
-    const uint32_t first = up ? W / 2 : 0;
+    const uint32_t first = second ? W / 2 : 0;
     if (!col_ok || n <= first)
         return;
     r0 += first;
@@ -257,6 +281,11 @@ __device__ __forceinline__ void finish_gated(const Epilogue &e, float (&a)[W], u
 struct LogitsPart {
     float m = -INFINITY, s = 0.f, t = 0.f;
 };
+// v = x if i is j (in assembly, so that no array is moved to memory to be indexed)
+__device__ __forceinline__ void pick(float &v, int i, int j, float x)
+{
+    asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, %2;\n\t@p mov.f32 %0, %3;\n\t}" : "+f"(v) : "r"(i), "r"(j), "f"(x));
+}
 // the next W logits, the first n of them in range; rel: the token's place among them
 template <int W>
 __device__ __forceinline__ void add_logits(const Epilogue &e, float (&a)[W], uint32_t n, float scale, int64_t rel, uint32_t c,
@@ -295,12 +324,56 @@ __device__ __forceinline__ void add_logits(const Epilogue &e, float (&a)[W], uin
     p.s = s.x + s.y;
     p.t = t.x + t.y;
     if (rel >= 0 && rel < (int64_t)n) {
-        float v = 0.f; // (a sum, so that y stays in registers)
+        float v = 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j)
-            v += j == (int)rel ? (j & 1 ? y[j / 2].y : y[j / 2].x) : 0.f;
+            pick(v, (int)rel, j, j & 1 ? y[j / 2].y : y[j / 2].x);
         e.token_logit[c] = v;
     }
+}
+
+// All of a share: the first n of W logits, at once (one maximum, one pass of exponentials)
+template <int W, bool ALL>
+__device__ __forceinline__ LogitsPart whole_part(const Epilogue &e, float2 (&a)[W / 2], uint32_t n, float scale, int64_t rel, uint32_t c)
+{
+    LogitsPart p;
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) {
+        a[j] = mul2(a[j], both(scale));
+        if (ALL || 2 * j < n)
+            top[j % 4] = fmaxf(top[j % 4], a[j].x);
+        if (ALL || 2 * j + 1 < n)
+            top[j % 4] = fmaxf(top[j % 4], a[j].y);
+    }
+    if (rel >= 0 && rel < (int64_t)n) {
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < W / 2; ++j) {
+            pick(v, (int)rel, 2 * j, a[j].x);
+            pick(v, (int)rel, 2 * j + 1, a[j].y);
+        }
+        e.token_logit[c] = v;
+    }
+    p.m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    float2 s[2] = {both(0.f), both(0.f)}, t[2] = {both(0.f), both(0.f)};
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) {
+        float2 d = add2(a[j], both(-p.m)), x = exp2_both(d);
+        if (!ALL) { // outside the vocabulary
+            if (2 * j >= n)
+                d.x = x.x = 0.f;
+            if (2 * j + 1 >= n)
+                d.y = x.y = 0.f;
+        }
+        s[j % 2] = add2(s[j % 2], x);
+        t[j % 2] = fma2(x, d, t[j % 2]);
+    }
+    s[0] = add2(s[0], s[1]);
+    t[0] = add2(t[0], t[1]);
+    p.s = s[0].x + s[0].y;
+    p.t = t[0].x + t[0].y;
+    return p;
 }
 
 // What a token's gradient with respect to its logits is made of:
@@ -355,7 +428,7 @@ __device__ __forceinline__ void store_slopes(const Epilogue &e, const float (&a)
 
 template <int MODE> __device__ __forceinline__ float bias_of(const Epilogue &e, uint32_t c, bool col_ok, uint32_t lane)
 {
-    const void *bias = MODE == kGated && (lane & 16) ? e.bias2 : e.bias;
+    const void *bias = MODE == kGated && e.swapped != (bool)(lane & 16) ? e.bias2 : e.bias;
     return bias && col_ok ? load_any(bias, c, e.bias_type) : 0.f;
 }
 // this thread's column of the output
@@ -429,20 +502,26 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *ma
     }
 }
 
-// P's rows for columns [p0, ...) of the output
+// P's rows for columns [p0, ...) of the output.  Gated: one box of a map over
+// both matrices where one can be made, or eight of 16 rows (which the copies'
+// rate does not keep up with: 8192 x 16384 x 4096 takes 1594 us with them, the
+// tensor pipe 56% active).
 template <int CG, bool MN, bool F8, int MODE>
 __device__ __forceinline__ void load_p(uint32_t dst, const CUtensorMap *map, const CUtensorMap *map2, uint64_t p0, uint32_t kb,
-                                       uint32_t kswitch, uint32_t bar)
+                                       const GemmArgs &g, uint32_t bar)
 {
     if constexpr (MODE == kGated) {
         constexpr int per = F8 ? 128 : 64;
+        if (g.one_box)
+            tma_load_turns<CG>(dst, map, (int)(kb * per), (int)(p0 / 16), bar);
+        else
 #pragma unroll
         for (uint32_t q = 0; q < 4; ++q) {
             tma_load<CG>(dst + q * 32 * kTileBytes, map, (int)(kb * per), (int)(p0 + q * 16), bar);
             tma_load<CG>(dst + (q * 32 + 16) * kTileBytes, map2, (int)(kb * per), (int)(p0 + q * 16), bar);
         }
-    } else if (MODE == kDual && kb >= kswitch) {
-        load_operand<CG, MN, F8>(dst, map2, p0, kPTile, kb - kswitch, bar);
+    } else if (MODE == kDual && kb >= g.kswitch) {
+        load_operand<CG, MN, F8>(dst, map2, p0, kPTile, kb - g.kswitch, bar);
     } else {
         load_operand<CG, MN, F8>(dst, map, p0, kPTile, kb, bar);
     }
@@ -478,8 +557,19 @@ __device__ __forceinline__ TilePos tile_pos(uint32_t t, uint32_t ptiles, uint32_
     return {p0 + r % w, r / w};
 }
 
+// kStats: the sums of 128 columns stay in a thread's registers, which the warps
+// that hold none of them give up: four warps of 40 and eight of 232, together
+// what twelve warps of 168 are launched with.
+constexpr int kStatsThreads = 384, kStatsRegisters = 168;
+constexpr int kFewRegisters = 40, kManyRegisters = 232;
+static_assert(kFewRegisters + 2 * kManyRegisters <= 3 * kStatsRegisters, "more registers than the launch has");
+template <int MODE> constexpr int kThreadsOf = MODE == kStats ? kStatsThreads : kPairThreads;
+template <int MODE> constexpr uint32_t kFirstEpilogueWarp = MODE == kStats ? 4 : 2;
+template <int N> __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 template <bool PMN, bool QMN, bool F8, int MODE>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap pmap2,
                      const __grid_constant__ CUtensorMap qmap, const __grid_constant__ GemmArgs g)
 {
@@ -518,9 +608,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tmem_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)&s.tmem;
     begin(g);
-
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < kFirstEpilogueWarp<MODE>) {
+        if constexpr (MODE == kStats)
+            give_registers<kFewRegisters>();
+        if (warp == 0 && lane == 0) {
             uint32_t st = 0, ph = 0, issued = 0;
             bool ok = true;
             for (uint32_t t = pair; t < tiles && ok; t += pairs) {
@@ -532,7 +623,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const uint32_t bar = cluster_addr(smem_u32(&s.full[st]), 0), at = stage0 + st * stage_bytes;
                     if (rank == 0)
                         mbar_expect_tx(&s.full[st], 2 * stage_bytes);
-                    load_p<2, PMN, F8, MODE>(at, &pmap, &pmap2, p0, kb, g.kswitch, bar);
+                    load_p<2, PMN, F8, MODE>(at, &pmap, &pmap2, p0, kb, g, bar);
                     load_operand<2, QMN, F8>(at + kPBytes, &qmap, q0, qn, kb, bar);
                     ++issued;
                     if (++st == g.stages) {
@@ -554,22 +645,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (warp == 1 && lane == 0 && rank == 0) {
             uint32_t st = 0, ph = 0, acc = 0, aph = 0;
             bool ok = true;
-            for (uint32_t t = pair; t < tiles && ok; t += pairs) {
+            uint32_t k0 = 0; // the accumulator's first reduction block
+            for (uint32_t t = pair; t < tiles && ok; k0 + kSegment < g.kblocks && MODE == kStats ? k0 += kSegment : (k0 = 0, t += pairs)) {
                 if (!(ok = mbar_wait(&s.tempty[acc], aph ^ 1, g.limit_ns)))
                     break;
                 tmem_fence_after();
-                for (uint32_t kb = 0; kb < g.kblocks; ++kb) {
+                const uint32_t k1 = MODE == kStats ? min(g.kblocks, k0 + kSegment) : g.kblocks;
+                for (uint32_t kb = k0; kb < k1; ++kb) {
                     if (!(ok = mbar_wait(&s.full[st], ph, g.limit_ns))) {
                         (void)mbar_wait(&s.full[st], ph, g.limit_ns);
                         break;
                     }
                     tmem_fence_after();
                     const uint32_t at = stage0 + st * stage_bytes;
-                    multiply_block<2, PMN, QMN, F8>(tmem + acc * g.bn, at, at + kPBytes, g.idesc, kb == 0);
+                    multiply_block<2, PMN, QMN, F8>(tmem + acc * g.bn, at, at + kPBytes, g.idesc, kb == k0);
                     tensor_commit<2>(smem_u32(&s.empty[st]));
                     if (++st == g.stages) {
                         st = 0;
@@ -585,8 +677,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 set_status(g.status, ECC_ERR_TIMEOUT);
         }
     } else {
+        if constexpr (MODE == kStats)
+            take_registers<kManyRegisters>();
         const uint32_t quad = warp & 3; // a warp reads the lanes of its number modulo 4
-        const uint32_t j0 = warp < 6 ? 0 : g.bn / 2, j1 = j0 + g.bn / 2;
+        const uint32_t j0 = warp < kFirstEpilogueWarp<MODE> + 4 ? 0 : g.bn / 2, j1 = j0 + g.bn / 2;
         uint32_t acc = 0, aph = 0;
         const float scale = scale_of<MODE>(g.e);
         for (uint32_t t = pair; t < tiles; t += pairs) {
@@ -596,10 +690,45 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const bool col_ok = c < g.cols;
             const float bias = bias_of<MODE>(g.e, c, col_ok, lane);
             const uint64_t left = g.rows - r0;
-            if constexpr (MODE == kStats || MODE == kSlopes) {
+            if constexpr (MODE == kStats) {
+                const int64_t token = g.e.tokens && col_ok ? g.e.tokens[c] : -1;
+                float2 a[64]; // (kStats: bn is 256)
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    a[i] = both(0.f);
+                bool ok = true;
+                for (uint32_t k0 = 0; ok && k0 < g.kblocks; k0 += kSegment) {
+                    if (!(ok = __all_sync(~0u, mbar_wait(&s.tfull[acc], aph, g.limit_ns))))
+                        break;
+                    tmem_fence_after();
+#pragma unroll
+                    for (uint32_t i = 0; i < 128; i += 16)
+                        tmem_add16(tmem + (quad * 32 << 16) + acc * 256 + j0 + i, a + i / 2);
+                    tmem_fence_before(); // the accumulator is read: products may fill it again
+                    __syncwarp();
+                    if (lane == 0)
+                        cluster_arrive(cluster_addr(smem_u32(&s.tempty[acc]), 0));
+                    if (acc)
+                        aph ^= 1;
+                    acc ^= 1;
+                }
+                if (!ok) {
+                    if (lane == 0)
+                        set_status(g.status, ECC_ERR_TIMEOUT);
+                    break;
+                }
                 LogitsPart p;
-                const int64_t token = MODE == kStats && g.e.tokens && col_ok ? g.e.tokens[c] : -1;
-                const LogitsSlope slope = MODE == kSlopes ? slope_of_token(g.e, c, col_ok) : LogitsSlope();
+                const int64_t rel = token - (int64_t)(r0 + j0);
+                if (col_ok && left >= j1)
+                    p = whole_part<128, true>(g.e, a, 128, scale, rel, c);
+                else if (col_ok && left > j0)
+                    p = whole_part<128, false>(g.e, a, (uint32_t)(left - j0), scale, rel, c);
+                if (col_ok)
+                    g.e.part[(pos.q * 2 + (j0 ? 1 : 0)) * g.cols + c] = make_float4(p.m, p.s, p.t, 0.f);
+                continue;
+            }
+            if constexpr (MODE == kSlopes) {
+                const LogitsSlope slope = slope_of_token(g.e, c, col_ok);
                 if (!__all_sync(~0u, mbar_wait(&s.tfull[acc], aph, g.limit_ns))) {
                     if (lane == 0)
                         set_status(g.status, ECC_ERR_TIMEOUT);
@@ -615,15 +744,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         if (lane == 0)
                             cluster_arrive(cluster_addr(smem_u32(&s.tempty[acc]), 0));
                     }
-                    if (!col_ok || j >= left)
-                        continue;
-                    if constexpr (MODE == kStats)
-                        add_logits(g.e, a, (uint32_t)min((uint64_t)32, left - j), scale, token - (int64_t)(r0 + j), c, p);
-                    else
+                    if (col_ok && j < left)
                         store_slopes(g.e, a, r0 + j, c, scale, slope.token - (int64_t)(g.e.first + r0 + j), slope);
                 }
-                if (MODE == kStats && col_ok)
-                    g.e.part[(pos.q * 2 + (j0 ? 1 : 0)) * g.cols + c] = make_float4(p.m, p.s, p.t, 0.f);
                 if (acc)
                     aph ^= 1;
                 acc ^= 1;
@@ -679,10 +802,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 // ---------------------------------------------------------------- clusters that share a tile's reduction
-// `wait` waits for the products (the first residual is asked for before)
+// `wait` waits for the products (the first residual is asked for before);
+// `used`: accumulators to add up (kStats)
 template <int W, int MODE, typename Wait>
 __device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, uint32_t quad, uint32_t lane, uint32_t c,
-                                              uint64_t r0, bool col_ok, float bias, bool direct, float *part, Wait wait)
+                                              uint64_t r0, bool col_ok, float bias, bool direct, float *part, uint32_t used, Wait wait)
 {
     const uint64_t left = g.rows - r0;
     const float scale = scale_of<MODE>(g.e);
@@ -698,10 +822,21 @@ __device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, 
         if (j == 0 && g.kblocks && !wait())
             return;
         if (g.kblocks) {
-            if constexpr (W == 32)
-                tmem_load32(tmem + (quad * 32 << 16) + j, a);
-            else
-                tmem_load16(tmem + (quad * 32 << 16) + j, a);
+            auto load = [&](uint32_t at, float (&v)[W]) {
+                if constexpr (W == 32)
+                    tmem_load32(tmem + (quad * 32 << 16) + at, v);
+                else
+                    tmem_load16(tmem + (quad * 32 << 16) + at, v);
+            };
+            load(j, a);
+            if constexpr (MODE == kStats)
+                for (uint32_t i = 1; i < used; ++i) {
+                    float v[W];
+                    load(i * g.bn + j, v);
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        a[k] += v[k];
+                }
         } else {
 #pragma unroll
             for (int i = 0; i < W; ++i)
@@ -748,7 +883,9 @@ __device__ __forceinline__ void split_tile(const CUtensorMap &pmap, const CUtens
     const uint64_t p0 = (uint64_t)(tile % g.ptiles) * kPCols<MODE>, q0 = (uint64_t)(tile / g.ptiles) * g.bn;
     const uint32_t kb0 = (uint32_t)((uint64_t)g.kblocks * rank / g.split);
     const uint32_t kb1 = (uint32_t)((uint64_t)g.kblocks * (rank + 1) / g.split);
-    const uint32_t tcols = g.bn < 32 ? 32 : g.bn;
+    // kStats: the reduction in up to 256 / bn accumulators, a segment each
+    const uint32_t segs = MODE == kStats ? min(g.bn < 64 ? 4u : 256u / g.bn, max(1u, (kb1 - kb0 + kSegment - 1) / kSegment)) : 1u;
+    const uint32_t tcols = MODE == kStats ? max(32u, g.bn * (segs == 3 ? 4 : segs)) : g.bn < 32 ? 32 : g.bn;
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < g.stages; ++i) {
             mbar_init(&s.full[i], 1);
@@ -787,7 +924,7 @@ __device__ __forceinline__ void split_tile(const CUtensorMap &pmap, const CUtens
                     break;
                 const uint32_t at = stage0 + st * stage_bytes;
                 mbar_expect_tx(&s.full[st], stage_bytes);
-                load_p<1, PMN, F8, MODE>(at, &pmap, &pmap2, p0, kb, g.kswitch, smem_u32(&s.full[st]));
+                load_p<1, PMN, F8, MODE>(at, &pmap, &pmap2, p0, kb, g, smem_u32(&s.full[st]));
                 load_operand<1, QMN, F8>(at + kPBytes, &qmap, q0, g.bn, kb, smem_u32(&s.full[st]));
                 if (++st == g.stages) {
                     st = 0;
@@ -816,7 +953,12 @@ __device__ __forceinline__ void split_tile(const CUtensorMap &pmap, const CUtens
                 }
                 tmem_fence_after();
                 const uint32_t at = stage0 + st * stage_bytes;
-                multiply_block<1, PMN, QMN, F8>(tmem, at, at + kPBytes, g.idesc, kb == kb0);
+                if constexpr (MODE == kStats) {
+                    const uint32_t per = (kb1 - kb0 + segs - 1) / segs, i = (kb - kb0) / per;
+                    multiply_block<1, PMN, QMN, F8>(tmem + i * g.bn, at, at + kPBytes, g.idesc, kb == kb0 + i * per);
+                } else {
+                    multiply_block<1, PMN, QMN, F8>(tmem, at, at + kPBytes, g.idesc, kb == kb0);
+                }
                 tensor_commit<1>(smem_u32(&s.empty[st]));
                 if (++st == g.stages) {
                     st = 0;
@@ -836,12 +978,14 @@ __device__ __forceinline__ void split_tile(const CUtensorMap &pmap, const CUtens
             tmem_fence_after();
             return ok;
         };
+        // accumulators in use
+        const uint32_t per = (kb1 - kb0 + segs - 1) / segs, used = per ? (kb1 - kb0 + per - 1) / per : 1;
         // once every product of this CTA is complete, the stages' memory holds its part
         float *part = reinterpret_cast<float *>(smem_raw + off);
         if (g.bn == 16)
-            split_columns<16, MODE>(g, tmem, quad, lane, c, q0, col_ok, bias, g.split == 1, part, wait);
+            split_columns<16, MODE>(g, tmem, quad, lane, c, q0, col_ok, bias, g.split == 1, part, used, wait);
         else
-            split_columns<32, MODE>(g, tmem, quad, lane, c, q0, col_ok, bias, g.split == 1, part, wait);
+            split_columns<32, MODE>(g, tmem, quad, lane, c, q0, col_ok, bias, g.split == 1, part, used, wait);
         tmem_fence_before();
     }
     __syncwarp();

@@ -23,6 +23,7 @@ struct Epilogue {
     void *pre2;
     uint64_t ldpre2;
     float scale2;
+    bool swapped; // the ups' rows come before the gates' in each turn
     // a second output: rows from rswitch on (a multiple of 64) go to out2, and
     // both have rows2 rows
     void *out2;
@@ -75,6 +76,7 @@ const void *dual_kernel(bool pair);
 const void *dual_both_kernel();
 const void *stats_kernel(bool f8, bool pair);
 const void *slopes_kernel(bool pair);
+const void *stats_stream(bool f8);
 // shares of the vocabulary that a kStats product writes parts for
 uint32_t stats_parts(const Product &x, uint32_t type);
 

@@ -63,6 +63,20 @@ template <int CG> __device__ __forceinline__ void tma_load(uint32_t dst, const C
                      "l"(map), "r"(x), "r"(y), "r"(bar)
                      : "memory");
 }
+// box at (x, 0, 0, z) of a 4-D map
+template <int CG> __device__ __forceinline__ void tma_load_turns(uint32_t dst, const CUtensorMap *map, int x, int z, uint32_t bar)
+{
+    if constexpr (CG == 2)
+        asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3, %3, %4}], [%5];" ::"r"(dst),
+                     "l"(map), "r"(x), "r"(0), "r"(z), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3, %3, %4}], [%5];" ::"r"(dst),
+                     "l"(map), "r"(x), "r"(0), "r"(z), "r"(bar)
+                     : "memory");
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -120,6 +134,36 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16])
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         v[i] = __uint_as_float(r[i]);
+}
+
+// 16 columns added to v (in one block of assembly, so that no more than 16
+// loaded values are held at a time)
+__device__ __forceinline__ void tmem_add16(uint32_t addr, float2 *v)
+{
+    asm volatile("{\n\t.reg .b32 t<16>;\n\t.reg .b64 u<8>;\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;\n\t"
+                 "mov.b64 u0, {t0, t1};\n\t"
+                 "mov.b64 u1, {t2, t3};\n\t"
+                 "mov.b64 u2, {t4, t5};\n\t"
+                 "mov.b64 u3, {t6, t7};\n\t"
+                 "mov.b64 u4, {t8, t9};\n\t"
+                 "mov.b64 u5, {t10, t11};\n\t"
+                 "mov.b64 u6, {t12, t13};\n\t"
+                 "mov.b64 u7, {t14, t15};\n\t"
+                 "add.rn.f32x2 %0, %0, u0;\n\t"
+                 "add.rn.f32x2 %1, %1, u1;\n\t"
+                 "add.rn.f32x2 %2, %2, u2;\n\t"
+                 "add.rn.f32x2 %3, %3, u3;\n\t"
+                 "add.rn.f32x2 %4, %4, u4;\n\t"
+                 "add.rn.f32x2 %5, %5, u5;\n\t"
+                 "add.rn.f32x2 %6, %6, u6;\n\t"
+                 "add.rn.f32x2 %7, %7, u7;\n\t"
+                 "}"
+                 : "+l"(reinterpret_cast<unsigned long long &>(v[0])), "+l"(reinterpret_cast<unsigned long long &>(v[1])), "+l"(reinterpret_cast<unsigned long long &>(v[2])), "+l"(reinterpret_cast<unsigned long long &>(v[3])), "+l"(reinterpret_cast<unsigned long long &>(v[4])), "+l"(reinterpret_cast<unsigned long long &>(v[5])), "+l"(reinterpret_cast<unsigned long long &>(v[6])), "+l"(reinterpret_cast<unsigned long long &>(v[7]))
+                 : "r"(addr)
+                 : "memory");
 }
 
 // Shared-memory operand descriptor: start address, the strides of the layout

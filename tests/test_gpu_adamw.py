@@ -158,6 +158,41 @@ def test_many_tensors_of_all_kinds_in_one_call():
             check(p, s, old[i][0], g, old[i][1], 20, grad_scale=0.5, **HYPER)
 
 
+def test_moments_round_as_separate_products_and_sums():
+    """To the bit: m beta1, g (1 - beta1), their sum; the 8-bit states follow from those."""
+    n = 40000
+    p, g, state = make(n, F32, F32, 32, False)
+    m, v = state.m[0].clone(), state.v[0].clone()
+    ecc.ecc_adamw([p], [g], state, step=5, **HYPER)
+    assert torch.equal(state.m[0], m * 0.9 + g * (1 - 0.9))
+    assert torch.equal(state.v[0], v * 0.95 + g * g * (1 - 0.95))
+
+
+@pytest.mark.parametrize("spread", [0.0, 1.0, 6.0, 20.0])
+def test_vectors_and_single_values_give_the_same_codes(spread):
+    """Groups with and without values below the smallest normal code, at aligned and unaligned addresses."""
+    n = 20 * G
+    p, g, state = make(n, F32, F32, 8, False, seed=3)
+    wide = torch.exp(torch.randn(n, device="cuda") * spread)
+    g = g * wide
+    state.m[0].view(E4M3)[::5] = 0
+    state.v[0].view(E4M3)[::5] = 0
+    g[::10] = 0                                          # zero moments among the others
+    other = [torch.empty(n + 1, dtype=t.dtype, device="cuda")[1:].copy_(t) for t in (p, g, state.m[0], state.v[0])]
+    old_p, old = p.clone(), copied(state)
+    s2 = ecc.AdamWState([other[2]], [other[3]], [state.m_scale[0].clone()], [state.v_scale[0].clone()])
+    ecc.ecc_adamw([p], [g], state, step=4, **HYPER)
+    ecc.ecc_adamw([other[0]], [other[1]], s2, step=4, **HYPER)
+    # (0.02 e^(20 * 4.5), the largest of 5120 gradients, has a square of 10^74: no float32 and no such update)
+    if float(g.double().square().max()) < 3e38:
+        check(p, state, old_p, g, old, 4, **HYPER)
+    assert torch.equal(p, other[0]) or bool((p.isnan() == other[0].isnan()).all())
+    for a, b in zip(state[:4], s2[:4]):
+        assert torch.equal(a[0].view(BYTE), b[0].view(BYTE))
+    if bool(torch.isfinite(state.m_scale[0]).all()):
+        assert not state.m[0].view(E4M3).float()[::10].any() and not state.v[0][::10].any()
+
+
 def test_nothing_beyond_the_tensors_is_written():
     n = 1000
     for bits in (8, 32):
