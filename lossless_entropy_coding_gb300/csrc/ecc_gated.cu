@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kRowThreads) gated_slope_kernel(const __grid_c
     for (int i = 0; i < H; ++i)
         sg[i] = su[i] = both(0.f);
     if (c < p.np)
+#pragma unroll 2
         for (uint64_t r = r0 + ty; r < r1; r += 8) {
             float2 v[H], g[H], u[H];
             if (c < p.N) {
@@ -185,7 +186,10 @@ GatedGradPlan gated_grad_plan(const ecc_gated_linear_grad_job &j)
     GatedGradPlan g{};
     g.np = (j.N + 63) / 64 * 64;
     g.t_bytes = j.dx || j.dw_gate ? pad256(j.M * 2 * g.np * type_bytes(j.in_type)) : 0;
-    g.parts = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(kGatedParts, j.M / 64));
+    // 64 rows a block, or down to 16 (two a warp) while there are fewer blocks than about two an SM: 257 x 1000
+    // takes 11 us on 16 blocks
+    const uint64_t across = (j.N + 255) / 256;
+    g.parts = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({kGatedParts, std::max(j.M / 64, 304 / std::max<uint64_t>(across, 1)), j.M / 16}));
     g.part_bytes = j.dbias_gate ? pad256(g.parts * 2 * j.N * sizeof(float)) : 0;
     g.bytes = g.t_bytes + g.part_bytes;
     if (j.dx)

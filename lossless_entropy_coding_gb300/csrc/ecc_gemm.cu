@@ -314,14 +314,23 @@ ecc_status gemm_backward(const Product &dx, const Product &dw, uint32_t type, ui
     if (sms <= 0)
         return ECC_ERR_CUDA;
     Shape s1 = shape_of(dx, type, sms), s2 = shape_of(dw, type, sms);
-    // in one launch where neither fills the GPU by itself and both fit it, two CTAs an SM
+    // In one launch where neither fills the GPU by itself and both fit it, two
+    // CTAs an SM, with their reductions shared out less if need be; or, as they
+    // are, where they make two such fillings at most: the second product's CTAs
+    // start as the first one's end (linear gradient of 512 x 2048 x 2048 34.5 us,
+    // 46.8 in two launches; 333 x 8001 x 515 52.9 and 62.1).
     // (dx is kPlain or kDual, dw kPlain: 128 columns a tile)
     const uint64_t t1 = up(dx.cols, kPTile) * up(dx.rows, s1.bn), t2 = up(dw.cols, kPTile) * up(dw.rows, s2.bn);
+    const Shape o1 = s1, o2 = s2;
     while (t1 * s1.split + t2 * s2.split > 2ull * sms && (s1.split > 1 || s2.split > 1)) {
         uint32_t &s = t1 * s1.split > t2 * s2.split ? (s1.split > 1 ? s1.split : s2.split) : (s2.split > 1 ? s2.split : s1.split);
         s /= 2;
     }
-    if (s1.pair || s2.pair || !dx.K || !dw.K || t1 * s1.split + t2 * s2.split > 2ull * sms) {
+    if (t1 * s1.split + t2 * s2.split > 2ull * sms) {
+        s1 = o1;
+        s2 = o2;
+    }
+    if (s1.pair || s2.pair || !dx.K || !dw.K || t1 * s1.split + t2 * s2.split > 4ull * sms) {
         const ecc_status rc = gemm(dx, type, status, clear_status, behind, st); // (each in its own shape)
         return rc == ECC_OK ? gemm(dw, type, status, false, true, st) : rc;
     }
