@@ -116,6 +116,71 @@ def train_step(x, tokens, par, rate):
     return bits, coded / values
 
 
+def serve_gated(x, tokens, par):
+    """One pass of the gated block over hidden states x, weights and activation coded as they move."""
+    received = {}
+    for k in ("gate", "up", "down", "head"):
+        q, scale = e4m3(par[k].float())
+        q2, _ = sent(q, book_of(q))
+        received[k] = (q2, scale)
+    h, _, _ = ecc.ecc_layer_norm(x, par["n1"], par["c1"], out_dtype=BYTES, out_scale=16.0)
+    (g, sg), (u, su), (d, sd), (w, sw) = (received[k] for k in ("gate", "up", "down", "head"))
+    a, s1 = ecc.ecc_gated_linear(h, g, u, act="gelu_tanh", scale=sg / 16, up_scale=su / 16, out_dtype=BYTES, out_scale=16.0)
+    a2, bits = sent(a, book_of(a[:64]))
+    y, s2 = ecc.ecc_linear(a2, d, residual=x, scale=sd / 16, out_dtype=BF16)
+    z, _, _ = ecc.ecc_layer_norm(y, par["n2"], par["c2"], out_dtype=BYTES, out_scale=16.0)
+    p = ecc.ecc_linear_logprob(z, w, tokens, scale=sw / 16)
+    ok(s1, s2, p.status)
+    return {"activation_bits": bits / a.numel(), "bits_per_token": float(-p.logprob.mean()) / math.log(2), "lossless": torch.equal(a, a2)}
+
+
+def train_gated(x, tokens, par, state, step, rate):
+    """One step of the gated block under AdamW; updates par and state; bits per token."""
+    rows = x.shape[0]
+    h, m1, r1 = ecc.ecc_layer_norm(x, par["n1"], par["c1"])
+    pre_g, pre_u = (torch.empty(rows, par["up"].shape[0], dtype=BF16, device=x.device) for _ in range(2))
+    a, s1 = ecc.ecc_gated_linear(h, par["gate"], par["up"], act="gelu_tanh", pre_gate=pre_g, pre_up=pre_u)
+    y, s2 = ecc.ecc_linear(a, par["down"], residual=x)
+    z, m2, r2 = ecc.ecc_layer_norm(y, par["n2"], par["c2"])
+    p = ecc.ecc_linear_logprob(z, par["head"], tokens)
+    dlogp = torch.full((rows,), -1.0 / rows, device=x.device)   # the loss is the mean of -log p
+    g = {}
+    dz, g["head"], s3 = ecc.ecc_linear_logprob_grad(z, par["head"], tokens, p.lse, None, dlogp)
+    dy, g["n2"], g["c2"] = ecc.ecc_layer_norm_grad(dz, y, par["n2"], m2, r2)
+    da, g["down"], _, s4 = ecc.ecc_linear_grad(dy, a, par["down"], want=("dx", "dw"))
+    dh, g["gate"], g["up"], _, _, s5 = ecc.ecc_gated_linear_grad(da, h, par["gate"], par["up"], pre_g, pre_u, act="gelu_tanh",
+                                                                want=("dx", "dw"))
+    _, g["n1"], g["c1"] = ecc.ecc_layer_norm_grad(dh, x, par["n1"], m1, r1)   # (dx = this + dy)
+    ok(s1, s2, p.status, s3, s4, s5)
+    for k, v in g.items():
+        if v.dtype == BF16:                       # weight gradients move coded
+            top7 = ecc.bf16_escape_table_sigma(max(float(v.float().std()), 1e-30))
+            enc = ecc.bf16_escape_encode(v, top7)
+            back, st = ecc.bf16_escape_decode(enc, top7)
+            ok(enc.status, st)
+            g[k] = back[:v.numel()].view(BF16).view(v.shape)
+    ecc.ecc_adamw(list(par.values()), [g[k] for k in par], state, step, lr=rate, weight_decay=0.01, seed=1)
+    return float(-p.logprob.mean()) / math.log(2)
+
+
+def gated_parameters(width, hidden, vocab, device="cuda", seed=0):
+    par = parameters(width, hidden, vocab, device, seed)
+    gate = parameters(width, hidden, vocab, device, seed + 1)["up"]
+    return {k: v for k, v in list(par.items()) + [("gate", gate)] if k not in ("bu", "bd")}
+
+
+def run_gated(rows=512, width=512, hidden=2048, vocab=8000, steps=6, rate=2e-3):
+    par = gated_parameters(width, hidden, vocab)
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.randn(rows, width, generator=g, device="cuda").to(BF16)
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    state = ecc.adamw_state(list(par.values()), bits=8)
+    history = [train_gated(x, tokens, par, state, step + 1, rate) for step in range(steps)]
+    moments = torch.cat([t.view(-1) for t in state.m + state.v])
+    back, bits = sent(moments, book_of(moments))   # the optimizer's bytes, as for a checkpoint
+    return serve_gated(x, tokens, par), history, {"lossless": torch.equal(back, moments), "bits": bits / moments.numel()}
+
+
 def parameters(width, hidden, vocab, device="cuda", seed=0):
     g = torch.Generator(device).manual_seed(seed)
 
@@ -145,3 +210,8 @@ if __name__ == "__main__":
           f"text {served['bits_per_token']:.2f} bits a token (entropy {served['entropy_bits']:.2f})")
     for i, (bits, grad) in enumerate(history):
         print(f"step {i}: {bits:.3f} bits a token, weight gradients {grad:.2f} bits a value")
+    served, history, moments = run_gated()
+    for i, bits in enumerate(history):
+        print(f"gated block, step {i}: {bits:.3f} bits a token")
+    print(f"served: {served['bits_per_token']:.3f} bits a token, activation {served['activation_bits']:.2f} bits a value, "
+          f"AdamW's moments {moments['bits']:.2f}")
