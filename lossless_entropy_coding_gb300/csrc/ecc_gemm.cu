@@ -49,6 +49,19 @@ bool make_map(CUtensorMap *map, const Operand &o, uint64_t rows, uint64_t K, uin
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// map of an output [rows, cols]: boxes of 32 x 32 values
+bool make_out_map(CUtensorMap *map, void *p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t type)
+{
+    const uint32_t size = type_bytes(type);
+    const cuuint64_t dims[2] = {cols, rows}, stride[1] = {rows > 1 ? ld * size : (cols * size + 15) / 16 * 16};
+    const cuuint32_t box[2] = {32, 32}, one[2] = {1, 1};
+    const CUtensorMapDataType t = type == ECC_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : type == ECC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return encode_tiled()(map, t, 2, p, dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // One map over two matrices of `rows` rows of one stride, 16 rows of each in
 // turns: the second one's distance is a stride.  Whether there can be one.
 bool make_turns_map(CUtensorMap *map, const Operand &lower, const Operand &upper, uint64_t rows, uint64_t K, uint32_t type)
@@ -121,9 +134,12 @@ Shape choose_shape(uint64_t rows, uint64_t cols, uint64_t K, uint32_t kblocks, b
     return best;
 }
 
+// Reductions of up to this many blocks hide no epilogue.
+constexpr uint32_t kStagedBlocks = 16;
+
 // A product made ready: its maps, its arguments.
 struct Plan {
-    CUtensorMap pm{}, pm2{}, qm{};
+    CUtensorMap pm{}, pm2{}, qm{}, om{}, om2{};
     GemmArgs g{};
     bool pair = false;
     uint32_t stage_bytes = 0;
@@ -170,6 +186,14 @@ ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t 
     // (kDual: the first matrix's reduction ends somewhere in its last block, whose rest reads as zeros)
     const uint32_t box = gated ? 16 : x.P.mn ? 64 : kPTile;
     const uint64_t k1 = x.mode == kDual ? x.kfirst : x.K;
+    // results through shared memory: of reductions that are shorter than the epilogue
+    const Epilogue &e = x.e;
+    const uint64_t orows = e.rswitch ? e.rows2 : x.rows;
+    if (shape.pair && x.mode == kPlain && g.kblocks <= kStagedBlocks && e.out_type != ECC_E4M3 && !e.pre && !e.residual &&
+        tma_rows(e.out, e.ldout, e.out_type, orows) && (!e.rswitch || tma_rows(e.out2, e.ldout2, e.out_type, orows)) && encode_tiled() &&
+        make_out_map(&plan.om, e.out, e.ldout, orows, x.cols, e.out_type) &&
+        (!e.rswitch || make_out_map(&plan.om2, e.out2, e.ldout2, orows, x.cols, e.out_type)))
+        g.staged = type_bytes(e.out_type);
     if (!encode_tiled() || !make_map(&plan.qm, x.Q, g.rows, x.K, type, x.Q.mn ? 64 : qn))
         return ECC_ERR_CUDA;
     if (gated) {
@@ -188,9 +212,10 @@ ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t 
 size_t stage_memory(Plan &plan, uint32_t ctas, int sms)
 {
     const bool alone = plan.pair || ctas <= (uint32_t)sms; // one CTA an SM
-    const uint32_t budget = (alone ? kAloneSmem : kSharedSmem) - kSmemHead - (uint32_t)sizeof(GemmBars);
+    const uint32_t out = plan.g.staged * 2048 * 8; // two stages of 32 x 32 values for each of eight warps
+    const uint32_t budget = (alone ? kAloneSmem : kSharedSmem) - kSmemHead - (uint32_t)sizeof(GemmBars) - out;
     plan.g.stages = std::min(kMaxStages, budget / plan.stage_bytes);
-    return kSmemHead + (size_t)plan.g.stages * plan.stage_bytes;
+    return kSmemHead + (size_t)plan.g.stages * plan.stage_bytes + out;
 }
 
 ecc_status launch_plan(const void *f, int threads, uint32_t ctas, uint32_t cluster, size_t smem, void **args, bool behind,
@@ -301,7 +326,9 @@ ecc_status gemm(const Product &x, uint32_t type, uint32_t *status, bool clear_st
     const uint32_t ctas = pair ? 2 * std::min<uint32_t>(plan.tiles(), sms / 2) : plan.tiles() * plan.g.split;
     const size_t smem = stage_memory(plan, ctas, sms);
     const void *f = kernel_of(x, type == ECC_E4M3, pair);
-    void *args[] = {&plan.pm, &plan.pm2, &plan.qm, &plan.g};
+    void *pair_args[] = {&plan.pm, &plan.pm2, &plan.qm, &plan.om, &plan.om2, &plan.g};
+    void *split_args[] = {&plan.pm, &plan.pm2, &plan.qm, &plan.g};
+    void **args = pair ? pair_args : split_args;
     if (pair && x.mode == kStats && !registers_of(f, kStatsRegisters))
         return ECC_ERR_CUDA;
     return launch_plan(f, pair ? (x.mode == kStats ? kStatsThreads : kPairThreads) : kSplitThreads, ctas, pair ? 2 : plan.g.split, smem, args, behind, st);

@@ -49,6 +49,7 @@ constexpr uint32_t kSmemHead = 1024; // room to align the stages to 1024 bytes
 struct GemmArgs {
     Epilogue e;
     uint32_t kswitch; // kDual: the reduction block where the second matrix starts
+    uint32_t staged;  // kPlain: bytes of an output value if results leave through shared memory, or 0
     bool one_box;     // kGated: P's map has both matrices, in turns of 16 rows
     uint64_t rows, cols;
     uint32_t kblocks; // reduction blocks of 128 bytes (64 reduction indices for MN-major operands)
@@ -222,6 +223,29 @@ template <int MODE> __device__ __forceinline__ float scale_of(const Epilogue &e)
         return e.scale * 1.44269504f;
     else
         return e.factor ? e.scale * *e.factor : e.scale;
+}
+
+// The same for results that leave through shared memory (no pre, no residual):
+// a warp's 32 rows of 32 columns at `stage`, a row after the other.
+template <typename T> __device__ __forceinline__ void stage_rows(uint8_t *stage, uint32_t lane, const float (&a)[32])
+{
+    T *s = reinterpret_cast<T *>(stage) + lane;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        s[j * 32] = from_f32<T>(a[j]);
+}
+__device__ __forceinline__ void finish_staged(const Epilogue &e, float (&a)[32], uint8_t *stage, uint32_t lane, float bias, float scale)
+{
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        a[j] = a[j] * scale + bias;
+    activate_by(e.act, a);
+    if (e.out_type == ECC_F32)
+        stage_rows<float>(stage, lane, a);
+    else if (e.out_type == ECC_BF16)
+        stage_rows<bf16>(stage, lane, a);
+    else
+        stage_rows<__half>(stage, lane, a);
 }
 
 // ---------------------------------------------------------------- gated epilogue
@@ -571,7 +595,8 @@ template <int N> __device__ __forceinline__ void take_registers() { asm volatile
 template <bool PMN, bool QMN, bool F8, int MODE>
 __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap pmap2,
-                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ GemmArgs g)
+                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
+                     const __grid_constant__ CUtensorMap omap2, const __grid_constant__ GemmArgs g)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ GemmBars s;
@@ -752,6 +777,49 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                 acc ^= 1;
                 continue;
             }
+            if (MODE == kPlain && g.staged) {
+                // Short reductions: results through shared memory, two stages a
+                // warp, by copies of 32 x 32 values.  (Half the instructions of
+                // store_rows, none of them an address.)
+                if (!__all_sync(~0u, mbar_wait(&s.tfull[acc], aph, g.limit_ns))) {
+                    if (lane == 0)
+                        set_status(g.status, ECC_ERR_TIMEOUT);
+                    break;
+                }
+                tmem_fence_after();
+                uint8_t *stage = smem_raw + (stage0 - smem_u32(smem_raw)) + g.stages * stage_bytes + (warp - 2) * 2048 * g.staged;
+                const uint32_t c0 = c - lane;
+                for (uint32_t j = j0; j < j1; j += 32) {
+                    float a[32];
+                    tmem_load32(tmem + (quad * 32 << 16) + acc * g.bn + j, a);
+                    if (j + 32 == j1) { // the accumulator is read: products may fill it again
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            cluster_arrive(cluster_addr(smem_u32(&s.tempty[acc]), 0));
+                    }
+                    if (j >= left || c0 >= g.cols)
+                        continue;
+                    uint8_t *at = stage + (j & 32) * 32 * g.staged;
+                    if (lane == 0)
+                        tma_stores_read<1>();
+                    __syncwarp();
+                    finish_staged(g.e, a, at, lane, bias, scale);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const uint64_t r = r0 + j;
+                        if (g.e.rswitch && r >= g.e.rswitch)
+                            tma_store(&omap2, smem_u32(at), (int)c0, (int)(r - g.e.rswitch));
+                        else
+                            tma_store(&omap, smem_u32(at), (int)c0, (int)r);
+                    }
+                }
+                if (acc)
+                    aph ^= 1;
+                acc ^= 1;
+                continue;
+            }
             uint32_t res[2][32]; // of this chunk of 32 rows and the next
             auto ask = [&](uint32_t j, uint32_t (&v)[32]) {
                 if (MODE != kGated && col_ok && j < j1 && j < left)
@@ -792,6 +860,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
             acc ^= 1;
         }
     }
+    if (MODE == kPlain && g.staged && lane == 0)
+        tma_stores_done();
     __syncthreads();
     __syncwarp();
     tmem_fence_before();
