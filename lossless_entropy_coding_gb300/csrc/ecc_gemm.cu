@@ -68,7 +68,7 @@ bool make_turns_map(CUtensorMap *map, const Operand &lower, const Operand &upper
 {
     const uint32_t size = type_bytes(type);
     const uint64_t apart = (const uint8_t *)upper.p - (const uint8_t *)lower.p;
-    if (rows % 16 || lower.ld != upper.ld || apart % 16 || apart >= 1ull << 40 || lower.ld * size >= 1ull << 36)
+    if (rows % 16 || lower.ld != upper.ld || !apart || apart % 16 || apart >= 1ull << 40 || lower.ld * size >= 1ull << 36)
         return false;
     const cuuint64_t dims[4] = {K, 16, 2, rows / 16}, stride[3] = {lower.ld * size, apart, 16 * lower.ld * size};
     const cuuint32_t box[4] = {kTileBytes / size, 16, 2, kPTile / 32}, one[4] = {1, 1, 1, 1};

@@ -236,7 +236,15 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
     Operand x, w;
     bool behind = readable({{j.x, j.ldx, j.rows, j.K, &x}, {j.w, j.ldw, j.vocab, j.K, &w}}, j.in_type, at, st);
     if (factor) {
-        const ecc_status rc = launch_status(launch_behind(factor_kernel, dim3(1), 1024, 0, st, j.dlogprob, j.dentropy, j.rows, factor));
+        // (as the call's first launch it starts after the one before it has ended, which may read this workspace)
+        cudaError_t e = cudaSuccess;
+        if (behind) {
+            e = launch_behind(factor_kernel, dim3(1), 1024, 0, st, j.dlogprob, j.dentropy, j.rows, factor);
+        } else {
+            factor_kernel<<<1, 1024, 0, st>>>(j.dlogprob, j.dentropy, j.rows, factor);
+            e = cudaGetLastError();
+        }
+        const ecc_status rc = launch_status(e);
         if (rc != ECC_OK)
             return rc;
         behind = true;

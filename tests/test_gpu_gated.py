@@ -120,6 +120,22 @@ def test_gated_few_rows(M, N, K, dtype):
         assert torch.equal(first.view(torch.uint8), again.view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("M", [20, 700])
+def test_gated_weights_wherever_they_lie(M, dtype):
+    """Gates above ups and below them, rows of one matrix in turns, the same matrix twice, other strides, far apart."""
+    gen = torch.Generator("cuda").manual_seed(17)
+    N, K = 160, 256
+    x, both = rows_of(gen, M, K, dtype), rows_of(gen, 2 * N, K, dtype, std=0.1)
+    far = torch.empty(3 << 30, dtype=torch.uint8, device="cuda")[-N * K * both.element_size():].view(dtype).view(N, K)
+    far.copy_(both[N:])
+    a, b = both[:N], both[N:]
+    bias = rows_of(gen, 2, N, F32)
+    for wg, wu in ((a, b), (b, a), (both[::2], both[1::2]), (both[1::2], both[::2]), (a, a), (a, both[::2]), (a, far), (far, a),
+                   (both[1:N + 1], both[:N])):
+        check(x, wg, wu, *bias, pre_dtype=BF16, up_scale=0.5)
+
+
 def test_gated_large_offsets_and_rows_beside_the_output():
     gen = torch.Generator("cuda").manual_seed(3)
     buf = torch.zeros((1 << 32) + 4096, dtype=BF16, device="cuda")       # rows 2^31 elements apart

@@ -265,6 +265,23 @@ def test_head_grad_in_pieces():
         assert bool(((dw[some].double() - ref).abs() <= e).all())
 
 
+def test_head_grad_calls_back_to_back_in_one_workspace():
+    """F16's power of two is each call's own, also where the next call's first kernel could start early."""
+    gen = torch.Generator("cuda").manual_seed(9)
+    M, V, K = 256, 20000, 512
+    x, w, tok = rows_of(gen, M, K, F16), rows_of(gen, V, K, F16, std=0.1), tokens_of(gen, M, V)
+    r = ecc.ecc_linear_logprob(x, w, tok)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    scales = [torch.full((M,), 2.0**(12 * (i % 3) - 12), device="cuda") for i in range(12)]
+    alone = []
+    for s in scales[:3]:
+        alone.append(ecc.ecc_linear_logprob_grad(x, w, tok, r.lse, None, s, dw_dtype=F32, ws=ws))
+        torch.cuda.synchronize()
+    got = [ecc.ecc_linear_logprob_grad(x, w, tok, r.lse, None, s, dw_dtype=F32, ws=ws) for s in scales]
+    for i, (dx, dw, st) in enumerate(got):
+        assert torch.equal(dx, alone[i % 3][0]) and torch.equal(dw, alone[i % 3][1]) and int(st.item()) == 0
+
+
 def test_head_grad_wanted_outputs_and_given_tensors():
     gen = torch.Generator("cuda").manual_seed(12)
     for M, V, K in ((130, 300, 200), (600, 2000, 320)):
