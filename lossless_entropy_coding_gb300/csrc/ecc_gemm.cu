@@ -49,6 +49,20 @@ bool make_map(CUtensorMap *map, const Operand &o, uint64_t rows, uint64_t K, uin
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// map of an operand down its columns, in groups of 64 rows: boxes of `groups`
+// of them by 64 reduction indices
+bool make_wide_map(CUtensorMap *map, const Operand &o, uint64_t rows, uint64_t K, uint32_t type, uint32_t groups)
+{
+    if (rows % 64)
+        return false;
+    const uint32_t size = type_bytes(type);
+    const cuuint64_t dims[3] = {64, K, rows / 64}, stride[2] = {K > 1 ? o.ld * size : rows * size, 64 * size};
+    const cuuint32_t box[3] = {64, 64, groups}, one[3] = {1, 1, 1};
+    return encode_tiled()(map, map_type(type), 3, const_cast<void *>(o.p), dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // map of an output [rows, cols]: boxes of 32 x 32 values
 bool make_out_map(CUtensorMap *map, void *p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t type)
 {
@@ -194,7 +208,10 @@ ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t 
         make_out_map(&plan.om, e.out, e.ldout, orows, x.cols, e.out_type) &&
         (!e.rswitch || make_out_map(&plan.om2, e.out2, e.ldout2, orows, x.cols, e.out_type)))
         g.staged = type_bytes(e.out_type);
-    if (!encode_tiled() || !make_map(&plan.qm, x.Q, g.rows, x.K, type, x.Q.mn ? 64 : qn))
+    if (!encode_tiled())
+        return ECC_ERR_CUDA;
+    g.qwide = x.Q.mn && make_wide_map(&plan.qm, x.Q, g.rows, x.K, type, qn / 64);
+    if (!g.qwide && !make_map(&plan.qm, x.Q, g.rows, x.K, type, x.Q.mn ? 64 : qn))
         return ECC_ERR_CUDA;
     if (gated) {
         g.e.swapped = x.P2.p < x.P.p;
@@ -202,8 +219,10 @@ ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t 
             return ECC_OK;
         g.e.swapped = false;
     }
-    if (!make_map(&plan.pm, x.P, g.cols, k1, type, box) ||
-        ((gated || x.mode == kDual) && !make_map(&plan.pm2, x.P2, g.cols, k1, type, box)))
+    g.pwide = x.P.mn && make_wide_map(&plan.pm, x.P, g.cols, k1, type, kPTile / 64) &&
+              (x.mode != kDual || make_wide_map(&plan.pm2, x.P2, g.cols, k1, type, kPTile / 64));
+    if (!g.pwide && (!make_map(&plan.pm, x.P, g.cols, k1, type, box) ||
+                     ((gated || x.mode == kDual) && !make_map(&plan.pm2, x.P2, g.cols, k1, type, box))))
         return ECC_ERR_CUDA;
     return ECC_OK;
 }

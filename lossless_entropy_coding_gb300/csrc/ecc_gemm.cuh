@@ -49,6 +49,7 @@ constexpr uint32_t kSmemHead = 1024; // room to align the stages to 1024 bytes
 struct GemmArgs {
     Epilogue e;
     uint32_t kswitch; // kDual: the reduction block where the second matrix starts
+    bool pwide, qwide; // operands down their columns: one box for all of a tile's rows
     uint32_t staged;  // kPlain: bytes of an output value if results leave through shared memory, or 0
     bool one_box;     // kGated: P's map has both matrices, in turns of 16 rows
     uint64_t rows, cols;
@@ -512,15 +513,21 @@ __device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint3
 }
 
 // ---------------------------------------------------------------- loads and products of a reduction block
-// rows [r0, r0 + n) of reduction block kb -> dst
+// rows [r0, r0 + n) of reduction block kb -> dst.  Down the columns, `wide`:
+// one box over groups of 64 rows where there are only whole groups, or a box
+// for each (a copy unit takes a box in about 120 cycles, and four of them
+// a block kept the tensor pipe 80% active).
 template <int CG, bool MN, bool F8>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, uint64_t r0, uint32_t n, uint32_t kb,
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, uint64_t r0, uint32_t n, uint32_t kb, bool wide,
                                              uint32_t bar)
 {
     constexpr int per = F8 ? 128 : 64; // reduction indices of a block
     if constexpr (MN) {
-        for (uint32_t c = 0; c < n; c += 64)
-            tma_load<CG>(dst + c * kTileBytes, map, (int)(r0 + c), (int)(kb * 64), bar);
+        if (wide)
+            tma_load_groups<CG>(dst, map, (int)(kb * 64), (int)(r0 / 64), bar);
+        else
+            for (uint32_t c = 0; c < n; c += 64)
+                tma_load<CG>(dst + c * kTileBytes, map, (int)(r0 + c), (int)(kb * 64), bar);
     } else {
         tma_load<CG>(dst, map, (int)(kb * per), (int)r0, bar);
     }
@@ -545,9 +552,9 @@ __device__ __forceinline__ void load_p(uint32_t dst, const CUtensorMap *map, con
             tma_load<CG>(dst + (q * 32 + 16) * kTileBytes, map2, (int)(kb * per), (int)(p0 + q * 16), bar);
         }
     } else if (MODE == kDual && kb >= g.kswitch) {
-        load_operand<CG, MN, F8>(dst, map2, p0, kPTile, kb - g.kswitch, bar);
+        load_operand<CG, MN, F8>(dst, map2, p0, kPTile, kb - g.kswitch, g.pwide, bar);
     } else {
-        load_operand<CG, MN, F8>(dst, map, p0, kPTile, kb, bar);
+        load_operand<CG, MN, F8>(dst, map, p0, kPTile, kb, g.pwide, bar);
     }
 }
 
@@ -649,7 +656,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                     if (rank == 0)
                         mbar_expect_tx(&s.full[st], 2 * stage_bytes);
                     load_p<2, PMN, F8, MODE>(at, &pmap, &pmap2, p0, kb, g, bar);
-                    load_operand<2, QMN, F8>(at + kPBytes, &qmap, q0, qn, kb, bar);
+                    load_operand<2, QMN, F8>(at + kPBytes, &qmap, q0, qn, kb, g.qwide, bar);
                     ++issued;
                     if (++st == g.stages) {
                         st = 0;
@@ -995,7 +1002,7 @@ __device__ __forceinline__ void split_tile(const CUtensorMap &pmap, const CUtens
                 const uint32_t at = stage0 + st * stage_bytes;
                 mbar_expect_tx(&s.full[st], stage_bytes);
                 load_p<1, PMN, F8, MODE>(at, &pmap, &pmap2, p0, kb, g, smem_u32(&s.full[st]));
-                load_operand<1, QMN, F8>(at + kPBytes, &qmap, q0, g.bn, kb, smem_u32(&s.full[st]));
+                load_operand<1, QMN, F8>(at + kPBytes, &qmap, q0, g.bn, kb, g.qwide, smem_u32(&s.full[st]));
                 if (++st == g.stages) {
                     st = 0;
                     ph ^= 1;

@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                         break;
                     const uint32_t at = stage0 + st * stage_bytes, bar = smem_u32(&s.full[st]);
                     mbar_expect_tx(&s.full[st], stage_bytes);
-                    load_operand<1, false, F8>(at, &wmap, (uint64_t)t * kPTile, kPTile, kb, bar);
-                    load_operand<1, false, F8>(at + kPBytes, &xmap, 0, g.bn, kb, bar);
+                    load_operand<1, false, F8>(at, &wmap, (uint64_t)t * kPTile, kPTile, kb, false, bar);
+                    load_operand<1, false, F8>(at + kPBytes, &xmap, 0, g.bn, kb, false, bar);
                     ++issued;
                     if (++st == g.stages) {
                         st = 0;

@@ -66,6 +66,20 @@ template <int CG> __device__ __forceinline__ void tma_load(uint32_t dst, const C
                      "l"(map), "r"(x), "r"(y), "r"(bar)
                      : "memory");
 }
+// box at (0, y, z) of a 3-D map
+template <int CG> __device__ __forceinline__ void tma_load_groups(uint32_t dst, const CUtensorMap *map, int y, int z, uint32_t bar)
+{
+    if constexpr (CG == 2)
+        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                     "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                     "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
+                     : "memory");
+}
 // box at (x, 0, 0, z) of a 4-D map
 template <int CG> __device__ __forceinline__ void tma_load_turns(uint32_t dst, const CUtensorMap *map, int x, int z, uint32_t bar)
 {
