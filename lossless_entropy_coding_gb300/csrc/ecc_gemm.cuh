@@ -113,12 +113,11 @@ template <int W> __device__ __forceinline__ void activate_by(uint32_t act, float
 
 // W rows of a column, the first n of them in range.  The rows' addresses are
 // the same for the whole warp (uniform registers); a lane adds its column.
-// A reduction of less than about 1024 takes as long as this does, 3.8 us a tile
-// of 256 x 256 (8192 x 16384 x 64: 107 us, 2.5 TB/s, and as long with float32 or e4m3
-// results).  Slower: four values a store, lanes' rows exchanged for columns by
-// shuffles, 119 us; whole rows by four warps through shared memory, 195; eight
-// warps of 16 rows at a time, 125.  Sixteen such warps: 103, but 168 instead
-// of 163 at a reduction of 1024.
+// A reduction of less than about 1024 takes as long as this does, 3.5 us a tile
+// of 256 x 256 (8192 x 16384 x 64: 103 us, 2.6 TB/s, and as long with e4m3
+// results; finish_staged: 68).  Slower: four values a store, lanes' rows
+// exchanged for columns by shuffles; whole rows by four warps through shared
+// memory; eight warps of 16 rows at a time.
 template <typename T, int W>
 __device__ __forceinline__ void store_rows(void *base, uint64_t ld, uint64_t r0, uint32_t n, uint32_t c, const float (&a)[W],
                                            float s)
@@ -227,7 +226,9 @@ template <int MODE> __device__ __forceinline__ float scale_of(const Epilogue &e)
 }
 
 // The same for results that leave through shared memory (no pre, no residual):
-// a warp's 32 rows of 32 columns at `stage`, a row after the other.
+// a warp's 32 rows of 32 columns at `stage`, a row after the other.  8192 x
+// 16384 x 64 68 us, 4 TB/s (103 by store_rows); at a reduction of 1024 156 us
+// (167).  For 16-bit and float32 results on 16-byte boundaries.
 template <typename T> __device__ __forceinline__ void stage_rows(uint8_t *stage, uint32_t lane, const float (&a)[32])
 {
     T *s = reinterpret_cast<T *>(stage) + lane;

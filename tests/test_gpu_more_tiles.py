@@ -1,0 +1,108 @@
+"""The persistent kernels of the gated projections and of the head with more
+tiles than CTAs: accumulators taken in turns, segments of the reduction,
+ragged last tiles, results through shared memory, both outputs of one product.
+The comparisons and their tolerances are those of the operators' own tests."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import lossless_entropy_coding_gb300 as ecc  # noqa: E402
+import test_gpu_gated as gated  # noqa: E402
+import test_gpu_head as head  # noqa: E402
+import test_gpu_linear as linear  # noqa: E402
+
+F32, BF16, F16, E4M3 = torch.float32, torch.bfloat16, torch.float16, torch.float8_e4m3fn
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, E4M3])
+@pytest.mark.parametrize("M,N,K,pad", [(2100, 4000, 520, 0), (4096, 2816, 192, 3), (1500, 5001, 264, 0)])
+def test_gated_tiles(M, N, K, pad, dtype):
+    gen = torch.Generator("cuda").manual_seed(M + N)
+    x, wg, wu = (gated.rows_of(gen, r, K, dtype, pad) for r in (M, N, N))
+    bg, bu = gated.rows_of(gen, 2, N, F32)
+    gated.check(x, wg, wu, bg, bu, "gelu", 1 / math.sqrt(K), pre_dtype=BF16, pre_pad=5)
+    gated.check(x, wu, wg, None, None, "silu", 1 / math.sqrt(K), out_dtype=E4M3, out_scale=8.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M,N,K,pad", [(2100, 3008, 1024, 0), (900, 4001, 2056, 0), (1111, 2500, 1030, 3), (300, 9000, 2304, 0)])
+def test_gated_grad_tiles(M, N, K, pad, dtype):
+    gen = torch.Generator("cuda").manual_seed(M + N)
+    x, wg, wu = (gated.rows_of(gen, r, K, dtype, pad, std=s) for r, s in ((M, 1.0), (N, N**-0.5), (N, N**-0.5)))
+    dy, g, u = (gated.rows_of(gen, M, N, dtype, pad) for _ in range(3))
+    a = gated.check_grad(dy, x, wg, wu, g, u, "silu", 1.0, 0.5)
+    b = gated.check_grad(dy, x, wg, wu, g, u, "silu", 1.0, 0.5, dw_dtype=F32)
+    assert torch.equal(a[0], b[0]) and all(torch.equal(p, q.to(dtype)) for p, q in zip(a[1:3], b[1:3]))
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("M,N,K", [(2300, 4104, 64), (5000, 3000, 200), (1030, 8200, 1024)])
+def test_short_reductions_through_shared_memory(M, N, K, out_dtype):
+    gen = torch.Generator("cuda").manual_seed(M + N)
+    x, w, bias = linear.rows_of(gen, M, K, BF16), linear.rows_of(gen, N, K, BF16), linear.rows_of(gen, 1, N, F32)[0]
+    plain = linear.check(x, w, bias, None, "gelu", 1 / math.sqrt(K), out_dtype)
+    # into rows that the copies cannot take, and into wider ones: the same values, nothing beside them
+    for pad, off in ((1, 1), (8, 8)):
+        whole = torch.full((M + 2, N + 2 * pad + 8), 7.0, dtype=out_dtype, device="cuda")
+        out = whole[1:M + 1, off:off + N]
+        ecc.ecc_linear(x, w, bias, act="gelu", scale=1 / math.sqrt(K), out=out)
+        assert torch.equal(out, plain)
+        out.fill_(7)
+        assert bool((whole == 7).all())
+
+
+def test_gradients_through_shared_memory_stay_in_their_rows():
+    gen = torch.Generator("cuda").manual_seed(5)
+    for M, N, K in ((64, 9001, 4096), (200, 8200, 2048)):
+        x, wg, wu = gated.rows_of(gen, M, K, BF16), gated.rows_of(gen, N, K, BF16, std=0.01), gated.rows_of(gen, N, K, BF16, std=0.01)
+        dy, g, u = (gated.rows_of(gen, M, N, BF16) for _ in range(3))
+        for dtype in (BF16, F32):
+            whole = [torch.full((N + 2, K + 16), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+            views = [t[1:N + 1, 8:K + 8] for t in whole]
+            gated.check_grad(dy, x, wg, wu, g, u, dw_gate=views[0], dw_up=views[1])
+            for t, v in zip(whole, views):
+                v.fill_(7)
+                assert bool((t == 7).all())
+
+
+# rows, vocab, K: streamed past few tokens, or in pairs; several segments of the reduction
+HEADS = [(3, 30001, 1100), (16, 20000, 2050), (40, 40000, 600), (64, 25000, 3000), (65, 20100, 1300), (600, 12000, 1300), (1030, 9001, 600)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, E4M3])
+@pytest.mark.parametrize("M,V,K", HEADS)
+def test_head_tiles(M, V, K, dtype):
+    gen = torch.Generator("cuda").manual_seed(M + V)
+    x, w = head.rows_of(gen, M, K, dtype), head.rows_of(gen, V, K, dtype)
+    tok = head.tokens_of(gen, M, V)
+    tok[:2] = torch.tensor([0, V - 1])
+    first = head.check(x, w, tok, 2 / math.sqrt(K))
+    again = ecc.ecc_linear_logprob(x, w, tok, scale=2 / math.sqrt(K))
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M,V,K", HEADS)
+def test_head_grad_tiles(M, V, K, dtype):
+    gen = torch.Generator("cuda").manual_seed(M + V)
+    x, w, tok = head.rows_of(gen, M, K, dtype), head.rows_of(gen, V, K, dtype, std=K**-0.5), head.tokens_of(gen, M, V)
+    head.check_grad(x, w, tok, 1.5, torch.randn(M, generator=gen, device="cuda"), torch.randn(M, generator=gen, device="cuda") * 0.1)
+
+
+def test_logits_sums_do_not_lose_what_a_long_accumulation_does():
+    """lse of 8192 products a logit to 2^-20 of itself: float32 additions of 16 segments, 512 truncated ones in each."""
+    gen = torch.Generator("cuda").manual_seed(7)
+    for M in (5, 300):
+        x, w = head.rows_of(gen, M, 8192, BF16), head.rows_of(gen, 20480, 8192, BF16, std=2.5 / math.sqrt(8192))
+        r = ecc.ecc_linear_logprob(x, w)
+        lse = torch.logsumexp(x.double() @ w.double().T, -1)
+        # logits near the largest, about 12, of sums that pass through 12 / 16 a segment: 32 steps of 16 products,
+        # each short by at most 2^-23 of that, 16 times over: 2^-18 at the most, half of it on average
+        assert float(((r.lse.double() - lse) / lse).abs().max()) < 2.0**-18
+        assert float(((r.lse.double() - lse) / lse).mean().abs()) < 2.0**-19
