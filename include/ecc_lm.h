@@ -4,7 +4,8 @@
  * (activations of a layer norm or a matrix product, gradients), multiply the
  * bytes a decoder returns, and give a model's own code lengths (token log
  * probabilities; -log2 p bits is the ideal length of a token, the entropy the
- * ideal rate, as ecc_entropy_bits is for bytes).
+ * ideal rate, as ecc_entropy_bits is for bytes), and update a model's
+ * parameters, with moments in bytes that the coders take.
  *
  * Conventions: those of ecc.h (status returns, caller-owned device memory and
  * workspaces, work only enqueued on `stream`, nothing kept between calls),
@@ -324,8 +325,9 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
  *           would never take a step smaller than half their distance), but a
  *           positive v is at least the smallest positive code.  The random bits of
  *           value i are mix((i mod 2^32) ^ mix(mix(mix(seed) + step) + i /
- *           2^32)), the upper 16 for m, the lower for v: the same call gives the
- *           same bytes.  (mix: see the kernel.)  A root is off by 4% a step on
+ *           2^32)), the upper 16 for m, the lower for v, with mix(x): x ^= x >> 16,
+ *           x *= 0x7FEB352D, x ^= x >> 15, x *= 0x846CA68B, x ^= x >> 16 in 32
+ *           bits: the same call gives the same bytes.  A root is off by 4% a step on
  *           average, and the errors of 1 / (1 - beta2) steps add up: at beta2 =
  *           0.95 to a sixth, at 0.999 to more than the root, which wants float32
  *           states.  A group with a NaN or an infinity gets scales of NaN, and

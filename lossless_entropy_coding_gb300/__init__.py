@@ -1,7 +1,8 @@
 """Python binding of libecc_gb300: lossless fixed-codebook coding of e4m3
 byte tensors on GB300 (Quad Length Codes and single-stage canonical Huffman),
 and the language-model operators next to the coders (layer norm, the matrix
-product with a fused epilogue, token log probabilities, and their gradients).
+product with a fused epilogue, the gated projections, token log probabilities
+of logits or of hidden states, their gradients, and AdamW).
 
 Argument marshalling only.  Every entry point has the name of the C function
 it calls (see include/ecc.h and include/ecc_lm.h for the contract); PyTorch supplies device memory

@@ -359,7 +359,7 @@ __device__ __noinline__ void group_by_values(const AdamTensor &t, uint32_t kind,
 
 // Blocks an SM: 3 for 8-bit states, whose instructions are the bound (265 M
 // values, bf16: 708 us, 3.8 TB/s; 4 blocks 710, 5 blocks 754), 2 for float32
-// states, which are bound by HBM (184 M values with masters: 797 us, 6.4 TB/s; 3
+// states, which are bound by HBM (170 M values with masters: 797 us, 6.4 TB/s; 3
 // blocks 859, 4 blocks 861).
 constexpr int kAdamBlocks = 2, kAdamBlocksBytes = 3;
 template <int CAP, bool BYTES>
