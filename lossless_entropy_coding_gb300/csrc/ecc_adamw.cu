@@ -208,48 +208,136 @@ __device__ __forceinline__ void unpack_e4m3(uint2 q, float scale, float2 (&f)[4]
     }
 }
 
-// A warp's group of a tensor whose arrays start on 16-byte boundaries (8 for
-// byte states) and that has all 256 values: 8 neighbours a lane.  Everything is
-// asked for before anything is used.
-template <bool BYTES>
-__device__ __forceinline__ void group_by_vectors(const AdamTensor &t, uint32_t kind, uint64_t e0, uint32_t lane, const AdamStep &s)
+// Value k of a lane's 8 in a group: 8 neighbours where the tensor's arrays
+// start on 16-byte boundaries (8 for byte states) and the group is whole,
+// else one of each 32, so that the lanes are neighbours.
+template <bool VECTORS> __device__ __forceinline__ uint32_t place_of(uint32_t lane, int k) { return VECTORS ? lane * 8 + k : k * 32 + lane; }
+
+// 8 values, by type
+template <typename T>
+__device__ __forceinline__ void read_each(const void *p, uint64_t e0, uint32_t left, uint32_t lane, float2 (&f)[4])
+{
+    const T *q = static_cast<const T *>(p) + e0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t i = place_of<false>(lane, k);
+        (k & 1 ? f[k / 2].y : f[k / 2].x) = i < left ? to_f32(q[i]) : 0.f;
+    }
+}
+__device__ __forceinline__ void read_each(const void *p, uint64_t e0, uint32_t left, uint32_t lane, uint32_t type, float2 (&f)[4])
+{
+    if (type == ECC_F32)
+        read_each<float>(p, e0, left, lane, f);
+    else if (type == ECC_BF16)
+        read_each<bf16>(p, e0, left, lane, f);
+    else
+        read_each<__half>(p, e0, left, lane, f);
+}
+template <typename T>
+__device__ __forceinline__ void write_each(void *p, uint64_t e0, uint32_t left, uint32_t lane, const float2 (&f)[4])
+{
+    T *q = static_cast<T *>(p) + e0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t i = place_of<false>(lane, k);
+        if (i < left)
+            q[i] = from_f32<T>(k & 1 ? f[k / 2].y : f[k / 2].x);
+    }
+}
+template <bool VECTORS>
+__device__ __forceinline__ void write_values(void *p, uint64_t e0, uint32_t left, uint32_t lane, uint32_t type, const float2 (&f)[4])
+{
+    if constexpr (VECTORS)
+        write8(p, e0 + lane * 8, type, f);
+    else if (type == ECC_F32)
+        write_each<float>(p, e0, left, lane, f);
+    else if (type == ECC_BF16)
+        write_each<bf16>(p, e0, left, lane, f);
+    else
+        write_each<__half>(p, e0, left, lane, f);
+}
+
+// A warp's group; everything is asked for before anything is used.  (67 M bf16
+// values with 8-bit states 259 us by values, 205 by vectors, with float32 states
+// 282 and 229.)
+template <bool BYTES, bool VECTORS>
+__device__ __forceinline__ void update_group(const AdamTensor &t, uint32_t kind, uint64_t e0, uint32_t lane, const AdamStep &s)
 {
     const uint32_t ptype = kind & 3, gtype = kind >> 2 & 3;
-    const uint64_t i = e0 + lane * 8;
+    const uint32_t left = (uint32_t)min(t.n - e0, (uint64_t)kAdamGroup);
     const void *from = t.master ? t.master : t.param;
-    const uint32_t from_type = t.master ? ECC_F32 : ptype;
-    uint4 pq[2], gq[2];
-    float2 p[4], g[4];
+    const uint32_t from_type = t.master ? (uint32_t)ECC_F32 : ptype;
+    float2 p[4], g[4], m[4], v[4];
+    float *msp = nullptr, *vsp = nullptr;
+    float ms = 1.f, vs = 1.f;
     if constexpr (BYTES) {
-        uint8_t *mp = static_cast<uint8_t *>(t.m) + i, *vp = static_cast<uint8_t *>(t.v) + i;
-        float *msp = t.m_scale + e0 / kAdamGroup, *vsp = t.v_scale + e0 / kAdamGroup;
-        const uint2 mq = __ldcs(reinterpret_cast<const uint2 *>(mp)), vq = __ldcs(reinterpret_cast<const uint2 *>(vp));
-        const float ms = *msp, vs = *vsp;
+        msp = t.m_scale + e0 / kAdamGroup;
+        vsp = t.v_scale + e0 / kAdamGroup;
+    }
+    if constexpr (VECTORS) {
+        const uint64_t i = e0 + lane * 8;
+        uint4 pq[2], gq[2], mq[2], vq[2];
+        if constexpr (BYTES) {
+            const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.m) + i));
+            const uint2 b = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.v) + i));
+            mq[0] = make_uint4(a.x, a.y, 0, 0);
+            vq[0] = make_uint4(b.x, b.y, 0, 0);
+            ms = *msp;
+            vs = *vsp;
+        } else {
+            read8(t.m, i, true, mq);
+            read8(t.v, i, true, vq);
+        }
         read8(from, i, from_type == ECC_F32, pq);
         read8(t.grad, i, gtype == ECC_F32, gq);
         unpack8(pq, from_type, p);
         unpack8(gq, gtype, g);
-        float2 m[4], r[4];
-        unpack_e4m3(mq, ms, m);
-        unpack_e4m3(vq, vs, r);
+        if constexpr (BYTES) {
+            unpack_e4m3(make_uint2(mq[0].x, mq[0].y), ms, m);
+            unpack_e4m3(make_uint2(vq[0].x, vq[0].y), vs, v);
+        } else {
+            unpack8(mq, ECC_F32, m);
+            unpack8(vq, ECC_F32, v);
+        }
+    } else {
+        if constexpr (BYTES) {
+            read_each<e4m3>(t.m, e0, left, lane, m);
+            read_each<e4m3>(t.v, e0, left, lane, v);
+            ms = *msp;
+            vs = *vsp;
+        } else {
+            read_each<float>(t.m, e0, left, lane, m);
+            read_each<float>(t.v, e0, left, lane, v);
+        }
+        read_each(from, e0, left, lane, from_type, p);
+        read_each(t.grad, e0, left, lane, gtype, g);
+        if constexpr (BYTES)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                m[k] = mul2(m[k], both(ms));
+                v[k] = mul2(v[k], both(vs));
+            }
+    }
+    if constexpr (BYTES) {
         float m_most = 0.f, v_most = 0.f, m_least = INFINITY, r_least = INFINITY;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            float2 v = mul2(r[k], r[k]);
-            r[k] = update2(s, g[k], p[k], m[k], v);
+            v[k] = mul2(v[k], v[k]);
+            const float2 r = update2(s, g[k], p[k], m[k], v[k]);
             m_most = max_nan(max_nan(m_most, fabsf(m[k].x)), fabsf(m[k].y));
-            v_most = max_nan(max_nan(v_most, v.x), v.y);
+            v_most = max_nan(max_nan(v_most, v[k].x), v[k].y);
             m_least = fminf(fminf(m_least, fabsf(m[k].x)), fabsf(m[k].y));
-            r_least = fminf(fminf(r_least, r[k].x), r[k].y);
+            r_least = fminf(fminf(r_least, r.x), r.y);
+            v[k] = r;
         }
         if (t.master)
-            write8(t.master, i, ECC_F32, p);
-        write8(t.param, i, ptype, p);
+            write_values<VECTORS>(t.master, e0, left, lane, ECC_F32, p);
+        write_values<VECTORS>(t.param, e0, left, lane, ptype, p);
         const uint32_t mm = __reduce_max_sync(~0u, __float_as_uint(m_most)), vm = __reduce_max_sync(~0u, __float_as_uint(v_most));
         const bool finite = mm < 0x7F800000u && vm < 0x7F800000u;
         const float mi = group_scale(msp, mm, false, finite, lane == 0);
         const float vi = group_scale(vsp, vm, true, finite, lane == 0);
-        const uint32_t key = mix32(s.key + (uint32_t)(e0 >> 32));
+        const uint32_t key = mix32(s.key + (uint32_t)(e0 >> 32)), low = (uint32_t)e0;
         uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
         // (no value so small that its neighbours are 2^-9 apart, which few groups have: a third fewer instructions)
         const bool normal = __all_sync(~0u, finite && __fmul_rn(m_least, mi) >= 0.015625f && __fmul_rn(r_least, vi) >= 0.015625f);
@@ -259,8 +347,8 @@ __device__ __forceinline__ void group_by_vectors(const AdamTensor &t, uint32_t k
                 uint32_t mc[4], vc[4], sign[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t d = mix32((uint32_t)(i + h * 4 + k) ^ key);
-                    const float2 y2 = mul2(m[h * 2 + k / 2], both(mi)), z2 = mul2(r[h * 2 + k / 2], both(vi));
+                    const uint32_t d = mix32((low + place_of<VECTORS>(lane, h * 4 + k)) ^ key);
+                    const float2 y2 = mul2(m[h * 2 + k / 2], both(mi)), z2 = mul2(v[h * 2 + k / 2], both(vi));
                     const float y = k & 1 ? y2.y : y2.x, z = k & 1 ? z2.y : z2.x;
                     sign[k] = __float_as_uint(y);
                     if (normal) {
@@ -275,93 +363,37 @@ __device__ __forceinline__ void group_by_vectors(const AdamTensor &t, uint32_t k
                 vw[h] = top_bytes(vc[0], vc[1], vc[2], vc[3]);
             }
         }
-        __stcs(reinterpret_cast<uint2 *>(mp), make_uint2(mw[0], mw[1]));
-        __stcs(reinterpret_cast<uint2 *>(vp), make_uint2(vw[0], vw[1]));
+        uint8_t *mp = static_cast<uint8_t *>(t.m) + e0, *vp = static_cast<uint8_t *>(t.v) + e0;
+        if constexpr (VECTORS) {
+            __stcs(reinterpret_cast<uint2 *>(mp + lane * 8), make_uint2(mw[0], mw[1]));
+            __stcs(reinterpret_cast<uint2 *>(vp + lane * 8), make_uint2(vw[0], vw[1]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t i = place_of<false>(lane, k);
+                if (i < left) {
+                    mp[i] = (uint8_t)(mw[k / 4] >> k % 4 * 8);
+                    vp[i] = (uint8_t)(vw[k / 4] >> k % 4 * 8);
+                }
+            }
+        }
     } else {
-        uint4 mq[2], vq[2];
-        read8(t.m, i, true, mq);
-        read8(t.v, i, true, vq);
-        read8(from, i, from_type == ECC_F32, pq);
-        read8(t.grad, i, gtype == ECC_F32, gq);
-        unpack8(pq, from_type, p);
-        unpack8(gq, gtype, g);
-        float2 m[4], v[4];
-        unpack8(mq, ECC_F32, m);
-        unpack8(vq, ECC_F32, v);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             update2(s, g[k], p[k], m[k], v[k]);
-        write8(t.m, i, ECC_F32, m);
-        write8(t.v, i, ECC_F32, v);
+        write_values<VECTORS>(t.m, e0, left, lane, ECC_F32, m);
+        write_values<VECTORS>(t.v, e0, left, lane, ECC_F32, v);
         if (t.master)
-            write8(t.master, i, ECC_F32, p);
-        write8(t.param, i, ptype, p);
+            write_values<VECTORS>(t.master, e0, left, lane, ECC_F32, p);
+        write_values<VECTORS>(t.param, e0, left, lane, ptype, p);
     }
 }
 
-// Any other group, a value at a time: the lanes on neighbours.
-template <bool BYTES>
-__device__ __noinline__ void group_by_values(const AdamTensor &t, uint32_t kind, uint64_t e0, uint32_t lane, const AdamStep &s)
-{
-    const uint32_t ptype = kind & 3, gtype = kind >> 2 & 3;
-    const uint64_t group = e0 / kAdamGroup;
-    const float ms = BYTES ? t.m_scale[group] : 1.f, vs = BYTES ? t.v_scale[group] : 1.f;
-    float m[8], r[8];
-    uint32_t mm = 0, vm = 0;
-#pragma unroll 2
-    for (int k = 0; k < 8; ++k) {
-        const uint64_t i = e0 + k * 32 + lane;
-        m[k] = r[k] = 0.f;
-        if (i >= t.n)
-            continue;
-        float2 p2 = both(t.master ? t.master[i] : load_any(t.param, i, ptype)), m2, v2;
-        if constexpr (BYTES) {
-            m2 = both(__fmul_rn(to_f32(static_cast<const e4m3 *>(t.m)[i]), ms));
-            v2 = both(__fmul_rn(to_f32(static_cast<const e4m3 *>(t.v)[i]), vs));
-            v2 = mul2(v2, v2);
-        } else {
-            m2 = both(static_cast<const float *>(t.m)[i]);
-            v2 = both(static_cast<const float *>(t.v)[i]);
-        }
-        r[k] = update2(s, both(load_any(t.grad, i, gtype)), p2, m2, v2).x;
-        m[k] = m2.x;
-        mm = max(mm, __float_as_uint(m2.x) & 0x7FFFFFFFu);
-        vm = max(vm, __float_as_uint(v2.x) & 0x7FFFFFFFu);
-        if (t.master)
-            t.master[i] = p2.x;
-        store_any(t.param, i, ptype, p2.x);
-        if constexpr (!BYTES) {
-            static_cast<float *>(t.m)[i] = m2.x;
-            static_cast<float *>(t.v)[i] = v2.x;
-        }
-    }
-    if constexpr (!BYTES)
-        return;
-    mm = __reduce_max_sync(~0u, mm);
-    vm = __reduce_max_sync(~0u, vm);
-    const bool finite = mm < 0x7F800000u && vm < 0x7F800000u;
-    const float mi = group_scale(t.m_scale + group, mm, false, finite, lane == 0);
-    const float vi = group_scale(t.v_scale + group, vm, true, finite, lane == 0);
-    const uint32_t key = mix32(s.key + (uint32_t)(e0 >> 32));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint64_t i = e0 + k * 32 + lane;
-        if (i >= t.n)
-            continue;
-        const uint32_t d = mix32((uint32_t)i ^ key);
-        const float y = __fmul_rn(m[k], mi);
-        const uint32_t mc = m_dithered(y, d) >> 24 | (__float_as_uint(y) >> 24 & 0x80u);
-        const uint32_t vc = v_dithered(__fmul_rn(r[k], vi), d) >> 24;
-        static_cast<uint8_t *>(t.m)[i] = finite ? (uint8_t)mc : 0;
-        static_cast<uint8_t *>(t.v)[i] = finite ? (uint8_t)vc : 0;
-    }
-}
-
-// Blocks an SM: 3 for 8-bit states, whose instructions are the bound (265 M
-// values, bf16: 708 us, 3.8 TB/s; 4 blocks 710, 5 blocks 754), 2 for float32
-// states, which are bound by HBM (170 M values with masters: 797 us, 6.4 TB/s; 3
-// blocks 859, 4 blocks 861).
-constexpr int kAdamBlocks = 2, kAdamBlocksBytes = 3;
+// Blocks an SM: 4 for 8-bit states, whose instructions are the bound (265 M
+// values, bf16: 688 us, 3.9 TB/s; 3 blocks 722, 5 blocks 744), 2 for float32
+// states, which are bound by HBM (170 M values with masters: 785 us, 6.5 TB/s; 3
+// blocks 859).
+constexpr int kAdamBlocks = 2, kAdamBlocksBytes = 4;
 template <int CAP, bool BYTES>
 __global__ void __launch_bounds__(kAdamThreads, BYTES ? kAdamBlocksBytes : kAdamBlocks) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a)
 {
@@ -386,9 +418,9 @@ __global__ void __launch_bounds__(kAdamThreads, BYTES ? kAdamBlocksBytes : kAdam
         if (e0 >= t.n)
             continue;
         if ((kind & kAdamVectors) && e0 + kAdamGroup <= t.n)
-            group_by_vectors<BYTES>(t, kind, e0, lane, s);
+            update_group<BYTES, true>(t, kind, e0, lane, s);
         else
-            group_by_values<BYTES>(t, kind, e0, lane, s);
+            update_group<BYTES, false>(t, kind, e0, lane, s);
     }
 }
 
