@@ -295,6 +295,24 @@ def test_step_rate_and_scale_on_the_device_and_replayed():
         assert (state.m[0] != s2.m[0]).float().mean() < 1e-3
 
 
+def test_many_tensors_captured_and_replayed():
+    """More tensors than a launch's parameters hold, of both kinds of states."""
+    items = [make(300 + i, BF16, BF16, 8 if i % 2 else 32, False, seed=i) for i in range(1000)]
+    params, grads = [p for p, _, _ in items], [g for _, g, _ in items]
+    state = ecc.AdamWState([s.m[0] for _, _, s in items], [s.v[0] for _, _, s in items],
+                           [s.m_scale[0] if s.m_scale else None for _, _, s in items],
+                           [s.v_scale[0] if s.v_scale else None for _, _, s in items])
+    start = [(p.clone(), copied(s)) for p, _, s in items]
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        ecc.ecc_adamw(params, grads, state, step=6, **HYPER)
+    graph.replay()
+    torch.cuda.synchronize()
+    for (p, g, s), (old_p, old) in list(zip(items, start))[::37]:
+        check(p, s, old_p, g, old, 6, **HYPER)
+
+
 def test_the_same_call_gives_the_same_bits_on_another_stream():
     p, g, state = make(30000, BF16, BF16, 8, False)
     q, s2 = p.clone(), copied(state)

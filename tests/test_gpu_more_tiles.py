@@ -106,3 +106,46 @@ def test_logits_sums_do_not_lose_what_a_long_accumulation_does():
         # each short by at most 2^-23 of that, 16 times over: 2^-18 at the most, half of it on average
         assert float(((r.lse.double() - lse) / lse).abs().max()) < 2.0**-18
         assert float(((r.lse.double() - lse) / lse).mean().abs()) < 2.0**-19
+
+
+def test_captured_calls_that_share_a_workspace():
+    """Two graphs over one workspace and status, replayed in turns: each leaves its own results."""
+    gen = torch.Generator("cuda").manual_seed(9)
+    ws = torch.empty(600 << 20, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cases = []
+    for M, V, K in ((500, 30000, 640), (24, 40000, 1100)):
+        x, w, tok = head.rows_of(gen, M, K, F16), head.rows_of(gen, V, K, F16, std=0.1), head.tokens_of(gen, M, V)
+        dlp = torch.randn(M, generator=gen, device="cuda")
+        args = (x, w, tok, dlp)
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=stream):
+            r = ecc.ecc_linear_logprob(x, w, tok, ws=ws, status=status)
+            g = ecc.ecc_linear_logprob_grad(x, w, tok, r.lse, None, dlp, ws=ws, status=status)
+        cases.append((args, graph, r, g))
+    for _ in range(3):
+        for (x, w, tok, dlp), graph, r, g in cases:
+            x.copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+            graph.replay()
+        torch.cuda.synchronize()
+        for (x, w, tok, dlp), graph, r, g in cases:
+            ref = head.check(x, w, tok)
+            want = ecc.ecc_linear_logprob_grad(x, w, tok, ref.lse, None, dlp)
+            assert all(torch.equal(a, b) for a, b in zip(r[:3], ref[:3])) and all(torch.equal(a, b) for a, b in zip(g[:2], want[:2]))
+            assert int(status.item()) == 0
+
+
+def test_gated_calls_in_a_row_share_a_workspace():
+    gen = torch.Generator("cuda").manual_seed(10)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    M, N, K = 300, 1500, 517                              # rows off 16-byte boundaries: copies in the workspace
+    sets = [[gated.rows_of(gen, r, c, BF16) for r, c in ((M, K), (N, K), (N, K), (M, N), (M, N), (M, N))] for _ in range(3)]
+    alone = []
+    for x, wg, wu, dy, g, u in sets:
+        alone.append((gated.check(x, wg, wu, scale=0.05), gated.check_grad(dy, x, wg, wu, g, u, scale=0.05)))
+    got = [(ecc.ecc_gated_linear(x, wg, wu, scale=0.05, ws=ws)[0], ecc.ecc_gated_linear_grad(dy, x, wg, wu, g, u, scale=0.05, ws=ws))
+           for _ in range(3) for x, wg, wu, dy, g, u in sets]
+    torch.cuda.synchronize()
+    for i, (y, r) in enumerate(got):
+        assert torch.equal(y, alone[i % 3][0]) and all(torch.equal(a, b) for a, b in zip(r, alone[i % 3][1]))
