@@ -43,48 +43,45 @@ static __global__ void __launch_bounds__(kRowThreads) sum_parts_kernel(const flo
 }
 
 // Rows of `cols` elements to rows of ldd elements on 16-byte boundaries, for
-// up to three operands in one launch (blockIdx.y).
+// up to three operands in one launch (blockIdx.y): the two vectors around each
+// 16 bytes, shifted, at the rate of a copy (820 MB read and written in 118 us;
+// five words around them 134).
 struct PadJob {
     const void *src;
     void *dst;
     uint64_t ld, rows, cols, ldd;
 };
-template <typename T> __global__ void __launch_bounds__(kRowThreads) pad_rows_kernel(PadJob a, PadJob b, PadJob c)
+struct PadJobs {
+    PadJob j[3];
+};
+template <typename T> __global__ void __launch_bounds__(kRowThreads) pad_rows_kernel(const __grid_constant__ PadJobs jobs)
 {
     constexpr int V = 16 / sizeof(T);
     let_next_start();
-    const PadJob &j = blockIdx.y == 2 ? c : blockIdx.y ? b : a;
+    const PadJob &j = jobs.j[blockIdx.y];
     const uint32_t vecs = (uint32_t)(j.ldd / V);
     const uint64_t n = j.rows * vecs;
+    const T *src = static_cast<const T *>(j.src), *end = src + (j.rows - 1) * j.ld + j.cols;
+    T *dst = static_cast<T *>(j.dst);
+#pragma unroll 2
     for (uint64_t i = (uint64_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += (uint64_t)gridDim.x * kRowThreads) {
         const uint64_t r = n >> 32 ? i / vecs : (uint32_t)i / vecs;
         const uint32_t at = (uint32_t)(i - r * vecs) * V;
-        const T *s = static_cast<const T *>(j.src) + r * j.ld + at;
-        uint32_t o[4];
-        const uint32_t off = (uint32_t)(uintptr_t)s & 3;
-        if (at + V + 4 / sizeof(T) <= j.cols && at) { // five words around the 16 bytes, all inside the row
-            const uint32_t *w = reinterpret_cast<const uint32_t *>((uintptr_t)s & ~(uintptr_t)3);
-            uint32_t q[5];
-#pragma unroll
-            for (int k = 0; k < 5; ++k)
-                q[k] = w[k];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                o[k] = __funnelshift_r(q[k], q[k + 1], off * 8);
-        } else { // a row's first and last ones
-            struct alignas(16) {
-                T v[V];
-            } t;
+        const T *s = src + r * j.ld + at;
+        uint4 q;
+        const uintptr_t low = (uintptr_t)s & ~(uintptr_t)15;
+        if (at + V <= j.cols && low >= (uintptr_t)src && low + 32 <= (uintptr_t)end) { // the two vectors around the 16 bytes
+            q = shift16<false>(*reinterpret_cast<const uint4 *>(low), *reinterpret_cast<const uint4 *>(low + 16),
+                               (uint32_t)((uintptr_t)s - low));
+        } else { // a row's last ones, the array's first and last
+            uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < V; ++k)
-                t.v[k] = at + k < j.cols ? s[k] : T(0);
-            const uint4 q = *reinterpret_cast<const uint4 *>(&t);
-            o[0] = q.x;
-            o[1] = q.y;
-            o[2] = q.z;
-            o[3] = q.w;
+                if (at + k < j.cols)
+                    w[k * sizeof(T) / 4] |= (uint32_t)s[k] << k * sizeof(T) % 4 * 8;
+            q = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4 *>(static_cast<T *>(j.dst) + r * j.ldd + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(dst + i * V) = q;
     }
 }
 
@@ -242,7 +239,7 @@ struct Array {
 };
 inline bool readable(std::initializer_list<Array> arrays, uint32_t type, uint8_t *&ws, cudaStream_t st)
 {
-    PadJob jobs[3];
+    PadJobs jobs{};
     int n = 0;
     uint64_t most = 0;
     for (const Array &x : arrays) {
@@ -250,7 +247,7 @@ inline bool readable(std::initializer_list<Array> arrays, uint32_t type, uint8_t
         const size_t bytes = copy_bytes(x.p, x.ld, x.rows, x.cols, type);
         if (bytes) {
             *x.o = {ws, padded(x.cols, type), false};
-            jobs[n++] = {x.p, ws, x.ld, x.rows, x.cols, x.o->ld};
+            jobs.j[n++] = {x.p, ws, x.ld, x.rows, x.cols, x.o->ld};
             most = std::max<uint64_t>(most, bytes / 16);
             ws += bytes;
         }
@@ -259,9 +256,9 @@ inline bool readable(std::initializer_list<Array> arrays, uint32_t type, uint8_t
         return false;
     const dim3 grid((unsigned)std::min<uint64_t>((most + kRowThreads - 1) / kRowThreads, 1u << 15), n);
     if (type == ECC_E4M3)
-        pad_rows_kernel<uint8_t><<<grid, kRowThreads, 0, st>>>(jobs[0], jobs[n > 1], jobs[n - 1]);
+        pad_rows_kernel<uint8_t><<<grid, kRowThreads, 0, st>>>(jobs);
     else
-        pad_rows_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>(jobs[0], jobs[n > 1], jobs[n - 1]);
+        pad_rows_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>(jobs);
     return true;
 }
 
