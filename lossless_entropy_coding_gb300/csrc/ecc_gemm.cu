@@ -63,15 +63,13 @@ bool make_wide_map(CUtensorMap *map, const Operand &o, uint64_t rows, uint64_t K
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// map of an output [rows, cols]: boxes of 32 x 32 values
-bool make_out_map(CUtensorMap *map, void *p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t type)
+// map of an output [rows, cols]: boxes of `across` x 32 values
+bool make_out_map(CUtensorMap *map, void *p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t type, uint32_t across)
 {
     const uint32_t size = type_bytes(type);
     const cuuint64_t dims[2] = {cols, rows}, stride[1] = {rows > 1 ? ld * size : (cols * size + 15) / 16 * 16};
-    const cuuint32_t box[2] = {32, 32}, one[2] = {1, 1};
-    const CUtensorMapDataType t = type == ECC_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                  : type == ECC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint32_t box[2] = {across, 32}, one[2] = {1, 1};
+    const CUtensorMapDataType t = type == ECC_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : map_type(type);
     return encode_tiled()(map, t, 2, p, dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -153,7 +151,7 @@ constexpr uint32_t kStagedBlocks = 16;
 
 // A product made ready: its maps, its arguments.
 struct Plan {
-    CUtensorMap pm{}, pm2{}, qm{}, om{}, om2{};
+    CUtensorMap pm{}, pm2{}, qm{}, om{}, om2{}, om3{};
     GemmArgs g{};
     bool pair = false;
     uint32_t stage_bytes = 0;
@@ -202,12 +200,22 @@ ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t 
     const uint64_t k1 = x.mode == kDual ? x.kfirst : x.K;
     // results through shared memory: of reductions that are shorter than the epilogue
     const Epilogue &e = x.e;
-    const uint64_t orows = e.rswitch ? e.rows2 : x.rows;
-    if (shape.pair && x.mode == kPlain && g.kblocks <= kStagedBlocks && e.out_type != ECC_E4M3 && !e.pre && !e.residual &&
-        tma_rows(e.out, e.ldout, e.out_type, orows) && (!e.rswitch || tma_rows(e.out2, e.ldout2, e.out_type, orows)) && encode_tiled() &&
-        make_out_map(&plan.om, e.out, e.ldout, orows, x.cols, e.out_type) &&
-        (!e.rswitch || make_out_map(&plan.om2, e.out2, e.ldout2, orows, x.cols, e.out_type)))
-        g.staged = type_bytes(e.out_type);
+    if (shape.pair && g.kblocks <= kStagedBlocks && encode_tiled() && tma_rows(e.out, e.ldout, e.out_type, e.rswitch ? e.rows2 : x.rows)) {
+        if (x.mode == kPlain && e.out_type != ECC_E4M3 && !e.pre && !e.residual) {
+            const uint64_t rows = e.rswitch ? e.rows2 : x.rows;
+            if (make_out_map(&plan.om, e.out, e.ldout, rows, x.cols, e.out_type, 32) &&
+                (!e.rswitch || (tma_rows(e.out2, e.ldout2, e.out_type, rows) &&
+                                make_out_map(&plan.om2, e.out2, e.ldout2, rows, x.cols, e.out_type, 32))))
+                g.staged = 1024 * type_bytes(e.out_type);
+        } else if (gated && e.pre) { // (the output alone gains nothing: 8192 x 8192 x 256 87 us, 85 by store_rows; with g and u 134, 154)
+            const uint32_t bytes = 512 * (type_bytes(e.out_type) + 2 * type_bytes(e.pre_type));
+            if (bytes <= 4096 && tma_rows(e.pre, e.ldpre, e.pre_type, x.rows) && tma_rows(e.pre2, e.ldpre2, e.pre_type, x.rows) &&
+                make_out_map(&plan.om, e.out, e.ldout, x.rows, x.cols, e.out_type, 16) &&
+                make_out_map(&plan.om2, e.pre, e.ldpre, x.rows, x.cols, e.pre_type, 16) &&
+                make_out_map(&plan.om3, e.pre2, e.ldpre2, x.rows, x.cols, e.pre_type, 16))
+                g.staged = (bytes + 127) / 128 * 128;
+        }
+    }
     if (!encode_tiled())
         return ECC_ERR_CUDA;
     g.qwide = x.Q.mn && make_wide_map(&plan.qm, x.Q, g.rows, x.K, type, qn / 64);
@@ -231,7 +239,7 @@ ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t 
 size_t stage_memory(Plan &plan, uint32_t ctas, int sms)
 {
     const bool alone = plan.pair || ctas <= (uint32_t)sms; // one CTA an SM
-    const uint32_t out = plan.g.staged * 2048 * 8; // two stages of 32 x 32 values for each of eight warps
+    const uint32_t out = plan.g.staged * 2 * 8; // two stages for each of eight warps
     const uint32_t budget = (alone ? kAloneSmem : kSharedSmem) - kSmemHead - (uint32_t)sizeof(GemmBars) - out;
     plan.g.stages = std::min(kMaxStages, budget / plan.stage_bytes);
     return kSmemHead + (size_t)plan.g.stages * plan.stage_bytes + out;
@@ -345,7 +353,7 @@ ecc_status gemm(const Product &x, uint32_t type, uint32_t *status, bool clear_st
     const uint32_t ctas = pair ? 2 * std::min<uint32_t>(plan.tiles(), sms / 2) : plan.tiles() * plan.g.split;
     const size_t smem = stage_memory(plan, ctas, sms);
     const void *f = kernel_of(x, type == ECC_E4M3, pair);
-    void *pair_args[] = {&plan.pm, &plan.pm2, &plan.qm, &plan.om, &plan.om2, &plan.g};
+    void *pair_args[] = {&plan.pm, &plan.pm2, &plan.qm, &plan.om, &plan.om2, &plan.om3, &plan.g};
     void *split_args[] = {&plan.pm, &plan.pm2, &plan.qm, &plan.g};
     void **args = pair ? pair_args : split_args;
     if (pair && x.mode == kStats && !registers_of(f, kStatsRegisters))

@@ -50,7 +50,7 @@ struct GemmArgs {
     Epilogue e;
     uint32_t kswitch; // kDual: the reduction block where the second matrix starts
     bool pwide, qwide; // operands down their columns: one box for all of a tile's rows
-    uint32_t staged;  // kPlain: bytes of an output value if results leave through shared memory, or 0
+    uint32_t staged;  // bytes of a warp's 32 rows if results leave through shared memory, or 0
     bool one_box;     // kGated: P's map has both matrices, in turns of 16 rows
     uint64_t rows, cols;
     uint32_t kblocks; // reduction blocks of 128 bytes (64 reduction indices for MN-major operands)
@@ -252,18 +252,40 @@ __device__ __forceinline__ void finish_staged(const Epilogue &e, float (&a)[32],
 
 // ---------------------------------------------------------------- gated epilogue
 // Lanes 0 to 15: W rows of column c's gate; lanes 16 to 31: of its up (or the
-// other way round).  They exchange halves, and each makes W / 2 rows of the
-// column.
+// other way round).  Each lane keeps its half of the rows, the even ones or the
+// odd ones, gets the other matrix's value of them and makes the result.  a
+// becomes g or u.
 template <int W>
-__device__ __forceinline__ void finish_gated(const Epilogue &e, float (&a)[W], uint64_t r0, uint32_t n, uint32_t c, bool col_ok,
-                                             float bias, uint32_t lane)
+__device__ __forceinline__ void gated_values(const Epilogue &e, float (&a)[W], float (&out)[W / 2], float bias, uint32_t lane)
 {
-    const bool up = e.swapped != (bool)(lane & 16);
+    const bool second = lane & 16, up = e.swapped != second;
     const float scale = up ? e.scale2 : e.scale;
 #pragma unroll
     for (int j = 0; j < W; ++j)
         a[j] = a[j] * scale + bias;
-    if (e.pre && col_ok) {
+    float other[W / 2];
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) {
+        const float got = __shfl_xor_sync(~0u, second ? a[2 * j] : a[2 * j + 1], 16), own = second ? a[2 * j + 1] : a[2 * j];
+        out[j] = up ? got : own;
+        other[j] = up ? own : got;
+    }
+    activate_by(e.act, out);
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j)
+        out[j] *= other[j];
+}
+template <int W>
+__device__ __forceinline__ void finish_gated(const Epilogue &e, float (&a)[W], uint64_t r0, uint32_t n, uint32_t c, bool col_ok,
+                                             float bias, uint32_t lane)
+{
+    float out[W / 2];
+    gated_values(e, a, out, bias, lane);
+    if (!col_ok)
+        return;
+    const uint32_t second = lane >> 4;
+    if (e.pre) {
+        const bool up = e.swapped != (bool)second;
         void *pre = up ? e.pre2 : e.pre;
         const uint64_t ld = up ? e.ldpre2 : e.ldpre;
         if (e.pre_type == ECC_F32)
@@ -273,31 +295,49 @@ __device__ __forceinline__ void finish_gated(const Epilogue &e, float (&a)[W], u
         else
             store_rows<__half>(pre, ld, r0, n, c, a, 1.f);
     }
-    const bool second = lane & 16; // of the halves of the rows
-    float gate[W / 2], other[W / 2];
-#pragma unroll
-    for (int j = 0; j < W / 2; ++j) {
-        const float got = __shfl_xor_sync(~0u, second ? a[j] : a[j + W / 2], 16), own = second ? a[j + W / 2] : a[j];
-        gate[j] = up ? got : own;
-        other[j] = up ? own : got;
-    }
-    activate_by(e.act, gate);
-#pragma unroll
-    for (int j = 0; j < W / 2; ++j)
-        gate[j] *= other[j];
-    const uint32_t first = second ? W / 2 : 0;
-    if (!col_ok || n <= first)
-        return;
-    r0 += first;
-    n = min(n - first, (uint32_t)(W / 2));
+    // every second row from r0 + second on
+    const uint64_t first = (r0 + second) * e.ldout;
+    n = (n + 1 - second) / 2;
     if (e.out_type == ECC_F32)
-        store_rows<float>(e.out, e.ldout, r0, n, c, gate, 1.f);
+        store_rows<float>(static_cast<float *>(e.out) + first, 2 * e.ldout, 0, n, c, out, 1.f);
     else if (e.out_type == ECC_BF16)
-        store_rows<bf16>(e.out, e.ldout, r0, n, c, gate, 1.f);
+        store_rows<bf16>(static_cast<bf16 *>(e.out) + first, 2 * e.ldout, 0, n, c, out, 1.f);
     else if (e.out_type == ECC_F16)
-        store_rows<__half>(e.out, e.ldout, r0, n, c, gate, 1.f);
+        store_rows<__half>(static_cast<__half *>(e.out) + first, 2 * e.ldout, 0, n, c, out, 1.f);
     else
-        store_rows<e4m3>(e.out, e.ldout, r0, n, c, gate, e.out_scale);
+        store_rows<e4m3>(static_cast<e4m3 *>(e.out) + first, 2 * e.ldout, 0, n, c, out, e.out_scale);
+}
+// Results through shared memory: 32 rows of 16 columns of the output, of g and
+// of u.
+template <typename T, int STEP, int N>
+__device__ __forceinline__ void stage_gated(uint8_t *stage, uint32_t at, const float (&v)[N], float s)
+{
+    T *p = reinterpret_cast<T *>(stage) + at;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        p[j * STEP] = from_f32<T>(sizeof(T) == 1 ? v[j] * s : v[j]);
+}
+__device__ __forceinline__ void finish_gated_staged(const Epilogue &e, float (&a)[32], uint8_t *stage, float bias, uint32_t lane)
+{
+    float out[16];
+    gated_values(e, a, out, bias, lane);
+    const uint32_t second = lane >> 4, col = lane & 15, at = second * 16 + col;
+    if (e.out_type == ECC_F32)
+        stage_gated<float, 32>(stage, at, out, 1.f);
+    else if (e.out_type == ECC_BF16)
+        stage_gated<bf16, 32>(stage, at, out, 1.f);
+    else if (e.out_type == ECC_F16)
+        stage_gated<__half, 32>(stage, at, out, 1.f);
+    else
+        stage_gated<e4m3, 32>(stage, at, out, e.out_scale);
+    stage += 512 * (e.out_type == ECC_F32 ? 4 : e.out_type == ECC_E4M3 ? 1 : 2);
+    const uint32_t from = (e.swapped != (bool)second ? 512 : 0) + col;
+    if (e.pre_type == ECC_F32)
+        stage_gated<float, 16>(stage, from, a, 1.f);
+    else if (e.pre_type == ECC_BF16)
+        stage_gated<bf16, 16>(stage, from, a, 1.f);
+    else
+        stage_gated<__half, 16>(stage, from, a, 1.f);
 }
 
 // ---------------------------------------------------------------- logits' epilogues
@@ -604,7 +644,8 @@ template <bool PMN, bool QMN, bool F8, int MODE>
 __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap pmap2,
                      const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
-                     const __grid_constant__ CUtensorMap omap2, const __grid_constant__ GemmArgs g)
+                     const __grid_constant__ CUtensorMap omap2, const __grid_constant__ CUtensorMap omap3,
+                     const __grid_constant__ GemmArgs g)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ GemmBars s;
@@ -785,9 +826,9 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                 acc ^= 1;
                 continue;
             }
-            if (MODE == kPlain && g.staged) {
+            if ((MODE == kPlain || MODE == kGated) && g.staged) {
                 // Short reductions: results through shared memory, two stages a
-                // warp, by copies of 32 x 32 values.  (Half the instructions of
+                // warp, by copies of 32 rows.  (Half the instructions of
                 // store_rows, none of them an address.)
                 if (!__all_sync(~0u, mbar_wait(&s.tfull[acc], aph, g.limit_ns))) {
                     if (lane == 0)
@@ -795,8 +836,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                     break;
                 }
                 tmem_fence_after();
-                uint8_t *stage = smem_raw + (stage0 - smem_u32(smem_raw)) + g.stages * stage_bytes + (warp - 2) * 2048 * g.staged;
-                const uint32_t c0 = c - lane;
+                uint8_t *stage = smem_raw + (stage0 - smem_u32(smem_raw)) + g.stages * stage_bytes + (warp - 2) * 2 * g.staged;
+                const uint32_t c0 = c - (MODE == kGated ? lane & 15 : lane);
                 for (uint32_t j = j0; j < j1; j += 32) {
                     float a[32];
                     tmem_load32(tmem + (quad * 32 << 16) + acc * g.bn + j, a);
@@ -808,19 +849,29 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                     }
                     if (j >= left || c0 >= g.cols)
                         continue;
-                    uint8_t *at = stage + (j & 32) * 32 * g.staged;
+                    uint8_t *at = stage + (j & 32 ? g.staged : 0);
                     if (lane == 0)
                         tma_stores_read<1>();
                     __syncwarp();
-                    finish_staged(g.e, a, at, lane, bias, scale);
+                    if constexpr (MODE == kGated)
+                        finish_gated_staged(g.e, a, at, bias, lane);
+                    else
+                        finish_staged(g.e, a, at, lane, bias, scale);
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
                         const uint64_t r = r0 + j;
-                        if (g.e.rswitch && r >= g.e.rswitch)
-                            tma_store(&omap2, smem_u32(at), (int)c0, (int)(r - g.e.rswitch));
-                        else
+                        if constexpr (MODE == kGated) {
+                            const uint32_t pre = smem_u32(at) + 512 * (g.e.out_type == ECC_F32 ? 4 : g.e.out_type == ECC_E4M3 ? 1 : 2);
                             tma_store(&omap, smem_u32(at), (int)c0, (int)r);
+                            tma_store(&omap2, pre, (int)c0, (int)r);
+                            tma_store(&omap3, pre + 512 * (g.e.pre_type == ECC_F32 ? 4 : 2), (int)c0, (int)r);
+                        } else if (g.e.rswitch && r >= g.e.rswitch) {
+                            tma_store(&omap2, smem_u32(at), (int)c0, (int)(r - g.e.rswitch));
+                        } else {
+                            tma_store(&omap, smem_u32(at), (int)c0, (int)r);
+                        }
+                        tma_stores_commit();
                     }
                 }
                 if (acc)
@@ -868,7 +919,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
             acc ^= 1;
         }
     }
-    if (MODE == kPlain && g.staged && lane == 0)
+    if ((MODE == kPlain || MODE == kGated) && g.staged && lane == 0)
         tma_stores_done();
     __syncthreads();
     __syncwarp();

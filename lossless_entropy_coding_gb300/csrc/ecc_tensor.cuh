@@ -94,14 +94,14 @@ template <int CG> __device__ __forceinline__ void tma_load_turns(uint32_t dst, c
                      "l"(map), "r"(x), "r"(0), "r"(z), "r"(bar)
                      : "memory");
 }
-// shared memory -> box at (x, y); the copies of a thread form groups
+// shared memory -> box at (x, y); tma_stores_commit ends a group of a thread's copies
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int y)
 {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
-                 "cp.async.bulk.commit_group;" ::"l"(map),
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
                  "r"(x), "r"(y), "r"(src)
                  : "memory");
 }
+__device__ __forceinline__ void tma_stores_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // all but the last N groups of this thread have read their shared memory
 template <int N> __device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }

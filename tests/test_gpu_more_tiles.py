@@ -57,6 +57,29 @@ def test_short_reductions_through_shared_memory(M, N, K, out_dtype):
         assert bool((whole == 7).all())
 
 
+@pytest.mark.parametrize("out_dtype,pre_dtype", [(BF16, BF16), (F32, F16), (E4M3, BF16), (F16, F32), (F32, F32)])
+@pytest.mark.parametrize("M,N,K", [(2300, 4112, 64), (4000, 2504, 712)])
+def test_gated_short_reductions_through_shared_memory(M, N, K, out_dtype, pre_dtype):
+    gen = torch.Generator("cuda").manual_seed(M + N)
+    x, wg, wu = (gated.rows_of(gen, r, K, BF16) for r in (M, N, N))
+    bg, bu = gated.rows_of(gen, 2, N, F32)
+    s = 1 / math.sqrt(K)
+    out_scale = 8.0 if out_dtype == E4M3 else 1.0
+    for a, b in ((wg, wu), (wu, wg)):
+        plain = gated.check(x, a, b, bg, bu, "silu", s, out_dtype=out_dtype, out_scale=out_scale, pre_dtype=pre_dtype)
+        results = []
+        for pad in (16, 1):                              # rows that the copies can take, and that they cannot
+            whole = [torch.full((M + 2, N + 2 * pad + 16), 7.0, device="cuda").to(t) for t in (out_dtype, pre_dtype, pre_dtype)]
+            out, g, u = (t[1:M + 1, pad:N + pad] for t in whole)
+            ecc.ecc_gated_linear(x, a, b, bg, bu, act="silu", scale=s, out=out, out_scale=out_scale, pre_gate=g, pre_up=u)
+            assert torch.equal(out.float(), plain.float())
+            results.append((g.clone(), u.clone()))
+            for t, v in zip(whole, (out, g, u)):
+                v.copy_(torch.full((M, N), 7.0, device="cuda").to(t.dtype))
+                assert bool((t.float() == 7).all())
+        assert all(torch.equal(p, q) for p, q in zip(*results))
+
+
 def test_gradients_through_shared_memory_stay_in_their_rows():
     gen = torch.Generator("cuda").manual_seed(5)
     for M, N, K in ((64, 9001, 4096), (200, 8200, 2048)):
