@@ -64,13 +64,15 @@ bool make_wide_map(CUtensorMap *map, const Operand &o, uint64_t rows, uint64_t K
 }
 
 // map of an output [rows, cols]: boxes of `across` x 32 values
-bool make_out_map(CUtensorMap *map, void *p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t type, uint32_t across)
+bool make_out_map(CUtensorMap *map, void *p, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t type, uint32_t across,
+                  bool swizzled = false)
 {
     const uint32_t size = type_bytes(type);
     const cuuint64_t dims[2] = {cols, rows}, stride[1] = {rows > 1 ? ld * size : (cols * size + 15) / 16 * 16};
     const cuuint32_t box[2] = {across, 32}, one[2] = {1, 1};
     const CUtensorMapDataType t = type == ECC_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : map_type(type);
-    return encode_tiled()(map, t, 2, p, dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+    return encode_tiled()(map, t, 2, p, dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swizzled ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -200,7 +202,10 @@ ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t 
     const uint64_t k1 = x.mode == kDual ? x.kfirst : x.K;
     // results through shared memory: of reductions that are shorter than the epilogue
     const Epilogue &e = x.e;
-    if (shape.pair && g.kblocks <= kStagedBlocks && encode_tiled() && tma_rows(e.out, e.ldout, e.out_type, e.rswitch ? e.rows2 : x.rows)) {
+    if (shape.pair && g.kblocks <= kStagedBlocks && x.mode == kSlopes) { // (t is the workspace's: tokens by the vocabulary's part)
+        if (encode_tiled() && make_out_map(&plan.om, e.out, e.ldout, x.cols, x.rows, e.out_type, 32, true))
+            g.staged = 2048;
+    } else if (shape.pair && g.kblocks <= kStagedBlocks && encode_tiled() && tma_rows(e.out, e.ldout, e.out_type, e.rswitch ? e.rows2 : x.rows)) {
         if (x.mode == kPlain && e.out_type != ECC_E4M3 && !e.pre && !e.residual) {
             const uint64_t rows = e.rswitch ? e.rows2 : x.rows;
             if (make_out_map(&plan.om, e.out, e.ldout, rows, x.cols, e.out_type, 32) &&

@@ -468,12 +468,10 @@ __device__ __forceinline__ LogitsSlope slope_of_token(const Epilogue &e, uint32_
     }
     return s;
 }
-// W logits from vocabulary index v of this launch's part (a multiple of 8) on; rel: the token's place among them
+// t of W logits; rel: the token's place among them
 template <int W>
-__device__ __forceinline__ void store_slopes(const Epilogue &e, const float (&a)[W], uint64_t v, uint32_t c, float scale, int64_t rel,
-                                             const LogitsSlope &s)
+__device__ __forceinline__ void slope_values(float2 (&t)[W / 2], const float (&a)[W], float scale, int64_t rel, const LogitsSlope &s)
 {
-    float2 t[W / 2];
 #pragma unroll
     for (int j = 0; j < W / 2; ++j) {
         const float2 d = fma2(make_float2(a[2 * j], a[2 * j + 1]), both(scale), both(-s.lse));
@@ -486,10 +484,30 @@ __device__ __forceinline__ void store_slopes(const Epilogue &e, const float (&a)
             t[j].y += 2 * j + 1 == (int)rel ? s.one : 0.f;
         }
     }
+}
+// W logits from vocabulary index v of this launch's part (a multiple of 8) on
+template <int W>
+__device__ __forceinline__ void store_slopes(const Epilogue &e, const float (&a)[W], uint64_t v, uint32_t c, float scale, int64_t rel,
+                                             const LogitsSlope &s)
+{
+    float2 t[W / 2];
+    slope_values(t, a, scale, rel, s);
     uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(e.out) + c * e.ldout + v);
 #pragma unroll
     for (int j = 0; j < W / 8; ++j)
         out[j] = e.out_type == ECC_BF16 ? pack2<bf16>(t + 4 * j) : pack2<__half>(t + 4 * j);
+}
+// 32 logits of a lane's token to shared memory, rows of 64 bytes in the 64-byte
+// swizzle (the lanes' 16-byte stores would otherwise meet in two groups of banks)
+__device__ __forceinline__ void stage_slopes(const Epilogue &e, const float (&a)[32], uint8_t *stage, uint32_t lane, float scale, int64_t rel,
+                                             const LogitsSlope &s)
+{
+    float2 t[16];
+    slope_values(t, a, scale, rel, s);
+    uint4 *row = reinterpret_cast<uint4 *>(stage + lane * 64);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        row[j ^ (lane >> 1 & 3)] = e.out_type == ECC_BF16 ? pack2<bf16>(t + 4 * j) : pack2<__half>(t + 4 * j);
 }
 
 template <int MODE> __device__ __forceinline__ float bias_of(const Epilogue &e, uint32_t c, bool col_ok, uint32_t lane)
@@ -818,8 +836,31 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                         if (lane == 0)
                             cluster_arrive(cluster_addr(smem_u32(&s.tempty[acc]), 0));
                     }
-                    if (col_ok && j < left)
-                        store_slopes(g.e, a, r0 + j, c, scale, slope.token - (int64_t)(g.e.first + r0 + j), slope);
+                    if (j >= left)
+                        continue;
+                    const int64_t rel = slope.token - (int64_t)(g.e.first + r0 + j);
+                    if (!g.staged) {
+                        if (col_ok)
+                            store_slopes(g.e, a, r0 + j, c, scale, rel, slope);
+                        continue;
+                    }
+                    // (through shared memory for short reductions: a store of 16 bytes in each of 32 rows takes 4.8 us a tile,
+                    // 4096 x 25088 x 256 101 us)
+                    const uint32_t c0 = c - lane;
+                    if (c0 >= g.cols)
+                        continue;
+                    uint8_t *at = smem_raw + (stage0 - smem_u32(smem_raw)) + g.stages * stage_bytes + (warp - 2) * 2 * g.staged +
+                                  (j & 32 ? g.staged : 0);
+                    if (lane == 0)
+                        tma_stores_read<1>();
+                    __syncwarp();
+                    stage_slopes(g.e, a, at, lane, scale, rel, slope);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store(&omap, smem_u32(at), (int)(r0 + j), (int)c0);
+                        tma_stores_commit();
+                    }
                 }
                 if (acc)
                     aph ^= 1;
@@ -919,7 +960,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
             acc ^= 1;
         }
     }
-    if ((MODE == kPlain || MODE == kGated) && g.staged && lane == 0)
+    if ((MODE == kPlain || MODE == kGated || MODE == kSlopes) && g.staged && lane == 0)
         tma_stores_done();
     __syncthreads();
     __syncwarp();
