@@ -172,3 +172,38 @@ def test_gated_calls_in_a_row_share_a_workspace():
     torch.cuda.synchronize()
     for i, (y, r) in enumerate(got):
         assert torch.equal(y, alone[i % 3][0]) and all(torch.equal(a, b) for a, b in zip(r, alone[i % 3][1]))
+
+
+def test_two_streams_at_once():
+    """The same operators on two streams at the same time, small and large, with their own tensors."""
+    gen = torch.Generator("cuda").manual_seed(11)
+    jobs = []
+    for M, N, V, K in ((40, 600, 3000, 192), (700, 3000, 20000, 640)):
+        x, wg, wu, w = (gated.rows_of(gen, r, K, BF16, std=s) for r, s in ((M, 1.0), (N, 0.1), (N, 0.1), (V, 0.1)))
+        dy, tok, dlp = gated.rows_of(gen, M, N, BF16), head.tokens_of(gen, M, V), torch.randn(M, generator=gen, device="cuda")
+
+        def job(x=x, wg=wg, wu=wu, w=w, dy=dy, tok=tok, dlp=dlp, M=M, N=N, stream=None):
+            g, u = (torch.empty(M, N, dtype=BF16, device="cuda") for _ in range(2))
+            y, _ = ecc.ecc_gated_linear(x, wg, wu, pre_gate=g, pre_up=u, stream=stream)
+            r = ecc.ecc_linear_logprob(x, w, tok, stream=stream)
+            a = ecc.ecc_gated_linear_grad(dy, x, wg, wu, g, u, stream=stream)
+            b = ecc.ecc_linear_logprob_grad(x, w, tok, r.lse, r.entropy, dlp, stream=stream)
+            p = wg.float()
+            state = ecc.adamw_state([p], 8)
+            for step in (1, 2):
+                ecc.ecc_adamw([p], [a[1]], state, step=step, stream=stream)
+            return [y, *r, *a, *b, p, *state.m, *state.v]
+
+        jobs.append((job, job()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        got = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for (job, _), s in zip(jobs * 2, streams[::-1] + streams):
+            with torch.cuda.stream(s):
+                got.append(job())
+        torch.cuda.synchronize()
+        for (_, want), g in zip(jobs * 2, got):
+            assert all(torch.equal(a, b) for a, b in zip(want, g))
