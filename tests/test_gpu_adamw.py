@@ -37,9 +37,9 @@ def mix(x):
     return x ^ (x >> 16)
 
 
-def random_bits(n, seed, step):
+def random_bits(n, seed, step, high=0):
     key = mix(torch.tensor((int(mix(torch.tensor(seed))) + step) & 0xFFFFFFFF))
-    bits = mix(torch.arange(n) ^ int(mix(key))).cuda()
+    bits = mix(torch.arange(n) ^ int(mix((key + high) & 0xFFFFFFFF))).cuda()
     return bits >> 16, bits & 0xFFFF
 
 
@@ -102,7 +102,7 @@ def copied(state):
     return ecc.AdamWState(*([t.clone() if t is not None else None for t in x] if x is not None else None for x in state))
 
 
-def check(p, state, old_p, grad, old, step, seed=0, **hyper):
+def check(p, state, old_p, grad, old, step, seed=0, high=0, **hyper):
     m, v, f, size, slack = reference(old_p, grad, old, step, **hyper)
     half = torch.finfo(p.dtype).eps / 2
     tiny = torch.finfo(p.dtype).smallest_normal * torch.finfo(p.dtype).eps / 2   # half a step of subnormals
@@ -113,9 +113,9 @@ def check(p, state, old_p, grad, old, step, seed=0, **hyper):
         assert ((state.m[0].double() - m).abs() <= 2.0**-22 * size + 1e-44).all()
         assert ((state.v[0].double() - v).abs() <= 2.0**-22 * v + 1e-44).all()
         return
-    high, low = random_bits(m.numel(), seed, step)
-    for got, scale, want, size, bits, positive in ((state.m[0], state.m_scale[0], m, size, high, False),
-                                                   (state.v[0], state.v_scale[0], v.sqrt(), v.sqrt(), low, True)):
+    upper, lower = random_bits(m.numel(), seed, step, high)
+    for got, scale, want, size, bits, positive in ((state.m[0], state.m_scale[0], m, size, upper, False),
+                                                   (state.v[0], state.v_scale[0], v.sqrt(), v.sqrt(), lower, True)):
         value, s, clear = coded(want, size, bits, positive)
         most = torch.zeros(s.numel() * G, dtype=torch.float64, device="cuda")
         most[:size.numel()] = size
@@ -191,6 +191,30 @@ def test_vectors_and_single_values_give_the_same_codes(spread):
         assert torch.equal(a[0].view(BYTE), b[0].view(BYTE))
     if bool(torch.isfinite(state.m_scale[0]).all()):
         assert not state.m[0].view(E4M3).float()[::10].any() and not state.v[0][::10].any()
+
+
+def test_more_values_than_32_bits_count():
+    big, tail = 1 << 32, 1000
+    for bits in (8, 32):
+        if bits == 32 and torch.cuda.mem_get_info()[0] < 80 << 30:
+            continue
+        p0, g0, s0 = make(tail, BF16, BF16, bits, False)
+        p, g = (torch.zeros(big + tail, dtype=BF16, device="cuda") for _ in range(2))
+        state = ecc.adamw_state([p], bits)
+        ends = [slice(0, tail), slice(big, big + tail)]
+        for e in ends:
+            p[e], g[e], state.m[0][e], state.v[0][e] = p0, g0, s0.m[0], s0.v[0]
+            if bits == 8:
+                groups = slice(e.start // G, e.start // G + s0.m_scale[0].numel())
+                state.m_scale[0][groups], state.v_scale[0][groups] = s0.m_scale[0], s0.v_scale[0]
+        ecc.ecc_adamw([p], [g], state, step=3, seed=5, **HYPER)
+        for high, e in enumerate(ends):
+            groups = slice(e.start // G, e.start // G + -(-tail // G))
+            got = ecc.AdamWState([state.m[0][e]], [state.v[0][e]], *([[x[0][groups]] for x in state[2:4]] if bits == 8 else (None, None)))
+            check(p[e], got, p0, g0, s0, 3, seed=5, high=high, **HYPER)
+        assert not p[tail:big].any()
+        del p, g, state
+        torch.cuda.empty_cache()
 
 
 def test_nothing_beyond_the_tensors_is_written():
