@@ -253,8 +253,9 @@ ecc_status ecc_token_logprob_grad(const void *logits, uint64_t ld, uint32_t type
  *         tokens; each may be NULL.
  *   A row with a logit that is not finite has NaN results.
  *   ws    16-byte aligned scratch of ecc_linear_logprob_workspace_bytes(job)
- *         bytes (16 bytes a row for each 64 to 128 tokens of the vocabulary, and
- *         a copy of x and w whose rows are not on 16-byte boundaries).
+ *         bytes (16 bytes a row for each share of the vocabulary, which is 128
+ *         tokens or fewer for small products, and copies of x and w whose rows
+ *         are not on 16-byte boundaries).
  * vocab from 1 to 2^31 - 1, rows and K below 2^31; K = 0 gives logits of 0.
  * status and errors as for ecc_linear (`reserved` is 0).
  */

@@ -16,10 +16,8 @@
 
 namespace ecc {
 
-constexpr int kAdamThreads = 256;
 constexpr uint32_t kAdamGroup = ECC_ADAMW_GROUP;
 constexpr uint32_t kAdamVectors = 16; // of a tensor's kind: 16-byte accesses
-constexpr uint32_t kAdamTile = kAdamThreads / 32 * kAdamGroup; // values of a block's step
 
 struct AdamTensor {
     void *param;
@@ -258,7 +256,7 @@ __device__ __forceinline__ void write_values(void *p, uint64_t e0, uint32_t left
 }
 
 // A warp's group; everything is asked for before anything is used.  (67 M bf16
-// values with 8-bit states 259 us by values, 205 by vectors, with float32 states
+// values with 8-bit states 235 us by values, 187 by vectors, with float32 states
 // 282 and 229.)
 template <bool BYTES, bool VECTORS>
 __device__ __forceinline__ void update_group(const AdamTensor &t, uint32_t kind, uint64_t e0, uint32_t lane, const AdamStep &s)
@@ -389,13 +387,8 @@ __device__ __forceinline__ void update_group(const AdamTensor &t, uint32_t kind,
     }
 }
 
-// Blocks an SM: 4 for 8-bit states, whose instructions are the bound (265 M
-// values, bf16: 688 us, 3.9 TB/s; 3 blocks 722, 5 blocks 744), 2 for float32
-// states, which are bound by HBM (170 M values with masters: 785 us, 6.5 TB/s; 3
-// blocks 859).
-constexpr int kAdamBlocks = 2, kAdamBlocksBytes = 4;
 template <int CAP, bool BYTES>
-__global__ void __launch_bounds__(kAdamThreads, BYTES ? kAdamBlocksBytes : kAdamBlocks) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a)
+__global__ void __launch_bounds__(BYTES ? 1024 : 256, BYTES ? 1 : 2) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a)
 {
     const AdamStep s = step_of(a.h);
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -414,7 +407,7 @@ __global__ void __launch_bounds__(kAdamThreads, BYTES ? kAdamBlocksBytes : kAdam
         }
         const AdamTensor &t = a.t[at];
         const uint32_t kind = a.kind[at];
-        const uint64_t e0 = (uint64_t)(tile - a.first[at]) * kAdamTile + warp * kAdamGroup;
+        const uint64_t e0 = ((uint64_t)(tile - a.first[at]) * (blockDim.x / 32) + warp) * kAdamGroup;
         if (e0 >= t.n)
             continue;
         if ((kind & kAdamVectors) && e0 + kAdamGroup <= t.n)
@@ -479,9 +472,37 @@ bool apart(const ecc_adamw_job &j)
     return true;
 }
 
-// the next tensors with states of the one kind
-template <int CAP, bool BYTES> ecc_status launch_tensors(const ecc_adamw_job &j, const AdamHyper &h, uint64_t &next, cudaStream_t st)
+// A launch's threads a block and blocks an SM.  Float32 states are bound by HBM,
+// where fewer accesses in flight are better: two blocks of 256 (170 M values with
+// masters: 793 us, 6.4 TB/s; three 859, one of 1024 877).  8-bit states are
+// bound by instructions, and take 1024 threads an SM: in one block while
+// parameters and gradients are of 16 bits (265 M values: 650 us, 4.1 TB/s; in
+// four 688, 768 threads 722), in four of 256 where more bytes move with a value
+// (67 M values with float32 gradients and masters: 240 us, in one 263; all in
+// float32 211 and 233).
+struct AdamShape {
+    int threads, blocks;
+};
+AdamShape adam_shape(const ecc_adamw_job &j, bool bytes)
 {
+    if (!bytes)
+        return {256, 2};
+    double total = 0, values = 0; // bytes of parameters, masters and gradients
+    for (uint64_t i = 0; i < j.count; ++i) {
+        const ecc_adamw_tensor &t = j.tensors[i];
+        if (t.state_type != ECC_E4M3)
+            continue;
+        total += (double)t.n * (type_bytes(t.param_type) * (t.master ? 1 : 2) + type_bytes(t.grad_type) + (t.master ? 8 : 0));
+        values += (double)t.n;
+    }
+    return total < 8 * values ? AdamShape{1024, 1} : AdamShape{256, 4};
+}
+
+// the next tensors with states of the one kind
+template <int CAP, bool BYTES>
+ecc_status launch_tensors(const ecc_adamw_job &j, const AdamHyper &h, AdamShape shape, uint64_t &next, cudaStream_t st)
+{
+    const uint64_t tile = (uint64_t)shape.threads / 32 * kAdamGroup; // values of a block's step
     AdamArgs<CAP> a;
     a.h = h;
     a.count = 0;
@@ -490,7 +511,7 @@ template <int CAP, bool BYTES> ecc_status launch_tensors(const ecc_adamw_job &j,
         const ecc_adamw_tensor &t = j.tensors[next];
         if ((t.state_type == ECC_E4M3) != BYTES)
             continue;
-        const uint64_t own = (t.n + kAdamTile - 1) / kAdamTile;
+        const uint64_t own = (t.n + tile - 1) / tile;
         if (!own)
             continue;
         if (tiles + own >= 1ull << 31)
@@ -507,8 +528,7 @@ template <int CAP, bool BYTES> ecc_status launch_tensors(const ecc_adamw_job &j,
     const int sms = sm_count();
     if (sms <= 0)
         return ECC_ERR_CUDA;
-    const uint64_t most = (uint64_t)sms * (BYTES ? kAdamBlocksBytes : kAdamBlocks);
-    adamw_kernel<CAP, BYTES><<<(unsigned)std::min(tiles, most), kAdamThreads, 0, st>>>(a);
+    adamw_kernel<CAP, BYTES><<<(unsigned)std::min(tiles, (uint64_t)sms * shape.blocks), shape.threads, 0, st>>>(a);
     return launch_status(cudaGetLastError());
 }
 
@@ -559,10 +579,11 @@ try {
     ecc_status rc = ECC_OK;
     // (parameters of 2 KiB or of 31 KiB: the launch copies them)
     cudaStream_t st = (cudaStream_t)stream;
+    const AdamShape wide = adam_shape(j, false), bytes = adam_shape(j, true);
     for (uint64_t next = 0; rc == ECC_OK && next < j.count;)
-        rc = j.count - next <= 24 ? launch_tensors<24, false>(j, h, next, st) : launch_tensors<448, false>(j, h, next, st);
+        rc = j.count - next <= 24 ? launch_tensors<24, false>(j, h, wide, next, st) : launch_tensors<448, false>(j, h, wide, next, st);
     for (uint64_t next = 0; rc == ECC_OK && next < j.count;)
-        rc = j.count - next <= 24 ? launch_tensors<24, true>(j, h, next, st) : launch_tensors<448, true>(j, h, next, st);
+        rc = j.count - next <= 24 ? launch_tensors<24, true>(j, h, bytes, next, st) : launch_tensors<448, true>(j, h, bytes, next, st);
     return rc;
 } catch (...) { // no memory for the list of spans
     return ECC_ERR_ARG;
