@@ -774,6 +774,11 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
         const uint32_t quad = warp & 3; // a warp reads the lanes of its number modulo 4
         const uint32_t j0 = warp < kFirstEpilogueWarp<MODE> + 4 ? 0 : g.bn / 2, j1 = j0 + g.bn / 2;
         uint32_t acc = 0, aph = 0;
+        // Results that leave through shared memory: which of this warp's two stages is written next.  It turns with
+        // every group of copies that is committed, over all of the warp's tiles (a tile may end after an odd number
+        // of them): a stage is written once all groups but the last one have read theirs, so the last one's has to
+        // be the other stage.
+        uint32_t turn = 0;
         const float scale = scale_of<MODE>(g.e);
         for (uint32_t t = pair; t < tiles; t += pairs) {
             const TilePos pos = tile_pos(t, g.ptiles, g.qtiles);
@@ -849,8 +854,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                     const uint32_t c0 = c - lane;
                     if (c0 >= g.cols)
                         continue;
-                    uint8_t *at = smem_raw + (stage0 - smem_u32(smem_raw)) + g.stages * stage_bytes + (warp - 2) * 2 * g.staged +
-                                  (j & 32 ? g.staged : 0);
+                    uint8_t *at = smem_raw + (stage0 - smem_u32(smem_raw)) + g.stages * stage_bytes + ((warp - 2) * 2 + turn) * g.staged;
                     if (lane == 0)
                         tma_stores_read<1>();
                     __syncwarp();
@@ -861,6 +865,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                         tma_store(&omap, smem_u32(at), (int)(r0 + j), (int)c0);
                         tma_stores_commit();
                     }
+                    turn ^= 1;
                 }
                 if (acc)
                     aph ^= 1;
@@ -890,7 +895,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                     }
                     if (j >= left || c0 >= g.cols)
                         continue;
-                    uint8_t *at = stage + (j & 32 ? g.staged : 0);
+                    uint8_t *at = stage + turn * g.staged;
                     if (lane == 0)
                         tma_stores_read<1>();
                     __syncwarp();
@@ -914,6 +919,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                         }
                         tma_stores_commit();
                     }
+                    turn ^= 1;
                 }
                 if (acc)
                     aph ^= 1;
