@@ -217,7 +217,7 @@ ecc_status ecc_linear_logprob(const ecc_linear_logprob_job *job, void *ws, size_
 
 size_t ecc_linear_logprob_grad_workspace_bytes(const ecc_linear_logprob_grad_job *job)
 {
-    return job ? head_grad_plan(*job).bytes : 0;
+    return job && head_grad_ok(*job) ? head_grad_plan(*job).bytes : 0;
 }
 
 ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void *ws, size_t ws_bytes, uint32_t *status, void *stream)
