@@ -285,9 +285,9 @@ ecc_status ecc_linear_logprob(const ecc_linear_logprob_job *job, void *ws, size_
  *         negative or >= vocab take no part in dlogprob.
  *   dw    [vocab, K] of dw_type (in_type or F32).
  *   dx, dw: NULL if not wanted.
- *   t is rounded to in_type before the products; with F16 the rows' largest
- *   dlogprob and dentropy give a power of two that keeps small probabilities
- *   in its range.
+ *   t is rounded to in_type before the products; with F16 the largest finite
+ *   dlogprob (of rows with a token) and dentropy give a power of two that
+ *   keeps small probabilities in its range.
  *   ws    16-byte aligned scratch of ecc_linear_logprob_grad_workspace_bytes(job)
  *         bytes (t of a piece, at most 256 MiB or 512 bytes a row, dx's sum
  *         over the pieces, copies as above).

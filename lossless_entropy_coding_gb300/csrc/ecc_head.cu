@@ -74,14 +74,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 
 // f[0] = 2^k, f[1] = 2^-k: t's magnitudes are at most max(|dlogprob| + |dentropy|
 // (log p + H) p), the latter below 16, and f[0] brings that to 2^14, so that a
-// float16 t keeps probabilities down to 2^-28 of it to 10 bits.
-__global__ void __launch_bounds__(1024) factor_kernel(const float *dlogprob, const float *dentropy, uint64_t rows, float *f)
+// float16 t keeps probabilities down to 2^-28 of it to 10 bits.  Only what t is
+// made of counts: no dlogprob of a row without a token, whatever it holds, and
+// no row whose t is not finite (dx of the other rows is).
+__global__ void __launch_bounds__(1024)
+    factor_kernel(const float *dlogprob, const float *dentropy, const int64_t *tokens, uint64_t rows, uint64_t vocab, float *f)
 {
     __shared__ float s[32];
     let_next_start();
     float top = 0.f;
-    for (uint64_t i = threadIdx.x; i < rows; i += 1024)
-        top = fmaxf(top, (dlogprob ? fabsf(dlogprob[i]) : 0.f) + (dentropy ? 16.f * fabsf(dentropy[i]) : 0.f));
+    for (uint64_t i = threadIdx.x; i < rows; i += 1024) {
+        const bool has = dlogprob && tokens && tokens[i] >= 0 && tokens[i] < (int64_t)vocab;
+        const float most = (has ? fabsf(dlogprob[i]) : 0.f) + (dentropy ? 16.f * fabsf(dentropy[i]) : 0.f);
+        top = fmaxf(top, most < INFINITY ? most : 0.f);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
@@ -93,7 +99,7 @@ __global__ void __launch_bounds__(1024) factor_kernel(const float *dlogprob, con
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        const int k = top > 0.f && top < INFINITY ? max(-100, min(100, 14 - ilogbf(top))) : 0;
+        const int k = top > 0.f ? max(-113, min(112, 14 - ilogbf(top))) : 0;
         if (threadIdx.x < 2)
             f[threadIdx.x] = ldexpf(1.f, threadIdx.x ? -k : k);
     }
@@ -245,9 +251,9 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
         // (as the call's first launch it starts after the one before it has ended, which may read this workspace)
         cudaError_t e = cudaSuccess;
         if (behind) {
-            e = launch_behind(factor_kernel, dim3(1), 1024, 0, st, j.dlogprob, j.dentropy, j.rows, factor);
+            e = launch_behind(factor_kernel, dim3(1), 1024, 0, st, j.dlogprob, j.dentropy, j.tokens, j.rows, j.vocab, factor);
         } else {
-            factor_kernel<<<1, 1024, 0, st>>>(j.dlogprob, j.dentropy, j.rows, factor);
+            factor_kernel<<<1, 1024, 0, st>>>(j.dlogprob, j.dentropy, j.tokens, j.rows, j.vocab, factor);
             e = cudaGetLastError();
         }
         const ecc_status rc = launch_status(e);
