@@ -89,12 +89,13 @@ __device__ __forceinline__ float rsqrt_approx(float x)
     return y;
 }
 // sqrt(x), x >= 0: a Newton step on the approximate reciprocal root (the
-// result is the nearest float32 but for about one in a million)
+// result is the nearest float32 but for about one in a million).  The step is
+// NaN, from 0 times infinity, where x is its own root: 0 and infinity.
 __device__ __forceinline__ float2 root2(float2 x)
 {
     const float2 y = make_float2(rsqrt_approx(x.x), rsqrt_approx(x.y)), r = mul2(x, y);
     const float2 e = fma2(mul2(r, both(-1.f)), r, x), f = fma2(e, mul2(y, both(0.5f)), r);
-    return make_float2(x.x > 0.f ? f.x : x.x, x.y > 0.f ? f.y : x.y);
+    return make_float2(f.x == f.x ? f.x : x.x, f.y == f.y ? f.y : x.y);
 }
 
 // p, m, v of two values.  The roundings of the moments are those of separate

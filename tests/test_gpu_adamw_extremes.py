@@ -1,0 +1,50 @@
+"""AdamW where float32's range ends: gradients whose squares are infinite.
+
+The second moment is then infinity in float32, its root too, and the step
+m / (root + eps) zero: the parameter only decays.  Tolerance: p (1 - lr
+weight_decay) is two roundings of 2^-24, and half a step of the parameter's
+type."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import lossless_entropy_coding_gb300 as ecc  # noqa: E402
+import test_gpu_adamw as adamw  # noqa: E402
+
+F32, BF16, BYTE, E4M3, G = torch.float32, torch.bfloat16, torch.uint8, torch.float8_e4m3fn, ecc.ADAMW_GROUP
+HYPER = adamw.HYPER
+
+
+@pytest.mark.parametrize("skew", [0, 3])
+@pytest.mark.parametrize("ptype,gtype,bits,master", [(F32, F32, 32, False), (BF16, BF16, 32, True), (BF16, F32, 8, True), (F32, BF16, 8, False)])
+@pytest.mark.parametrize("size,grad_scale", [(1e20, 1.0), (-3e38, 1.0), (2e10, 1e10)])
+def test_squares_beyond_the_range(ptype, gtype, bits, master, size, grad_scale, skew):
+    n = 4 * G + 100
+    p, g, state = adamw.make(n, ptype, gtype, bits, master, skew=skew)
+    far = torch.zeros(n, dtype=torch.bool, device="cuda")
+    far[[5, G + 1, G + 2, n - 1]] = True
+    groups = torch.tensor([True, True, False, False, True], device="cuda")
+    g /= grad_scale
+    clean = g.clone()
+    g[far] = size
+    values = state.master[0] if master else p
+    for step in (1, 2, 3):
+        old_p, old, was = p.clone(), adamw.copied(state), values.clone()
+        q, s2 = p.clone(), adamw.copied(state)
+        ecc.ecc_adamw([p], [g], state, step=step, grad_scale=grad_scale, **HYPER)
+        ecc.ecc_adamw([q], [clean], s2, step=step, grad_scale=grad_scale, **HYPER)
+        want = was.double()[far] * (1 - HYPER["lr"] * HYPER["weight_decay"])
+        assert bool(((values.double()[far] - want).abs() <= (2.0**-22 + torch.finfo(values.dtype).eps / 2) * want.abs()).all())
+        if bits == 32:
+            assert bool(torch.isinf(state.v[0][far]).all()) and bool(torch.isfinite(state.m[0]).all())
+            assert torch.equal(p[~far], q[~far]) and torch.equal(state.v[0][~far], s2.v[0][~far])
+            # (the others' moments are the clean ones: the next steps start from them)
+        else:
+            assert torch.equal(torch.isnan(state.v_scale[0]), groups) and torch.equal(torch.isnan(state.m_scale[0]), groups)
+            whole = ~groups.repeat_interleave(G)[:n]
+            assert torch.equal(p[~far], q[~far]) and torch.equal(state.m[0][whole], s2.m[0][whole])
+            break                                        # (a group of NaN stays one)
