@@ -156,7 +156,9 @@ __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c
 }
 
 // A group's scales from the bits of its largest magnitudes (a NaN or infinity
-// lies above all others); returns 448 / largest
+// lies above all others); returns 448 / largest, which is finite from
+// kAdamLeast on, or 0 below it.
+constexpr float kAdamLeast = 1.5046328e-36f; // 2^-119; 448 / float32's largest is 1.3166e-36
 __device__ __forceinline__ float group_scale(float *scale, uint32_t bits, bool root, bool finite, bool write)
 {
     float top = __uint_as_float(bits);
@@ -164,7 +166,7 @@ __device__ __forceinline__ float group_scale(float *scale, uint32_t bits, bool r
         top = root2(both(top)).x;
     if (write)
         *scale = finite ? __fmul_rn(top, 1.f / 448.f) : __int_as_float(0x7FC00000);
-    return finite && top > 1e-36f ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
+    return finite && top >= kAdamLeast ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
 }
 
 // 8 values from element i, as read: 4-byte types fill both vectors

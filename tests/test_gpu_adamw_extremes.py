@@ -1,9 +1,12 @@
-"""AdamW where float32's range ends: gradients whose squares are infinite.
+"""AdamW where float32's range ends: gradients whose squares are infinite, groups
+of 8-bit states whose largest value is next to nothing.
 
 The second moment is then infinity in float32, its root too, and the step
 m / (root + eps) zero: the parameter only decays.  Tolerance: p (1 - lr
 weight_decay) is two roundings of 2^-24, and half a step of the parameter's
-type."""
+type.  A group's codes are within a step of e4m3 of value / scale, which is
+off by 2^-21 of itself.  Scales below float32's smallest normal value (2^-126)
+have a rounding of 2^-150 more, relative to at least 2^-119 / 448: 2^-22."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -48,3 +51,30 @@ def test_squares_beyond_the_range(ptype, gtype, bits, master, size, grad_scale, 
             whole = ~groups.repeat_interleave(G)[:n]
             assert torch.equal(p[~far], q[~far]) and torch.equal(state.m[0][whole], s2.m[0][whole])
             break                                        # (a group of NaN stays one)
+
+
+@pytest.mark.parametrize("skew", [0, 3])
+@pytest.mark.parametrize("top", [0.9e-36, 1.05e-36, 1.1e-36, 1.3e-36, 1.32e-36, 2.0**-119, 1.6e-36, 3e-36, 1e-35, 1e-30])
+def test_groups_of_next_to_nothing(top, skew):
+    """m = (1 - beta1) g of at most `top`: codes and scale hold it from 2^-119 on, below that the codes are zeros."""
+    n = 2 * G + 60
+    p, g, state = (torch.zeros(n + 16, dtype=t, device="cuda")[skew:skew + n] for t in (F32, F32, BYTE))
+    state = ecc.AdamWState([state], [state.clone()], [torch.zeros(3, device="cuda")], [torch.zeros(3, device="cuda")])
+    gen = torch.Generator("cuda").manual_seed(1)
+    share = torch.rand(n, generator=gen, device="cuda") * 2 - 1
+    share[[0, G, 2 * G]] = 1.0
+    share[[1, G + 7, 2 * G + 3]] = 0.0
+    m = (share.double() * top).float()
+    g.copy_(m)
+    ecc.ecc_adamw([p], [g], state, step=1, beta1=0.0, lr=0.0, seed=3)
+    value = state.m[0].view(E4M3).double()
+    assert not bool(state.v[0].any()) and not bool(p.any())
+    if float(m[0]) < 2.0**-119:
+        assert not bool(value.any())
+        return
+    scale = m[0].double() / 448
+    assert bool(((state.m_scale[0].double() - scale).abs() <= 2.0**-21 * scale).all())
+    assert bool((value[[0, G, 2 * G]] == 448).all()) and not bool(value[[1, G + 7, 2 * G + 3]].any())
+    want = (m.double() / scale).clamp(-448, 448)
+    step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0**-6))) - 3)
+    assert bool(((value - want).abs() <= 1.01 * step).all())
