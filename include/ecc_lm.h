@@ -175,8 +175,12 @@ ecc_status ecc_gated_linear(const ecc_gated_linear_job *job, void *ws, size_t ws
  *   dw_gate, dw_up  [N, K] of dw_type (in_type or F32), both or neither.
  *   dbias_gate, dbias_up  float32[N], both or neither.
  *   dx, dw_*, dbias_*: NULL if not wanted.
- *   tg and tu, each times its scale's share of the larger scale, are rounded to
- *   in_type before the products; the dbias sums are taken before that.
+ *   tg and tu are rounded to in_type before the products; the dbias sums are
+ *   taken before that.  BF16: each times its scale's share of the larger scale.
+ *   F16: for dx the same, times a power of two that brings the largest finite
+ *   value to 2^14; for the weights' gradients each as it is, times a power of
+ *   two of its own that does (so that products dy u outside float16's range
+ *   and scales far apart cost no bits; the workspace holds both forms).
  * ws, status and errors as for ecc_linear.
  */
 typedef struct ecc_gated_linear_grad_job {

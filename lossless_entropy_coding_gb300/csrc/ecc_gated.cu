@@ -21,15 +21,110 @@
 
 namespace ecc {
 
+// What tg and tu are rounded to.  bfloat16 has float32's exponents: both halves
+// of one t, each times its scale's share of the larger scale, for all three
+// products.  float16 has not: a product dy u may leave its range, or lose its
+// bits below it, where dx and the weights' gradients are ordinary numbers.  So
+// gated_range_kernel finds the largest |tg| and |tu| first, and a power of two
+// brings the largest value of an operand to 2^14.  dx's operand (t) needs one
+// power for both halves, since its reduction runs over them; the weights'
+// gradients are different rows of theirs (tw), and each half has its own power
+// there, so that the smaller one of very unequal halves keeps its bits too.
+// (8192 x 8192 x 4096 float16 1.51 ms, 257 x 1000 x 771 39 us with cold caches;
+// with one t in float16's own range 1.37 ms and 28 us.)
 struct GatedSlopeParams {
     const void *dy, *gate, *up;
-    void *t;     // [M, 2 * np]; NULL: only the sums
-    float *part; // [parts][2 * N]; NULL: no sums
+    void *t, *tw; // [M, 2 * np], for dx and (float16) for the weights' gradients; NULL: not wanted
+    float *part;  // [parts][2 * N]; NULL: no sums
     uint64_t M, N, np, lddy, ldgate, ldup;
     float gate_factor, up_factor; // of t's two halves
     uint32_t act, parts;
     uint32_t *status;
+    float2 *range; // float16: a block's largest |tg| and |tu|, of `ranges` blocks
+    uint32_t ranges;
+    float *factor; // float16: the inverse powers of two of t, of tw's gates and of its ups
 };
+
+// tg and tu of 2 H values, in place of g and u
+template <int H>
+__device__ __forceinline__ void gated_slopes(uint32_t by, const float2 (&v)[H], float2 (&g)[H], float2 (&u)[H])
+{
+    auto each = [&](auto act) {
+        constexpr uint32_t ACT = decltype(act)::value;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float2 slope = act_slope2<ACT>(g[i]), value = act_value2<ACT>(g[i]);
+            g[i] = mul2(mul2(v[i], u[i]), slope);
+            u[i] = mul2(v[i], value);
+        }
+    };
+    if (by == ECC_ACT_RELU)
+        each(std::integral_constant<uint32_t, ECC_ACT_RELU>());
+    else if (by == ECC_ACT_GELU)
+        each(std::integral_constant<uint32_t, ECC_ACT_GELU>());
+    else if (by == ECC_ACT_GELU_TANH)
+        each(std::integral_constant<uint32_t, ECC_ACT_GELU_TANH>());
+    else if (by == ECC_ACT_SILU)
+        each(std::integral_constant<uint32_t, ECC_ACT_SILU>());
+    else
+        each(std::integral_constant<uint32_t, ECC_ACT_NONE>());
+}
+
+// the larger one of x and a finite |v|
+__device__ __forceinline__ float finite_max(float x, float v) { return fabsf(v) < INFINITY ? fmaxf(x, fabsf(v)) : x; }
+// the block's largest values, in every thread (called by all of them)
+__device__ __forceinline__ float2 block_range(float2 top)
+{
+    __shared__ float2 s[kRowThreads / 32];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        top.x = fmaxf(top.x, __shfl_xor_sync(~0u, top.x, o));
+        top.y = fmaxf(top.y, __shfl_xor_sync(~0u, top.y, o));
+    }
+    if ((threadIdx.x & 31) == 0)
+        s[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRowThreads / 32; ++i)
+        top = make_float2(fmaxf(top.x, s[i].x), fmaxf(top.y, s[i].y));
+    return top;
+}
+
+// The largest |tg| and |tu| that are finite, a pair for each block.  Pieces of
+// 32 * V columns and 64 rows in turns.
+constexpr uint32_t kRangeBlocks = 608, kRangeRows = 64; // four blocks an SM
+template <typename T, typename PT, int V>
+__global__ void __launch_bounds__(kRowThreads) gated_range_kernel(const __grid_constant__ GatedSlopeParams p)
+{
+    constexpr int H = (V + 1) / 2;
+    let_next_start();
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const uint64_t across = (p.N + 32 * V - 1) / (32 * V), pieces = across * ((p.M + kRangeRows - 1) / kRangeRows);
+    float2 top = both(0.f);
+    for (uint64_t i = blockIdx.x; i < pieces; i += gridDim.x) {
+        const uint64_t c = (i % across * 32 + tx) * V, r0 = i / across * kRangeRows, r1 = min(p.M, r0 + kRangeRows);
+        if (c >= p.N)
+            continue;
+#pragma unroll 2
+        for (uint64_t r = r0 + ty; r < r1; r += 8) {
+            float2 v[H], g[H], u[H];
+            load_values<T, V>(p.dy, r * p.lddy + c, v);
+            load_values<PT, V>(p.gate, r * p.ldgate + c, g);
+            load_values<PT, V>(p.up, r * p.ldup + c, u);
+            gated_slopes(p.act, v, g, u);
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                top.x = finite_max(finite_max(top.x, g[k].x), g[k].y);
+                top.y = finite_max(finite_max(top.y, u[k].x), u[k].y);
+            }
+        }
+    }
+    top = block_range(top);
+    if (threadIdx.x == 0)
+        p.range[blockIdx.x] = top;
+    // (launched behind the padding: whatever waits for this kernel waits for both)
+    wait_for_previous();
+}
 
 // a block: 32 * V columns, one share of the rows, eight warps a row each
 template <typename T, typename PT, int V>
@@ -43,6 +138,24 @@ __global__ void __launch_bounds__(kRowThreads) gated_slope_kernel(const __grid_c
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const uint64_t c = ((uint64_t)blockIdx.x * 32 + tx) * V;
     const uint64_t per = (p.M + p.parts - 1) / p.parts, r0 = blockIdx.y * per, r1 = min(p.M, r0 + per);
+    float gate_factor = p.gate_factor, up_factor = p.up_factor;
+    float2 tw_factor = both(1.f);
+    if constexpr (std::is_same_v<T, __half>) {
+        if (p.range) {
+            wait_for_previous();
+            float2 top = both(0.f);
+            for (uint32_t i = threadIdx.x; i < p.ranges; i += kRowThreads)
+                top = make_float2(fmaxf(top.x, p.range[i].x), fmaxf(top.y, p.range[i].y));
+            top = block_range(top);
+            const int kt = half_power(fmaxf(fabsf(gate_factor) * top.x, fabsf(up_factor) * top.y));
+            const int kg = half_power(top.x), ku = half_power(top.y);
+            gate_factor *= ldexpf(1.f, kt);
+            up_factor *= ldexpf(1.f, kt);
+            tw_factor = make_float2(ldexpf(1.f, kg), ldexpf(1.f, ku));
+            if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 3)
+                p.factor[threadIdx.x] = ldexpf(1.f, threadIdx.x == 0 ? -kt : threadIdx.x == 1 ? -kg : -ku);
+        }
+    }
     float2 sg[H], su[H];
 #pragma unroll
     for (int i = 0; i < H; ++i)
@@ -55,47 +168,38 @@ __global__ void __launch_bounds__(kRowThreads) gated_slope_kernel(const __grid_c
                 load_values<T, V>(p.dy, r * p.lddy + c, v);
                 load_values<PT, V>(p.gate, r * p.ldgate + c, g);
                 load_values<PT, V>(p.up, r * p.ldup + c, u);
-                auto each = [&](auto act) {
-                    constexpr uint32_t ACT = decltype(act)::value;
-#pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const float2 slope = act_slope2<ACT>(g[i]), value = act_value2<ACT>(g[i]);
-                        g[i] = mul2(mul2(v[i], u[i]), slope);
-                        u[i] = mul2(v[i], value);
-                    }
-                };
-                if (p.act == ECC_ACT_RELU)
-                    each(std::integral_constant<uint32_t, ECC_ACT_RELU>());
-                else if (p.act == ECC_ACT_GELU)
-                    each(std::integral_constant<uint32_t, ECC_ACT_GELU>());
-                else if (p.act == ECC_ACT_GELU_TANH)
-                    each(std::integral_constant<uint32_t, ECC_ACT_GELU_TANH>());
-                else if (p.act == ECC_ACT_SILU)
-                    each(std::integral_constant<uint32_t, ECC_ACT_SILU>());
-                else
-                    each(std::integral_constant<uint32_t, ECC_ACT_NONE>());
+                gated_slopes(p.act, v, g, u);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     sg[i] = add2(sg[i], g[i]);
                     su[i] = add2(su[i], u[i]);
-                    g[i] = mul2(g[i], both(p.gate_factor));
-                    u[i] = mul2(u[i], both(p.up_factor));
                 }
             } else { // the halves' ends, which the products read
 #pragma unroll
                 for (int i = 0; i < H; ++i)
                     g[i] = u[i] = both(0.f);
             }
-            if (p.t) {
-                T *o = static_cast<T *>(p.t) + r * 2 * p.np + c;
-                if constexpr (V == 1) {
-                    *o = from_f32<T>(g[0].x);
-                    o[p.np] = from_f32<T>(u[0].x);
-                } else {
-                    *reinterpret_cast<uint4 *>(o) = pack2<T>(g);
-                    *reinterpret_cast<uint4 *>(o + p.np) = pack2<T>(u);
+            auto store = [&](void *t, float fg, float fu) {
+                float2 a[H], b[H];
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    a[i] = mul2(g[i], both(fg));
+                    b[i] = mul2(u[i], both(fu));
                 }
-            }
+                T *o = static_cast<T *>(t) + r * 2 * p.np + c;
+                if constexpr (V == 1) {
+                    *o = from_f32<T>(a[0].x);
+                    o[p.np] = from_f32<T>(b[0].x);
+                } else {
+                    *reinterpret_cast<uint4 *>(o) = pack2<T>(a);
+                    *reinterpret_cast<uint4 *>(o + p.np) = pack2<T>(b);
+                }
+            };
+            if (p.t)
+                store(p.t, gate_factor, up_factor);
+            if constexpr (std::is_same_v<T, __half>)
+                if (p.tw)
+                    store(p.tw, tw_factor.x, tw_factor.y);
         }
     // (launched behind the padding, which it does not read: whatever waits for this kernel waits for both)
     wait_for_previous();
@@ -184,19 +288,24 @@ bool gated_grad_ok(const ecc_gated_linear_grad_job &j)
 struct GatedGradPlan {
     uint64_t np; // columns of a half of t
     uint32_t parts;
-    size_t t_bytes, part_bytes, bytes;
+    bool own_tw; // float16: the weights' gradients have an operand of their own
+    size_t t_bytes, tw_bytes, range_bytes, part_bytes, bytes;
 };
 GatedGradPlan gated_grad_plan(const ecc_gated_linear_grad_job &j)
 {
     GatedGradPlan g{};
     g.np = (j.N + 63) / 64 * 64;
-    g.t_bytes = j.dx || j.dw_gate ? pad256(j.M * 2 * g.np * type_bytes(j.in_type)) : 0;
+    g.own_tw = j.in_type == ECC_F16;
+    const size_t t = pad256(j.M * 2 * g.np * type_bytes(j.in_type));
+    g.t_bytes = j.dx || (j.dw_gate && !g.own_tw) ? t : 0;
+    g.tw_bytes = j.dw_gate && g.own_tw ? t : 0;
+    g.range_bytes = g.own_tw && g.t_bytes + g.tw_bytes ? 256 + pad256(kRangeBlocks * sizeof(float2)) : 0;
     // 64 rows a block, or down to 16 (two a warp) while there are fewer blocks than about two an SM: 257 x 1000
     // takes 11 us on 16 blocks
     const uint64_t across = (j.N + 255) / 256;
     g.parts = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({kGatedParts, std::max(j.M / 64, 304 / std::max<uint64_t>(across, 1)), j.M / 16}));
     g.part_bytes = j.dbias_gate ? pad256(g.parts * 2 * j.N * sizeof(float)) : 0;
-    g.bytes = g.t_bytes + g.part_bytes;
+    g.bytes = g.t_bytes + g.tw_bytes + g.range_bytes + g.part_bytes;
     if (j.dx)
         g.bytes += copy_bytes(j.w_gate, j.ldgate, j.N, j.K, j.in_type) + copy_bytes(j.w_up, j.ldup, j.N, j.K, j.in_type);
     if (j.dw_gate)
@@ -210,13 +319,22 @@ template <typename T, typename PT> ecc_status gated_slope_launch(const GatedSlop
     // eight values a load where the rows allow it
     const bool v8 = p.N % 8 == 0 && whole(p.dy, p.lddy, sizeof(T)) && whole(p.gate, p.ldgate, sizeof(PT)) &&
                     whole(p.up, p.ldup, sizeof(PT));
+    auto launch = [&](auto f, dim3 grid) {
+        if (behind)
+            return launch_status(launch_behind(f, grid, kRowThreads, 0, st, p));
+        f<<<grid, kRowThreads, 0, st>>>(p);
+        return launch_status(cudaGetLastError());
+    };
+    if constexpr (std::is_same_v<T, __half>) {
+        if (p.range) {
+            const ecc_status rc = launch(v8 ? gated_range_kernel<T, PT, 8> : gated_range_kernel<T, PT, 1>, dim3(p.ranges));
+            if (rc != ECC_OK)
+                return rc;
+            behind = true;
+        }
+    }
     const uint64_t per = v8 ? 256 : 32;
-    const dim3 grid((unsigned)((p.np + per - 1) / per), p.parts);
-    const auto f = v8 ? gated_slope_kernel<T, PT, 8> : gated_slope_kernel<T, PT, 1>;
-    if (behind)
-        return launch_status(launch_behind(f, grid, kRowThreads, 0, st, p));
-    f<<<grid, kRowThreads, 0, st>>>(p);
-    return launch_status(cudaGetLastError());
+    return launch(v8 ? gated_slope_kernel<T, PT, 8> : gated_slope_kernel<T, PT, 1>, dim3((unsigned)((p.np + per - 1) / per), p.parts));
 }
 template <typename T> ecc_status gated_slope_launch(const GatedSlopeParams &p, uint32_t pre_type, bool behind, cudaStream_t st)
 {
@@ -310,6 +428,11 @@ ecc_status ecc_gated_linear_grad(const ecc_gated_linear_grad_job *job, void *ws,
     uint8_t *w = (uint8_t *)ws;
     void *t = g.t_bytes ? w : nullptr;
     w += g.t_bytes;
+    void *tw = g.tw_bytes ? w : nullptr;
+    w += g.tw_bytes;
+    float *factor = g.range_bytes && (t || tw) ? (float *)w : nullptr; // three, then the ranges
+    float2 *range = factor ? (float2 *)(w + 256) : nullptr;
+    w += g.range_bytes;
     float *part = j.dbias_gate ? (float *)w : nullptr;
     w += g.part_bytes;
     ecc_status rc = ECC_OK;
@@ -322,10 +445,13 @@ ecc_status ecc_gated_linear_grad(const ecc_gated_linear_grad_job *job, void *ws,
     dw.P.mn = dx.P.mn = dx.P2.mn = true;
     // the products' common scale is the larger one; t's halves carry what is left
     const float scale = std::max(std::fabs(j.scale), std::fabs(j.up_scale)), inv = scale > 0.f ? 1.f : 0.f;
-    const bool slope = j.N && (t || part);
+    const bool slope = j.N && (t || tw || part);
     if (slope) {
-        const GatedSlopeParams p{j.dy, j.pre_gate, j.pre_up, t, part, j.M, j.N, g.np, j.lddy, j.ldpre_gate, j.ldpre_up,
-                                 inv > 0.f ? j.scale / scale : 0.f, inv > 0.f ? j.up_scale / scale : 0.f, j.act, g.parts, status};
+        // (a block of the range kernel for each of its pieces, or as many as there are places)
+        const uint64_t pieces = (j.N + 31) / 32 * ((j.M + kRangeRows - 1) / kRangeRows);
+        const GatedSlopeParams p{j.dy, j.pre_gate, j.pre_up, t, tw, part, j.M, j.N, g.np, j.lddy, j.ldpre_gate, j.ldpre_up,
+                                 inv > 0.f ? j.scale / scale : 0.f, inv > 0.f ? j.up_scale / scale : 0.f, j.act, g.parts, status,
+                                 range, (uint32_t)std::min<uint64_t>(pieces, kRangeBlocks), factor};
         rc = j.in_type == ECC_BF16 ? gated_slope_launch<bf16>(p, j.pre_type, own, st)
                                    : gated_slope_launch<__half>(p, j.pre_type, own, st);
         own = true;
@@ -341,7 +467,7 @@ ecc_status ecc_gated_linear_grad(const ecc_gated_linear_grad_job *job, void *ws,
     dx.e.out = j.dx;
     dx.e.ldout = j.lddx;
     dx.e.out_type = j.in_type;
-    dw.Q = {t, 2 * g.np, true};
+    dw.Q = {g.own_tw ? tw : t, 2 * g.np, true};
     dw.rows = 2 * g.np;
     dw.cols = j.K;
     dw.K = j.M;
@@ -352,7 +478,11 @@ ecc_status ecc_gated_linear_grad(const ecc_gated_linear_grad_job *job, void *ws,
     dw.e.ldout2 = j.lddw_up;
     dw.e.rswitch = g.np;
     dw.e.rows2 = j.N;
-    dx.e.scale = dw.e.scale = scale;
+    dx.e.scale = scale;
+    dw.e.scale = g.own_tw ? j.scale : scale;
+    dw.e.scale2 = g.own_tw ? j.up_scale : scale;
+    dx.e.factor = factor;
+    dw.e.factor = factor ? factor + 1 : nullptr;
     dx.e.out_scale = dw.e.out_scale = 1.f;
     const bool want_dx = j.dx && j.M && j.K, want_dw = j.dw_gate && j.N && j.K;
     if (rc == ECC_OK && want_dx && want_dw)

@@ -225,6 +225,14 @@ template <int MODE> __device__ __forceinline__ float scale_of(const Epilogue &e)
         return e.factor ? e.scale * *e.factor : e.scale;
 }
 
+// the scale of the output that row r0 belongs to
+__device__ __forceinline__ float scale_at(const Epilogue &e, uint64_t r0, float scale)
+{
+    if (!e.rswitch || r0 < e.rswitch)
+        return scale;
+    return e.factor ? e.scale2 * e.factor[1] : e.scale2;
+}
+
 // The same for results that leave through shared memory (no pre, no residual):
 // a warp's 32 rows of 32 columns at `stage`, a row after the other.  8192 x
 // 16384 x 64 68 us, 4 TB/s (103 by store_rows); at a reduction of 1024 156 us
@@ -565,7 +573,7 @@ __device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint3
         else if constexpr (MODE == kSlopes)
             store_slopes(g.e, a, r0 + j, c, scale, slope.token - (int64_t)(g.e.first + r0 + j), slope);
         else
-            finish(g.e, a, res, r0 + j, min(8u, j1 - j), c, bias, scale);
+            finish(g.e, a, res, r0 + j, min(8u, j1 - j), c, bias, scale_at(g.e, r0 + j, scale));
     }
     if constexpr (MODE == kStats)
         g.e.part[(r0 / g.bn * g.split + share) * g.cols + c] = make_float4(p.m, p.s, p.t, 0.f);
@@ -902,7 +910,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                     if constexpr (MODE == kGated)
                         finish_gated_staged(g.e, a, at, bias, lane);
                     else
-                        finish_staged(g.e, a, at, lane, bias, scale);
+                        finish_staged(g.e, a, at, lane, bias, scale_at(g.e, r0 + j, scale));
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
@@ -952,7 +960,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                         finish_gated(g.e, a, r0 + j, (uint32_t)min((uint64_t)32, left - j), c, col_ok, bias, lane);
                 } else {
                     if (col_ok && j < left)
-                        finish(g.e, a, v, r0 + j, (uint32_t)min((uint64_t)32, left - j), c, bias, scale);
+                        finish(g.e, a, v, r0 + j, (uint32_t)min((uint64_t)32, left - j), c, bias, scale_at(g.e, r0 + j, scale));
                 }
             };
             for (uint32_t j = j0; j < j1; j += 64) { // (bn is 128 or 256)
@@ -1028,7 +1036,7 @@ __device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, 
                 if (col_ok)
                     store_slopes(g.e, a, r0 + j, c, scale, slope.token - (int64_t)(g.e.first + r0 + j), slope);
             } else if (col_ok)
-                finish(g.e, a, res, r0 + j, n, c, bias, scale);
+                finish(g.e, a, res, r0 + j, n, c, bias, scale_at(g.e, r0 + j, scale));
         } else {
             keep_part(part, a, j, quad * 32 + lane);
         }

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        const int k = top > 0.f ? max(-113, min(112, 14 - ilogbf(top))) : 0;
+        const int k = half_power(top);
         if (threadIdx.x < 2)
             f[threadIdx.x] = ldexpf(1.f, threadIdx.x ? -k : k);
     }

@@ -42,6 +42,10 @@ static __global__ void __launch_bounds__(kRowThreads) sum_parts_kernel(const flo
     *(c < n1 ? out + c : out2 + (c - n1)) = s;
 }
 
+// k such that 2^k brings the largest of a float16 operand's magnitudes, `top`,
+// to at least 2^14 and below 2^15 (as far as 2^k and 2^-k are ordinary numbers)
+__device__ __forceinline__ int half_power(float top) { return top > 0.f ? max(-113, min(112, 14 - ilogbf(top))) : 0; }
+
 // Rows of `cols` elements to rows of ldd elements on 16-byte boundaries, for
 // up to three operands in one launch (blockIdx.y): the two vectors around each
 // 16 bytes, shifted, at the rate of a copy (820 MB read and written in 118 us;
