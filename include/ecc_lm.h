@@ -341,7 +341,8 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
  *           float32 read by the kernel in place of step, lr and grad_scale (for
  *           a captured step that is replayed), or NULL.
  * All arrays contiguous, aligned to an element; none that is written may
- * overlap another one of the job.  Tensors with n = 0 are passed over.
+ * overlap another one of the job (gradients and what step_at, lr_at and
+ * grad_scale_at point to included).  Tensors with n = 0 are passed over.
  * Errors: ECC_ERR_ARG (a NULL or misaligned pointer, overlapping arrays, a
  * type not listed, n >= 2^40, beta outside [0, 1), eps below 0, a value that is
  * not finite, step = 0), ECC_ERR_CUDA.

@@ -444,11 +444,14 @@ bool by_vectors(const ecc_adamw_tensor &t)
            (states & (t.state_type == ECC_E4M3 ? 7 : 15)) == 0;
 }
 
-// Whether two of the written arrays overlap (a tensor given twice would be
-// updated by two warps at once).
+// Whether nothing that is written overlaps anything else (a tensor given twice
+// would be updated by two warps at once, a gradient in another's parameter read
+// before or after its update).
 bool apart(const ecc_adamw_job &j)
 {
-    std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+    using Span = std::pair<uintptr_t, uintptr_t>; // first byte, end
+    const auto by_first = [](const Span &a, const Span &b) { return a.first < b.first; };
+    std::vector<Span> spans; // that are written, in order
     spans.reserve(j.count * 6);
     auto add = [&](const void *p, uint64_t bytes) {
         if (p)
@@ -468,11 +471,19 @@ bool apart(const ecc_adamw_job &j)
             add(t.v_scale, scales);
         }
     }
-    std::sort(spans.begin(), spans.end());
+    std::sort(spans.begin(), spans.end(), by_first);
     for (size_t i = 1; i < spans.size(); ++i)
         if (spans[i].first < spans[i - 1].second)
             return false;
-    return true;
+    // the last one that starts before an array's end has ended before it starts
+    const auto clear_of = [&](const void *p, uint64_t bytes) {
+        const auto next = std::lower_bound(spans.begin(), spans.end(), Span((uintptr_t)p + bytes, 0), by_first);
+        return !p || next == spans.begin() || (next - 1)->second <= (uintptr_t)p;
+    };
+    for (uint64_t i = 0; i < j.count; ++i)
+        if (j.tensors[i].n && !clear_of(j.tensors[i].grad, j.tensors[i].n * type_bytes(j.tensors[i].grad_type)))
+            return false;
+    return clear_of(j.step_at, sizeof(int64_t)) && clear_of(j.lr_at, sizeof(float)) && clear_of(j.grad_scale_at, sizeof(float));
 }
 
 // A launch's threads a block and blocks an SM.  Float32 states are bound by HBM,
