@@ -785,7 +785,10 @@ def ecc_adamw(params, grads, state: AdamWState, step, lr=1e-3, beta1: float = 0.
     rest = (step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed)
     if stream is None:
         return m.adamw(params, grads, *state, *rest)
-    if any(p.device != stream.device for p in params[:1]):
+    if not isinstance(params, (list, tuple)) or not isinstance(grads, (list, tuple)):
+        raise EccError(ERR_ARG, "ecc_adamw: params and grads")
+    # (those that are updated are all of one device, or refused)
+    if any(getattr(p, "device", None) != stream.device for p, g in zip(params, grads) if g is not None):
         raise EccError(ERR_ARG, "ecc_adamw: stream of another device")
     with _torch().cuda.stream(stream):
         return m.adamw(params, grads, *state, *rest)
