@@ -772,7 +772,7 @@ def adamw_state(params, bits: int = 32, master: bool = False) -> AdamWState:
         return [torch.zeros(-(-p.numel() // ADAMW_GROUP), device=p.device) for p in params] if bits == 8 else None
 
     return AdamWState(zeros(), zeros(), scales(), scales(),
-                      [p.float() if p.dtype != torch.float32 else None for p in params] if master else None)
+                      [p.detach().float() if p.dtype != torch.float32 else None for p in params] if master else None)
 
 
 def ecc_adamw(params, grads, state: AdamWState, step, lr=1e-3, beta1: float = 0.9, beta2: float = 0.95,

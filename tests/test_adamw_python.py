@@ -18,3 +18,14 @@ def test_a_stream_of_another_device_than_the_tensors_that_are_updated():
     for params, grads in ((x, [x]), ([x], x), (None, None), ([x], [x])):     # lists, and tensors of a GPU
         with pytest.raises(ecc.EccError):
             ecc.ecc_adamw(params, grads, state, step=1, stream=SimpleNamespace(device=a))
+
+
+def test_masters_are_apart_from_autograd():
+    params = [torch.nn.Parameter(torch.randn(5).to(t)) for t in (torch.bfloat16, torch.float16, torch.float32)]
+    params.append((params[0] * 2))                        # with a graph behind it
+    state = ecc.adamw_state(params, 8, master=True)
+    for p, m in zip(params, state.master):
+        if p.dtype == torch.float32:
+            assert m is None
+        else:
+            assert m.dtype == torch.float32 and not m.requires_grad and m.grad_fn is None and torch.equal(m, p.detach().float())
