@@ -345,7 +345,7 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
  * grad_scale_at point to included).  Tensors with n = 0 are passed over.
  * Errors: ECC_ERR_ARG (a NULL or misaligned pointer, overlapping arrays, a
  * type not listed, n >= 2^40, beta outside [0, 1), eps below 0, a value that is
- * not finite, step = 0), ECC_ERR_CUDA.
+ * not finite in float32, step = 0), ECC_ERR_CUDA.
  */
 #define ECC_ADAMW_GROUP 256
 typedef struct ecc_adamw_tensor {

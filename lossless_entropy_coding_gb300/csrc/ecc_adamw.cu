@@ -548,9 +548,10 @@ ecc_status launch_tensors(const ecc_adamw_job &j, const AdamHyper &h, AdamShape 
 
 bool job_ok(const ecc_adamw_job &j)
 {
-    if ((j.count && !j.tensors) || j.reserved || !std::isfinite(j.lr) || !(j.beta1 >= 0 && j.beta1 < 1) ||
-        !(j.beta2 >= 0 && j.beta2 < 1) || !(j.eps >= 0) || !std::isfinite(j.eps) || !std::isfinite(j.weight_decay) ||
-        !std::isfinite(j.grad_scale) || (!j.step_at && j.step < 1) || ((uintptr_t)j.step_at & 7) || !aligned_to(j.lr_at, ECC_F32) ||
+    const auto number = [](double v) { return std::isfinite((float)v); };
+    if ((j.count && !j.tensors) || j.reserved || !number(j.lr) || !(j.beta1 >= 0 && j.beta1 < 1) ||
+        !(j.beta2 >= 0 && j.beta2 < 1) || !(j.eps >= 0) || !number(j.eps) || !number(j.weight_decay) || !number(j.grad_scale) ||
+        (!j.step_at && j.step < 1) || ((uintptr_t)j.step_at & 7) || !aligned_to(j.lr_at, ECC_F32) ||
         !aligned_to(j.grad_scale_at, ECC_F32))
         return false;
     for (uint64_t i = 0; i < j.count; ++i)
