@@ -337,6 +337,7 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
  *           0.95 to a sixth, at 0.999 to more than the root, which wants float32
  *           states.  A group with a NaN or an infinity gets scales of NaN, and
  *           one of magnitudes below 2^-119 (1.5e-36) zeros.
+ *   eps     0, or any positive number; below 2^-126 it counts as that.
  *   step    1 for the first.  step_at, lr_at, grad_scale_at: device int64 and
  *           float32 read by the kernel in place of step, lr and grad_scale (for
  *           a captured step that is replayed), or NULL.

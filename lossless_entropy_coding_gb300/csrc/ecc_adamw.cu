@@ -578,7 +578,8 @@ try {
     // (beta = 0: 1 - beta^step is 1 for every step)
     h.log_beta1 = j.beta1 > 0 ? (float)std::log(j.beta1) : -200.f;
     h.log_beta2 = j.beta2 > 0 ? (float)std::log(j.beta2) : -200.f;
-    h.eps = (float)j.eps;
+    // (the reciprocal takes a subnormal denominator for 0, and 0 / eps is 0)
+    h.eps = j.eps > 0 ? std::max((float)j.eps, std::numeric_limits<float>::min()) : 0.f;
     h.weight_decay = (float)j.weight_decay;
     h.lr = (float)j.lr;
     h.grad_scale = (float)j.grad_scale;

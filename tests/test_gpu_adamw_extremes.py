@@ -78,3 +78,16 @@ def test_groups_of_next_to_nothing(top, skew):
     want = (m.double() / scale).clamp(-448, 448)
     step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0**-6))) - 3)
     assert bool(((value - want).abs() <= 1.01 * step).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 1.1e-38, 1.2e-38])
+def test_an_epsilon_next_to_nothing(eps, bits):
+    """Values without a gradient or moments stay where they are; the others step by lr times their sign."""
+    p = torch.randn(1000, device="cuda")
+    g = torch.randn(1000, device="cuda")
+    g[::3] = 0
+    q, state = p.clone(), ecc.adamw_state([p], bits)
+    ecc.ecc_adamw([q], [g], state, step=1, lr=0.125, weight_decay=0.0, eps=eps)
+    # m / sqrt(v) is 1 to 2^-19, the parameter rounds to 2^-24 of at most 8
+    assert bool(((p - q) - 0.125 * torch.sign(g)).abs().max() < 2.0**-20) and torch.equal(p[::3], q[::3])
