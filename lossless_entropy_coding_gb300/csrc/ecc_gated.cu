@@ -401,8 +401,11 @@ ecc_status ecc_gated_linear(const ecc_gated_linear_job *job, void *ws, size_t ws
     }
     uint8_t *w = (uint8_t *)ws;
     Product p{};
-    const bool copied = readable({{j.x, j.ldx, j.M, j.K, &p.Q}, {j.w_gate, j.ldgate, j.N, j.K, &p.P}, {j.w_up, j.ldup, j.N, j.K, &p.P2}},
-                                 j.in_type, w, st);
+    bool copied;
+    const ecc_status rc = readable({{j.x, j.ldx, j.M, j.K, &p.Q}, {j.w_gate, j.ldgate, j.N, j.K, &p.P}, {j.w_up, j.ldup, j.N, j.K, &p.P2}},
+                                   j.in_type, w, st, copied);
+    if (rc != ECC_OK)
+        return rc;
     p.rows = j.M;
     p.cols = j.N;
     p.K = j.K;
@@ -435,13 +438,15 @@ ecc_status ecc_gated_linear_grad(const ecc_gated_linear_grad_job *job, void *ws,
     w += g.range_bytes;
     float *part = j.dbias_gate ? (float *)w : nullptr;
     w += g.part_bytes;
-    ecc_status rc = ECC_OK;
     // read down their columns
     Product dx{}, dw{};
-    bool own = readable({{j.x, j.ldx, j.dw_gate ? j.M : 0, j.K, &dw.P},
-                         {j.w_gate, j.ldgate, j.dx ? j.N : 0, j.K, &dx.P},
-                         {j.w_up, j.ldup, j.dx ? j.N : 0, j.K, &dx.P2}},
-                        j.in_type, w, st);
+    bool own;
+    ecc_status rc = readable({{j.x, j.ldx, j.dw_gate ? j.M : 0, j.K, &dw.P},
+                              {j.w_gate, j.ldgate, j.dx ? j.N : 0, j.K, &dx.P},
+                              {j.w_up, j.ldup, j.dx ? j.N : 0, j.K, &dx.P2}},
+                             j.in_type, w, st, own);
+    if (rc != ECC_OK)
+        return rc;
     dw.P.mn = dx.P.mn = dx.P2.mn = true;
     // the products' common scale is the larger one; t's halves carry what is left
     const float scale = std::max(std::fabs(j.scale), std::fabs(j.up_scale)), inv = scale > 0.f ? 1.f : 0.f;

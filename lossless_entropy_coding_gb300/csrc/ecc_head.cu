@@ -210,8 +210,10 @@ ecc_status ecc_linear_logprob(const ecc_linear_logprob_job *job, void *ws, size_
     w += pad256(j.rows * sizeof(float));
     p.e.part = (float4 *)w;
     w += pad256((size_t)parts * j.rows * sizeof(float4));
-    const bool copied = readable({{j.x, j.ldx, j.rows, j.K, &p.P}, {j.w, j.ldw, j.vocab, j.K, &p.Q}}, j.in_type, w, st);
-    const ecc_status rc = gemm(p, j.in_type, status, true, copied, st);
+    bool copied;
+    ecc_status rc = readable({{j.x, j.ldx, j.rows, j.K, &p.P}, {j.w, j.ldw, j.vocab, j.K, &p.Q}}, j.in_type, w, st, copied);
+    if (rc == ECC_OK)
+        rc = gemm(p, j.in_type, status, true, copied, st);
     if (rc != ECC_OK)
         return rc;
     uint32_t each = 1; // rows of a joining block: as many as leave a block an SM
@@ -246,7 +248,10 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
     void *sum = at;
     at += g.sum_bytes;
     Operand x, w;
-    bool behind = readable({{j.x, j.ldx, j.rows, j.K, &x}, {j.w, j.ldw, j.vocab, j.K, &w}}, j.in_type, at, st);
+    bool behind;
+    ecc_status rc = readable({{j.x, j.ldx, j.rows, j.K, &x}, {j.w, j.ldw, j.vocab, j.K, &w}}, j.in_type, at, st, behind);
+    if (rc != ECC_OK)
+        return rc;
     if (factor) {
         // (as the call's first launch it starts after the one before it has ended, which may read this workspace)
         cudaError_t e = cudaSuccess;
@@ -256,13 +261,11 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
             factor_kernel<<<1, 1024, 0, st>>>(j.dlogprob, j.dentropy, j.tokens, j.rows, j.vocab, factor);
             e = cudaGetLastError();
         }
-        const ecc_status rc = launch_status(e);
-        if (rc != ECC_OK)
+        if ((rc = launch_status(e)) != ECC_OK)
             return rc;
         behind = true;
     }
     bool clear = true;
-    ecc_status rc = ECC_OK;
     for (uint64_t v = 0; rc == ECC_OK && v < j.vocab; v += g.piece) {
         const uint64_t n = std::min(g.piece, j.vocab - v);
         const Operand piece{(const uint8_t *)w.p + v * w.ld * 2, w.ld, false};

@@ -242,8 +242,9 @@ ecc_status ecc_linear(const ecc_linear_job *job, void *ws, size_t ws_bytes, uint
     }
     uint8_t *w = (uint8_t *)ws;
     Operand x, wt;
-    const bool copied = readable({{j.x, j.ldx, j.M, j.K, &x}, {j.w, j.ldw, j.N, j.K, &wt}}, j.in_type, w, st);
-    return gemm({wt, x, j.M, j.N, j.K, e}, j.in_type, status, true, copied, st);
+    bool copied;
+    const ecc_status rc = readable({{j.x, j.ldx, j.M, j.K, &x}, {j.w, j.ldw, j.N, j.K, &wt}}, j.in_type, w, st, copied);
+    return rc != ECC_OK ? rc : gemm({wt, x, j.M, j.N, j.K, e}, j.in_type, status, true, copied, st);
 }
 
 size_t ecc_linear_grad_workspace_bytes(const ecc_linear_grad_job *job)
@@ -265,9 +266,11 @@ ecc_status ecc_linear_grad(const ecc_linear_grad_job *job, void *ws, size_t ws_b
     w += g.t_bytes;
     float *part = j.dbias ? (float *)w : nullptr;
     w += g.part_bytes;
-    ecc_status rc = ECC_OK;
     Operand x, wt; // read down their columns
-    bool own = readable({{j.x, j.ldx, j.dw ? j.M : 0, j.K, &x}, {j.w, j.ldw, j.dx ? j.N : 0, j.K, &wt}}, j.in_type, w, st);
+    bool own;
+    ecc_status rc = readable({{j.x, j.ldx, j.dw ? j.M : 0, j.K, &x}, {j.w, j.ldw, j.dx ? j.N : 0, j.K, &wt}}, j.in_type, w, st, own);
+    if (rc != ECC_OK)
+        return rc;
     x.mn = wt.mn = true;
     const bool slope = j.N && (j.M || j.dbias) && (g.make_t || j.dbias);
     if (slope) {

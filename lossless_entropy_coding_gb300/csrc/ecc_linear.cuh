@@ -235,14 +235,15 @@ inline size_t copy_bytes(const void *p, uint64_t ld, uint64_t rows, uint64_t col
 }
 
 // The operands (arrays of `type`), each itself or its copy at ws (advanced
-// past it); rows = 0: not wanted.  Whether something was launched.
+// past it); rows = 0: not wanted.  `launched`: whether something was.
 struct Array {
     const void *p;
     uint64_t ld, rows, cols;
     Operand *o;
 };
-inline bool readable(std::initializer_list<Array> arrays, uint32_t type, uint8_t *&ws, cudaStream_t st)
+inline ecc_status readable(std::initializer_list<Array> arrays, uint32_t type, uint8_t *&ws, cudaStream_t st, bool &launched)
 {
+    launched = false;
     PadJobs jobs{};
     int n = 0;
     uint64_t most = 0;
@@ -257,13 +258,14 @@ inline bool readable(std::initializer_list<Array> arrays, uint32_t type, uint8_t
         }
     }
     if (!n)
-        return false;
+        return ECC_OK;
     const dim3 grid((unsigned)std::min<uint64_t>((most + kRowThreads - 1) / kRowThreads, 1u << 15), n);
     if (type == ECC_E4M3)
         pad_rows_kernel<uint8_t><<<grid, kRowThreads, 0, st>>>(jobs);
     else
         pad_rows_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>(jobs);
-    return true;
+    launched = true;
+    return launch_status(cudaGetLastError());
 }
 
 template <typename T, bool GATED> void few_rows_launch(uint64_t M, FewRows p, int sms, cudaStream_t st)
