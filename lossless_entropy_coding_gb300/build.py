@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -44,11 +45,34 @@ def _deps():
     return files
 
 
+# Kernels whose warps share out the launch's registers among themselves, by the number that they are written for
+# (kStatsRegisters): with another number their launches are refused, so such a library is not built.
+STATS_SOURCE, STATS_KERNELS = "ecc_head_gemm.cu", r"gemm_pair_kernelILb0ELb0ELb[01]ELi3E"
+
+
+def check_registers(report: str, pattern: str, registers: int) -> None:
+    """report: what ptxas -v says of a file's kernels."""
+    found = re.findall(r"Compiling entry function '(\S+)'.*?Used (\d+) registers", report, re.S)
+    counts = {name: int(n) for name, n in found if re.search(pattern, name)}
+    if len(counts) != 2 or set(counts.values()) != {registers}:
+        raise RuntimeError(f"the statistics' kernels (8-bit and 16-bit operands) have to have {registers} registers a thread, "
+                           f"and this compiler gives {counts}: change kStatsRegisters and the shares beside it (ecc_gemm.cuh)")
+
+
 def _compile(src: str, nvcc: str, extra, out_dir: str = OUT_DIR) -> str:
     obj = os.path.join(out_dir, os.path.basename(src) + ".o")
     cmd = [nvcc, *ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
            *extra, "-c", src, "-o", obj]
-    subprocess.check_call(cmd)
+    if os.path.basename(src) != STATS_SOURCE:
+        subprocess.check_call(cmd)
+        return obj
+    r = subprocess.run([*cmd, "-Xptxas", "-v"], capture_output=True, text=True)
+    if r.returncode:
+        sys.stderr.write(r.stderr)
+        raise subprocess.CalledProcessError(r.returncode, cmd)
+    with open(os.path.join(CSRC, "ecc_gemm.cuh")) as f:
+        registers = int(re.search(r"kStatsRegisters = (\d+)", f.read()).group(1))
+    check_registers(r.stderr + r.stdout, STATS_KERNELS, registers)
     return obj
 
 

@@ -657,7 +657,9 @@ __device__ __forceinline__ TilePos tile_pos(uint32_t t, uint32_t ptiles, uint32_
 
 // kStats: the sums of 128 columns stay in a thread's registers, which the warps
 // that hold none of them give up: four warps of 40 and eight of 232, together
-// what twelve warps of 168 are launched with.
+// what twelve warps of 168 are launched with (the build checks that the
+// compiler gives this kernel 168, and the launch that it has them; 12 bytes a
+// thread spill).
 constexpr int kStatsThreads = 384, kStatsRegisters = 168;
 constexpr int kFewRegisters = 40, kManyRegisters = 232;
 static_assert(kFewRegisters + 2 * kManyRegisters <= 3 * kStatsRegisters, "more registers than the launch has");
