@@ -261,6 +261,7 @@ ecc_status ecc_token_logprob_grad(const void *logits, uint64_t ld, uint32_t type
  *         tokens or fewer for small products, and copies of x and w whose rows
  *         are not on 16-byte boundaries).
  * vocab from 1 to 2^31 - 1, rows and K below 2^31; K = 0 gives logits of 0.
+ * scale of any sign, its magnitude below 2^127 (here and in the gradient).
  * status and errors as for ecc_linear (`reserved` is 0).
  */
 typedef struct ecc_linear_logprob_job {

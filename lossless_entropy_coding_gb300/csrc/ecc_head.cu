@@ -114,9 +114,11 @@ namespace {
 // is a few percent of what the products move.
 constexpr size_t kPieceBytes = 256ull << 20;
 
+constexpr float kMostScale = 0x1p127f; // times log2 e it is finite
+
 bool head_ok(const ecc_linear_logprob_job &j)
 {
-    if ((j.in_type != ECC_BF16 && j.in_type != ECC_F16 && j.in_type != ECC_E4M3) || !std::isfinite(j.scale) || j.rows >= kMostDim ||
+    if ((j.in_type != ECC_BF16 && j.in_type != ECC_F16 && j.in_type != ECC_E4M3) || !(std::fabs(j.scale) < kMostScale) || j.rows >= kMostDim ||
         !j.vocab || j.vocab >= kMostDim || j.K >= kMostDim || j.reserved)
         return false;
     if (!j.rows)
@@ -142,7 +144,7 @@ Product head_product(const ecc_linear_logprob_job &j)
 
 bool head_grad_ok(const ecc_linear_logprob_grad_job &j)
 {
-    if ((j.in_type != ECC_BF16 && j.in_type != ECC_F16) || !std::isfinite(j.scale) || j.rows >= kMostDim || !j.vocab ||
+    if ((j.in_type != ECC_BF16 && j.in_type != ECC_F16) || !(std::fabs(j.scale) < kMostScale) || j.rows >= kMostDim || !j.vocab ||
         j.vocab >= kMostDim || j.K >= kMostDim || j.reserved || (j.dw && j.dw_type != j.in_type && j.dw_type != ECC_F32))
         return false;
     if (j.rows && (!j.lse || !aligned_to(j.lse, ECC_F32) || (j.dentropy && !j.entropy) || !aligned_to(j.entropy, ECC_F32) ||

@@ -45,3 +45,9 @@ def test_a_head_without_a_vocabulary_is_refused():
     from test_lm_more_arguments import head, head_grad
     for kw in (dict(vocab=0), dict(vocab=0, rows=0), dict(vocab=0, K=0)):
         assert head(ws=P, ws_bytes=1 << 30, **kw) == head_grad(ws=P, ws_bytes=1 << 30, **kw) == ecc.ERR_ARG
+
+
+def test_scales_whose_product_with_log2_e_is_infinite():
+    from test_lm_more_arguments import head, head_grad
+    for scale in (2.0**127, -(2.0**127), 3e38):
+        assert head(ws=P, ws_bytes=1 << 30, scale=scale) == head_grad(ws=P, ws_bytes=1 << 30, scale=scale) == ecc.ERR_ARG
