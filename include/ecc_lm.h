@@ -255,7 +255,10 @@ ecc_status ecc_token_logprob_grad(const void *logits, uint64_t ld, uint32_t type
  *         probability is 0.  A token >= vocab gets NaN.
  *   logprob, entropy, lse  float32[rows]; logprob is not written without
  *         tokens; each may be NULL.
- *   A row with a logit that is not finite has NaN results.
+ *   A row with a logit that is not finite has NaN results.  Exponentials are
+ *   computed to a relative 2^-22 (1 + |argument|); a logit's products are summed
+ *   by the tensor cores in accumulators of 512 (E4M3 1024) or, for few tokens, up
+ *   to a quarter of K, whose additions truncate, and those in float32.
  *   ws    16-byte aligned scratch of ecc_linear_logprob_workspace_bytes(job)
  *         bytes (16 bytes a row for each share of the vocabulary, which is 128
  *         tokens or fewer for small products, and copies of x and w whose rows
@@ -317,7 +320,8 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
  * grad_scale * grad, t = step:
  *   m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
- * in float32, with m and v as they are before they are stored.
+ * in float32, with m and v as they are before they are stored (the quotient's
+ * root and reciprocal to a relative 2^-22).
  *   param   [n] of param_type, grad [n] of grad_type (F32, BF16 or F16).
  *   master  float32[n] or NULL: with it, p is read from and written to it,
  *           and param receives its rounding.
@@ -333,7 +337,11 @@ ecc_status ecc_linear_logprob_grad(const ecc_linear_logprob_grad_job *job, void 
  *           value i are mix((i mod 2^32) ^ mix(mix(mix(seed) + step) + i /
  *           2^32)), the upper 16 for m, the lower for v, with mix(x): x ^= x >> 16,
  *           x *= 0x7FEB352D, x ^= x >> 15, x *= 0x846CA68B, x ^= x >> 16 in 32
- *           bits: the same call gives the same bytes.  A root is off by 4% a step on
+ *           bits (a mixing published by C. Wellons, "Prospecting for Hash
+ *           Functions", 2018): the same call gives the same bytes, and equal
+ *           places of a call's tensors have the same random bits (each value's
+ *           mean is kept all the same; calls with seeds of their own keep
+ *           tensors' roundings apart).  A root is off by 4% a step on
  *           average, and the errors of 1 / (1 - beta2) steps add up: at beta2 =
  *           0.95 to a sixth, at 0.999 to more than the root, which wants float32
  *           states.  A group with a NaN or an infinity gets scales of NaN, and

@@ -780,7 +780,9 @@ def ecc_adamw(params, grads, state: AdamWState, step, lr=1e-3, beta1: float = 0.
     """One step of AdamW, in place: params, grads lists of contiguous device
     tensors (a gradient of None leaves its parameter and state alone).  step
     counts from 1; step, lr and grad_scale may be device tensors of one value
-    (int64, float32, float32), which a captured and replayed call reads anew."""
+    (int64, float32, float32), which a captured and replayed call reads anew.
+    With 8-bit moments `seed` and step give the rounding's random bits, the
+    same for equal places of the call's tensors."""
     m = _torch_lib or _marshal()
     rest = (step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed)
     if stream is None:

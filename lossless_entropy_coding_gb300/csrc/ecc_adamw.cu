@@ -44,7 +44,9 @@ template <int CAP> struct AdamArgs {
     uint8_t kind[CAP];
 };
 
-// A mixing of 32-bit numbers: two multiplications between three shifts.
+// A mixing of 32-bit numbers: two multiplications between three shifts, with
+// the constants that C. Wellons published for it ("Prospecting for Hash
+// Functions", 2018).
 __host__ __device__ inline uint32_t mix32(uint32_t x)
 {
     x = (x ^ x >> 16) * 0x7FEB352Du;
