@@ -294,8 +294,9 @@ struct GatedGradPlan {
 GatedGradPlan gated_grad_plan(const ecc_gated_linear_grad_job &j)
 {
     GatedGradPlan g{};
-    g.np = (j.N + 63) / 64 * 64;
     g.own_tw = j.in_type == ECC_F16;
+    const uint64_t whole = g.own_tw ? 128 : 64; // the weights' gradients have a scale each: no half of a tile has rows of both
+    g.np = (j.N + whole - 1) / whole * whole;
     const size_t t = pad256(j.M * 2 * g.np * type_bytes(j.in_type));
     g.t_bytes = j.dx || (j.dw_gate && !g.own_tw) ? t : 0;
     g.tw_bytes = j.dw_gate && g.own_tw ? t : 0;

@@ -221,6 +221,8 @@ ecc_status make_plan(Plan &plan, const Product &x, const Shape &shape, uint32_t 
                 g.staged = (bytes + 127) / 128 * 128;
         }
     }
+    const uint32_t last = (uint32_t)(x.rows - (qtiles - 1) * g.bn), half = g.bn / 2; // rows of the last tile
+    g.odd = (up(std::min(last, half), 32) & 1) | (last > half ? (up(last - half, 32) & 1) << 1 : 0);
     if (!encode_tiled())
         return ECC_ERR_CUDA;
     g.qwide = x.Q.mn && make_wide_map(&plan.qm, x.Q, g.rows, x.K, type, qn / 64);

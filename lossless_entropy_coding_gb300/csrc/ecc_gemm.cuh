@@ -51,6 +51,7 @@ struct GemmArgs {
     uint32_t kswitch; // kDual: the reduction block where the second matrix starts
     bool pwide, qwide; // operands down their columns: one box for all of a tile's rows
     uint32_t staged;  // bytes of a warp's 32 rows if results leave through shared memory, or 0
+    uint32_t odd;     // then: whether the last tile's rows are an odd number of 32s in its first half (1), its second (2)
     bool one_box;     // kGated: P's map has both matrices, in turns of 16 rows
     uint64_t rows, cols;
     uint32_t kblocks; // reduction blocks of 128 bytes (64 reduction indices for MN-major operands)
@@ -225,14 +226,25 @@ template <int MODE> __device__ __forceinline__ float scale_of(const Epilogue &e)
         return e.factor ? e.scale * *e.factor : e.scale;
 }
 
-// the scale of the output that row r0 belongs to
-__device__ __forceinline__ float scale_at(const Epilogue &e, uint64_t r0, float scale)
+// the scale of the output that row r0 belongs to (only products of two operands down their columns have two)
+template <bool TWO> __device__ __forceinline__ float scale_at(const Epilogue &e, uint64_t r0, float scale)
 {
-    if (!e.rswitch || r0 < e.rswitch)
+    if (!TWO || !e.rswitch || r0 < e.rswitch)
         return scale;
     return e.factor ? e.scale2 * e.factor[1] : e.scale2;
 }
 
+// Results that leave through shared memory take a warp's two stages in turns:
+// 32 rows' stage is written once all copies but the last 32 rows' have read
+// theirs, which is the other stage's.  A tile starts with the first stage: behind
+// one that ended with it, after an odd number of 32 rows, the last copies have to
+// have read theirs too.  (A stage that turns on over the tiles took a register
+// too many, and spills: 8192 x 16384 x 64 76 us, 72 so.)
+__device__ __forceinline__ void first_stage_read(const GemmArgs &g, uint32_t lane, uint32_t j0)
+{
+    if (lane == 0 && (g.odd & (j0 ? 2 : 1)))
+        tma_stores_read<0>();
+}
 // The same for results that leave through shared memory (no pre, no residual):
 // a warp's 32 rows of 32 columns at `stage`, a row after the other.  8192 x
 // 16384 x 64 68 us, 4 TB/s (103 by store_rows); at a reduction of 1024 156 us
@@ -573,7 +585,7 @@ __device__ __forceinline__ void join_parts(const GemmArgs &g, uint32_t at, uint3
         else if constexpr (MODE == kSlopes)
             store_slopes(g.e, a, r0 + j, c, scale, slope.token - (int64_t)(g.e.first + r0 + j), slope);
         else
-            finish(g.e, a, res, r0 + j, min(8u, j1 - j), c, bias, scale_at(g.e, r0 + j, scale));
+            finish(g.e, a, res, r0 + j, min(8u, j1 - j), c, bias, scale_at<true>(g.e, r0 + j, scale));
     }
     if constexpr (MODE == kStats)
         g.e.part[(r0 / g.bn * g.split + share) * g.cols + c] = make_float4(p.m, p.s, p.t, 0.f);
@@ -784,11 +796,6 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
         const uint32_t quad = warp & 3; // a warp reads the lanes of its number modulo 4
         const uint32_t j0 = warp < kFirstEpilogueWarp<MODE> + 4 ? 0 : g.bn / 2, j1 = j0 + g.bn / 2;
         uint32_t acc = 0, aph = 0;
-        // Results that leave through shared memory: which of this warp's two stages is written next.  It turns with
-        // every group of copies that is committed, over all of the warp's tiles (a tile may end after an odd number
-        // of them): a stage is written once all groups but the last one have read theirs, so the last one's has to
-        // be the other stage.
-        uint32_t turn = 0;
         const float scale = scale_of<MODE>(g.e);
         for (uint32_t t = pair; t < tiles; t += pairs) {
             const TilePos pos = tile_pos(t, g.ptiles, g.qtiles);
@@ -797,6 +804,9 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
             const bool col_ok = c < g.cols;
             const float bias = bias_of<MODE>(g.e, c, col_ok, lane);
             const uint64_t left = g.rows - r0;
+            // (where there are two scales no half of a tile has rows of both; asked for with each 32 rows, 64 x 65536 x 4096
+            // down the columns takes 144 us in place of 139)
+            const float half_scale = scale_at<PMN && QMN>(g.e, r0 + j0, scale);
             if constexpr (MODE == kStats) {
                 const int64_t token = g.e.tokens && col_ok ? g.e.tokens[c] : -1;
                 float2 a[64]; // (kStats: bn is 256)
@@ -842,6 +852,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                     break;
                 }
                 tmem_fence_after();
+                if (g.staged)
+                    first_stage_read(g, lane, j0);
                 for (uint32_t j = j0; j < j1; j += 32) {
                     float a[32];
                     tmem_load32(tmem + (quad * 32 << 16) + acc * g.bn + j, a);
@@ -864,7 +876,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                     const uint32_t c0 = c - lane;
                     if (c0 >= g.cols)
                         continue;
-                    uint8_t *at = smem_raw + (stage0 - smem_u32(smem_raw)) + g.stages * stage_bytes + ((warp - 2) * 2 + turn) * g.staged;
+                    uint8_t *at = smem_raw + (stage0 - smem_u32(smem_raw)) + g.stages * stage_bytes + (warp - 2) * 2 * g.staged +
+                                  (j & 32 ? g.staged : 0);
                     if (lane == 0)
                         tma_stores_read<1>();
                     __syncwarp();
@@ -875,7 +888,6 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                         tma_store(&omap, smem_u32(at), (int)(r0 + j), (int)c0);
                         tma_stores_commit();
                     }
-                    turn ^= 1;
                 }
                 if (acc)
                     aph ^= 1;
@@ -894,6 +906,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                 tmem_fence_after();
                 uint8_t *stage = smem_raw + (stage0 - smem_u32(smem_raw)) + g.stages * stage_bytes + (warp - 2) * 2 * g.staged;
                 const uint32_t c0 = c - (MODE == kGated ? lane & 15 : lane);
+                first_stage_read(g, lane, j0);
                 for (uint32_t j = j0; j < j1; j += 32) {
                     float a[32];
                     tmem_load32(tmem + (quad * 32 << 16) + acc * g.bn + j, a);
@@ -905,14 +918,14 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                     }
                     if (j >= left || c0 >= g.cols)
                         continue;
-                    uint8_t *at = stage + turn * g.staged;
+                    uint8_t *at = stage + (j & 32 ? g.staged : 0);
                     if (lane == 0)
                         tma_stores_read<1>();
                     __syncwarp();
                     if constexpr (MODE == kGated)
                         finish_gated_staged(g.e, a, at, bias, lane);
                     else
-                        finish_staged(g.e, a, at, lane, bias, scale_at(g.e, r0 + j, scale));
+                        finish_staged(g.e, a, at, lane, bias, half_scale);
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
@@ -929,7 +942,6 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                         }
                         tma_stores_commit();
                     }
-                    turn ^= 1;
                 }
                 if (acc)
                     aph ^= 1;
@@ -962,7 +974,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                         finish_gated(g.e, a, r0 + j, (uint32_t)min((uint64_t)32, left - j), c, col_ok, bias, lane);
                 } else {
                     if (col_ok && j < left)
-                        finish(g.e, a, v, r0 + j, (uint32_t)min((uint64_t)32, left - j), c, bias, scale_at(g.e, r0 + j, scale));
+                        finish(g.e, a, v, r0 + j, (uint32_t)min((uint64_t)32, left - j), c, bias, half_scale);
                 }
             };
             for (uint32_t j = j0; j < j1; j += 64) { // (bn is 128 or 256)
@@ -1038,7 +1050,7 @@ __device__ __forceinline__ void split_columns(const GemmArgs &g, uint32_t tmem, 
                 if (col_ok)
                     store_slopes(g.e, a, r0 + j, c, scale, slope.token - (int64_t)(g.e.first + r0 + j), slope);
             } else if (col_ok)
-                finish(g.e, a, res, r0 + j, n, c, bias, scale_at(g.e, r0 + j, scale));
+                finish(g.e, a, res, r0 + j, n, c, bias, scale_at<true>(g.e, r0 + j, scale));
         } else {
             keep_part(part, a, j, quad * 32 + lane);
         }

@@ -24,8 +24,8 @@ struct Epilogue {
     uint64_t ldpre2;
     float scale2;
     bool swapped; // the ups' rows come before the gates' in each turn
-    // a second output: rows from rswitch on (a multiple of 64) go to out2, by
-    // scale2, and both have rows2 rows
+    // a second output: rows from rswitch on (a multiple of 64, of 128 where the
+    // scales differ) go to out2, by scale2, and both have rows2 rows
     void *out2;
     uint64_t ldout2, rswitch, rows2;
     const float *factor; // multiplies scale (read on the device; a second output's scale2: the next one); NULL: 1
