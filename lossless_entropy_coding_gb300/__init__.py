@@ -763,6 +763,7 @@ def adamw_state(params, bits: int = 32, master: bool = False) -> AdamWState:
     torch = _torch()
     if bits not in (8, 32):
         raise EccError(ERR_ARG, "adamw_state: bits")
+    params = list(params)
     kind = torch.float32 if bits == 32 else torch.uint8
 
     def zeros():

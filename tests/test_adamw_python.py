@@ -29,3 +29,12 @@ def test_masters_are_apart_from_autograd():
             assert m is None
         else:
             assert m.dtype == torch.float32 and not m.requires_grad and m.grad_fn is None and torch.equal(m, p.detach().float())
+
+
+def test_a_state_for_any_iterable_of_parameters():
+    layer = torch.nn.Linear(300, 5).to(torch.bfloat16)
+    for bits, master in ((32, False), (32, True), (8, False), (8, True)):
+        want, got = (ecc.adamw_state(p, bits, master) for p in (list(layer.parameters()), layer.parameters()))
+        for a, b in zip(want, got):
+            assert (a is None) == (b is None)
+            assert a is None or (len(a) == len(b) == 2 and all(p.shape == q.shape and p.dtype == q.dtype for p, q in zip(a, b)))
