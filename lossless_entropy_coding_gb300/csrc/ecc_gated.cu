@@ -6,9 +6,9 @@
 // (ecc_gemm.cuh, kGated), so that x is read once for both and neither g nor u
 // goes through memory unless it is wanted.  Backward: one elementwise kernel
 // makes tg = dy u act'(g) and tu = dy act(g) side by side, [M, 2 N'] with N' = N
-// rounded up to the products' block of 64; dx is one product whose reduction
-// runs over both weights (kDual), both weights' gradients are the rows of
-// another one.
+// rounded up to the products' block of 64 (float16: to 128, and twice, by powers
+// of two that another kernel finds); dx is one product whose reduction runs over
+// both weights (kDual), both weights' gradients are the rows of another one.
 //
 // 8192 x 16384 x 4096 bf16 with g and u kept takes 1.20 ms in a burst (1.83
 // PFLOP/s, the tensor pipe 89% active), 1.37 ms under the power limit; one token
@@ -255,7 +255,8 @@ bool gated_ok(const ecc_gated_linear_job &j)
 }
 
 // few_rows_kernel in place of the tensor cores' kernels, by the rule of the
-// linear layer over both weights together
+// linear layer over both weights together (16384 x 4096 bf16 one token 45.2 us,
+// 8 by the tensor cores 46.0; e4m3 26.8 by the tensor cores)
 bool gated_few_rows(const ecc_gated_linear_job &j)
 {
     if (j.M > 4 || !j.K)
