@@ -19,6 +19,9 @@
  *  - sums, statistics and products are held in float32; a value is rounded
  *    once, to nearest even, when it is stored.  A stored e4m3 byte holds
  *    value * y_scale, saturated to +-448, NaN kept;
+ *  - the tensor cores' additions truncate: a sum of K products of a matrix
+ *    product, float32 outputs' too, is off by up to (K + 8) 2^-23 of the sum of
+ *    their magnitudes (K = 3464: 4e-6 of the outputs' size on average);
  *  - outputs never depend on the order in which blocks run: the same call on
  *    the same inputs gives the same bits;
  *  - an output may not overlap an input unless the entry says so;
